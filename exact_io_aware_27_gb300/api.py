@@ -27,6 +27,7 @@ FA_ERR_UNSUPPORTED_DEVICE = -4
 FA_ERR_WORKSPACE_TOO_SMALL = -5
 FA_ERR_CUDA = -6
 FA_ERR_DEVICE_TIMEOUT = -7
+FA_ERR_BAD_INDEX = -8
 
 # Every entry point of include/fa.h and include/fa_selftest.h with its ctypes
 # signature: (restype, argtypes).
@@ -34,6 +35,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _S = ctypes.c_size_t
+_LL = ctypes.c_longlong
 SIGNATURES = {
     "fa_forward": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
     "fa_backward_workspace_size": (_S, [_I, _I, _I, _I, _I]),
@@ -54,6 +56,10 @@ SIGNATURES = {
     "fa_session_step": (_I, [_P, _P, _P, _P, _P, _I, _F, _P, _P, _P, _P, _P]),
     "fa_session_submit": (_I, [_P, _P, _P, _P, _P, _I, _F, _P, _P, _P, _P, _P]),
     "fa_session_sync": (_I, [_P]),
+    "fa_packed_plan_bytes": (_S, [_I, _I]),
+    "fa_packed_plan": (_I, [_P, _I, _I, _I, _P, _S, _P]),
+    "fa_packed_forward": (_I, [_P, _P, _P, _LL, _LL, _LL, _I, _I, _I, _I, _I, _F, _P, _I, _P, _P,
+                               _I, _P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_get_device_status": (_I, [ctypes.POINTER(_I)]),
     "fa_version": (_I, []),

@@ -5,7 +5,9 @@
 #include <mutex>
 
 #include "fa.h"
+#include "fa_check.h"
 #include "fa_internal.h"
+#include "fa_packed.h"
 #include "sm103.cuh"
 
 namespace fa {
@@ -156,6 +158,8 @@ int prepare_backward(const void* Q, const void* K, const void* V, const void* O,
 
 }  // namespace
 
+int require_device() { return check_device(); }
+
 int validate_sizes(int B, int H, int n, int m, int d) { return check_sizes(B, H, n, m, d); }
 
 int heads_per_group(int BH, int tiles_per_head) {
@@ -220,6 +224,7 @@ const char* fa_status_string(int status) {
     case FA_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
     case FA_ERR_CUDA: return "CUDA error";
     case FA_ERR_DEVICE_TIMEOUT: return "device barrier wait timed out";
+    case FA_ERR_BAD_INDEX: return "an index in a device table is out of range";
     default: return "unknown status";
   }
 }
@@ -380,13 +385,15 @@ int fa_standard_forward(const void* Q, const void* K, const void* V, int B, int 
 
 int fa_get_device_status(int* status_out) {
   if (!status_out) return FA_ERR_INVALID_ARG;
-  unsigned int f = 0, b = 0, t = 0, sd = 0;
+  unsigned int f = 0, b = 0, t = 0, sd = 0, pl = 0, pk = 0;
   if (forward_read_status(&f) != cudaSuccess || bwd_read_status(&b) != cudaSuccess ||
-      selftest_read_status(&t) != cudaSuccess || standard_read_status(&sd) != cudaSuccess)
+      selftest_read_status(&t) != cudaSuccess || standard_read_status(&sd) != cudaSuccess ||
+      plan_read_status(&pl) != cudaSuccess || packed_read_status(&pk) != cudaSuccess)
     return FA_ERR_CUDA;
-  const unsigned int bits = f | b | t | sd;
+  const unsigned int bits = f | b | t | sd | pl | pk;
   *status_out = (bits & kDeviceTimeoutBit)  ? FA_ERR_DEVICE_TIMEOUT
                 : (bits & kDeviceLayoutBit) ? FA_ERR_UNSUPPORTED_DEVICE
+                : (bits & kDeviceIndexBit)  ? FA_ERR_BAD_INDEX
                                             : FA_OK;
   return FA_OK;
 }

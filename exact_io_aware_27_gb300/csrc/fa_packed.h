@@ -1,0 +1,69 @@
+// Plans of packed batches (sequences one after another in one tensor), shared by
+// the plan kernel and the passes that read a plan.
+#pragma once
+
+#include "fa_internal.h"
+
+namespace fa {
+
+// One entry of a plan's work lists: a tile of one sequence.
+//   x  first row of the sequence in the packed tensors
+//   y  length of the sequence
+//   z  tile within the sequence
+//   w  first workspace row of the sequence (a multiple of kWorkspaceRowAlign)
+using PlanTile = int4;
+
+// The plan's first 64 bytes, written by the plan kernel.
+constexpr int kPlanMagic = 0x50415131;
+struct PlanHead {
+  int magic;        // kPlanMagic
+  int total, nseq;  // the sizes the plan was made for
+  int covered;      // rows the sequences cover; the rest of the tensors belongs to none
+  int tiles256;     // entries of the list of 256-row tiles (forward items)
+  int tiles128;     // entries of each list of 128-row tiles (backward blocks)
+  int pad[10];
+};
+static_assert(sizeof(PlanHead) == 64, "the lists start 64 bytes into a plan");
+
+// Where a plan's parts lie. The lists hold at most total / tile + nseq entries.
+struct PlanLayout {
+  long long cap256, cap128;
+  size_t off256, off_kv, off_q, off_scan, bytes;
+};
+inline PlanLayout plan_layout(int nseq, int total) {
+  PlanLayout l;
+  l.cap256 = (long long)total / 256 + nseq;
+  l.cap128 = (long long)total / 128 + nseq;
+  l.off256 = sizeof(PlanHead);
+  l.off_kv = l.off256 + (size_t)l.cap256 * sizeof(PlanTile);
+  l.off_q = l.off_kv + (size_t)l.cap128 * sizeof(PlanTile);
+  l.off_scan = l.off_q + (size_t)l.cap128 * sizeof(PlanTile);
+  l.bytes = l.off_scan + ((size_t)nseq + 1) * 2 * sizeof(int);
+  l.bytes = (l.bytes + 15) / 16 * 16;
+  return l;
+}
+
+// bf16 [rows, H, d] with `ld` elements from row to row, as boxes of 64 columns x
+// one head x box_rows rows with 128-byte swizzle (loads), or of 32 columns x one
+// head x 32 rows with 64-byte swizzle (stores).
+CUresult make_bf16_packed_map(CUtensorMap* map, const void* base, int rows, int H, int d,
+                              long long ld, int box_rows);
+CUresult make_bf16_packed_store_map(CUtensorMap* map, void* base, int rows, int H, int d,
+                                    long long ld);
+
+struct PackedFwdArgs {
+  const void *Q, *K, *V;
+  long long ldq, ldk, ldv;  // elements from row to row
+  void* O;
+  float* L;
+  const void* plan;
+  int total, nseq, Hq, Hkv, d, causal, fill;
+  float scale;
+};
+cudaError_t launch_packed_plan(const int* cu_seqlens, int nseq, int total, int causal, void* plan,
+                               cudaStream_t s);
+cudaError_t launch_packed_forward(const PackedFwdArgs& a, cudaStream_t s);
+cudaError_t plan_read_status(unsigned int* out);
+cudaError_t packed_read_status(unsigned int* out);
+
+}  // namespace fa

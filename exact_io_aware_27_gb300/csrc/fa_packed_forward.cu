@@ -1,0 +1,152 @@
+// The forward pass over packed sequences: the forward kernel (fa_forward.cuh) over
+// Q [total, Hq, d] and K, V [total, Hkv, d], whose rows are sequences one after
+// another; query head h reads key/value head h / (Hq / Hkv). Work items are (256-row
+// tile of a sequence, head), from the plan's list: heads a group at a time, inside a
+// group the heaviest tiles of all sequences first, and the query heads of one
+// key/value head next to each other, so that its K and V are read once into L2.
+//
+// A sequence's last key block and last query tile run into the next sequence's rows
+// (or into rows of no sequence): keys past the end are masked, their V rows are
+// zeroed in shared memory before the product reads them (the forward kernel's
+// kForeignTail), and query rows past the end stay in their own TMEM lanes and are
+// not stored.
+#include "fa_forward.cuh"
+#include "fa_packed.cuh"
+
+namespace fa {
+
+__device__ unsigned int g_packed_status;
+
+namespace {
+
+struct Packed {
+  struct Params {
+    const uint8_t* plan;
+    float* L;
+    __nv_bfloat16* O;
+    int total, nseq, Hq, per_kv, causal, group, fill;
+  };
+  struct View {
+    const Params& p;
+    int tiles, covered;
+  };
+  FA_DEV static View view(const Params& p) {
+    const PlanHead* head = reinterpret_cast<const PlanHead*>(p.plan);
+    const bool ok = plan_matches(head, p.total, p.nseq, status());
+    return {p, ok ? head->tiles256 : 0, ok ? head->covered : p.total};
+  }
+  struct Item {
+    PlanTile s;  // sequence start, length, 256-row tile
+    int h;
+  };
+  FA_DEV static unsigned int* status() { return &g_packed_status; }
+  static constexpr bool kForeignTail = true;
+  FA_DEV static int items(const View& g) { return g.tiles * g.p.Hq; }
+  FA_DEV static Item item(const View& g, int i) {
+    int rank, h;
+    grouped_tile(i, g.p.Hq, g.tiles, g.p.group, rank, h);
+    return {__ldg(reinterpret_cast<const PlanTile*>(g.p.plan + sizeof(PlanHead)) + rank), h};
+  }
+  FA_DEV static int first_query(const View&, const Item& it) { return it.s.z * 256; }
+  FA_DEV static int steps(const View& g, const Item& it, int t) {
+    return tile_steps(it.s.z * 256 + t * 128, it.s.y, it.s.y, g.p.causal);
+  }
+  FA_DEV static int keys(const View&, const Item& it) { return it.s.y; }
+  FA_DEV static int causal(const View& g) { return g.p.causal; }
+  FA_DEV static void load_q(void* dst, const CUtensorMap* map, uint64_t* f, int col, const View&,
+                            const Item& it, int t) {
+    tma_load_3d(dst, map, f, col, it.h, it.s.x + it.s.z * 256 + t * 128);
+  }
+  template <class C>
+  FA_DEV static uint32_t block_bytes(const View&, const Item&, int) {
+    return 2 * C::TILE;
+  }
+  template <class C>
+  FA_DEV static void load_kv(uint8_t* kdst, uint8_t* vdst, const CUtensorMap* mk,
+                             const CUtensorMap* mv, uint64_t* f, const View& g, const Item& it,
+                             int block) {
+    const int hk = it.h / g.p.per_kv, row = it.s.x + block * C::BN;
+#pragma unroll
+    for (int c = 0; c < C::KCH; ++c) {
+      tma_load_3d(kdst + c * C::CHUNK, mk, f, c * 64, hk, row);
+      tma_load_3d(vdst + c * C::CHUNK, mv, f, c * 64, hk, row);
+    }
+  }
+  template <int D>
+  FA_DEV static void store(const View& g, const Item& it, int t, int warp, int lane, uint32_t ocol,
+                           float m_ref, float l, uint8_t* stage, const CUtensorMap* mo, int d) {
+    const int q0 = it.s.z * 256 + t * 128 + warp * 32;  // within the sequence
+    const int row0 = it.s.x + q0, valid = it.s.y - q0;
+    const long long ld = (long long)g.p.Hq * d;
+    packed_rows_store<D>(ocol, 1.f / l, stage, mo, it.h, row0, valid, d,
+                         g.p.O + row0 * ld + (long long)it.h * d, ld);
+    if (lane < valid) g.p.L[(size_t)it.h * g.p.total + row0 + lane] = (m_ref + lg2(l)) * kLn2;
+  }
+  // Rows that no sequence covers: O = 0 and L = -inf (what attention to no key
+  // gives), where the caller asked for it.
+  FA_DEV static void idle_warps(const View& g, int thread, int threads, int d) {
+    const long long t = (long long)blockIdx.x * threads + thread;
+    const long long nt = (long long)gridDim.x * threads;
+    const Params& p = g.p;
+    if (p.fill & 1) zero_rows(p.O, g.covered, p.total, p.Hq * d, (long long)p.Hq * d, t, nt);
+    if (p.fill & 2) {
+      const long long rest = p.total - g.covered;
+      for (long long i = t; i < rest * p.Hq; i += nt)
+        p.L[(i / rest) * p.total + g.covered + i % rest] = -INFINITY;
+    }
+  }
+};
+
+template <int D>
+cudaError_t launch_packed_d(const PackedFwdArgs& a, cudaStream_t stream) {
+  using C = FwdCfg<D>;
+  CUtensorMap mq, mk, mv, mo;
+  if (make_bf16_packed_map(&mq, a.Q, a.total, a.Hq, a.d, a.ldq, C::BM) != CUDA_SUCCESS ||
+      make_bf16_packed_map(&mk, a.K, a.total, a.Hkv, a.d, a.ldk, C::BN) != CUDA_SUCCESS ||
+      make_bf16_packed_map(&mv, a.V, a.total, a.Hkv, a.d, a.ldv, C::BN) != CUDA_SUCCESS ||
+      make_bf16_packed_store_map(&mo, a.O, a.total, a.Hq, a.d, (long long)a.Hq * a.d) !=
+          CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  FwdParams p;
+  p.d = a.d;
+  p.scale_log2 = a.scale * 1.44269504088896340736f;
+  Packed::Params g;
+  g.plan = static_cast<const uint8_t*>(a.plan);
+  g.L = a.L;
+  g.O = static_cast<__nv_bfloat16*>(a.O);
+  g.total = a.total;
+  g.nseq = a.nseq;
+  g.Hq = a.Hq;
+  g.per_kv = a.Hq / a.Hkv;
+  g.causal = a.causal;
+  g.fill = a.fill;
+  // Whole key/value heads per group. The plan's tile count is known on the device
+  // only; the rows give it up to the sequences' last tiles.
+  const int tiles = ceil_div(a.total, 256);
+  g.group = round_up(heads_per_group(a.Hq, tiles), g.per_kv);
+  cudaError_t e = cudaFuncSetAttribute(fwd_kernel<D, Packed>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const long long items = plan_layout(a.nseq, a.total).cap256 * a.Hq;
+  const unsigned grid = (unsigned)(items < sms ? items : sms);
+  fwd_kernel<D, Packed><<<grid, C::THREADS, C::SMEM, stream>>>(mq, mk, mv, mo, p, g);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_packed_forward(const PackedFwdArgs& a, cudaStream_t s) {
+  return a.d > 64 ? launch_packed_d<128>(a, s) : launch_packed_d<64>(a, s);
+}
+
+cudaError_t packed_read_status(unsigned int* out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_packed_status, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_packed_status, &zero, sizeof(unsigned int));
+}
+
+}  // namespace fa

@@ -1,0 +1,177 @@
+// Plans of packed batches: from cu_seqlens on the device to the work lists of the
+// forward and backward passes, without a host synchronisation.
+//
+// A sequence of length n has ceil(n / 256) forward items per head and ceil(n / 128)
+// key blocks and query blocks. The persistent kernels deal a list out in snake order,
+// which balances only a list whose heaviest entries come first, so the three lists
+// are sorted by cost: under causal masking tile t of a forward or dQ list costs
+// t + 1 and key block t of a dK/dV list costs (blocks - t); without it every tile
+// costs its sequence's length. A counting sort over at most 1024 cost classes is
+// enough (the order inside a class does not matter, and no result depends on the
+// order of a list).
+//
+// One block of 1024 threads: the lists are short (a batch of 2^20 rows has 16384
+// entries in the longest), and a plan serves every layer that runs the batch.
+// Bounds that are not 0 = cu[0] <= cu[1] <= ... <= cu[nseq] <= total give empty
+// lists and raise kDeviceIndexBit.
+#include "fa_packed.h"
+#include "sm103.cuh"
+
+namespace fa {
+
+__device__ unsigned int g_plan_status;
+
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kBins = 1024;
+
+// Exclusive scan of one value per thread over the block; `total` gets the sum.
+__device__ int block_scan(int v, int* warp_sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // warp_sums of an earlier call have been read
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  total = warp_sums[31];
+  return x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
+}
+
+// Last i with first[i] <= x, for first[0] = 0 <= ... <= first[n] and x < first[n].
+__device__ int find_sequence(const int* first, int n, int x) {
+  int lo = 0, hi = n;  // first[lo] <= x < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) plan_kernel(const int* __restrict__ cu, int nseq,
+                                                        int total, int causal, uint8_t* plan,
+                                                        PlanLayout lay) {
+  __shared__ int warp_sums[32];
+  __shared__ int bins[kBins];
+  __shared__ int max_tiles;
+  const int tid = threadIdx.x;
+  PlanHead* head = reinterpret_cast<PlanHead*>(plan);
+
+  int bad = 0;
+  for (int i = tid; i < nseq; i += kThreads) bad |= cu[i] > cu[i + 1] ? 1 : 0;
+  if (tid == 0) {
+    bad |= (cu[0] != 0 || cu[nseq] > total) ? 1 : 0;
+    max_tiles = 0;
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) {
+      *head = PlanHead{kPlanMagic, total, nseq, total, 0, 0, {}};
+      atomicOr(&g_plan_status, kDeviceIndexBit);
+    }
+    return;
+  }
+
+  // Tiles before each sequence.
+  int* first128 = reinterpret_cast<int*>(plan + lay.off_scan);
+  int* first256 = first128 + nseq + 1;
+  int n128 = 0, n256 = 0, longest = 0;
+  for (int base = 0; base < nseq; base += kThreads) {
+    const int i = base + tid;
+    const int len = i < nseq ? cu[i + 1] - cu[i] : 0;
+    const int t128 = (len + 127) / 128, t256 = (len + 255) / 256;
+    longest = max(longest, t128);
+    int s128, s256;
+    const int e128 = block_scan(t128, warp_sums, s128);
+    const int e256 = block_scan(t256, warp_sums, s256);
+    if (i < nseq) {
+      first128[i] = n128 + e128;
+      first256[i] = n256 + e256;
+    }
+    n128 += s128;
+    n256 += s256;
+  }
+  atomicMax(&max_tiles, longest);
+  if (tid == 0) {
+    first128[nseq] = n128;
+    first256[nseq] = n256;
+    *head = PlanHead{kPlanMagic, total, nseq, cu[nseq], n256, n128, {}};
+  }
+  __syncthreads();
+  const int most = max_tiles;
+  int shift = 0;
+  while ((most >> shift) >= kBins) ++shift;
+
+  // list 0: forward items (256 rows); 1: key blocks; 2: query blocks (128 rows)
+  for (int list = 0; list < 3; ++list) {
+    const int n = list == 0 ? n256 : n128;
+    const int* first = list == 0 ? first256 : first128;
+    PlanTile* out = reinterpret_cast<PlanTile*>(
+        plan + (list == 0 ? lay.off256 : list == 1 ? lay.off_kv : lay.off_q));
+    auto entry = [&](int i, int& bin) {
+      const int s = find_sequence(first, nseq, i);
+      const int start = cu[s], len = cu[s + 1] - start, tile = i - first[s];
+      const int tiles = first[s + 1] - first[s];
+      const int cost = !causal ? (len + 127) / 128
+                       : list == 0 ? min(2 * (tile + 1), (len + 127) / 128)
+                       : list == 1 ? tiles - tile
+                                   : tile + 1;  // 1 <= cost <= most, in 128-row tiles
+      bin = (most - cost) >> shift;
+      return make_int4(start, len, tile, first128[s] * kWorkspaceRowAlign);
+    };
+    for (int b = tid; b < kBins; b += kThreads) bins[b] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+      int bin;
+      entry(i, bin);
+      atomicAdd(&bins[bin], 1);
+    }
+    __syncthreads();
+    int sum;
+    const int at = block_scan(bins[tid], warp_sums, sum);
+    bins[tid] = at;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+      int bin;
+      const PlanTile e = entry(i, bin);
+      out[atomicAdd(&bins[bin], 1)] = e;
+    }
+    __syncthreads();
+  }
+}
+static_assert(kBins == kThreads, "one cost class per thread in the scan");
+static_assert(kWorkspaceRowAlign == 128, "workspace rows are counted in 128-row tiles");
+
+}  // namespace
+
+cudaError_t launch_packed_plan(const int* cu_seqlens, int nseq, int total, int causal, void* plan,
+                               cudaStream_t s) {
+  plan_kernel<<<1, kThreads, 0, s>>>(cu_seqlens, nseq, total, causal,
+                                     static_cast<uint8_t*>(plan), plan_layout(nseq, total));
+  return cudaGetLastError();
+}
+
+cudaError_t plan_read_status(unsigned int* out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_plan_status, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_plan_status, &zero, sizeof(unsigned int));
+}
+
+}  // namespace fa

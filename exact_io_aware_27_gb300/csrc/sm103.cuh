@@ -19,6 +19,9 @@ constexpr unsigned int kDeviceTimeoutBit = 1u;
 // Set by a kernel that found its dynamic shared memory at an address its layout
 // does not allow (it then returns before touching anything).
 constexpr unsigned int kDeviceLayoutBit = 2u;
+// Set by a kernel that met an index outside its range in a device table (sequence
+// bounds, a plan, a page number) and did not follow it.
+constexpr unsigned int kDeviceIndexBit = 4u;
 constexpr long long kWaitMaxCycles = 4000000000ll;  // ~2 s at 2 GHz
 constexpr uint32_t kWaitMaxPolls = 1u << 28;
 

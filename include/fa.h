@@ -62,7 +62,8 @@ typedef enum {
   FA_ERR_UNSUPPORTED_DEVICE = -4,   /* current device is not compute capability 10.3 */
   FA_ERR_WORKSPACE_TOO_SMALL = -5,  /* workspace_bytes < fa_backward_workspace_size() */
   FA_ERR_CUDA = -6,                 /* a CUDA runtime / driver call failed */
-  FA_ERR_DEVICE_TIMEOUT = -7        /* a kernel gave up waiting on a barrier */
+  FA_ERR_DEVICE_TIMEOUT = -7,       /* a kernel gave up waiting on a barrier */
+  FA_ERR_BAD_INDEX = -8             /* a device table holds an index out of range */
 } fa_status;
 
 /*
@@ -210,6 +211,46 @@ FA_API int fa_online_softmax_stats(const float* x, long long rows, long long col
                                    float* l, void* stream);
 
 /*
+ * Packed sequences: attention over a batch whose sequences lie one after another in
+ * one tensor, without padding, with grouped heads. For every sequence, rows
+ * [cu_seqlens[i], cu_seqlens[i + 1]), the operation of fa_forward and fa_backward on
+ * its own rows (n = m = the sequence's length), where query head h reads key/value
+ * head h / (Hq / Hkv).
+ *
+ * Layouts. Q, O, dO, dQ: bf16 [total, Hq, d]; K, V, dK, dV: bf16 [total, Hkv, d];
+ * L: fp32 [Hq, total]. Heads and columns are dense; Q, K, V and dQ, dK, dV have a row
+ * stride of their own (elements from row to row: at least heads * d, a multiple of 8,
+ * at most 2^30), so that they may be slices of one [total, (Hq + 2 Hkv) d] projection.
+ * O, dO and L are dense. Hq a multiple of Hkv, d as in fa_forward, total <= 2^24,
+ * nseq <= 65535, (total / 128 + nseq) * Hq < 2^31. Sequences may be empty. No value of
+ * one sequence reaches another's results, NaN included.
+ *
+ * fa_packed_plan reads cu_seqlens, int32 [nseq + 1] in device memory with
+ * 0 = cu_seqlens[0] <= ... <= cu_seqlens[nseq] <= total, and writes the work lists that
+ * the other calls read into `plan` (device memory of fa_packed_plan_bytes(nseq, total)
+ * bytes, 16-byte aligned). One plan serves any number of calls on that batch, of any
+ * head counts, until it is written again; cu_seqlens is not read after it. `causal`
+ * chooses the order of the lists: a plan made for the other setting gives the same
+ * results, less evenly dealt. Bounds that break the rule give an empty plan (calls
+ * that read it write nothing) and FA_ERR_BAD_INDEX in fa_get_device_status(), and so
+ * does a plan that was made for another nseq or total.
+ *
+ * Rows behind the last sequence (cu_seqlens[nseq] < total) are left as they were.
+ * `fill` asks for values there instead: in fa_packed_forward 1 sets them to 0 in O and
+ * 2 to -inf in L; in fa_packed_backward 1, 2 and 4 set them to 0 in dQ, dK and dV.
+ *
+ * fa_packed_forward: one kernel launch on `stream`. Returns FA_OK or a negative
+ * fa_status.
+ */
+FA_API size_t fa_packed_plan_bytes(int nseq, int total);
+FA_API int fa_packed_plan(const int* cu_seqlens, int nseq, int total, int causal, void* plan,
+                          size_t plan_bytes, void* stream);
+FA_API int fa_packed_forward(const void* Q, const void* K, const void* V, long long q_stride,
+                             long long k_stride, long long v_stride, int total, int Hq, int Hkv,
+                             int d, int causal, float scale, const void* plan, int nseq, void* O,
+                             float* L, int fill, void* stream);
+
+/*
  * Host-buffer sessions: one forward + backward step whose inputs and outputs are
  * in host memory, for callers that keep their tensors on the host. A session owns
  * device buffers for `chunk_heads` heads at a time (four sets), a backward
@@ -276,7 +317,9 @@ FA_API const char* fa_status_string(int status);
  * Reads the device status word of the current device into *status_out
  * (FA_OK; FA_ERR_DEVICE_TIMEOUT if a kernel gave up waiting since the last
  * read; FA_ERR_UNSUPPORTED_DEVICE if a kernel found its shared memory placed
- * other than on a 1024-byte boundary and returned without work) and clears it.
+ * other than on a 1024-byte boundary and returned without work; FA_ERR_BAD_INDEX
+ * if a kernel met an index out of range in a device table, for example sequence
+ * bounds that decrease, and did not follow it) and clears it.
  * Synchronises with the device. Returns FA_OK or FA_ERR_CUDA /
  * FA_ERR_INVALID_ARG.
  */

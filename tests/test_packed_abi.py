@@ -1,0 +1,83 @@
+"""Argument checks of the packed-sequence entry points (no GPU: every call is refused
+before any CUDA work, or reaches the device check)."""
+import pytest
+import torch
+
+import exact_io_aware_27_gb300 as fa
+from exact_io_aware_27_gb300 import api
+from exact_io_aware_27_gb300 import packed
+
+BASE = 1 << 20  # aligned addresses that are never followed
+
+
+def at(i):
+    return BASE + (i << 26)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    fa.build()
+    return fa.lib()
+
+
+REACHED = (api.FA_ERR_CUDA, api.FA_ERR_UNSUPPORTED_DEVICE)
+
+
+def test_plan(lib):
+    size = lib.fa_packed_plan_bytes(5, 1000)
+    # header, one list of 256-row tiles, two of 128-row tiles, two scans
+    assert size == 64 + 16 * (3 + 5) + 2 * 16 * (7 + 5) + 6 * 2 * 4
+    assert lib.fa_packed_plan_bytes(0, 10) == 0
+    assert lib.fa_packed_plan_bytes(70000, 10) == 0
+    assert lib.fa_packed_plan_bytes(1, 0) == 0
+    assert lib.fa_packed_plan_bytes(1, (1 << 24) + 1) == 0
+    f = lambda cu=at(0), nseq=5, total=1000, plan=at(1), size=size: lib.fa_packed_plan(  # noqa: E731
+        cu, nseq, total, 1, plan, size, None)
+    assert f(cu=None) == api.FA_ERR_INVALID_ARG
+    assert f(plan=None) == api.FA_ERR_INVALID_ARG
+    assert f(total=0) == api.FA_ERR_INVALID_ARG
+    assert f(cu=at(0) + 2) == api.FA_ERR_MISALIGNED
+    assert f(plan=at(1) + 8) == api.FA_ERR_MISALIGNED
+    assert f(size=size - 1) == api.FA_ERR_WORKSPACE_TOO_SMALL
+    assert f(cu=at(1) + 64) == api.FA_ERR_INVALID_ARG  # cu_seqlens inside the plan
+
+
+def test_forward(lib):
+    def f(Q=at(0), K=at(1), V=at(2), sq=512, sk=128, sv=128, total=100, Hq=8, Hkv=2, d=64,
+          scale=0.125, plan=at(3), nseq=3, O=at(4), L=at(5), fill=0):
+        return lib.fa_packed_forward(Q, K, V, sq, sk, sv, total, Hq, Hkv, d, 1, scale, plan, nseq,
+                                     O, L, fill, None)
+
+    for bad in (dict(Q=None), dict(V=None), dict(plan=None), dict(O=None), dict(L=None),
+                dict(total=0), dict(nseq=0), dict(Hkv=3), dict(Hkv=0), dict(Hq=0),
+                dict(sq=504), dict(sq=516), dict(sk=120), dict(sv=1 << 31), dict(scale=0.0),
+                dict(scale=float("nan")), dict(fill=4), dict(O=at(0)), dict(L=at(4)),
+                dict(O=at(3)), dict(total=1 << 24, nseq=65535, Hq=65535, Hkv=1, sq=65535 * 64)):
+        assert f(**bad) == api.FA_ERR_INVALID_ARG, bad
+    for d in (0, 4, 12, 136):
+        assert f(d=d) == api.FA_ERR_UNSUPPORTED_HEAD_DIM
+    for bad in (dict(Q=at(0) + 8), dict(plan=at(3) + 4), dict(O=at(4) + 2), dict(L=at(5) + 2)):
+        assert f(**bad) == api.FA_ERR_MISALIGNED, bad
+    if not torch.cuda.is_available():
+        assert f() in REACHED
+        # slices of one projection, side by side in its rows
+        assert f(K=at(0) + 1024, V=at(0) + 1280, sq=768, sk=768, sv=768) in REACHED
+        assert f(sq=1 << 30, total=1) in REACHED
+
+
+def test_binding_refuses(lib):
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    cu = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        fa.fa_packed_plan(cu, 4)  # not on a GPU
+    with pytest.raises(TypeError):
+        fa.fa_packed_forward(x, x, x, None)
+    meta = packed.PackedPlan(torch.zeros(8, dtype=torch.uint8, device="meta"), 1, 4, True)
+    with pytest.raises(ValueError):
+        fa.fa_packed_forward(x, x, x, meta)  # not on a GPU
+    with pytest.raises(TypeError):
+        packed._row_stride("Q", None)
+    with pytest.raises(ValueError):
+        packed._int32("cu_seqlens", cu, (3,), cu.device)
+    with pytest.raises(ValueError):
+        packed._int32("cu_seqlens", cu.long(), (2,), cu.device)

@@ -1,0 +1,163 @@
+"""Attention over packed sequences with grouped heads, against 64-bit values with
+elementwise bounds (tests/packed_ref.py)."""
+import math
+
+import pytest
+import torch
+
+import exact_io_aware_27_gb300 as fa
+from tests.packed_ref import assert_close, packed64, packed_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _built():
+    fa.build()
+    yield
+    assert fa.fa_get_device_status() == 0
+
+
+LENS = {
+    "one_token": [1],
+    "one_tile": [128],
+    "tile_and_one": [129, 257],
+    "empty_between": [0, 5, 0, 0, 300, 1, 0],
+    "half_steps": [63, 64, 65, 191, 192, 193],
+    "long_and_short": [700, 3, 2, 1, 90],
+    "many": [(7 * i) % 41 for i in range(150)],
+}
+
+
+def _check(q, k, v, cu, lens, causal, scale=None):
+    plan = fa.fa_packed_plan(cu, q.shape[0], causal)
+    O, L = fa.fa_packed_forward(q, k, v, plan, scale)
+    want = packed64(q, k, v, lens, causal, scale)
+    n = sum(lens)
+    assert_close("O", O[:n], tuple(x[:n] for x in want["O"]))
+    assert_close("L", L[:, :n], tuple(x[:, :n] for x in want["L"]))
+    assert torch.all(O[n:] == 0) and torch.all(L[:, n:] == -math.inf)
+    return O, L
+
+
+@pytest.mark.parametrize("name", list(LENS))
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (3, 3, 128)])
+def test_forward(name, causal, hq, hkv, d):
+    lens = LENS[name]
+    q, k, v, _, cu = packed_inputs(lens, hq, hkv, d, 11 + len(lens))
+    _check(q, k, v, cu, lens, causal)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(1, 1, 8), (8, 1, 40), (6, 3, 96), (14, 2, 72), (5, 1, 120)])
+def test_forward_heads_and_dims(hq, hkv, d):
+    lens = [70, 0, 301, 33]
+    q, k, v, _, cu = packed_inputs(lens, hq, hkv, d, 5, rest=9)
+    _check(q, k, v, cu, lens, True, scale=0.3)
+
+
+def test_forward_many_items_per_cta():
+    lens = [(37 * i) % 400 + 1 for i in range(90)]
+    q, k, v, _, cu = packed_inputs(lens, 16, 4, 64, 77)
+    _check(q, k, v, cu, lens, True)
+
+
+def test_forward_matches_dense():
+    """Sequences of one length are a dense batch: the same kernel, the same bits."""
+    B, n, h, d = 3, 384, 4, 128
+    q, k, v, _, cu = packed_inputs([n] * B, h, h, d, 21)
+    O, L = fa.fa_packed_forward(q, k, v, fa.fa_packed_plan(cu, B * n))
+    dense = [x.view(B, n, h, d).transpose(1, 2).contiguous() for x in (q, k, v)]
+    Od, Ld = fa.fa_forward(*dense, causal=True)
+    assert torch.equal(O.view(B, n, h, d).transpose(1, 2), Od)
+    assert torch.equal(L.view(h, B, n).transpose(0, 1), Ld)
+
+
+def test_forward_projection_slices():
+    """Q, K, V as column slices of one projection."""
+    lens, hq, hkv, d = [50, 210, 7], 6, 2, 64
+    q, k, v, _, cu = packed_inputs(lens, hq, hkv, d, 31)
+    wide = torch.cat([x.flatten(1) for x in (q, k, v)], 1)
+    qs = wide[:, :hq * d].unflatten(1, (hq, d))
+    ks = wide[:, hq * d:(hq + hkv) * d].unflatten(1, (hkv, d))
+    vs = wide[:, (hq + hkv) * d:].unflatten(1, (hkv, d))
+    plan = fa.fa_packed_plan(cu, q.shape[0])
+    a, b = fa.fa_packed_forward(q, k, v, plan), fa.fa_packed_forward(qs, ks, vs, plan)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_forward_sequences_do_not_leak(d):
+    """NaN and infinities in one sequence, and in rows of no sequence, stay there."""
+    lens = [100, 60, 130, 1]
+    q, k, v, _, cu = packed_inputs(lens, 4, 2, d, 41, rest=70)
+    plan = fa.fa_packed_plan(cu, q.shape[0])
+    clean = fa.fa_packed_forward(q, k, v, plan)
+    for t, value in ((q, math.nan), (k, math.nan), (v, math.nan)):
+        t[100:160] = value
+        t[291:] = math.inf
+    O, L = fa.fa_packed_forward(q, k, v, plan)
+    keep = torch.ones(q.shape[0], dtype=torch.bool, device="cuda")
+    keep[100:160] = False
+    assert torch.equal(O[keep], clean[0][keep]) and torch.equal(L[:, keep], clean[1][:, keep])
+    assert torch.isnan(O[100:160].float()).all()
+
+
+def test_forward_leaves_the_rest():
+    """Outputs that are passed in keep their rows behind the last sequence."""
+    lens = [33, 100]
+    q, k, v, _, cu = packed_inputs(lens, 2, 1, 64, 51, rest=40)
+    plan = fa.fa_packed_plan(cu, q.shape[0])
+    O = torch.full_like(q, 7.0)
+    L = torch.full((2, q.shape[0]), 5.0, device="cuda")
+    fa.fa_packed_forward(q, k, v, plan, O=O, L=L)
+    assert torch.all(O[133:] == 7.0) and torch.all(L[:, 133:] == 5.0)
+    want = packed64(q, k, v, lens, True)
+    assert_close("O", O[:133], tuple(x[:133] for x in want["O"]))
+
+
+def test_all_sequences_empty():
+    q, k, v, _, cu = packed_inputs([0, 0, 0], 2, 2, 64, 3, rest=5)
+    O, L = fa.fa_packed_forward(q, k, v, fa.fa_packed_plan(cu, 5))
+    assert torch.all(O == 0) and torch.all(L == -math.inf)
+
+
+@pytest.mark.parametrize("bounds", [[0, 5, 3, 10], [1, 5, 10], [0, 5, 11], [0, -2, 10],
+                                    [0, 2 ** 31 - 1, 10]])
+def test_bad_bounds_are_reported(bounds):
+    q, k, v, _, _ = packed_inputs([10], 2, 2, 64, 3)
+    cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    plan = fa.fa_packed_plan(cu, 10)
+    O = torch.full_like(q, 3.0)
+    L = torch.full((2, 10), 3.0, device="cuda")
+    fa.fa_packed_forward(q, k, v, plan, O=O, L=L)
+    assert fa.fa_get_device_status() == -8
+    assert torch.all(O == 3.0) and torch.all(L == 3.0)
+    assert fa.fa_get_device_status() == 0
+
+
+def test_forward_in_a_graph_and_on_another_stream():
+    lens = [40, 260, 3]
+    q, k, v, _, cu = packed_inputs(lens, 4, 2, 64, 61)
+    plan = fa.fa_packed_plan(cu, q.shape[0])
+    want = fa.fa_packed_forward(q, k, v, plan)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        got = fa.fa_packed_forward(q, k, v, plan, stream=stream)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # The plan and the pass captured together: a replay follows new bounds.
+    graph = torch.cuda.CUDAGraph()
+    O, L = torch.empty_like(q), torch.empty(4, q.shape[0], device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        fa.fa_packed_plan(cu, q.shape[0], plan=plan)
+        fa.fa_packed_forward(q, k, v, plan, O=O, L=L)
+    lens = [100, 3, 200]
+    cu.copy_(torch.tensor([0, 100, 103, 303], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    ref = packed64(q, k, v, lens, True)
+    assert_close("O", O, ref["O"])
+    assert_close("L", L, ref["L"])

@@ -385,12 +385,13 @@ int fa_standard_forward(const void* Q, const void* K, const void* V, int B, int 
 
 int fa_get_device_status(int* status_out) {
   if (!status_out) return FA_ERR_INVALID_ARG;
-  unsigned int f = 0, b = 0, t = 0, sd = 0, pl = 0, pk = 0;
+  unsigned int f = 0, b = 0, t = 0, sd = 0, pl = 0, pk = 0, pb = 0;
   if (forward_read_status(&f) != cudaSuccess || bwd_read_status(&b) != cudaSuccess ||
       selftest_read_status(&t) != cudaSuccess || standard_read_status(&sd) != cudaSuccess ||
-      plan_read_status(&pl) != cudaSuccess || packed_read_status(&pk) != cudaSuccess)
+      plan_read_status(&pl) != cudaSuccess || packed_read_status(&pk) != cudaSuccess ||
+      packed_bwd_read_status(&pb) != cudaSuccess)
     return FA_ERR_CUDA;
-  const unsigned int bits = f | b | t | sd | pl | pk;
+  const unsigned int bits = f | b | t | sd | pl | pk | pb;
   *status_out = (bits & kDeviceTimeoutBit)  ? FA_ERR_DEVICE_TIMEOUT
                 : (bits & kDeviceLayoutBit) ? FA_ERR_UNSUPPORTED_DEVICE
                 : (bits & kDeviceIndexBit)  ? FA_ERR_BAD_INDEX

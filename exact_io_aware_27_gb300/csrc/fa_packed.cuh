@@ -15,16 +15,17 @@ FA_DEV bool plan_matches(const PlanHead* h, int total, int nseq, unsigned int* s
   return false;
 }
 
-// tmem_rows_store for rows of a packed tensor [rows, H, d]: columns [0, NCOL) of this
-// warp's 32 TMEM lanes, times `mul`, to rows row0 + [0, valid) (valid may be <= 0 or
-// above 32) of head h. A full piece leaves through the staging buffers and TMA; a
+// tmem_rows_store for rows of a packed tensor [rows, H, d]: NCOL columns of this
+// warp's 32 TMEM lanes, times `mul`, to columns [col0, d) of rows row0 + [0, valid)
+// (valid may be <= 0 or above 32) of head h. A full piece leaves through the staging buffers and TMA; a
 // piece that ends inside its 32 rows, where the next row belongs to another sequence,
-// is written lane by lane to out + lane * ld.
+// is written lane by lane (`out` is the tensor, `ld` its row stride).
 template <int NCOL>
 FA_DEV void packed_rows_store(uint32_t tcol, float mul, uint8_t* stage, const CUtensorMap* map,
-                              int h, int row0, int valid, int valid_cols, __nv_bfloat16* out,
+                              int h, int row0, int valid, int col0, int d, __nv_bfloat16* out,
                               long long ld) {
   if (valid <= 0) return;  // warp-uniform
+  const int valid_cols = d - col0;
   const int lane = threadIdx.x & 31;
   const bool full = valid >= 32;
   if (full) {
@@ -44,7 +45,8 @@ FA_DEV void packed_rows_store(uint32_t tcol, float mul, uint8_t* stage, const CU
       w[e] = pack_bf16(__uint_as_float(o[2 * e]) * mul, __uint_as_float(o[2 * e + 1]) * mul);
     if (!full) {
       if (lane < valid) {
-        uint4* dst = reinterpret_cast<uint4*>(out + lane * ld + 32 * c);
+        uint4* dst = reinterpret_cast<uint4*>(out + (row0 + lane) * ld + (long long)h * d + col0 +
+                                              32 * c);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (32 * c + 8 * k < valid_cols)
@@ -66,7 +68,7 @@ FA_DEV void packed_rows_store(uint32_t tcol, float mul, uint8_t* stage, const CU
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_3d(map, buf, 32 * c, h, row0);
+      tma_store_3d(map, buf, col0 + 32 * c, h, row0);
       bulk_commit();
     }
   }

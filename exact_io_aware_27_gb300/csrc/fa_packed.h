@@ -60,6 +60,24 @@ struct PackedFwdArgs {
   int total, nseq, Hq, Hkv, d, causal, fill;
   float scale;
 };
+// Backward workspace: -D and -L * log2(e), fp32 [Hq, packed_ws_rows] each; a
+// sequence's rows start at its tiles' PlanTile::w.
+inline long long packed_ws_rows(int nseq, int total) {
+  return plan_layout(nseq, total).cap128 * kWorkspaceRowAlign;
+}
+struct PackedBwdArgs {
+  const void *Q, *K, *V, *O, *dO;
+  const float* L;
+  long long ldq, ldk, ldv;
+  void *dQ, *dK, *dV;
+  long long lddq, lddk, lddv;
+  float *ws_nD, *ws_nL2;
+  const void* plan;
+  int total, nseq, Hq, Hkv, d, causal, fill;
+  float scale;
+};
+cudaError_t launch_packed_backward(const PackedBwdArgs& a, cudaStream_t s);
+cudaError_t packed_bwd_read_status(unsigned int* out);
 cudaError_t launch_packed_plan(const int* cu_seqlens, int nseq, int total, int causal, void* plan,
                                cudaStream_t s);
 cudaError_t launch_packed_forward(const PackedFwdArgs& a, cudaStream_t s);

@@ -129,4 +129,78 @@ int fa_packed_forward(const void* Q, const void* K, const void* V, long long q_s
                                                                                     : FA_ERR_CUDA;
 }
 
+size_t fa_packed_workspace_bytes(int nseq, int total, int Hq) {
+  if (check_plan_sizes(nseq, total) != FA_OK || check_heads(nseq, total, Hq, 1, 8) != FA_OK)
+    return 0;
+  return (size_t)packed_ws_rows(nseq, total) * Hq * 2 * sizeof(float);
+}
+
+int fa_packed_backward(const void* Q, const void* K, const void* V, long long q_stride,
+                       long long k_stride, long long v_stride, const void* O, const float* L,
+                       const void* dO, int total, int Hq, int Hkv, int d, int causal, float scale,
+                       const void* plan, int nseq, void* dQ, void* dK, void* dV,
+                       long long dq_stride, long long dk_stride, long long dv_stride, int fill,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_plan_sizes(nseq, total);
+  if (rc != FA_OK) return rc;
+  if ((rc = check_heads(nseq, total, Hq, Hkv, d)) != FA_OK) return rc;
+  if ((rc = check_scale_value(scale)) != FA_OK) return rc;
+  if (!Q || !K || !V || !O || !L || !dO || !plan || !dQ || !dK || !dV || !workspace || (fill & ~7))
+    return FA_ERR_INVALID_ARG;
+  if (bad_stride(q_stride, Hq, d) || bad_stride(k_stride, Hkv, d) || bad_stride(v_stride, Hkv, d) ||
+      bad_stride(dq_stride, Hq, d) || bad_stride(dk_stride, Hkv, d) || bad_stride(dv_stride, Hkv, d))
+    return FA_ERR_INVALID_ARG;
+  for (const void* p : {Q, K, V, O, dO, plan, static_cast<const void*>(dQ),
+                        static_cast<const void*>(dK), static_cast<const void*>(dV),
+                        static_cast<const void*>(workspace)})
+    if (!is_aligned(p, 16)) return FA_ERR_MISALIGNED;
+  if (!is_aligned(L, 4)) return FA_ERR_MISALIGNED;
+  const size_t need = fa_packed_workspace_bytes(nseq, total, Hq);
+  if (workspace_bytes < need) return FA_ERR_WORKSPACE_TOO_SMALL;
+  const Rows ins[] = {rows16(Q, total, Hq, d, q_stride), rows16(K, total, Hkv, d, k_stride),
+                      rows16(V, total, Hkv, d, v_stride),
+                      rows16(O, total, Hq, d, (long long)Hq * d),
+                      rows16(dO, total, Hq, d, (long long)Hq * d),
+                      bytes_of(L, (size_t)Hq * total * 4),
+                      bytes_of(plan, plan_layout(nseq, total).bytes)};
+  const Rows outs[] = {rows16(dQ, total, Hq, d, dq_stride), rows16(dK, total, Hkv, d, dk_stride),
+                       rows16(dV, total, Hkv, d, dv_stride), bytes_of(workspace, need)};
+  for (const Rows& o : outs)
+    for (const Rows& i : ins)
+      if (rows_overlap(o, i)) return FA_ERR_INVALID_ARG;
+  for (int x = 0; x < 4; ++x)
+    for (int y = x + 1; y < 4; ++y)
+      if (rows_overlap(outs[x], outs[y])) return FA_ERR_INVALID_ARG;
+  if ((rc = require_device()) != FA_OK) return rc;
+  PackedBwdArgs a;
+  a.Q = Q;
+  a.K = K;
+  a.V = V;
+  a.O = O;
+  a.dO = dO;
+  a.L = L;
+  a.ldq = q_stride;
+  a.ldk = k_stride;
+  a.ldv = v_stride;
+  a.dQ = dQ;
+  a.dK = dK;
+  a.dV = dV;
+  a.lddq = dq_stride;
+  a.lddk = dk_stride;
+  a.lddv = dv_stride;
+  a.ws_nD = static_cast<float*>(workspace);
+  a.ws_nL2 = a.ws_nD + (size_t)packed_ws_rows(nseq, total) * Hq;
+  a.plan = plan;
+  a.total = total;
+  a.nseq = nseq;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.causal = causal ? 1 : 0;
+  a.fill = fill;
+  a.scale = scale;
+  return launch_packed_backward(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
+                                                                                     : FA_ERR_CUDA;
+}
+
 }  // extern "C"

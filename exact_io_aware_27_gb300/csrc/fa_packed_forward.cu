@@ -77,9 +77,8 @@ struct Packed {
                            float m_ref, float l, uint8_t* stage, const CUtensorMap* mo, int d) {
     const int q0 = it.s.z * 256 + t * 128 + warp * 32;  // within the sequence
     const int row0 = it.s.x + q0, valid = it.s.y - q0;
-    const long long ld = (long long)g.p.Hq * d;
-    packed_rows_store<D>(ocol, 1.f / l, stage, mo, it.h, row0, valid, d,
-                         g.p.O + row0 * ld + (long long)it.h * d, ld);
+    packed_rows_store<D>(ocol, 1.f / l, stage, mo, it.h, row0, valid, 0, d, g.p.O,
+                         (long long)g.p.Hq * d);
     if (lane < valid) g.p.L[(size_t)it.h * g.p.total + row0 + lane] = (m_ref + lg2(l)) * kLn2;
   }
   // Rows that no sequence covers: O = 0 and L = -inf (what attention to no key

@@ -6,6 +6,9 @@ Query head h reads key/value head h // (Hq / Hkv).
 
     plan = fa_packed_plan(cu_seqlens, Q.shape[0])     # once per batch
     O, L = fa_packed_forward(Q, K, V, plan)           # every layer
+    dQ, dK, dV = fa_packed_backward(Q, K, V, O, L, dO, plan)
+
+flash_attention_packed(Q, K, V, plan) is the two of them under autograd.
 
 Q, K and V may be slices of one projection [total, (Hq + 2 Hkv) d]: rows may lie any
 stride apart, heads and columns are dense.
@@ -14,7 +17,7 @@ from __future__ import annotations
 
 import torch
 
-from .api import _check, _out, _same_device, _scale, lib
+from .api import _check, _out, _same_device, _scale, _workspace_bytes, lib
 
 
 def _placed(device, stream):
@@ -63,10 +66,11 @@ def _int32(name, t, shape, device):
 class PackedPlan:
     """The work lists of one packed batch, on the device (fa_packed_plan)."""
 
-    __slots__ = ("buffer", "nseq", "total", "causal")
+    __slots__ = ("buffer", "nseq", "total", "causal", "version")
 
     def __init__(self, buffer, nseq, total, causal):
         self.buffer, self.nseq, self.total, self.causal = buffer, nseq, total, causal
+        self.version = 0  # times it has been written over
 
     @property
     def device(self):
@@ -97,6 +101,7 @@ def fa_packed_plan(cu_seqlens, total: int, causal: bool = True, plan: PackedPlan
     if plan is None:
         return PackedPlan(buffer, nseq, total, bool(causal))
     plan.causal = bool(causal)
+    plan.version += 1
     return plan
 
 
@@ -141,3 +146,87 @@ def fa_packed_forward(Q, K, V, plan: PackedPlan, scale: float | None = None, O=N
                                        plan.buffer.data_ptr(), plan.nseq, O.data_ptr(),
                                        L.data_ptr(), fill, _raw_stream(device)))
     return O, L
+
+
+def alloc_packed_workspace(plan: PackedPlan, Hq: int, d: int) -> torch.Tensor:
+    """Workspace of fa_packed_backward for the plan's batch and Hq query heads (of any
+    head dimension d; it does not change the size)."""
+    size = int(lib().fa_packed_workspace_bytes(plan.nseq, plan.total, Hq))
+    if size == 0:
+        raise ValueError("invalid sizes for the backward workspace")
+    return torch.empty(size, dtype=torch.uint8, device=plan.device)
+
+
+def _gradient(name, like, t):
+    """(tensor, row stride, allocated here) of a gradient with the shape of `like`."""
+    if t is None:
+        return torch.empty(like.shape, dtype=torch.bfloat16, device=like.device), \
+            like.shape[1] * like.shape[2], True
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != like.shape or t.device != like.device:
+        raise ValueError(f"{name} must have the shape {tuple(like.shape)} on {like.device}")
+    return t, _row_stride(name, t), False
+
+
+def fa_packed_backward(Q, K, V, O, L, dO, plan: PackedPlan, scale: float | None = None, dQ=None,
+                       dK=None, dV=None, workspace=None, stream=None):
+    """dQ [total, Hq, d], dK and dV [total, Hkv, d] (bf16) for the gradient dO of the
+    forward's O. Rows behind the last sequence are 0 in gradients allocated here and left
+    as they were in tensors that are passed in, which may be slices of one
+    [total, (Hq + 2 Hkv) d] buffer."""
+    (ldq, ldk, ldv), Hq, Hkv, d = _packed_inputs(Q, K, V, plan)
+    total, device = plan.total, Q.device
+    for name, t in (("O", O), ("dO", dO)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if (t.dtype != torch.bfloat16 or t.shape != Q.shape or not t.is_contiguous()
+                or t.device != device):
+            raise ValueError(f"{name} must be a contiguous bf16 tensor of Q's shape on {device}")
+    if (not isinstance(L, torch.Tensor) or L.dtype != torch.float32 or L.device != device
+            or tuple(L.shape) != (Hq, total) or not L.is_contiguous()):
+        raise ValueError("L must be a contiguous fp32 [Hq, total] tensor on the inputs' device")
+    with _placed(device, stream):
+        dQ, lddq, new_q = _gradient("dQ", Q, dQ)
+        dK, lddk, new_k = _gradient("dK", K, dK)
+        dV, lddv, new_v = _gradient("dV", V, dV)
+        if workspace is None:
+            workspace = alloc_packed_workspace(plan, Hq, d)
+        size = _workspace_bytes(workspace, device)
+        _check("fa_packed_backward",
+               lib().fa_packed_backward(Q.data_ptr(), K.data_ptr(), V.data_ptr(), ldq, ldk, ldv,
+                                        O.data_ptr(), L.data_ptr(), dO.data_ptr(), total, Hq, Hkv,
+                                        d, int(plan.causal), _scale(scale, d),
+                                        plan.buffer.data_ptr(), plan.nseq, dQ.data_ptr(),
+                                        dK.data_ptr(), dV.data_ptr(), lddq, lddk, lddv,
+                                        new_q | new_k << 1 | new_v << 2, workspace.data_ptr(),
+                                        size, _raw_stream(device)))
+    return dQ, dK, dV
+
+
+class FlashAttentionPacked(torch.autograd.Function):
+    """Autograd wrapper of fa_packed_forward and fa_packed_backward; saves Q, K, V, O
+    and L."""
+
+    @staticmethod
+    def forward(ctx, Q, K, V, plan, scale=None):
+        O, L = fa_packed_forward(Q, K, V, plan, scale)
+        ctx.save_for_backward(Q, K, V, O, L)
+        ctx.plan, ctx.version = plan, plan.version
+        ctx.scale = scale
+        return O
+
+    @staticmethod
+    def backward(ctx, dO):
+        Q, K, V, O, L = ctx.saved_tensors
+        if ctx.plan.version != ctx.version:
+            raise RuntimeError("the plan was written for another batch between the forward and "
+                               "the backward pass")
+        dQ, dK, dV = fa_packed_backward(Q, K, V, O, L, dO.contiguous(), ctx.plan, ctx.scale)
+        return dQ, dK, dV, None, None
+
+
+def flash_attention_packed(Q, K, V, plan: PackedPlan, scale: float | None = None):
+    """Attention over the plan's packed sequences, differentiable in Q, K and V. The plan
+    has to hold this batch until the backward pass has run."""
+    return FlashAttentionPacked.apply(Q, K, V, plan, scale)

@@ -239,8 +239,13 @@ FA_API int fa_online_softmax_stats(const float* x, long long rows, long long col
  * `fill` asks for values there instead: in fa_packed_forward 1 sets them to 0 in O and
  * 2 to -inf in L; in fa_packed_backward 1, 2 and 4 set them to 0 in dQ, dK and dV.
  *
- * fa_packed_forward: one kernel launch on `stream`. Returns FA_OK or a negative
- * fa_status.
+ * fa_packed_forward: one kernel launch on `stream`. fa_packed_backward: dQ, dK, dV for
+ * the forward's O and L and a gradient dO; dK and dV sum over the query heads of their
+ * key/value head, in a fixed order. `workspace`: caller-owned device memory of at least
+ * fa_packed_workspace_bytes() bytes (8 bytes per query head and row, rows counted up to
+ * each sequence's next multiple of 128), 16-byte aligned, contents on entry do not
+ * matter; calls that may run at the same time need one each. Two kernel launches. Both
+ * return FA_OK or a negative fa_status.
  */
 FA_API size_t fa_packed_plan_bytes(int nseq, int total);
 FA_API int fa_packed_plan(const int* cu_seqlens, int nseq, int total, int causal, void* plan,
@@ -249,6 +254,14 @@ FA_API int fa_packed_forward(const void* Q, const void* K, const void* V, long l
                              long long k_stride, long long v_stride, int total, int Hq, int Hkv,
                              int d, int causal, float scale, const void* plan, int nseq, void* O,
                              float* L, int fill, void* stream);
+FA_API size_t fa_packed_workspace_bytes(int nseq, int total, int Hq);
+FA_API int fa_packed_backward(const void* Q, const void* K, const void* V, long long q_stride,
+                              long long k_stride, long long v_stride, const void* O,
+                              const float* L, const void* dO, int total, int Hq, int Hkv, int d,
+                              int causal, float scale, const void* plan, int nseq, void* dQ,
+                              void* dK, void* dV, long long dq_stride, long long dk_stride,
+                              long long dv_stride, int fill, void* workspace,
+                              size_t workspace_bytes, void* stream);
 
 /*
  * Host-buffer sessions: one forward + backward step whose inputs and outputs are

@@ -65,6 +65,34 @@ def test_forward(lib):
         assert f(sq=1 << 30, total=1) in REACHED
 
 
+def test_backward(lib):
+    assert lib.fa_packed_workspace_bytes(3, 1000, 4) == (7 + 3) * 128 * 4 * 8
+    assert lib.fa_packed_workspace_bytes(0, 1000, 4) == 0
+    ws = lib.fa_packed_workspace_bytes(3, 100, 8)
+
+    def f(Q=at(0), K=at(1), V=at(2), sq=512, sk=128, sv=128, O=at(3), L=at(4), dO=at(5), d=64,
+          scale=0.125, plan=at(6), dQ=at(7), dK=at(8), dV=at(9), sdq=512, sdk=128, sdv=128,
+          fill=0, w=at(10), wb=ws, Hkv=2):
+        return lib.fa_packed_backward(Q, K, V, sq, sk, sv, O, L, dO, 100, 8, Hkv, d, 1, scale,
+                                      plan, 3, dQ, dK, dV, sdq, sdk, sdv, fill, w, wb, None)
+
+    for bad in (dict(K=None), dict(O=None), dict(L=None), dict(dO=None), dict(dQ=None),
+                dict(dV=None), dict(w=None), dict(plan=None), dict(Hkv=3), dict(fill=8),
+                dict(scale=-1.0), dict(sdq=256), dict(sdk=132), dict(dQ=at(0)), dict(dK=at(8) + 64,
+                dV=at(8)), dict(w=at(7)), dict(dV=at(6)), dict(w=at(5))):
+        assert f(**bad) == api.FA_ERR_INVALID_ARG, bad
+    assert f(d=20) == api.FA_ERR_UNSUPPORTED_HEAD_DIM
+    for bad in (dict(dK=at(8) + 8), dict(w=at(10) + 8), dict(L=at(4) + 2)):
+        assert f(**bad) == api.FA_ERR_MISALIGNED, bad
+    assert f(wb=ws - 1) == api.FA_ERR_WORKSPACE_TOO_SMALL
+    if not torch.cuda.is_available():
+        assert f() in REACHED
+        one = dict(dQ=at(7), dK=at(7) + 1024, dV=at(7) + 1280, sdq=768, sdk=768, sdv=768)
+        assert f(**one) in REACHED  # gradients side by side in one buffer
+        one["dV"] -= 16
+        assert f(**one) == api.FA_ERR_INVALID_ARG
+
+
 def test_binding_refuses(lib):
     x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     cu = torch.zeros(2, dtype=torch.int32)

@@ -161,3 +161,146 @@ def test_forward_in_a_graph_and_on_another_stream():
     ref = packed64(q, k, v, lens, True)
     assert_close("O", O, ref["O"])
     assert_close("L", L, ref["L"])
+
+
+def _grads(q, k, v, do, cu, lens, causal, scale=None, **kw):
+    plan = fa.fa_packed_plan(cu, q.shape[0], causal)
+    O, L = fa.fa_packed_forward(q, k, v, plan, scale)
+    got = fa.fa_packed_backward(q, k, v, O, L, do, plan, scale, **kw)
+    want = packed64(q, k, v, lens, causal, scale, do)
+    n = sum(lens)
+    for name, t in zip(("dQ", "dK", "dV"), got):
+        assert_close(name, t[:n], tuple(x[:n] for x in want[name]))
+        if not kw:
+            assert torch.all(t[n:] == 0), f"{name}: rows of no sequence"
+    return got
+
+
+@pytest.mark.parametrize("name", list(LENS))
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (3, 3, 128)])
+def test_backward(name, causal, hq, hkv, d):
+    lens = LENS[name]
+    q, k, v, do, cu = packed_inputs(lens, hq, hkv, d, 111 + len(lens))
+    _grads(q, k, v, do, cu, lens, causal)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(1, 1, 8), (8, 1, 40), (6, 3, 96), (14, 2, 72), (5, 1, 120)])
+def test_backward_heads_and_dims(hq, hkv, d):
+    lens = [70, 0, 301, 33]
+    q, k, v, do, cu = packed_inputs(lens, hq, hkv, d, 105, rest=9)
+    _grads(q, k, v, do, cu, lens, True, scale=0.3)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_many_items_per_cta(d):
+    lens = [(37 * i) % 400 + 1 for i in range(90)]
+    q, k, v, do, cu = packed_inputs(lens, 16, 4, d, 177)
+    first = _grads(q, k, v, do, cu, lens, True)
+    again = _grads(q, k, v, do, cu, lens, True)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))  # no order of atomics
+
+
+def test_backward_matches_dense():
+    B, n, h, d = 3, 384, 4, 128
+    q, k, v, do, cu = packed_inputs([n] * B, h, h, d, 121)
+    plan = fa.fa_packed_plan(cu, B * n)
+    O, L = fa.fa_packed_forward(q, k, v, plan)
+    got = fa.fa_packed_backward(q, k, v, O, L, do, plan)
+    dense = [x.view(B, n, h, d).transpose(1, 2).contiguous() for x in (q, k, v, O, do)]
+    Ld = L.view(h, B, n).transpose(0, 1).contiguous()
+    want = fa.fa_backward(*dense[:4], Ld, dense[4], causal=True)
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(B, n, h, d).transpose(1, 2), b)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_backward_sequences_do_not_leak(d, causal):
+    lens = [100, 60, 130, 1]
+    q, k, v, do, cu = packed_inputs(lens, 4, 2, d, 141, rest=70)
+    plan = fa.fa_packed_plan(cu, q.shape[0], causal)
+
+    def grads():
+        O, L = fa.fa_packed_forward(q, k, v, plan)
+        return fa.fa_packed_backward(q, k, v, O, L, do, plan)
+
+    clean = grads()
+    for t in (q, k, v, do):
+        t[100:160] = math.nan
+        t[291:] = math.inf
+    keep = torch.ones(q.shape[0], dtype=torch.bool, device="cuda")
+    keep[100:160] = False
+    for a, b in zip(grads(), clean):
+        assert torch.equal(a[keep], b[keep])
+
+
+def test_gradients_into_one_buffer_leave_the_rest():
+    """Q, K, V and their gradients as slices of one projection and of its gradient."""
+    lens, hq, hkv, d = [50, 210, 7], 6, 2, 64
+    q, k, v, do, cu = packed_inputs(lens, hq, hkv, d, 131, rest=12)
+    cut = [0, hq * d, (hq + hkv) * d, (hq + 2 * hkv) * d]
+    parts = lambda x: [x[:, a:b].unflatten(1, (-1, d)) for a, b in zip(cut, cut[1:])]  # noqa: E731
+    wide = torch.cat([x.flatten(1) for x in (q, k, v)], 1)
+    dwide = torch.full_like(wide, 9.0)
+    plan = fa.fa_packed_plan(cu, q.shape[0])
+    O, L = fa.fa_packed_forward(*parts(wide), plan)
+    dq, dk, dv = parts(dwide)
+    fa.fa_packed_backward(*parts(wide), O, L, do, plan, dQ=dq, dK=dk, dV=dv)
+    want = fa.fa_packed_backward(q, k, v, O, L, do, plan)
+    for a, b in zip((dq, dk, dv), want):
+        assert torch.equal(a[:267], b[:267])
+    assert torch.all(dwide[267:] == 9.0)
+
+
+def test_autograd_and_differences():
+    """flash_attention_packed's gradients against central differences of the 64-bit
+    attention along random directions, and against fa_packed_backward."""
+    lens, hq, hkv, d = [17, 1, 40], 4, 2, 32
+    q, k, v, do, cu = packed_inputs(lens, hq, hkv, d, 151, rest=3)
+    plan = fa.fa_packed_plan(cu, q.shape[0])
+    leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+    out = fa.flash_attention_packed(*leaves, plan)
+    out.backward(do)
+    n = sum(lens)
+
+    def loss(*x):
+        return float((packed64(*x, lens, True)["O"][0][:n] * do[:n].double()).sum())
+
+    want = packed64(q, k, v, lens, True, None, do)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for i, name in enumerate(("dQ", "dK", "dV")):
+        step = torch.randn(leaves[i].shape, generator=g, device="cuda", dtype=torch.float64)
+        x = [y.double() for y in (q, k, v)]
+        up, down = list(x), list(x)
+        up[i], down[i] = x[i] + 1e-5 * step, x[i] - 1e-5 * step
+        slope = (loss(*up) - loss(*down)) / 2e-5
+        got = float((leaves[i].grad[:n].double() * step[:n]).sum())
+        room = float((want[name][1][:n] * step[:n].abs()).sum())
+        assert abs(slope - got) <= room + 1e-5 * abs(slope)
+        assert torch.all(leaves[i].grad[n:] == 0)
+    # A plan that was written for another batch in between is refused.
+    out = fa.flash_attention_packed(*leaves, plan)
+    fa.fa_packed_plan(cu, q.shape[0], plan=plan)
+    with pytest.raises(RuntimeError):
+        out.backward(do)
+
+
+def test_backward_in_a_graph():
+    lens = [40, 260, 3]
+    q, k, v, do, cu = packed_inputs(lens, 4, 2, 64, 161)
+    plan = fa.fa_packed_plan(cu, q.shape[0])
+    O, L = fa.fa_packed_forward(q, k, v, plan)
+    want = fa.fa_packed_backward(q, k, v, O, L, do, plan)
+    got = [torch.empty_like(x) for x in (q, k, v)]
+    ws = fa.alloc_packed_workspace(plan, 4, 64)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fa.fa_packed_forward(q, k, v, plan, O=O, L=L)
+        fa.fa_packed_backward(q, k, v, O, L, do, plan, dQ=got[0], dK=got[1], dV=got[2],
+                              workspace=ws)
+    ws.fill_(255)  # contents on entry do not matter
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -11,6 +11,7 @@ from .api import (FAError, FlashAttention, Session, alloc_workspace, fa_backward
                   fa_backward_workspace_size, fa_forward, fa_get_device_status,
                   fa_online_softmax_stats, fa_standard_forward, fa_standard_matrix_bytes,
                   fa_selftest_mma, fa_selftest_wait_timeout, flash_attention, lib, status_string, version)
+from .decode import alloc_prefix_workspace, fa_cache_append, fa_prefix_decode  # noqa: F401
 from .packed import (FlashAttentionPacked, PackedPlan, alloc_packed_workspace,  # noqa: F401
                      fa_packed_backward, fa_packed_forward, fa_packed_plan,
                      flash_attention_packed)

@@ -21,7 +21,8 @@ LIBRARY = os.path.join(PKG_DIR, "libfa_gb300.so")
 
 SOURCES = ["fa_api.cu", "fa_forward.cu", "fa_backward.cu", "fa_softmax.cu", "fa_selftest.cu",
            "fa_noalloc.cu", "fa_session.cu", "fa_standard.cu", "fa_packed_plan.cu",
-           "fa_packed_forward.cu", "fa_packed_backward.cu", "fa_packed_api.cu"]
+           "fa_packed_forward.cu", "fa_packed_backward.cu", "fa_packed_api.cu",
+           "fa_cache.cu", "fa_prefix.cu", "fa_decode_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-fvisibility=hidden", "-I" + INCLUDE, "-I" + CSRC]

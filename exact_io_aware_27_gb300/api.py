@@ -63,6 +63,11 @@ SIGNATURES = {
     "fa_packed_workspace_bytes": (_S, [_I, _I, _I]),
     "fa_packed_backward": (_I, [_P, _P, _P, _LL, _LL, _LL, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P,
                                 _I, _P, _P, _P, _LL, _LL, _LL, _I, _P, _S, _P]),
+    "fa_cache_append": (_I, [_P, _P, _LL, _LL, _I, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I,
+                             _P]),
+    "fa_prefix_workspace_bytes": (_S, [_I, _I, _I, _I, _I, _I]),
+    "fa_prefix_decode": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _P,
+                              _P, _P, _S, _P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_get_device_status": (_I, [ctypes.POINTER(_I)]),
     "fa_version": (_I, []),

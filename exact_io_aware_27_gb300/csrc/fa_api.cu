@@ -6,6 +6,7 @@
 
 #include "fa.h"
 #include "fa_check.h"
+#include "fa_decode.h"
 #include "fa_internal.h"
 #include "fa_packed.h"
 #include "sm103.cuh"
@@ -385,13 +386,14 @@ int fa_standard_forward(const void* Q, const void* K, const void* V, int B, int 
 
 int fa_get_device_status(int* status_out) {
   if (!status_out) return FA_ERR_INVALID_ARG;
-  unsigned int f = 0, b = 0, t = 0, sd = 0, pl = 0, pk = 0, pb = 0;
+  unsigned int f = 0, b = 0, t = 0, sd = 0, pl = 0, pk = 0, pb = 0, ap = 0, px = 0;
   if (forward_read_status(&f) != cudaSuccess || bwd_read_status(&b) != cudaSuccess ||
       selftest_read_status(&t) != cudaSuccess || standard_read_status(&sd) != cudaSuccess ||
       plan_read_status(&pl) != cudaSuccess || packed_read_status(&pk) != cudaSuccess ||
-      packed_bwd_read_status(&pb) != cudaSuccess)
+      packed_bwd_read_status(&pb) != cudaSuccess || append_read_status(&ap) != cudaSuccess ||
+      prefix_read_status(&px) != cudaSuccess)
     return FA_ERR_CUDA;
-  const unsigned int bits = f | b | t | sd | pl | pk | pb;
+  const unsigned int bits = f | b | t | sd | pl | pk | pb | ap | px;
   *status_out = (bits & kDeviceTimeoutBit)  ? FA_ERR_DEVICE_TIMEOUT
                 : (bits & kDeviceLayoutBit) ? FA_ERR_UNSUPPORTED_DEVICE
                 : (bits & kDeviceIndexBit)  ? FA_ERR_BAD_INDEX

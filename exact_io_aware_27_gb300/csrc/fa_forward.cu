@@ -19,6 +19,7 @@ struct Dense {
     int qs, bh;  // first query, head
   };
   FA_DEV static unsigned int* status() { return &g_fwd_status; }
+  static constexpr bool kSplit = false;
   static constexpr bool kForeignTail = false;  // TMA reads zeros past a head's rows
   FA_DEV static int items(const Params& g) { return g.num_pairs * g.BH; }
   // Heads a group at a time (their K/V stay in L2 while the group runs), inside a
@@ -38,6 +39,10 @@ struct Dense {
   FA_DEV static void load_q(void* dst, const CUtensorMap* map, uint64_t* f, int col,
                             const Params&, const Item& it, int t) {
     tma_load_3d(dst, map, f, col, it.qs + t * 128, it.bh);
+  }
+  template <class C>
+  FA_DEV static uint32_t tile_bytes(const Params&) {
+    return C::TILE;
   }
   template <class C>
   FA_DEV static uint32_t block_bytes(const Params&, const Item&, int) {

@@ -45,12 +45,15 @@
 // get: the Params, or a copy with what the device had to look up), Item (one work
 // item, a plain struct) and the functions
 //   view(params)              read once at the kernel's start
-//   items(g)                  number of work items (tile pair, head, ...)
-//   item(g, i)                item i of the launch order; read one item ahead
+//   items(g), item(g, i)      the work items (tile pair, head, ...) in launch order,
+//                             dealt out in snake order; read one item ahead
+//   segments, segment         instead of them (kSplit): what each CTA works on, an
+//                             equal share of a long axis
 //   steps(g, it, t)           64-key steps of tile t (tile 0 always has some)
 //   keys(g, it)               keys of the item; steps past them are masked
 //   causal(g), first_query(g, it)  query position of row 0 of tile 0
-//   load_q, load_kv, block_bytes   TMA loads of a Q tile / a 128-key block
+//   load_q, load_kv           TMA loads of a Q tile / a 128-key block
+//   tile_bytes, block_bytes   the bytes that they bring
 //   store                     the epilogue of one warp's 32 rows
 //   idle_warps                work of the warps that have no role
 //   status()                  the translation unit's device status word
@@ -153,11 +156,20 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
   // stay in L2 while the group runs), inside a group the heaviest tile pairs (the
   // last ones, under causal masking) first.
   const int P = gridDim.x, cta = blockIdx.x;
-  const int n_items = G::items(g);
   int n_mine = 0;
-  while (snake_item(n_mine, cta, P) < n_items) ++n_mine;
+  if constexpr (G::kSplit) {
+    n_mine = G::segments(g, cta, P);
+  } else {
+    const int n_items = G::items(g);
+    while (snake_item(n_mine, cta, P) < n_items) ++n_mine;
+  }
   // Item j of this CTA.
-  auto fetch = [&](int j) { return G::item(g, snake_item(j, cta, P)); };
+  auto fetch = [&](int j) {
+    if constexpr (G::kSplit)
+      return G::segment(g, cta, P, j);
+    else
+      return G::item(g, snake_item(j, cta, P));
+  };
   // The 64-key steps of each tile of an item (tile 0 always has some); returns the
   // steps of the longest tile.
   auto steps = [&](const Item& it, int (&nht)[C::TILES]) {
@@ -226,7 +238,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
           const bool q_use = u < C::QUSES;
           const bool two = !q_use || 2 * u + 1 < C::TILES;
           if (q_use)
-            mbar_arrive_expect_tx(f, (two ? 2 : 1) * C::TILE);
+            mbar_arrive_expect_tx(f, (two ? 2 : 1) * G::template tile_bytes<C>(g));
           else
             mbar_arrive_expect_tx(f, G::template block_bytes<C>(g, it, u - C::QUSES));
           uint8_t* kdst = smem + C::OFF_K + s * C::TILE;

@@ -40,6 +40,7 @@ struct Packed {
     int h;
   };
   FA_DEV static unsigned int* status() { return &g_packed_status; }
+  static constexpr bool kSplit = false;
   static constexpr bool kForeignTail = true;
   FA_DEV static int items(const View& g) { return g.tiles * g.p.Hq; }
   FA_DEV static Item item(const View& g, int i) {
@@ -56,6 +57,10 @@ struct Packed {
   FA_DEV static void load_q(void* dst, const CUtensorMap* map, uint64_t* f, int col, const View&,
                             const Item& it, int t) {
     tma_load_3d(dst, map, f, col, it.h, it.s.x + it.s.z * 256 + t * 128);
+  }
+  template <class C>
+  FA_DEV static uint32_t tile_bytes(const View&) {
+    return C::TILE;
   }
   template <class C>
   FA_DEV static uint32_t block_bytes(const View&, const Item&, int) {

@@ -1,0 +1,720 @@
+// Decode attention behind a shared prefix: one new token for each of B requests, whose
+// keys are the prefix that all of them share and then their own, both in pages of a
+// cache. Per query row the keys are split into parts, each part gives
+//   o = softmax over its keys times V,   e = log2 sum 2^(s * scale * log2(e))
+// and the parts are joined exactly: O = sum 2^(e - M) o / sum 2^(e - M), M = max e.
+//
+//   prefix kernel  the shared keys, once for all requests: the query rows of all
+//                  requests and of the query heads of one key/value head are the rows
+//                  of one matrix product, so that K and V are read once for 256 rows.
+//                  This is the forward kernel (fa_forward.cuh, tcgen05) with rows
+//                  (request, query head), non-causal, keys from pages.
+//   own kernel     each request's own keys. Hq / Hkv rows share a key, far fewer than a
+//                  tcgen05 tile has: bound by reading the keys from HBM, so the
+//                  products are warp-level ones of 16 rows and every warp streams its
+//                  own keys through a private ring of shared memory.
+//   join kernel    joins the parts of each row, prefix and own.
+//
+// Both kernels split their keys evenly, whatever the lengths: the blocks of all (row
+// group, key/value head) units are laid end to end and worker c of P takes the c-th of
+// P equal pieces of that axis (Split). A worker's piece covers whole units and at most
+// two partial ones, so the parts need one slot per unit and two per worker. Lengths are
+// read on the device; nothing depends on the order in which workers finish.
+#include "fa_decode.h"
+#include "fa_forward.cuh"
+
+namespace fa {
+
+__device__ unsigned int g_prefix_status;
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kMaxSms = 160;       // slots are reserved for this many thread blocks
+constexpr int kOwnWarps = 4;       // warps of a thread block of the own kernel
+constexpr int kOwnBlocksPerSm = 2;
+constexpr int kOwnChunk = 64;      // keys per step of the own keys' split
+constexpr int kMinPrefixBlocks = 2;  // 128-key blocks a prefix worker takes at least
+
+// `total` steps dealt to `workers` in equal, contiguous pieces.
+struct Split {
+  long long total;
+  int workers;
+  FA_DEV Split(long long steps, int most) : total(steps), workers((int)min(steps, (long long)most)) {}
+  FA_DEV long long start(int w) const { return total * w / workers; }
+  // The worker whose piece holds step x (0 <= x < total).
+  FA_DEV int owner(long long x) const { return (int)(((x + 1) * workers - 1) / total); }
+  // The slot of a unit's part number `part` of `parts` (its first worker is `first`):
+  // unit's own slot, or the worker's slot for the unit that starts in its piece and goes
+  // on (odd) or came from the piece before (even).
+  FA_DEV static long long slot(long long unit, long long units, int parts, int first, int part) {
+    return parts == 1 ? unit : units + 2LL * (first + part) + (part == 0 ? 1 : 0);
+  }
+};
+
+// Sizes that the three kernels agree on.
+struct DecodeSizes {
+  int B, Hq, Hkv, per_kv, d;
+  int per_tile;       // requests per 128-row tile of the prefix kernel
+  int pairs;          // tile pairs
+  int pair_rows;      // rows of a prefix slot
+  int row_tiles;      // 16-row tiles of a key/value head's rows in the own kernel
+  int own_rows;       // rows of an own slot
+  int prefix_workers, own_workers;
+  float *prefix_o, *prefix_e;  // [slot][pair_rows][d], [slot][pair_rows]
+  float *own_o, *own_e;        // [slot][own_rows][d], [slot][own_rows]
+  int* first;                  // [B + 1] own chunks before each request
+};
+
+// Lays the workspace out for prefixes of at most `prefix_cap` and own parts of at most
+// `own_cap` keys (a worker without steps has no slots); returns its bytes.
+size_t lay_out(DecodeSizes* s, void* base, int prefix_cap, int own_cap) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* q = p + at;
+    at += (bytes + 255) / 256 * 256;
+    return q;
+  };
+  auto slots = [](size_t units, size_t steps_each, size_t workers) {
+    const size_t steps = units * steps_each;
+    return steps == 0 ? 0 : units + 2 * (steps < workers ? steps : workers);
+  };
+  const size_t pslots = slots((size_t)s->pairs * s->Hkv, ((size_t)prefix_cap + 127) / 128, kMaxSms);
+  const size_t oslots = slots((size_t)s->Hkv * s->row_tiles * s->B,
+                              ((size_t)own_cap + kOwnChunk - 1) / kOwnChunk,
+                              (size_t)kMaxSms * kOwnBlocksPerSm * kOwnWarps);
+  s->prefix_o = reinterpret_cast<float*>(take(pslots * s->pair_rows * s->d * 4));
+  s->prefix_e = reinterpret_cast<float*>(take(pslots * s->pair_rows * 4));
+  s->own_o = reinterpret_cast<float*>(take(oslots * s->own_rows * s->d * 4));
+  s->own_e = reinterpret_cast<float*>(take(oslots * s->own_rows * 4));
+  s->first = reinterpret_cast<int*>(take(((size_t)s->B + 1) * 4));
+  return at;
+}
+
+DecodeSizes sizes_of(int B, int Hq, int Hkv, int d) {
+  DecodeSizes s{};
+  s.B = B;
+  s.Hq = Hq;
+  s.Hkv = Hkv;
+  s.per_kv = Hq / Hkv;
+  s.d = d;
+  s.per_tile = 128 / s.per_kv;
+  s.pairs = ceil_div(B, 2 * s.per_tile);
+  s.pair_rows = (B < 2 * s.per_tile ? B : 2 * s.per_tile) * s.per_kv;
+  s.row_tiles = ceil_div(s.per_kv, 16);
+  s.own_rows = s.per_kv < 16 ? s.per_kv : 16;
+  return s;
+}
+
+// The prefix's length, at most what the listed pages hold.
+FA_DEV int prefix_keys(const int* prefix_len, int cap) {
+  const int n = prefix_len ? __ldg(prefix_len) : 0;
+  return max(0, min(n, cap));
+}
+FA_DEV Split prefix_split(const DecodeSizes& s, int keys) {
+  const long long steps = (long long)s.pairs * s.Hkv * ((keys + 127) / 128);
+  return Split(steps, (int)max(1LL, min((long long)s.prefix_workers,
+                                        (steps + kMinPrefixBlocks - 1) / kMinPrefixBlocks)));
+}
+
+// ================================================================== prefix kernel
+struct Prefix {
+  struct Params {
+    DecodeSizes s;
+    const int *pages, *len;
+    int cap, page, page_shift, box, num_pages;  // cap: keys; box: rows of a TMA copy
+  };
+  struct View {
+    const Params& p;
+    int keys;
+  };
+  struct Item {
+    int pair, hk, k0, m;  // tile pair, head, first key, keys
+    long long slot;
+  };
+  static constexpr bool kSplit = true;
+  static constexpr bool kForeignTail = true;
+  FA_DEV static unsigned int* status() { return &g_prefix_status; }
+  FA_DEV static View view(const Params& p) {
+    const int n = __ldg(p.len);
+    if ((n < 0 || n > p.cap) && blockIdx.x == 0 && threadIdx.x == 0)
+      atomicOr(status(), kDeviceIndexBit);
+    return {p, prefix_keys(p.len, p.cap)};
+  }
+  FA_DEV static int segments(const View& g, int cta, int) {
+    const int blocks = (g.keys + 127) / 128;
+    const Split sp = prefix_split(g.p.s, g.keys);
+    if (cta >= sp.workers) return 0;
+    return (int)((sp.start(cta + 1) - 1) / blocks - sp.start(cta) / blocks) + 1;
+  }
+  FA_DEV static Item segment(const View& g, int cta, int, int j) {
+    const int blocks = (g.keys + 127) / 128;
+    const Split sp = prefix_split(g.p.s, g.keys);
+    const long long a = sp.start(cta), b = sp.start(cta + 1);
+    const long long unit = a / blocks + j, u0 = unit * blocks, u1 = u0 + blocks;
+    const long long x0 = max(a, u0), x1 = min(b, u1);
+    Item it;
+    it.pair = (int)(unit / g.p.s.Hkv);
+    it.hk = (int)(unit - (long long)it.pair * g.p.s.Hkv);
+    it.k0 = (int)(x0 - u0) * 128;
+    it.m = min(g.keys, (int)(x1 - u0) * 128) - it.k0;
+    const long long units = (long long)g.p.s.pairs * g.p.s.Hkv;
+    it.slot = x0 == u0 && x1 == u1 ? unit : units + 2LL * cta + (x0 == u0 ? 1 : 0);
+    return it;
+  }
+  FA_DEV static int steps(const View& g, const Item& it, int t) {
+    return (2 * it.pair + t) * g.p.s.per_tile < g.p.s.B ? (it.m + 63) / 64 : 0;
+  }
+  FA_DEV static int keys(const View&, const Item& it) { return it.m; }
+  FA_DEV static constexpr int causal(const View&) { return 0; }
+  FA_DEV static int first_query(const View&, const Item&) { return 0; }
+  template <class C>
+  FA_DEV static uint32_t tile_bytes(const View& g) {
+    return (uint32_t)(g.p.s.per_tile * g.p.s.per_kv) * 128u * C::KCH;
+  }
+  // Rows (request, query head of the key/value head): the rows past per_tile * per_kv of
+  // a tile keep what the buffer held; nothing of them is stored.
+  FA_DEV static void load_q(void* dst, const CUtensorMap* map, uint64_t* f, int col,
+                            const View& g, const Item& it, int t) {
+    tma_load_4d(dst, map, f, col, 0, it.hk, (2 * it.pair + t) * g.p.s.per_tile);
+  }
+  // Copies of `box` rows (a page or 128 keys) of a block; pages wholly past the item's
+  // keys are not read.
+  FA_DEV static int boxes(const View& g, const Item& it, int block) {
+    return (min(128, it.m - block * 128) + g.p.box - 1) / g.p.box;
+  }
+  template <class C>
+  FA_DEV static uint32_t block_bytes(const View& g, const Item& it, int block) {
+    return (uint32_t)(boxes(g, it, block) * g.p.box) * 256u * C::KCH;
+  }
+  template <class C>
+  FA_DEV static void load_kv(uint8_t* kdst, uint8_t* vdst, const CUtensorMap* mk,
+                             const CUtensorMap* mv, uint64_t* f, const View& g, const Item& it,
+                             int block) {
+    const int n = boxes(g, it, block), key0 = it.k0 + block * 128;
+    for (int i = 0; i < n; ++i) {
+      const int key = key0 + i * g.p.box;
+      int page = __ldg(g.p.pages + (key >> g.p.page_shift));
+      if ((unsigned)page >= (unsigned)g.p.num_pages) {
+        atomicOr(status(), kDeviceIndexBit);
+        page = 0;
+      }
+      const int row = key & (g.p.page - 1), at = page * g.p.s.Hkv + it.hk;
+#pragma unroll
+      for (int c = 0; c < C::KCH; ++c) {
+        tma_load_3d(kdst + c * C::CHUNK + i * g.p.box * 128, mk, f, c * 64, row, at);
+        tma_load_3d(vdst + c * C::CHUNK + i * g.p.box * 128, mv, f, c * 64, row, at);
+      }
+    }
+  }
+  // The part's o (fp32) and e of one warp's 32 rows, lane by lane.
+  template <int D>
+  FA_DEV static void store(const View& g, const Item& it, int t, int warp, int lane, uint32_t ocol,
+                           float m_ref, float l, uint8_t*, const CUtensorMap*, int d) {
+    const DecodeSizes& s = g.p.s;
+    const int r = warp * 32 + lane;
+    const int in_pair = t * s.per_tile * s.per_kv + r;  // row of the slot
+    const bool valid = r < s.per_tile * s.per_kv &&
+                       (2 * it.pair + t) * s.per_tile + r / s.per_kv < s.B;
+    float* o = s.prefix_o + ((size_t)it.slot * s.pair_rows + in_pair) * d;
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      if (32 * c >= d) break;
+      uint32_t v[32];
+      tmem_ld32(ocol + 32 * c, v);
+      tmem_ld_wait();
+      reg_fence32(v);
+      if (valid) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (32 * c + 4 * k < d)
+            reinterpret_cast<float4*>(o + 32 * c)[k] =
+                make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
+                            __uint_as_float(v[4 * k + 2]) * inv,
+                            __uint_as_float(v[4 * k + 3]) * inv);
+      }
+    }
+    if (valid) s.prefix_e[(size_t)it.slot * s.pair_rows + in_pair] = m_ref + lg2(l);
+  }
+  FA_DEV static void idle_warps(const View&, int, int, int) {}
+};
+
+// ================================================================== own kernel
+struct OwnParams {
+  DecodeSizes s;
+  const __nv_bfloat16 *Q, *Kc, *Vc;
+  const int *table, *lens;
+  int max_pages, num_pages, page_shift;
+  float scale_log2;
+};
+
+template <int D>
+struct OwnCfg {
+  static constexpr int ROW = D * 2;          // bytes of a key
+  static constexpr int KEYS = 16;            // keys of a ring stage
+  static constexpr int STAGES = 3;
+  static constexpr int PART = KEYS * ROW;    // K or V of a stage
+  static constexpr int STAGE = 2 * PART;
+  static constexpr int WARP = STAGES * STAGE;
+  static constexpr int RINGS = kOwnWarps * WARP;  // then first[B + 1]
+};
+
+// Length of request b's own keys, at most what its table row holds.
+FA_DEV int own_keys(const OwnParams& p, int b) {
+  return max(0, min(__ldg(p.lens + b), p.max_pages << p.page_shift));
+}
+
+// Pages are read 16 keys at a time (a page holds a multiple of 16): per stage 16 rows of
+// K and of V, 16-byte piece j of row r at j ^ (r % 8), which ldmatrix reads without bank
+// conflicts. Three stages a warp keep two in flight: 128 KB per SM, above the
+// latency-bandwidth product of its share of HBM.
+template <int D>
+__global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_constant__ OwnParams p) {
+  using C = OwnCfg<D>;
+  extern __shared__ __align__(128) uint8_t smem_own[];
+  __shared__ int warp_sums[kOwnWarps];
+  int* first = reinterpret_cast<int*>(smem_own + C::RINGS);
+  const DecodeSizes& s = p.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kThreads = 32 * kOwnWarps;
+
+  // Chunks before each request (exclusive scan of the lengths).
+  int run = 0;
+  for (int b0 = 0; b0 < s.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int n = 0;
+    if (b < s.B) {
+      const int len = __ldg(p.lens + b);
+      if ((len < 0 || len > p.max_pages << p.page_shift) && blockIdx.x == 0)
+        atomicOr(&g_prefix_status, kDeviceIndexBit);
+      n = (own_keys(p, b) + kOwnChunk - 1) / kOwnChunk;
+    }
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int before = run, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kOwnWarps; ++w) {
+      if (w < warp) before += warp_sums[w];
+      sum += warp_sums[w];
+    }
+    if (b < s.B) first[b] = before + x - n;
+    run += sum;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) first[s.B] = run;
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b <= s.B; b += kThreads) s.first[b] = first[b];
+
+  const int chunks = run;  // of one (head, row tile)
+  const long long units = (long long)s.Hkv * s.row_tiles * s.B;
+  const Split sp((long long)s.Hkv * s.row_tiles * chunks, s.own_workers);
+  const int me = blockIdx.x * kOwnWarps + warp;
+  if (me >= sp.workers) return;  // no barrier of the block follows
+  const long long x_end = sp.start(me + 1), x_begin = sp.start(me);
+
+  // A run of chunks of one unit.
+  struct Run {
+    int b, ht, key, key_end, len;  // request, head and row tile, keys [key, key_end)
+    long long x0, x1, u0, u1;      // this run's steps, the unit's steps
+  };
+  auto run_at = [&](long long x) {
+    Run r;
+    r.ht = (int)(x / chunks);
+    const int in = (int)(x - (long long)r.ht * chunks);
+    int lo = 0, hi = s.B;  // first[lo] <= in < first[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= in)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    r.b = lo;
+    r.u0 = (long long)r.ht * chunks + first[lo];
+    r.u1 = (long long)r.ht * chunks + first[lo + 1];
+    r.x0 = x;
+    r.x1 = min(r.u1, x_end);
+    r.len = own_keys(p, lo);
+    r.key = (int)(x - r.u0) * kOwnChunk;
+    r.key_end = min(r.len, (int)(r.x1 - r.u0) * kOwnChunk);
+    return r;
+  };
+
+  const uint32_t ring = smem_u32(smem_own) + warp * C::WARP;
+  // ---- the issuing side: runs STAGES - 1 stages ahead of the products
+  Run ir = run_at(x_begin);
+  int i_page = 0, i_at = 32;  // pages of 32 stages, one per lane; the next of them
+  bool i_more = true;
+  int i_stage = 0;
+  constexpr int PPR = D / 8;  // 16-byte pieces of a row
+  const int l_row = lane / PPR, l_piece = lane % PPR;
+  const size_t head_rows = (size_t)1 << p.page_shift;
+  auto issue = [&]() {
+    if (i_more) {
+      if (i_at == 32) {
+        const int key = ir.key + lane * C::KEYS;
+        int page = 0;
+        if (key < ir.key_end)
+          page = __ldg(p.table + (size_t)ir.b * p.max_pages + (key >> p.page_shift));
+        if ((unsigned)page >= (unsigned)p.num_pages) {
+          atomicOr(&g_prefix_status, kDeviceIndexBit);
+          page = 0;
+        }
+        i_page = page;
+        i_at = 0;
+      }
+      const int page = __shfl_sync(0xffffffffu, i_page, i_at);
+      const int hk = ir.ht / s.row_tiles;
+      const size_t row0 = ((size_t)page * s.Hkv + hk) * head_rows + (ir.key & (head_rows - 1));
+      const uint32_t dst = ring + i_stage * C::STAGE;
+#pragma unroll
+      for (int i = 0; i < C::KEYS * PPR / 32; ++i) {
+        const int r = l_row + i * (32 / PPR);
+        const bool in = ir.key + r < ir.key_end && 8 * l_piece < s.d;
+        const size_t at = in ? (row0 + r) * s.d + 8 * l_piece : 0;
+        const uint32_t to = dst + r * C::ROW + ((l_piece ^ (r & 7)) << 4);
+        cp_async16(to, p.Kc + at, in ? 16 : 0);
+        cp_async16(to + C::PART, p.Vc + at, in ? 16 : 0);
+      }
+      ++i_at;
+      ir.key += C::KEYS;
+      if (ir.key >= ir.key_end) {
+        if (ir.x1 < x_end) {
+          ir = run_at(ir.x1);
+          i_at = 32;
+        } else {
+          i_more = false;
+        }
+      }
+    }
+    i_stage = i_stage + 1 == C::STAGES ? 0 : i_stage + 1;
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < C::STAGES - 1; ++i) issue();
+
+  // ---- the products
+  const int qr = lane >> 2, qc = (lane & 3) * 2;  // row and first column of a fragment
+  int stage = 0;
+  for (long long x = x_begin; x < x_end;) {
+    const Run r = run_at(x);
+    x = r.x1;
+    const int hk = r.ht / s.row_tiles, rt = r.ht - hk * s.row_tiles;
+    const int rows = min(16, s.per_kv - rt * 16);
+    const __nv_bfloat16* q = p.Q + ((size_t)r.b * s.Hq + hk * s.per_kv + rt * 16) * s.d;
+    uint32_t qa[D / 16][4];
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = qr + (e & 1) * 8, col = kk * 16 + (e >> 1) * 8 + qc;
+        qa[kk][e] = row < rows && col < s.d
+                        ? __ldg(reinterpret_cast<const unsigned int*>(q + (size_t)row * s.d + col))
+                        : 0u;
+      }
+    float o[D / 8][4];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows qr and qr + 8
+
+    for (int key = r.key; key < r.key_end; key += C::KEYS) {
+      cp_async_wait<C::STAGES - 2>();
+      __syncwarp();  // the stage has landed for every lane, and the last one is read
+      issue();
+      const uint32_t kb = ring + stage * C::STAGE, vb = kb + C::PART;
+      stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};  // keys 0..7, 8..15
+      {
+        const int row = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t b[4];
+          ldmatrix_x4(b, kb + row * C::ROW + (((kk * 2 + half) ^ (row & 7)) << 4));
+          mma_16816(sa, qa[kk], b[0], b[1]);
+          mma_16816(sb, qa[kk], b[2], b[3]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sa[e] *= p.scale_log2;
+        sb[e] *= p.scale_log2;
+      }
+      if (r.key_end - key < C::KEYS) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (key + qc + (e & 1) >= r.key_end) sa[e] = -INFINITY;
+          if (key + 8 + qc + (e & 1) >= r.key_end) sb[e] = -INFINITY;
+        }
+      }
+      float x0 = fmaxf(fmaxf(sa[0], sa[1]), fmaxf(sb[0], sb[1]));
+      float x1 = fmaxf(fmaxf(sa[2], sa[3]), fmaxf(sb[2], sb[3]));
+      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+      // The reference maximum moves only when a row passes it by 2^8 (as in the forward
+      // kernel): most steps need no rescaling.
+      if (__any_sync(0xffffffffu, x0 > m0 + kRescaleThreshold || x1 > m1 + kRescaleThreshold)) {
+        const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+        const float c0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
+        const float c1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= c0;
+        l1 *= c1;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          o[n][0] *= c0;
+          o[n][1] *= c0;
+          o[n][2] *= c1;
+          o[n][3] *= c1;
+        }
+      }
+      const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+      sa[0] = ex2(sa[0] - u0);
+      sa[1] = ex2(sa[1] - u0);
+      sb[0] = ex2(sb[0] - u0);
+      sb[1] = ex2(sb[1] - u0);
+      sa[2] = ex2(sa[2] - u1);
+      sa[3] = ex2(sa[3] - u1);
+      sb[2] = ex2(sb[2] - u1);
+      sb[3] = ex2(sb[3] - u1);
+      l0 += (sa[0] + sa[1]) + (sb[0] + sb[1]);
+      l1 += (sa[2] + sa[3]) + (sb[2] + sb[3]);
+      // P in bf16 (the products' operand type), l from the values before rounding
+      const uint32_t pa[4] = {pack_bf16(sa[0], sa[1]), pack_bf16(sa[2], sa[3]),
+                              pack_bf16(sb[0], sb[1]), pack_bf16(sb[2], sb[3])};
+      {
+        const int row = (lane & 7) + (((lane >> 3) & 1) << 3), half = lane >> 4;
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t b[4];
+          ldmatrix_x4_trans(b, vb + row * C::ROW + (((n * 2 + half) ^ (row & 7)) << 4));
+          mma_16816(o[2 * n], pa, b[0], b[1]);
+          mma_16816(o[2 * n + 1], pa, b[2], b[3]);
+        }
+      }
+    }
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    const long long unit = (long long)r.ht * s.B + r.b;
+    const long long slot = r.x0 == r.u0 && r.x1 == r.u1
+                               ? unit
+                               : units + 2LL * me + (r.x0 == r.u0 ? 1 : 0);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = qr + 8 * e;
+      if (row >= rows) continue;
+      const float inv = 1.f / (e ? l1 : l0);
+      float* out = s.own_o + ((size_t)slot * s.own_rows + row) * s.d;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        if (8 * n < s.d)
+          *reinterpret_cast<float2*>(out + 8 * n + qc) =
+              make_float2(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
+      if ((lane & 3) == 0)
+        s.own_e[(size_t)slot * s.own_rows + row] = e ? m1 + lg2(l1) : m0 + lg2(l0);
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// ================================================================== join kernel
+struct JoinParams {
+  DecodeSizes s;
+  const int* prefix_len;
+  int prefix_cap;  // keys
+  __nv_bfloat16* O;
+  float* L;
+};
+
+// One thread block per row (request, query head), four columns a lane; its warps take
+// every fourth part. A row without keys gets O = 0, L = -inf.
+constexpr int kJoinWarps = 4;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ JoinParams p) {
+  __shared__ float4 sums[kJoinWarps][32];
+  __shared__ float weights[kJoinWarps];
+  const DecodeSizes& s = p.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.x / s.Hq, hq = blockIdx.x - b * s.Hq;
+  const int hk = hq / s.per_kv, in = hq - hk * s.per_kv;
+
+  // Parts of the prefix, then of the request's own keys.
+  const int keys = prefix_keys(p.prefix_len, p.prefix_cap), blocks = (keys + 127) / 128;
+  int pparts = 0, pfirst = 0;
+  long long punit = 0;
+  if (blocks > 0) {
+    const Split sp = prefix_split(s, keys);
+    punit = (long long)(b / (2 * s.per_tile)) * s.Hkv + hk;
+    pfirst = sp.owner(punit * blocks);
+    pparts = sp.owner((punit + 1) * blocks - 1) - pfirst + 1;
+  }
+  const int prow = (b % (2 * s.per_tile)) * s.per_kv + in;
+  const int chunks = __ldg(s.first + s.B), f0 = __ldg(s.first + b), f1 = __ldg(s.first + b + 1);
+  const int ht = hk * s.row_tiles + in / 16;
+  int oparts = 0, ofirst = 0;
+  if (f1 > f0) {
+    const Split sp((long long)s.Hkv * s.row_tiles * chunks, s.own_workers);
+    ofirst = sp.owner((long long)ht * chunks + f0);
+    oparts = sp.owner((long long)ht * chunks + f1 - 1) - ofirst + 1;
+  }
+  const long long punits = (long long)s.pairs * s.Hkv, ounits = (long long)s.Hkv * s.row_tiles * s.B;
+  const int parts = pparts + oparts;
+  auto where = [&](int i) -> long long {  // row of the part: >= 0 prefix, else own (~row)
+    if (i < pparts) return Split::slot(punit, punits, pparts, pfirst, i) * s.pair_rows + prow;
+    return ~(Split::slot((long long)ht * s.B + b, ounits, oparts, ofirst, i - pparts) *
+                 s.own_rows + in % 16);
+  };
+  auto log_weight = [&](int i) {
+    const long long w = where(i);
+    return w >= 0 ? s.prefix_e[w] : s.own_e[~w];
+  };
+  float M = -INFINITY;
+  for (int i = lane; i < parts; i += 32) M = fmaxf(M, log_weight(i));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float ref = M == -INFINITY ? 0.f : M;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < parts; i += kJoinWarps) {
+    const long long w = where(i);
+    const float* o = (w >= 0 ? s.prefix_o + w * s.d : s.own_o + ~w * s.d);
+    const float f = ex2((w >= 0 ? s.prefix_e[w] : s.own_e[~w]) - ref);
+    sum += f;
+    if (4 * lane < s.d) {
+      const float4 v = reinterpret_cast<const float4*>(o)[lane];
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+    }
+  }
+  sums[warp][lane] = acc;
+  if (lane == 0) weights[warp] = sum;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) {
+    const float4 v = sums[w][lane];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+    sum += weights[w];
+  }
+  const float inv = parts > 0 ? 1.f / sum : 0.f;
+  if (4 * lane < s.d)
+    reinterpret_cast<uint2*>(p.O + (size_t)blockIdx.x * s.d)[lane] =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (lane == 0) p.L[blockIdx.x] = parts > 0 ? (M + lg2(sum)) * kLn2 : -INFINITY;
+}
+
+int decode_sms() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms < kMaxSms ? sms : kMaxSms;
+}
+
+template <int D>
+cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
+  using C = FwdCfg<D>;
+  DecodeSizes s = sizes_of(a.B, a.Hq, a.Hkv, a.d);
+  lay_out(&s, a.workspace, a.prefix_cap * a.page, a.max_pages * a.page);
+  const int sms = decode_sms();
+  s.prefix_workers = sms;
+  s.own_workers = sms * kOwnBlocksPerSm * kOwnWarps;
+  int shift = 0;
+  while ((1 << shift) < a.page) ++shift;
+  cudaError_t e;
+  const int cap = a.prefix_cap << shift;
+  if (a.prefix_cap > 0) {
+    Prefix::Params g;
+    g.s = s;
+    g.pages = a.prefix_pages;
+    g.len = a.prefix_len;
+    g.cap = cap;
+    g.page = a.page;
+    g.page_shift = shift;
+    g.box = a.page < 128 ? a.page : 128;
+    g.num_pages = a.num_pages;
+    CUtensorMap mq, mk, mv;
+    const cuuint64_t qd[4] = {(cuuint64_t)a.d, (cuuint64_t)s.per_kv, (cuuint64_t)a.Hkv,
+                              (cuuint64_t)a.B};
+    const cuuint64_t qs[3] = {(cuuint64_t)a.d * 2, (cuuint64_t)s.per_kv * a.d * 2,
+                              (cuuint64_t)a.Hq * a.d * 2};
+    const cuuint32_t qb[4] = {64, (cuuint32_t)s.per_kv, 1, (cuuint32_t)s.per_tile};
+    if (encode_tensor_map(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.Q), qd, qs,
+                          qb, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+        make_bf16_head_map(&mk, a.Kc, a.num_pages * a.Hkv, a.page, a.d, g.box) != CUDA_SUCCESS ||
+        make_bf16_head_map(&mv, a.Vc, a.num_pages * a.Hkv, a.page, a.d, g.box) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+    FwdParams p;
+    p.d = a.d;
+    p.scale_log2 = a.scale * kLog2e;
+    e = cudaFuncSetAttribute(fwd_kernel<D, Prefix>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::SMEM);
+    if (e != cudaSuccess) return e;
+    fwd_kernel<D, Prefix><<<sms, C::THREADS, C::SMEM, stream>>>(mq, mk, mv, mk, p, g);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  OwnParams op;
+  op.s = s;
+  op.Q = static_cast<const __nv_bfloat16*>(a.Q);
+  op.Kc = static_cast<const __nv_bfloat16*>(a.Kc);
+  op.Vc = static_cast<const __nv_bfloat16*>(a.Vc);
+  op.table = a.table;
+  op.lens = a.lens;
+  op.max_pages = a.max_pages;
+  op.num_pages = a.num_pages;
+  op.page_shift = shift;
+  op.scale_log2 = a.scale * kLog2e;
+  const int own_smem = OwnCfg<D>::RINGS + (a.B + 1) * 4;
+  e = cudaFuncSetAttribute(own_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           OwnCfg<D>::RINGS + (kMaxBatch + 1) * 4);
+  if (e != cudaSuccess) return e;
+  own_kernel<D><<<sms * kOwnBlocksPerSm, 32 * kOwnWarps, own_smem, stream>>>(op);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  JoinParams jp;
+  jp.s = s;
+  jp.prefix_len = a.prefix_cap > 0 ? a.prefix_len : nullptr;
+  jp.prefix_cap = cap;
+  jp.O = static_cast<__nv_bfloat16*>(a.O);
+  jp.L = a.L;
+  join_kernel<<<(unsigned)a.B * a.Hq, 32 * kJoinWarps, 0, stream>>>(jp);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t decode_workspace_bytes(int B, int Hq, int Hkv, int d, int prefix_cap, int own_cap) {
+  DecodeSizes s = sizes_of(B, Hq, Hkv, d);
+  return lay_out(&s, nullptr, prefix_cap, own_cap);
+}
+
+cudaError_t launch_prefix_decode(const DecodeArgs& a, cudaStream_t s) {
+  return a.d > 64 ? launch_decode_d<128>(a, s) : launch_decode_d<64>(a, s);
+}
+
+cudaError_t prefix_read_status(unsigned int* out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_prefix_status, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_prefix_status, &zero, sizeof(unsigned int));
+}
+
+}  // namespace fa

@@ -264,6 +264,57 @@ FA_API int fa_packed_backward(const void* Q, const void* K, const void* V, long 
                               size_t workspace_bytes, void* stream);
 
 /*
+ * Paged cache of keys and values: K_cache and V_cache, bf16 [num_pages, Hkv, page, d] in
+ * device memory, page a power of two from 16 to 1024, num_pages * Hkv < 2^31. Position
+ * p of a request lies in row p % page of page block_table[request, p / page];
+ * block_table is int32 [requests, max_pages] in device memory, max_pages * page <= 2^30,
+ * and entries past a request's length are not read.
+ *
+ * Indices in device tables are checked by the kernels: a page number outside
+ * [0, num_pages), or a length or position that the table row cannot hold, gives
+ * FA_ERR_BAD_INDEX in fa_get_device_status(). fa_cache_append does not write such a row;
+ * fa_prefix_decode reads page 0, or as many keys as the table row holds, instead, and the
+ * results of the requests concerned (all of them for the prefix) are undefined.
+ *
+ * fa_cache_append: writes the rows of K and V, bf16 [total, Hkv, d] with row strides of
+ * their own (as in fa_packed_forward), of `nseq` requests that lie one after another:
+ * rows [cu_seqlens[i], cu_seqlens[i + 1]) go to positions starts[i], starts[i] + 1, ...
+ * of request i. cu_seqlens is int32 [nseq + 1] and starts int32 [nseq] in device memory,
+ * with 0 = cu_seqlens[0] <= ... <= cu_seqlens[nseq] <= total; rows behind the last are
+ * not written. Two rows for one place leave one of the two there, in 16-byte pieces.
+ * total <= 2^24, nseq <= 65535. One kernel launch.
+ */
+FA_API int fa_cache_append(const void* K, const void* V, long long k_stride, long long v_stride,
+                           int total, const int* cu_seqlens, const int* starts, int nseq,
+                           const int* block_table, int max_pages, void* K_cache, void* V_cache,
+                           int num_pages, int Hkv, int page, int d, void* stream);
+
+/*
+ * Decode attention behind a shared prefix: one new token for each of B requests. The
+ * keys of request b are the first prefix_len[0] positions of the pages prefix_pages
+ * (int32 [num_prefix_pages]), which all requests share and which are read once for all
+ * of them, and then the first lens[b] positions of its own row of block_table, the new
+ * token's among them. Query head h reads key/value head h / (Hq / Hkv).
+ *   O[b, h] = softmax(scale Q[b, h] K^T) V     L[b, h] = logsumexp of the scores
+ * Q, O: bf16 [B, Hq, d], dense; L: fp32 [B, Hq]. prefix_len (int32 [1]) and lens
+ * (int32 [B]) are in device memory, so that a captured call follows them. A request
+ * without keys gets O = 0 and L = -inf. num_prefix_pages and max_pages may be 0, and the
+ * pointers that they size are then not read. Hq a multiple of Hkv, Hq / Hkv <= 128,
+ * B <= 8192, d as in fa_forward. `workspace`: caller-owned device memory of at least
+ * fa_prefix_workspace_bytes() bytes for num_prefix_pages * page and max_pages * page keys
+ * (more for larger capacities), 16-byte aligned, contents on entry do not matter; calls
+ * that may run at the same time need one each. Up to three kernel launches on
+ * `stream`. Returns FA_OK or a negative fa_status.
+ */
+FA_API size_t fa_prefix_workspace_bytes(int B, int Hq, int Hkv, int d, int prefix_capacity,
+                                        int own_capacity);
+FA_API int fa_prefix_decode(const void* Q, const void* K_cache, const void* V_cache,
+                            const int* prefix_pages, int num_prefix_pages, const int* prefix_len,
+                            const int* block_table, int max_pages, const int* lens, int B, int Hq,
+                            int Hkv, int d, int num_pages, int page, float scale, void* O,
+                            float* L, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Host-buffer sessions: one forward + backward step whose inputs and outputs are
  * in host memory, for callers that keep their tensors on the host. A session owns
  * device buffers for `chunk_heads` heads at a time (four sets), a backward

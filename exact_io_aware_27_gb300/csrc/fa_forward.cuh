@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + C::NBAR);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const WaitCtx wc{abort_flag, G::status()};
+  if constexpr (G::kSplit) grid_launch_dependents();
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;

@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
   using C = OwnCfg<D>;
   extern __shared__ __align__(128) uint8_t smem_own[];
   __shared__ int warp_sums[kOwnWarps];
+  grid_launch_dependents();
   int* first = reinterpret_cast<int*>(smem_own + C::RINGS);
   const DecodeSizes& s = p.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -317,8 +318,11 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
   const int chunks = run;  // of one (head, row tile)
   const long long units = (long long)s.Hkv * s.row_tiles * s.B;
   const Split sp((long long)s.Hkv * s.row_tiles * chunks, s.own_workers);
-  const int me = blockIdx.x * kOwnWarps + warp;
-  if (me >= sp.workers) return;  // no barrier of the block follows
+  const int me = warp * gridDim.x + blockIdx.x;  // the first workers on different SMs
+  if (me >= sp.workers) {  // no barrier of the block follows
+    grid_wait();
+    return;
+  }
   const long long x_end = sp.start(me + 1), x_begin = sp.start(me);
 
   // A run of chunks of one unit.
@@ -530,6 +534,9 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
     }
   }
   cp_async_wait<0>();
+  // This kernel needs nothing of the prefix kernel, beside which it may run, but it
+  // completes after it: the join kernel waits for this one.
+  grid_wait();
 }
 
 // ================================================================== join kernel
@@ -551,6 +558,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.x / s.Hq, hq = blockIdx.x - b * s.Hq;
   const int hk = hq / s.per_kv, in = hq - hk * s.per_kv;
+  grid_wait();
 
   // Parts of the prefix, then of the request's own keys.
   const int keys = prefix_keys(p.prefix_len, p.prefix_cap), blocks = (keys + 127) / 128;
@@ -630,14 +638,38 @@ int decode_sms() {
   return sms < kMaxSms ? sms : kMaxSms;
 }
 
+// An ordinary launch, or one that may start while the stream's previous kernel runs.
+template <class K, class P>
+cudaError_t launch(K kernel, unsigned grid, int threads, int smem, cudaStream_t stream, bool early,
+                   const P& params) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, params);
+}
+
 template <int D>
 cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
   using C = FwdCfg<D>;
   DecodeSizes s = sizes_of(a.B, a.Hq, a.Hkv, a.d);
   lay_out(&s, a.workspace, a.prefix_cap * a.page, a.max_pages * a.page);
   const int sms = decode_sms();
-  s.prefix_workers = sms;
-  s.own_workers = sms * kOwnBlocksPerSm * kOwnWarps;
+  // No more blocks than the capacities can keep busy.
+  const long long prefix_steps = (long long)s.pairs * s.Hkv * ceil_div(a.prefix_cap * a.page, 128);
+  const long long own_steps =
+      (long long)s.Hkv * s.row_tiles * s.B * ceil_div(a.max_pages * a.page, kOwnChunk);
+  auto least = [](long long x, long long y) { return (unsigned)(x < y ? x : y); };
+  const unsigned prefix_grid = least(sms, prefix_steps);
+  const unsigned own_grid = least(sms * kOwnBlocksPerSm, own_steps > 0 ? own_steps : 1);
+  s.prefix_workers = (int)prefix_grid;
+  s.own_workers = (int)own_grid * kOwnWarps;
   int shift = 0;
   while ((1 << shift) < a.page) ++shift;
   cudaError_t e;
@@ -669,7 +701,7 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
     e = cudaFuncSetAttribute(fwd_kernel<D, Prefix>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::SMEM);
     if (e != cudaSuccess) return e;
-    fwd_kernel<D, Prefix><<<sms, C::THREADS, C::SMEM, stream>>>(mq, mk, mv, mk, p, g);
+    fwd_kernel<D, Prefix><<<prefix_grid, C::THREADS, C::SMEM, stream>>>(mq, mk, mv, mk, p, g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   OwnParams op;
@@ -687,16 +719,15 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
   e = cudaFuncSetAttribute(own_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            OwnCfg<D>::RINGS + (kMaxBatch + 1) * 4);
   if (e != cudaSuccess) return e;
-  own_kernel<D><<<sms * kOwnBlocksPerSm, 32 * kOwnWarps, own_smem, stream>>>(op);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch(own_kernel<D>, own_grid, 32 * kOwnWarps, own_smem, stream, a.prefix_cap > 0, op);
+  if (e != cudaSuccess) return e;
   JoinParams jp;
   jp.s = s;
   jp.prefix_len = a.prefix_cap > 0 ? a.prefix_len : nullptr;
   jp.prefix_cap = cap;
   jp.O = static_cast<__nv_bfloat16*>(a.O);
   jp.L = a.L;
-  join_kernel<<<(unsigned)a.B * a.Hq, 32 * kJoinWarps, 0, stream>>>(jp);
-  return cudaGetLastError();
+  return launch(join_kernel, (unsigned)a.B * a.Hq, 32 * kJoinWarps, 0, stream, true, jp);
 }
 
 }  // namespace

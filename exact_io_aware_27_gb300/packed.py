@@ -17,7 +17,17 @@ from __future__ import annotations
 
 import torch
 
-from .api import _check, _out, _same_device, _scale, _workspace_bytes, lib
+from .api import _check, _out, _scale, _workspace_bytes, lib
+
+_BF16 = torch.bfloat16
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current stream of a device, as a handle
+
+
+def _elsewhere(device, stream) -> bool:
+    """True when a call has to enter _placed first: `stream` is given, or the tensors are
+    not on the current device. The common call is neither, and costs no context."""
+    return stream is not None or device.index != _current_device()
 
 
 def _placed(device, stream):
@@ -34,16 +44,12 @@ def _placed(device, stream):
     return torch.cuda.stream(stream)
 
 
-def _raw_stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
 def _row_stride(name, t):
     """Elements from row to row of a bf16 [rows, heads, d] CUDA tensor whose heads and
     columns are dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
+    if not t.is_cuda or t.dtype is not _BF16 or t.dim() != 3:
         raise ValueError(f"{name} must be a bf16 CUDA tensor [rows, heads, d]")
     rows, heads, d = t.shape
     s0, s1, s2 = t.stride()
@@ -92,12 +98,13 @@ def fa_packed_plan(cu_seqlens, total: int, causal: bool = True, plan: PackedPlan
         raise ValueError(f"invalid sizes for a plan: {nseq} sequences, {total} rows")
     if plan is not None and (plan.nseq, plan.total, plan.device) != (nseq, total, device):
         raise ValueError("plan was made for other sizes or another device")
-    with _placed(device, stream):
-        buffer = (torch.empty(size, dtype=torch.uint8, device=device) if plan is None
-                  else plan.buffer)
-        _check("fa_packed_plan",
-               lib().fa_packed_plan(cu_seqlens.data_ptr(), nseq, total, int(bool(causal)),
-                                    buffer.data_ptr(), size, _raw_stream(device)))
+    if _elsewhere(device, stream):
+        with _placed(device, stream):
+            return fa_packed_plan(cu_seqlens, total, causal, plan)
+    buffer = torch.empty(size, dtype=torch.uint8, device=device) if plan is None else plan.buffer
+    _check("fa_packed_plan",
+           lib().fa_packed_plan(cu_seqlens.data_ptr(), nseq, total, int(bool(causal)),
+                                buffer.data_ptr(), size, _raw_stream(device.index)))
     if plan is None:
         return PackedPlan(buffer, nseq, total, bool(causal))
     plan.causal = bool(causal)
@@ -110,16 +117,18 @@ def _packed_inputs(Q, K, V, plan):
     (Hq, Hkv, d)."""
     if not isinstance(plan, PackedPlan):
         raise TypeError("plan must be a PackedPlan")
-    strides = [_row_stride(n, t) for n, t in (("Q", Q), ("K", K), ("V", V))]
+    strides = _row_stride("Q", Q), _row_stride("K", K), _row_stride("V", V)
     total, Hq, d = Q.shape
-    Hkv = K.shape[1]
-    if K.shape != V.shape or K.shape[0] != total or K.shape[2] != d:
+    rows, Hkv, dk = K.shape
+    if K.shape != V.shape or rows != total or dk != d:
         raise ValueError("K and V must be [total, Hkv, d] with Q's rows and d")
     if Hkv == 0 or Hq % Hkv:
         raise ValueError("the number of query heads must be a multiple of the key/value heads")
     if total != plan.total:
         raise ValueError(f"the plan is for {plan.total} rows, Q has {total}")
-    _same_device(Q, K, V, plan.buffer)
+    at = Q.get_device()
+    if K.get_device() != at or V.get_device() != at or plan.buffer.get_device() != at:
+        raise ValueError("all tensors of a call must be on the same device")
     return strides, Hq, Hkv, d
 
 
@@ -130,21 +139,23 @@ def fa_packed_forward(Q, K, V, plan: PackedPlan, scale: float | None = None, O=N
     left as they were in tensors that are passed in."""
     (ldq, ldk, ldv), Hq, Hkv, d = _packed_inputs(Q, K, V, plan)
     total, device = plan.total, Q.device
-    with _placed(device, stream):
-        fill = 0
-        if O is None:
-            O, fill = torch.empty((total, Hq, d), dtype=torch.bfloat16, device=device), 1
-        else:
-            _out("O", O, (total, Hq, d), torch.bfloat16, device)
-        if L is None:
-            L, fill = torch.empty((Hq, total), dtype=torch.float32, device=device), fill | 2
-        else:
-            _out("L", L, (Hq, total), torch.float32, device)
-        _check("fa_packed_forward",
-               lib().fa_packed_forward(Q.data_ptr(), K.data_ptr(), V.data_ptr(), ldq, ldk, ldv,
-                                       total, Hq, Hkv, d, int(plan.causal), _scale(scale, d),
-                                       plan.buffer.data_ptr(), plan.nseq, O.data_ptr(),
-                                       L.data_ptr(), fill, _raw_stream(device)))
+    if _elsewhere(device, stream):
+        with _placed(device, stream):
+            return fa_packed_forward(Q, K, V, plan, scale, O, L)
+    fill = 0
+    if O is None:
+        O, fill = torch.empty((total, Hq, d), dtype=_BF16, device=device), 1
+    else:
+        _out("O", O, (total, Hq, d), _BF16, device)
+    if L is None:
+        L, fill = torch.empty((Hq, total), dtype=torch.float32, device=device), fill | 2
+    else:
+        _out("L", L, (Hq, total), torch.float32, device)
+    _check("fa_packed_forward",
+           lib().fa_packed_forward(Q.data_ptr(), K.data_ptr(), V.data_ptr(), ldq, ldk, ldv, total,
+                                   Hq, Hkv, d, plan.causal, _scale(scale, d),
+                                   plan.buffer.data_ptr(), plan.nseq, O.data_ptr(), L.data_ptr(),
+                                   fill, _raw_stream(device.index)))
     return O, L
 
 
@@ -160,7 +171,7 @@ def alloc_packed_workspace(plan: PackedPlan, Hq: int, d: int) -> torch.Tensor:
 def _gradient(name, like, t):
     """(tensor, row stride, allocated here) of a gradient with the shape of `like`."""
     if t is None:
-        return torch.empty(like.shape, dtype=torch.bfloat16, device=like.device), \
+        return torch.empty(like.shape, dtype=_BF16, device=like.device), \
             like.shape[1] * like.shape[2], True
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -180,27 +191,28 @@ def fa_packed_backward(Q, K, V, O, L, dO, plan: PackedPlan, scale: float | None 
     for name, t in (("O", O), ("dO", dO)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if (t.dtype != torch.bfloat16 or t.shape != Q.shape or not t.is_contiguous()
+        if (t.dtype is not _BF16 or t.shape != Q.shape or not t.is_contiguous()
                 or t.device != device):
             raise ValueError(f"{name} must be a contiguous bf16 tensor of Q's shape on {device}")
     if (not isinstance(L, torch.Tensor) or L.dtype != torch.float32 or L.device != device
             or tuple(L.shape) != (Hq, total) or not L.is_contiguous()):
         raise ValueError("L must be a contiguous fp32 [Hq, total] tensor on the inputs' device")
-    with _placed(device, stream):
-        dQ, lddq, new_q = _gradient("dQ", Q, dQ)
-        dK, lddk, new_k = _gradient("dK", K, dK)
-        dV, lddv, new_v = _gradient("dV", V, dV)
-        if workspace is None:
-            workspace = alloc_packed_workspace(plan, Hq, d)
-        size = _workspace_bytes(workspace, device)
-        _check("fa_packed_backward",
-               lib().fa_packed_backward(Q.data_ptr(), K.data_ptr(), V.data_ptr(), ldq, ldk, ldv,
-                                        O.data_ptr(), L.data_ptr(), dO.data_ptr(), total, Hq, Hkv,
-                                        d, int(plan.causal), _scale(scale, d),
-                                        plan.buffer.data_ptr(), plan.nseq, dQ.data_ptr(),
-                                        dK.data_ptr(), dV.data_ptr(), lddq, lddk, lddv,
-                                        new_q | new_k << 1 | new_v << 2, workspace.data_ptr(),
-                                        size, _raw_stream(device)))
+    if _elsewhere(device, stream):
+        with _placed(device, stream):
+            return fa_packed_backward(Q, K, V, O, L, dO, plan, scale, dQ, dK, dV, workspace)
+    dQ, lddq, new_q = _gradient("dQ", Q, dQ)
+    dK, lddk, new_k = _gradient("dK", K, dK)
+    dV, lddv, new_v = _gradient("dV", V, dV)
+    if workspace is None:
+        workspace = alloc_packed_workspace(plan, Hq, d)
+    size = _workspace_bytes(workspace, device)
+    _check("fa_packed_backward",
+           lib().fa_packed_backward(Q.data_ptr(), K.data_ptr(), V.data_ptr(), ldq, ldk, ldv,
+                                    O.data_ptr(), L.data_ptr(), dO.data_ptr(), total, Hq, Hkv, d,
+                                    plan.causal, _scale(scale, d), plan.buffer.data_ptr(),
+                                    plan.nseq, dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), lddq,
+                                    lddk, lddv, new_q | new_k << 1 | new_v << 2,
+                                    workspace.data_ptr(), size, _raw_stream(device.index)))
     return dQ, dK, dV
 
 

@@ -108,6 +108,13 @@ int fa_prefix_decode(const void* Q, const void* K_cache, const void* V_cache,
   if (num_prefix_pages < 0 || (long long)num_prefix_pages * page > kMaxKeys || max_pages < 0 ||
       (long long)max_pages * page > kMaxKeys)
     return FA_ERR_INVALID_ARG;
+  // the kernels count steps of 128 shared and 64 own keys in 32 bits
+  const long long groups = (long long)Hkv * ((Hq / Hkv + 15) / 16);
+  const int tile = 128 / (Hq / Hkv);
+  if ((long long)((B + 2 * tile - 1) / (2 * tile)) * Hkv *
+              (((long long)num_prefix_pages * page + 127) / 128) > 0x7fffffffLL ||
+      groups * B * (((long long)max_pages * page + 63) / 64) > 0x7fffffffLL)
+    return FA_ERR_INVALID_ARG;
   if (!Q || !K_cache || !V_cache || !lens || !O || !L || !workspace) return FA_ERR_INVALID_ARG;
   if ((num_prefix_pages > 0 && (!prefix_pages || !prefix_len)) || (max_pages > 0 && !block_table))
     return FA_ERR_INVALID_ARG;

@@ -56,6 +56,8 @@
 //   tile_bytes, block_bytes   the bytes that they bring
 //   store                     the epilogue of one warp's 32 rows
 //   idle_warps                work of the warps that have no role
+//   kAlternate                both tiles of an item hold the same rows (see half_of),
+//                             and store_joined writes the join of the two
 //   status()                  the translation unit's device status word
 //   kForeignTail              rows past the item's keys hold foreign values
 #pragma once
@@ -98,7 +100,9 @@ struct FwdCfg {
                                                  // (for a tile with no steps: the item's
                                                  // products done)
   static constexpr int B_DRAIN = B_PVD + TILES;
-  static constexpr int NBAR = B_DRAIN + 1;
+  static constexpr int B_X = B_DRAIN + 1;        // kAlternate: both tiles' row sums written
+  static constexpr int B_Y = B_DRAIN + 2;        // kAlternate: both tiles' O read out
+  static constexpr int NBAR = B_DRAIN + 3;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   // TMEM columns: Q_t as bf16 pairs (the A operand of S_t = Q_t K^T), S_t of one
   // 64-key step (then P_t as bf16 pairs over its first 32 columns), O_t.
@@ -171,6 +175,10 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
     else
       return G::item(g, snake_item(j, cta, P));
   };
+  // With kAlternate the two tiles hold the same rows and take the halves of each
+  // 128-key block in turn, so that one tile's rows keep both softmax groups busy.
+  auto half_of = [](int t, int k) { return G::kAlternate ? 2 * k + t : k; };
+  auto blocks = [](int nh) { return G::kAlternate ? nh : (nh + 1) / 2; };
   // The 64-key steps of each tile of an item (tile 0 always has some); returns the
   // steps of the longest tile.
   auto steps = [&](const Item& it, int (&nht)[C::TILES]) {
@@ -198,6 +206,8 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       mbar_init(&bar[C::B_PVD + t], 1);
     }
     mbar_init(&bar[C::B_DRAIN], 1);
+    mbar_init(&bar[C::B_X], 128 * C::TILES);
+    mbar_init(&bar[C::B_Y], 128 * C::TILES);
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -226,7 +236,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         const Item it = nxt;
         if (j + 1 < n_mine) nxt = fetch(j + 1);
         int nht[C::TILES];
-        const int nkb = (steps(it, nht) + 1) / 2;  // 128-key blocks
+        const int nkb = blocks(steps(it, nht));  // 128-key blocks
         for (int u = 0; u < C::QUSES + nkb; ++u, ++ru) {
           const int s = ru % C::STAGES;
           if (ru >= C::STAGES &&
@@ -276,11 +286,13 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         const Item it = nxt;
         if (j + 1 < n_mine) nxt = fetch(j + 1);
         int nht[C::TILES];
-        const int nh = steps(it, nht), nkb = (nh + 1) / 2;
-        auto use_of = [&](int k) { return ru + C::QUSES + (k >> 1); };  // ring use of step k's block
+        const int nh = steps(it, nht), nkb = blocks(nh);
+        // ring use of the block that holds half `u` of the item's keys
+        auto use_of = [&](int u) { return ru + C::QUSES + (u >> 1); };
         auto scores = [&](int t, int k) {
+          const int u = half_of(t, k);
           const uint64_t b_k = sdesc_sw128(
-              smem_u32(smem + C::OFF_K + (use_of(k) % C::STAGES) * C::TILE + (k & 1) * C::HALF_ROWS),
+              smem_u32(smem + C::OFF_K + (use_of(u) % C::STAGES) * C::TILE + (u & 1) * C::HALF_ROWS),
               16, 1024);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -291,8 +303,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
           umma_commit_w(&bar[C::B_SF + t]);
         };
         auto pv = [&](int t, int k) {
+          const int u = half_of(t, k);
           const uint64_t b_mn = sdesc_sw128(
-              smem_u32(smem + C::OFF_V + (use_of(k) % C::STAGES) * C::TILE + (k & 1) * C::HALF_ROWS),
+              smem_u32(smem + C::OFF_V + (use_of(u) % C::STAGES) * C::TILE + (u & 1) * C::HALF_ROWS),
               C::CHUNK, 1024);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
@@ -312,8 +325,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         for (int t = 0; t < C::TILES; ++t)
           if (nht[t] > 0) scores(t, 0);
         for (int k = 0; ok && k < nh; ++k) {
-          if (k + 1 < nh && ((k + 1) & 1) == 0) {  // step k+1 opens block (k+1)/2
-            const int u = use_of(k + 1);
+          // step k + 1 opens a block
+          if (k + 1 < nh && (half_of(0, k + 1) & 1) == 0) {
+            const int u = use_of(half_of(0, k + 1));
             if (!warp_wait(&bar[C::B_KVF + u % C::STAGES], (u / C::STAGES) & 1, wc)) { ok = false; break; }
           }
 #pragma unroll
@@ -327,9 +341,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
             else
               umma_commit_w(&bar[C::B_PVD + t]);
           }
-          // both tiles are done with block k/2 once its second step is issued
-          if (ok && ((k & 1) || k + 1 == nh))
-            umma_commit_w(&bar[C::B_KVE + use_of(k) % C::STAGES]);
+          // both tiles are done with a block once its second half's step is issued
+          if (ok && (G::kAlternate || (k & 1) || k + 1 == nh))
+            umma_commit_w(&bar[C::B_KVE + use_of(half_of(0, k)) % C::STAGES]);
         }
         // A tile with no steps (the second tile of a head's last pair when n mod 256
         // <= 128) is signalled once the item's products are done, so that its
@@ -389,7 +403,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
     for (int j = 0; ok && j < n_mine; ++j) {
       const Item it = nxt;
       int nht[C::TILES];
-      const int nkb = (steps(it, nht) + 1) / 2;
+      const int nkb = blocks(steps(it, nht));
       const int nh_t = nht[t];
       const int m_keys = G::keys(g, it);
       const int qg = G::causal(g) ? G::first_query(g, it) + t * C::BM + row : 0;
@@ -409,7 +423,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         reg_fence32(sr + 32);
 
         // Last visible column of this step for this row (ragged m, causal k <= q).
-        const int ks = 64 * k;
+        const int ks = 64 * half_of(t, k);
         int lim = m_keys - 1 - ks;
         if (G::causal(g)) lim = min(lim, qg - ks);
         if (lim < 63) {
@@ -471,8 +485,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         // them gets zeros. Both tiles' groups may write them (the same zeros).
         if constexpr (G::kForeignTail) {
           if (m_keys - ks < 64) {
-            uint8_t* v = smem + C::OFF_V + ((ru + C::QUSES + (k >> 1)) % C::STAGES) * C::TILE +
-                         (k & 1) * C::HALF_ROWS;
+            const int u = half_of(t, k);
+            uint8_t* v = smem + C::OFF_V + ((ru + C::QUSES + (u >> 1)) % C::STAGES) * C::TILE +
+                         (u & 1) * C::HALF_ROWS;
             for (int i = (m_keys - ks) * 8 + row_thread; i < 64 * 8; i += 128)
 #pragma unroll
               for (int c = 0; c < C::KCH; ++c)
@@ -502,7 +517,32 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       // next item's first S products run while the O rows are written.
       if (ok && j + 1 < n_mine && !move_q(ru + C::QUSES + nkb)) ok = false;
       // ---------------------------------------------------------- epilogue
-      if (ok && nh_t > 0) {
+      if constexpr (G::kAlternate) {
+        // Both groups hold partial results of the same rows: they exchange the rows'
+        // (m, l) through the second half of each warp's staging area, and group t
+        // joins and writes columns [t D/2, (t + 1) D/2).
+        if (!ok) break;
+        if (!warp_wait(&bar[C::B_PVD], j & 1, wc) || !warp_wait(&bar[C::B_PVD + 1], j & 1, wc)) {
+          ok = false;
+          break;
+        }
+        if (nh_t > 0) ++pvd_t;
+        uint8_t* mine = smem + C::OFF_EPI + (warp - C::SOFT0) * kStoreStageBytes;
+        uint8_t* other = smem + C::OFF_EPI + ((warp - C::SOFT0) ^ 4) * kStoreStageBytes;
+        *reinterpret_cast<float2*>(mine + 2048 + lane * 8) = make_float2(m_ref, l_run);
+        mbar_arrive(&bar[C::B_X]);
+        if (!warp_wait(&bar[C::B_X], j & 1, wc)) { ok = false; break; }
+        tc_fence_after();
+        const float2 o = *reinterpret_cast<const float2*>(other + 2048 + lane * 8);
+        const float2 s0 = t == 0 ? make_float2(m_ref, l_run) : o;
+        const float2 s1 = t == 0 ? o : make_float2(m_ref, l_run);
+        G::template store_joined<D>(g, it, t, warp & 3, lane, lane_base + C::COL_O, s0, s1,
+                                    nht[1] > 0, mine, p.d);
+        tc_fence_before();
+        mbar_arrive(&bar[C::B_Y]);
+        // the next item's products overwrite both accumulators
+        if (!warp_wait(&bar[C::B_Y], j & 1, wc)) { ok = false; break; }
+      } else if (ok && nh_t > 0) {
         if (!warp_wait(&bar[C::B_PVD + t], pvd_t & 1, wc)) { ok = false; break; }
         tc_fence_after();
         G::template store<D>(g, it, t, warp & 3, lane, ocol, m_ref, l_run,

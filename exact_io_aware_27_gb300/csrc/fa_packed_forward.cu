@@ -40,7 +40,7 @@ struct Packed {
     int h;
   };
   FA_DEV static unsigned int* status() { return &g_packed_status; }
-  static constexpr bool kSplit = false;
+  static constexpr bool kSplit = false, kAlternate = false;
   static constexpr bool kForeignTail = true;
   FA_DEV static int items(const View& g) { return g.tiles * g.p.Hq; }
   FA_DEV static Item item(const View& g, int i) {

@@ -36,19 +36,27 @@ constexpr int kOwnBlocksPerSm = 2;
 constexpr int kOwnChunk = 64;      // keys per step of the own keys' split
 constexpr int kMinPrefixBlocks = 2;  // 128-key blocks a prefix worker takes at least
 
-// `total` steps dealt to `workers` in equal, contiguous pieces.
+// `total` steps (below 2^31) dealt to at most `most` workers in contiguous pieces that
+// differ by one step at most; the longer pieces come first.
 struct Split {
-  long long total;
+  unsigned total, base, longer;
   int workers;
-  FA_DEV Split(long long steps, int most) : total(steps), workers((int)min(steps, (long long)most)) {}
-  FA_DEV long long start(int w) const { return total * w / workers; }
+  FA_DEV Split(unsigned steps, unsigned most) : total(steps) {
+    workers = (int)min(steps, most);
+    base = workers > 0 ? steps / (unsigned)workers : 0u;
+    longer = steps - base * (unsigned)workers;
+  }
+  FA_DEV unsigned start(int w) const { return (unsigned)w * base + min((unsigned)w, longer); }
   // The worker whose piece holds step x (0 <= x < total).
-  FA_DEV int owner(long long x) const { return (int)(((x + 1) * workers - 1) / total); }
+  FA_DEV int owner(unsigned x) const {
+    const unsigned in_longer = longer * (base + 1);
+    return (int)(x < in_longer ? x / (base + 1) : longer + (x - in_longer) / base);
+  }
   // The slot of a unit's part number `part` of `parts` (its first worker is `first`):
   // unit's own slot, or the worker's slot for the unit that starts in its piece and goes
   // on (odd) or came from the piece before (even).
-  FA_DEV static long long slot(long long unit, long long units, int parts, int first, int part) {
-    return parts == 1 ? unit : units + 2LL * (first + part) + (part == 0 ? 1 : 0);
+  FA_DEV static unsigned slot(unsigned unit, unsigned units, int parts, int first, int part) {
+    return parts == 1 ? unit : units + 2u * (unsigned)(first + part) + (part == 0 ? 1u : 0u);
   }
 };
 
@@ -112,59 +120,71 @@ FA_DEV int prefix_keys(const int* prefix_len, int cap) {
   const int n = prefix_len ? __ldg(prefix_len) : 0;
   return max(0, min(n, cap));
 }
-FA_DEV Split prefix_split(const DecodeSizes& s, int keys) {
-  const long long steps = (long long)s.pairs * s.Hkv * ((keys + 127) / 128);
-  return Split(steps, (int)max(1LL, min((long long)s.prefix_workers,
-                                        (steps + kMinPrefixBlocks - 1) / kMinPrefixBlocks)));
+FA_DEV Split prefix_split(const DecodeSizes& s, int blocks) {
+  const unsigned steps = (unsigned)(s.pairs * s.Hkv) * (unsigned)blocks;
+  return Split(steps, min((unsigned)s.prefix_workers,
+                          (steps + kMinPrefixBlocks - 1) / kMinPrefixBlocks));
 }
 
 // ================================================================== prefix kernel
+struct PrefixParams {
+  DecodeSizes s;
+  const int *pages, *len;
+  int cap, page, page_shift, box, num_pages;  // cap: keys; box: rows of a TMA copy
+};
+
+// ONE_TILE: all rows of a key/value head fit one 128-row tile (so there is one pair, and
+// its second tile is empty): both softmax groups work on that tile, each on every other
+// 64 keys.
+template <bool ONE_TILE>
 struct Prefix {
-  struct Params {
-    DecodeSizes s;
-    const int *pages, *len;
-    int cap, page, page_shift, box, num_pages;  // cap: keys; box: rows of a TMA copy
-  };
+  using Params = PrefixParams;
   struct View {
     const Params& p;
-    int keys;
+    int keys, blocks;
+    Split split;
   };
   struct Item {
     int pair, hk, k0, m;  // tile pair, head, first key, keys
-    long long slot;
+    unsigned slot;
   };
-  static constexpr bool kSplit = true;
+  static constexpr bool kSplit = true, kAlternate = ONE_TILE;
   static constexpr bool kForeignTail = true;
   FA_DEV static unsigned int* status() { return &g_prefix_status; }
   FA_DEV static View view(const Params& p) {
     const int n = __ldg(p.len);
     if ((n < 0 || n > p.cap) && blockIdx.x == 0 && threadIdx.x == 0)
       atomicOr(status(), kDeviceIndexBit);
-    return {p, prefix_keys(p.len, p.cap)};
+    const int keys = max(0, min(n, p.cap)), blocks = (keys + 127) / 128;
+    return {p, keys, blocks, prefix_split(p.s, blocks)};
   }
   FA_DEV static int segments(const View& g, int cta, int) {
-    const int blocks = (g.keys + 127) / 128;
-    const Split sp = prefix_split(g.p.s, g.keys);
-    if (cta >= sp.workers) return 0;
-    return (int)((sp.start(cta + 1) - 1) / blocks - sp.start(cta) / blocks) + 1;
+    if (cta >= g.split.workers) return 0;
+    const unsigned a = g.split.start(cta), b = g.split.start(cta + 1), n = (unsigned)g.blocks;
+    return (int)((a % n + (b - a) + n - 1) / n);
   }
   FA_DEV static Item segment(const View& g, int cta, int, int j) {
-    const int blocks = (g.keys + 127) / 128;
-    const Split sp = prefix_split(g.p.s, g.keys);
-    const long long a = sp.start(cta), b = sp.start(cta + 1);
-    const long long unit = a / blocks + j, u0 = unit * blocks, u1 = u0 + blocks;
-    const long long x0 = max(a, u0), x1 = min(b, u1);
+    const unsigned a = g.split.start(cta), b = g.split.start(cta + 1);
+    const unsigned unit = a / (unsigned)g.blocks + (unsigned)j, u0 = unit * (unsigned)g.blocks;
+    const unsigned x0 = max(a, u0), x1 = min(b, u0 + (unsigned)g.blocks);
     Item it;
-    it.pair = (int)(unit / g.p.s.Hkv);
-    it.hk = (int)(unit - (long long)it.pair * g.p.s.Hkv);
+    it.pair = (int)(unit / (unsigned)g.p.s.Hkv);
+    it.hk = (int)unit - it.pair * g.p.s.Hkv;
     it.k0 = (int)(x0 - u0) * 128;
     it.m = min(g.keys, (int)(x1 - u0) * 128) - it.k0;
-    const long long units = (long long)g.p.s.pairs * g.p.s.Hkv;
-    it.slot = x0 == u0 && x1 == u1 ? unit : units + 2LL * cta + (x0 == u0 ? 1 : 0);
+    const unsigned units = (unsigned)(g.p.s.pairs * g.p.s.Hkv);
+    it.slot = x1 - x0 == (unsigned)g.blocks ? unit
+                                            : units + 2u * (unsigned)cta + (x0 == u0 ? 1u : 0u);
     return it;
   }
   FA_DEV static int steps(const View& g, const Item& it, int t) {
-    return (2 * it.pair + t) * g.p.s.per_tile < g.p.s.B ? (it.m + 63) / 64 : 0;
+    const int halves = (it.m + 63) / 64;
+    if (ONE_TILE) return (halves + 1 - t) / 2;
+    return (2 * it.pair + t) * g.p.s.per_tile < g.p.s.B ? halves : 0;
+  }
+  // The first request of tile t.
+  FA_DEV static int request(const View& g, const Item& it, int t) {
+    return (2 * it.pair + (ONE_TILE ? 0 : t)) * g.p.s.per_tile;
   }
   FA_DEV static int keys(const View&, const Item& it) { return it.m; }
   FA_DEV static constexpr int causal(const View&) { return 0; }
@@ -177,7 +197,7 @@ struct Prefix {
   // a tile keep what the buffer held; nothing of them is stored.
   FA_DEV static void load_q(void* dst, const CUtensorMap* map, uint64_t* f, int col,
                             const View& g, const Item& it, int t) {
-    tma_load_4d(dst, map, f, col, 0, it.hk, (2 * it.pair + t) * g.p.s.per_tile);
+    tma_load_4d(dst, map, f, col, 0, it.hk, request(g, it, t));
   }
   // Copies of `box` rows (a page or 128 keys) of a block; pages wholly past the item's
   // keys are not read.
@@ -208,35 +228,89 @@ struct Prefix {
       }
     }
   }
-  // The part's o (fp32) and e of one warp's 32 rows, lane by lane.
-  template <int D>
-  FA_DEV static void store(const View& g, const Item& it, int t, int warp, int lane, uint32_t ocol,
-                           float m_ref, float l, uint8_t*, const CUtensorMap*, int d) {
-    const DecodeSizes& s = g.p.s;
-    const int r = warp * 32 + lane;
-    const int in_pair = t * s.per_tile * s.per_kv + r;  // row of the slot
-    const bool valid = r < s.per_tile * s.per_kv &&
-                       (2 * it.pair + t) * s.per_tile + r / s.per_kv < s.B;
-    float* o = s.prefix_o + ((size_t)it.slot * s.pair_rows + in_pair) * d;
-    const float inv = 1.f / l;
+  // Writes columns [c0, c0 + NCOL) of a warp's 32 rows of a part, fp32 [pair_rows, d]:
+  // 16 columns at a time through 2 KB of shared memory (16-byte piece k of row r at
+  // k ^ ((r >> 1) & 3)), so that a row's 64 bytes leave together. `fetch(c, v)` gives this
+  // lane's columns c .. c + 15; `rows` of the 32 rows are written.
+  template <int NCOL, class F>
+  FA_DEV static void write_part(float* out, int rows, int c0, int d, int lane, uint8_t* stage,
+                                F fetch) {
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      if (32 * c >= d) break;
-      uint32_t v[32];
-      tmem_ld32(ocol + 32 * c, v);
-      tmem_ld_wait();
-      reg_fence32(v);
-      if (valid) {
+    for (int c = 0; c < NCOL; c += 16) {
+      if (c0 + c >= d) break;  // warp-uniform
+      float v[16];
+      fetch(c0 + c, v);
+      __syncwarp();  // the previous piece has been read
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (32 * c + 4 * k < d)
-            reinterpret_cast<float4*>(o + 32 * c)[k] =
-                make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
-                            __uint_as_float(v[4 * k + 2]) * inv,
-                            __uint_as_float(v[4 * k + 3]) * inv);
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<float4*>(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
+            make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), k = lane & 3;
+        const float4 x =
+            *reinterpret_cast<const float4*>(stage + r * 64 + ((k ^ ((r >> 1) & 3)) << 4));
+        if (r < rows && c0 + c + 4 * k < d)
+          *reinterpret_cast<float4*>(out + (size_t)r * d + c0 + c + 4 * k) = x;
       }
     }
-    if (valid) s.prefix_e[(size_t)it.slot * s.pair_rows + in_pair] = m_ref + lg2(l);
+  }
+  // Rows of tile t that hold a request's query head, and its first row in a slot.
+  FA_DEV static int tile_rows(const View& g, const Item& it, int t) {
+    return min(g.p.s.per_tile, g.p.s.B - request(g, it, t)) * g.p.s.per_kv;
+  }
+  // The part's o and e of one warp's 32 rows.
+  template <int D>
+  FA_DEV static void store(const View& g, const Item& it, int t, int warp, int lane, uint32_t ocol,
+                           float m_ref, float l, uint8_t* stage, const CUtensorMap*, int d) {
+    const DecodeSizes& s = g.p.s;
+    const int rows = tile_rows(g, it, t) - warp * 32;
+    if (rows <= 0) return;  // warp-uniform
+    const size_t at = (size_t)it.slot * s.pair_rows + t * s.per_tile * s.per_kv + warp * 32;
+    const float inv = 1.f / l;
+    write_part<D>(s.prefix_o + at * d, rows, 0, d, lane, stage, [&](int c, float (&v)[16]) {
+      uint32_t x[16];
+      tmem_ld16(ocol + c, x);
+      tmem_ld_wait();
+      reg_fence16(x);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(x[e]) * inv;
+    });
+    if (lane < rows) s.prefix_e[at + lane] = m_ref + lg2(l);
+  }
+  // The same from the two halves of the keys: (m, l) = s0 with O in columns ocol, s1 with
+  // O in ocol + D (nothing there where `second` is false). Group t writes half of the
+  // columns.
+  template <int D>
+  FA_DEV static void store_joined(const View& g, const Item& it, int t, int warp, int lane,
+                                  uint32_t ocol, float2 s0, float2 s1, bool second,
+                                  uint8_t* stage, int d) {
+    const DecodeSizes& s = g.p.s;
+    const int rows = tile_rows(g, it, 0) - warp * 32;
+    if (rows <= 0) return;  // warp-uniform
+    const size_t at = (size_t)it.slot * s.pair_rows + warp * 32;
+    const float top = second ? fmaxf(s0.x, s1.x) : s0.x;
+    const float ref = top == -INFINITY ? 0.f : top;
+    float f0 = ex2(s0.x - ref), f1 = second ? ex2(s1.x - ref) : 0.f;
+    const float l = second ? s0.y * f0 + s1.y * f1 : s0.y * f0;
+    f0 /= l;
+    f1 /= l;
+    write_part<D / 2>(s.prefix_o + at * d, rows, t * (D / 2), d, lane, stage,
+                      [&](int c, float (&v)[16]) {
+                        uint32_t x[16], y[16];
+                        tmem_ld16(ocol + c, x);
+                        if (second) tmem_ld16(ocol + D + c, y);
+                        tmem_ld_wait();
+                        reg_fence16(x);
+                        if (second) reg_fence16(y);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                          v[e] = __uint_as_float(x[e]) * f0;
+                          if (second) v[e] += __uint_as_float(y[e]) * f1;
+                        }
+                      });
+    if (t == 0 && lane < rows) s.prefix_e[at + lane] = ref + lg2(l);
   }
   FA_DEV static void idle_warps(const View&, int, int, int) {}
 };
@@ -316,24 +390,24 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
     for (int b = threadIdx.x; b <= s.B; b += kThreads) s.first[b] = first[b];
 
   const int chunks = run;  // of one (head, row tile)
-  const long long units = (long long)s.Hkv * s.row_tiles * s.B;
-  const Split sp((long long)s.Hkv * s.row_tiles * chunks, s.own_workers);
+  const unsigned units = (unsigned)(s.Hkv * s.row_tiles * s.B);
+  const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)chunks, (unsigned)s.own_workers);
   const int me = warp * gridDim.x + blockIdx.x;  // the first workers on different SMs
   if (me >= sp.workers) {  // no barrier of the block follows
     grid_wait();
     return;
   }
-  const long long x_end = sp.start(me + 1), x_begin = sp.start(me);
+  const unsigned x_end = sp.start(me + 1), x_begin = sp.start(me);
 
   // A run of chunks of one unit.
   struct Run {
     int b, ht, key, key_end, len;  // request, head and row tile, keys [key, key_end)
-    long long x0, x1, u0, u1;      // this run's steps, the unit's steps
+    unsigned x0, x1, u0, u1;       // this run's steps, the unit's steps
   };
-  auto run_at = [&](long long x) {
+  auto run_at = [&](unsigned x) {
     Run r;
-    r.ht = (int)(x / chunks);
-    const int in = (int)(x - (long long)r.ht * chunks);
+    r.ht = (int)(x / (unsigned)chunks);
+    const int in = (int)(x - (unsigned)(r.ht * chunks));
     int lo = 0, hi = s.B;  // first[lo] <= in < first[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -343,8 +417,8 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
         hi = mid;
     }
     r.b = lo;
-    r.u0 = (long long)r.ht * chunks + first[lo];
-    r.u1 = (long long)r.ht * chunks + first[lo + 1];
+    r.u0 = (unsigned)(r.ht * chunks + first[lo]);
+    r.u1 = (unsigned)(r.ht * chunks + first[lo + 1]);
     r.x0 = x;
     r.x1 = min(r.u1, x_end);
     r.len = own_keys(p, lo);
@@ -409,7 +483,7 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
   // ---- the products
   const int qr = lane >> 2, qc = (lane & 3) * 2;  // row and first column of a fragment
   int stage = 0;
-  for (long long x = x_begin; x < x_end;) {
+  for (unsigned x = x_begin; x < x_end;) {
     const Run r = run_at(x);
     x = r.x1;
     const int hk = r.ht / s.row_tiles, rt = r.ht - hk * s.row_tiles;
@@ -514,10 +588,10 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    const long long unit = (long long)r.ht * s.B + r.b;
-    const long long slot = r.x0 == r.u0 && r.x1 == r.u1
-                               ? unit
-                               : units + 2LL * me + (r.x0 == r.u0 ? 1 : 0);
+    const unsigned unit = (unsigned)(r.ht * s.B + r.b);
+    const unsigned slot = r.x0 == r.u0 && r.x1 == r.u1
+                              ? unit
+                              : units + 2u * (unsigned)me + (r.x0 == r.u0 ? 1u : 0u);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int row = qr + 8 * e;
@@ -548,87 +622,129 @@ struct JoinParams {
   float* L;
 };
 
-// One thread block per row (request, query head), four columns a lane; its warps take
-// every fourth part. A row without keys gets O = 0, L = -inf.
-constexpr int kJoinWarps = 4;
+// A row (request, query head) is joined by one warp, or by kJoinWarps where there are
+// too few rows to fill the GPU and each has many parts. Lane j of a warp looks up every
+// 32nd part (its slot and e); then the warp adds the parts up, four columns a lane and
+// eight parts in flight: the kernel is bound by the latency of these loads. A row
+// without keys gets O = 0, L = -inf.
+constexpr int kJoinWarps = 8;
+template <int WARPS>  // of a row
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ JoinParams p) {
   __shared__ float4 sums[kJoinWarps][32];
-  __shared__ float weights[kJoinWarps];
+  __shared__ float2 stats[kJoinWarps];  // a warp's reference and weight sum
   const DecodeSizes& s = p.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / s.Hq, hq = blockIdx.x - b * s.Hq;
-  const int hk = hq / s.per_kv, in = hq - hk * s.per_kv;
+  const int row = WARPS == 1 ? blockIdx.x * kJoinWarps + warp : blockIdx.x;
+  const int mine = WARPS == 1 ? 0 : warp;  // this warp of the row's
   grid_wait();
+  if (row >= s.B * s.Hq) return;  // WARPS == 1 only: no barrier follows
+  const int b = row / s.Hq, hq = row - b * s.Hq;
+  const int hk = hq / s.per_kv, in = hq - hk * s.per_kv;
 
   // Parts of the prefix, then of the request's own keys.
-  const int keys = prefix_keys(p.prefix_len, p.prefix_cap), blocks = (keys + 127) / 128;
-  int pparts = 0, pfirst = 0;
-  long long punit = 0;
-  if (blocks > 0) {
-    const Split sp = prefix_split(s, keys);
-    punit = (long long)(b / (2 * s.per_tile)) * s.Hkv + hk;
-    pfirst = sp.owner(punit * blocks);
-    pparts = sp.owner((punit + 1) * blocks - 1) - pfirst + 1;
-  }
-  const int prow = (b % (2 * s.per_tile)) * s.per_kv + in;
+  const int blocks = (prefix_keys(p.prefix_len, p.prefix_cap) + 127) / 128;
   const int chunks = __ldg(s.first + s.B), f0 = __ldg(s.first + b), f1 = __ldg(s.first + b + 1);
+  int pparts = 0, pfirst = 0;
+  const int pair = b / (2 * s.per_tile);
+  const unsigned punit = (unsigned)(pair * s.Hkv + hk);
+  if (blocks > 0) {
+    const Split sp = prefix_split(s, blocks);
+    pfirst = sp.owner(punit * (unsigned)blocks);
+    pparts = sp.owner((punit + 1) * (unsigned)blocks - 1) - pfirst + 1;
+  }
+  const int prow = (b - pair * 2 * s.per_tile) * s.per_kv + in;
   const int ht = hk * s.row_tiles + in / 16;
   int oparts = 0, ofirst = 0;
   if (f1 > f0) {
-    const Split sp((long long)s.Hkv * s.row_tiles * chunks, s.own_workers);
-    ofirst = sp.owner((long long)ht * chunks + f0);
-    oparts = sp.owner((long long)ht * chunks + f1 - 1) - ofirst + 1;
+    const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)chunks, (unsigned)s.own_workers);
+    ofirst = sp.owner((unsigned)(ht * chunks + f0));
+    oparts = sp.owner((unsigned)(ht * chunks + f1) - 1u) - ofirst + 1;
   }
-  const long long punits = (long long)s.pairs * s.Hkv, ounits = (long long)s.Hkv * s.row_tiles * s.B;
+  const unsigned punits = (unsigned)(s.pairs * s.Hkv);
+  const unsigned ounits = (unsigned)(s.Hkv * s.row_tiles * s.B);
   const int parts = pparts + oparts;
-  auto where = [&](int i) -> long long {  // row of the part: >= 0 prefix, else own (~row)
-    if (i < pparts) return Split::slot(punit, punits, pparts, pfirst, i) * s.pair_rows + prow;
-    return ~(Split::slot((long long)ht * s.B + b, ounits, oparts, ofirst, i - pparts) *
-                 s.own_rows + in % 16);
-  };
-  auto log_weight = [&](int i) {
-    const long long w = where(i);
-    return w >= 0 ? s.prefix_e[w] : s.own_e[~w];
-  };
-  float M = -INFINITY;
-  for (int i = lane; i < parts; i += 32) M = fmaxf(M, log_weight(i));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ref = M == -INFINITY ? 0.f : M;
+
+  float ref = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < parts; i += kJoinWarps) {
-    const long long w = where(i);
-    const float* o = (w >= 0 ? s.prefix_o + w * s.d : s.own_o + ~w * s.d);
-    const float f = ex2((w >= 0 ? s.prefix_e[w] : s.own_e[~w]) - ref);
-    sum += f;
-    if (4 * lane < s.d) {
-      const float4 v = reinterpret_cast<const float4*>(o)[lane];
+  for (int base = 0; base < parts; base += 32 * WARPS) {
+    const int i = base + lane * WARPS + mine;
+    const float* o = nullptr;
+    float e = -INFINITY;
+    if (i < pparts) {
+      const size_t at = (size_t)Split::slot(punit, punits, pparts, pfirst, i) * s.pair_rows + prow;
+      o = s.prefix_o + at * s.d;
+      e = s.prefix_e[at];
+    } else if (i < parts) {
+      const unsigned slot =
+          Split::slot((unsigned)(ht * s.B + b), ounits, oparts, ofirst, i - pparts);
+      const size_t at = (size_t)slot * s.own_rows + in % 16;
+      o = s.own_o + at * s.d;
+      e = s.own_e[at];
+    }
+    float top = e;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float next = fmaxf(ref, top);
+    const float back = ref == next ? 1.f : ex2(ref - next);  // 0 on the first round
+    ref = next;
+    const float weight = o ? ex2(e - (ref == -INFINITY ? 0.f : ref)) : 0.f;
+    sum = sum * back + weight;  // this lane's parts
+    acc.x *= back;
+    acc.y *= back;
+    acc.z *= back;
+    acc.w *= back;
+    const int n = min(32, (parts - base - mine + WARPS - 1) / WARPS);  // lanes with a part
+    for (int j = 0; j < n; j += 8) {
+      float4 v[8];
+      float w[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float* src = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (j + u) & 31));
+        w[u] = __shfl_sync(0xffffffffu, weight, (j + u) & 31);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j + u < n && 4 * lane < s.d) v[u] = reinterpret_cast<const float4*>(src)[lane];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (j + u >= n) break;
+        acc.x += w[u] * v[u].x;
+        acc.y += w[u] * v[u].y;
+        acc.z += w[u] * v[u].z;
+        acc.w += w[u] * v[u].w;
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  if (WARPS > 1) {
+    sums[warp][lane] = acc;
+    if (lane == 0) stats[warp] = make_float2(ref, sum);
+    __syncthreads();
+    if (warp != 0) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, stats[w].x);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      // a warp without parts has reference -inf and adds nothing
+      const float f = w < parts ? ex2(stats[w].x - (top == -INFINITY ? 0.f : top)) : 0.f;
+      const float4 v = sums[w][lane];
       acc.x += f * v.x;
       acc.y += f * v.y;
       acc.z += f * v.z;
       acc.w += f * v.w;
+      sum += f * stats[w].y;
     }
-  }
-  sums[warp][lane] = acc;
-  if (lane == 0) weights[warp] = sum;
-  __syncthreads();
-  if (warp != 0) return;
-#pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) {
-    const float4 v = sums[w][lane];
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
-    sum += weights[w];
+    ref = top;
   }
   const float inv = parts > 0 ? 1.f / sum : 0.f;
   if (4 * lane < s.d)
-    reinterpret_cast<uint2*>(p.O + (size_t)blockIdx.x * s.d)[lane] =
+    reinterpret_cast<uint2*>(p.O + (size_t)row * s.d)[lane] =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (lane == 0) p.L[blockIdx.x] = parts > 0 ? (M + lg2(sum)) * kLn2 : -INFINITY;
+  if (lane == 0) p.L[row] = parts > 0 ? (ref + lg2(sum)) * kLn2 : -INFINITY;
 }
 
 int decode_sms() {
@@ -675,7 +791,7 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
   cudaError_t e;
   const int cap = a.prefix_cap << shift;
   if (a.prefix_cap > 0) {
-    Prefix::Params g;
+    PrefixParams g;
     g.s = s;
     g.pages = a.prefix_pages;
     g.len = a.prefix_len;
@@ -698,10 +814,11 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
     FwdParams p;
     p.d = a.d;
     p.scale_log2 = a.scale * kLog2e;
-    e = cudaFuncSetAttribute(fwd_kernel<D, Prefix>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::SMEM);
+    const bool one_tile = a.B <= s.per_tile;
+    auto kernel = one_tile ? fwd_kernel<D, Prefix<true>> : fwd_kernel<D, Prefix<false>>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    fwd_kernel<D, Prefix><<<prefix_grid, C::THREADS, C::SMEM, stream>>>(mq, mk, mv, mk, p, g);
+    kernel<<<prefix_grid, C::THREADS, C::SMEM, stream>>>(mq, mk, mv, mk, p, g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   OwnParams op;
@@ -727,7 +844,12 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
   jp.prefix_cap = cap;
   jp.O = static_cast<__nv_bfloat16*>(a.O);
   jp.L = a.L;
-  return launch(join_kernel, (unsigned)a.B * a.Hq, 32 * kJoinWarps, 0, stream, true, jp);
+  // A warp per row once there is a row for every fourth warp slot of the GPU's SMs.
+  const int rows = a.B * a.Hq;
+  return rows >= sms * 4
+             ? launch(join_kernel<1>, (unsigned)ceil_div(rows, kJoinWarps), 32 * kJoinWarps, 0,
+                      stream, true, jp)
+             : launch(join_kernel<kJoinWarps>, (unsigned)rows, 32 * kJoinWarps, 0, stream, true, jp);
 }
 
 }  // namespace

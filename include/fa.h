@@ -300,7 +300,8 @@ FA_API int fa_cache_append(const void* K, const void* V, long long k_stride, lon
  * (int32 [B]) are in device memory, so that a captured call follows them. A request
  * without keys gets O = 0 and L = -inf. num_prefix_pages and max_pages may be 0, and the
  * pointers that they size are then not read. Hq a multiple of Hkv, Hq / Hkv <= 128,
- * B <= 8192, d as in fa_forward. `workspace`: caller-owned device memory of at least
+ * B <= 8192, ceil(Hq / Hkv / 16) * Hkv * B * max_pages * page < 2^37, d as in
+ * fa_forward. `workspace`: caller-owned device memory of at least
  * fa_prefix_workspace_bytes() bytes for num_prefix_pages * page and max_pages * page keys
  * (more for larger capacities), 16-byte aligned, contents on entry do not matter; calls
  * that may run at the same time need one each. Up to three kernel launches on

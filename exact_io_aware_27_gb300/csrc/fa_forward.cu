@@ -35,7 +35,9 @@ struct Dense {
   }
   FA_DEV static int keys(const Params& g, const Item&) { return g.m; }
   FA_DEV static int causal(const Params& g) { return g.causal; }
-  FA_DEV static int first_query(const Params&, const Item& it) { return it.qs; }
+  FA_DEV static int query(const Params&, const Item& it, int t, int row) {
+    return it.qs + t * 128 + row;
+  }
   FA_DEV static void load_q(void* dst, const CUtensorMap* map, uint64_t* f, int col,
                             const Params&, const Item& it, int t) {
     tma_load_3d(dst, map, f, col, it.qs + t * 128, it.bh);

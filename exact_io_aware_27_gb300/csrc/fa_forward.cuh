@@ -51,7 +51,7 @@
 //                             equal share of a long axis
 //   steps(g, it, t)           64-key steps of tile t (tile 0 always has some)
 //   keys(g, it)               keys of the item; steps past them are masked
-//   causal(g), first_query(g, it)  query position of row 0 of tile 0
+//   causal(g), query(g, it, t, row)  the query position of a tile's row
 //   load_q, load_kv           TMA loads of a Q tile / a 128-key block
 //   tile_bytes, block_bytes   the bytes that they bring
 //   store                     the epilogue of one warp's 32 rows
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       const int nkb = blocks(steps(it, nht));
       const int nh_t = nht[t];
       const int m_keys = G::keys(g, it);
-      const int qg = G::causal(g) ? G::first_query(g, it) + t * C::BM + row : 0;
+      const int qg = G::causal(g) ? G::query(g, it, t, row) : 0;
       float m_ref = -INFINITY;  // reference maximum of S * scale * log2(e)
       float l_run = 0.f;        // sum of exp2(S * scale * log2(e) - m_ref)
       for (int k = 0; ok && k < nh_t; ++k) {

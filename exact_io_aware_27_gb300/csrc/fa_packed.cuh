@@ -16,14 +16,15 @@ FA_DEV bool plan_matches(const PlanHead* h, int total, int nseq, unsigned int* s
 }
 
 // tmem_rows_store for rows of a packed tensor [rows, H, d]: NCOL columns of this
-// warp's 32 TMEM lanes, times `mul`, to columns [col0, d) of rows row0 + [0, valid)
-// (valid may be <= 0 or above 32) of head h. A full piece leaves through the staging buffers and TMA; a
+// warp's 32 TMEM lanes, times `mul`, to columns [col0, d). Lane i is head h + i % heads
+// (heads = 1 << head_shift) of row row0 + i / heads; the first `valid` lanes are stored
+// (valid may be <= 0 or above 32). A full piece leaves through the staging buffers and TMA; a
 // piece that ends inside its 32 rows, where the next row belongs to another sequence,
 // is written lane by lane (`out` is the tensor, `ld` its row stride).
 template <int NCOL>
 FA_DEV void packed_rows_store(uint32_t tcol, float mul, uint8_t* stage, const CUtensorMap* map,
                               int h, int row0, int valid, int col0, int d, __nv_bfloat16* out,
-                              long long ld) {
+                              long long ld, int head_shift = 0) {
   if (valid <= 0) return;  // warp-uniform
   const int valid_cols = d - col0;
   const int lane = threadIdx.x & 31;
@@ -45,8 +46,9 @@ FA_DEV void packed_rows_store(uint32_t tcol, float mul, uint8_t* stage, const CU
       w[e] = pack_bf16(__uint_as_float(o[2 * e]) * mul, __uint_as_float(o[2 * e + 1]) * mul);
     if (!full) {
       if (lane < valid) {
-        uint4* dst = reinterpret_cast<uint4*>(out + (row0 + lane) * ld + (long long)h * d + col0 +
-                                              32 * c);
+        const int at = h + (lane & ((1 << head_shift) - 1));
+        uint4* dst = reinterpret_cast<uint4*>(out + (row0 + (lane >> head_shift)) * ld +
+                                              (long long)at * d + col0 + 32 * c);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (32 * c + 8 * k < valid_cols)

@@ -19,37 +19,43 @@ struct PlanHead {
   int magic;        // kPlanMagic
   int total, nseq;  // the sizes the plan was made for
   int covered;      // rows the sequences cover; the rest of the tensors belongs to none
-  int tiles256;     // entries of the list of 256-row tiles (forward items)
-  int tiles128;     // entries of each list of 128-row tiles (backward blocks)
-  int pad[10];
+  int tiles256;     // entries of the list of 256-row tiles
+  int tiles128;     // entries of each list of 128-row tiles
+  int tiles64, tiles32;
+  int pad[8];
 };
 static_assert(sizeof(PlanHead) == 64, "the lists start 64 bytes into a plan");
 
-// Where a plan's parts lie. The lists hold at most total / tile + nseq entries.
+// A plan's lists: tiles of 256 >> i rows for i = 0..3, the last rows of a sequence (the
+// most expensive under causal masking) first; and the 128-row key blocks, the first rows
+// first. Each holds at most total / tile + nseq entries.
+constexpr int kPlanLists = 5, kKeyList = 4;
+__host__ __device__ constexpr int plan_tile_rows(int list) { return list == kKeyList ? 128 : 256 >> list; }
 struct PlanLayout {
-  long long cap256, cap128;
-  size_t off256, off_kv, off_q, off_scan, bytes;
+  long long cap[kPlanLists];
+  size_t off[kPlanLists], off_scan, bytes;
 };
 inline PlanLayout plan_layout(int nseq, int total) {
   PlanLayout l;
-  l.cap256 = (long long)total / 256 + nseq;
-  l.cap128 = (long long)total / 128 + nseq;
-  l.off256 = sizeof(PlanHead);
-  l.off_kv = l.off256 + (size_t)l.cap256 * sizeof(PlanTile);
-  l.off_q = l.off_kv + (size_t)l.cap128 * sizeof(PlanTile);
-  l.off_scan = l.off_q + (size_t)l.cap128 * sizeof(PlanTile);
-  l.bytes = l.off_scan + ((size_t)nseq + 1) * 2 * sizeof(int);
+  size_t at = sizeof(PlanHead);
+  for (int i = 0; i < kPlanLists; ++i) {
+    l.cap[i] = (long long)total / plan_tile_rows(i) + nseq;
+    l.off[i] = at;
+    at += (size_t)l.cap[i] * sizeof(PlanTile);
+  }
+  l.off_scan = at;
+  l.bytes = at + ((size_t)nseq + 1) * 4 * sizeof(int);
   l.bytes = (l.bytes + 15) / 16 * 16;
   return l;
 }
 
 // bf16 [rows, H, d] with `ld` elements from row to row, as boxes of 64 columns x
-// one head x box_rows rows with 128-byte swizzle (loads), or of 32 columns x one
-// head x 32 rows with 64-byte swizzle (stores).
+// box_heads heads x box_rows rows with 128-byte swizzle (loads), or of 32 columns x
+// box_heads heads x 32 / box_heads rows with 64-byte swizzle (stores).
 CUresult make_bf16_packed_map(CUtensorMap* map, const void* base, int rows, int H, int d,
-                              long long ld, int box_rows);
+                              long long ld, int box_rows, int box_heads = 1);
 CUresult make_bf16_packed_store_map(CUtensorMap* map, void* base, int rows, int H, int d,
-                                    long long ld);
+                                    long long ld, int box_heads = 1);
 
 struct PackedFwdArgs {
   const void *Q, *K, *V;
@@ -63,7 +69,7 @@ struct PackedFwdArgs {
 // Backward workspace: -D and -L * log2(e), fp32 [Hq, packed_ws_rows] each; a
 // sequence's rows start at its tiles' PlanTile::w.
 inline long long packed_ws_rows(int nseq, int total) {
-  return plan_layout(nseq, total).cap128 * kWorkspaceRowAlign;
+  return plan_layout(nseq, total).cap[kKeyList] * kWorkspaceRowAlign;
 }
 struct PackedBwdArgs {
   const void *Q, *K, *V, *O, *dO;

@@ -8,10 +8,11 @@ namespace fa {
 namespace {
 
 int packed_map(CUtensorMap* map, const void* base, int rows, int H, int d, long long ld,
-               cuuint32_t cols, cuuint32_t box_rows, CUtensorMapSwizzle swizzle) {
+               cuuint32_t cols, cuuint32_t box_heads, cuuint32_t box_rows,
+               CUtensorMapSwizzle swizzle) {
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2};
-  const cuuint32_t box[3] = {cols, 1, box_rows};
+  const cuuint32_t box[3] = {cols, box_heads, box_rows};
   return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
                            dims, strides, box, swizzle);
 }
@@ -30,7 +31,7 @@ int check_heads(int nseq, int total, int Hq, int Hkv, int d) {
   if (Hq < 1 || Hkv < 1 || Hq > 65535 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (d < 8 || d > 128 || d % 8 != 0) return FA_ERR_UNSUPPORTED_HEAD_DIM;
   // work items are counted in 32 bits
-  if (plan_layout(nseq, total).cap128 * Hq > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  if (plan_layout(nseq, total).cap[kKeyList] * Hq > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
 
@@ -45,14 +46,15 @@ Rows rows16(const void* p, int rows, int H, int d, long long ld) {
 }  // namespace
 
 CUresult make_bf16_packed_map(CUtensorMap* map, const void* base, int rows, int H, int d,
-                              long long ld, int box_rows) {
-  return (CUresult)packed_map(map, base, rows, H, d, ld, 64, (cuuint32_t)box_rows,
-                              CU_TENSOR_MAP_SWIZZLE_128B);
+                              long long ld, int box_rows, int box_heads) {
+  return (CUresult)packed_map(map, base, rows, H, d, ld, 64, (cuuint32_t)box_heads,
+                              (cuuint32_t)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 CUresult make_bf16_packed_store_map(CUtensorMap* map, void* base, int rows, int H, int d,
-                                    long long ld) {
-  return (CUresult)packed_map(map, base, rows, H, d, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+                                    long long ld, int box_heads) {
+  return (CUresult)packed_map(map, base, rows, H, d, ld, 32, (cuuint32_t)box_heads,
+                              (cuuint32_t)(32 / box_heads), CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace fa

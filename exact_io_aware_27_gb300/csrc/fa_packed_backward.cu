@@ -197,11 +197,11 @@ cudaError_t launch_packed_bwd_d(const PackedBwdArgs& a, cudaStream_t stream) {
   const PlanLayout lay = plan_layout(a.nseq, a.total);
   const long long ws_rows = packed_ws_rows(a.nseq, a.total);
   const int sms = sm_count();
-  const long long pairs = lay.cap128 * a.Hq;
+  const long long pairs = lay.cap[kKeyList] * a.Hq;
   packed_preprocess_kernel<D><<<(unsigned)(pairs < 8LL * sms ? pairs : 8LL * sms), 256, 0,
                                 stream>>>(
       static_cast<const __nv_bfloat16*>(a.O), static_cast<const __nv_bfloat16*>(a.dO), a.L,
-      static_cast<const uint8_t*>(a.plan), (long long)lay.off_kv, a.ws_nD, a.ws_nL2, ws_rows,
+      static_cast<const uint8_t*>(a.plan), (long long)lay.off[kKeyList], a.ws_nD, a.ws_nL2, ws_rows,
       a.total, a.nseq, a.Hq, a.d);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -229,8 +229,8 @@ cudaError_t launch_packed_bwd_d(const PackedBwdArgs& a, cudaStream_t stream) {
   p.scale_log2 = a.scale * kLog2e;
   PackedBwd::Params g;
   g.plan = static_cast<const uint8_t*>(a.plan);
-  g.off_kv = (long long)lay.off_kv;
-  g.off_q = (long long)lay.off_q;
+  g.off_kv = (long long)lay.off[kKeyList];
+  g.off_q = (long long)lay.off[1];
   g.dQ = static_cast<__nv_bfloat16*>(a.dQ);
   g.dK = static_cast<__nv_bfloat16*>(a.dK);
   g.dV = static_cast<__nv_bfloat16*>(a.dV);
@@ -254,7 +254,7 @@ cudaError_t launch_packed_bwd_d(const PackedBwdArgs& a, cudaStream_t stream) {
   e = cudaFuncSetAttribute(bwd_kernel<D, PackedBwd>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            smem);
   if (e != cudaSuccess) return e;
-  const long long items = pairs + lay.cap128 * a.Hkv;
+  const long long items = pairs + lay.cap[kKeyList] * a.Hkv;
   bwd_kernel<D, PackedBwd><<<(unsigned)(items < sms ? items : sms), KvCfg<D>::THREADS, smem,
                              stream>>>(mq, mk, mv, mdo, ml2, md, mdq, mdk, mdv, p, g);
   return cudaGetLastError();

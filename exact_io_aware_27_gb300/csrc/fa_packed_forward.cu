@@ -1,9 +1,17 @@
 // The forward pass over packed sequences: the forward kernel (fa_forward.cuh) over
 // Q [total, Hq, d] and K, V [total, Hkv, d], whose rows are sequences one after
-// another; query head h reads key/value head h / (Hq / Hkv). Work items are (256-row
-// tile of a sequence, head), from the plan's list: heads a group at a time, inside a
-// group the heaviest tiles of all sequences first, and the query heads of one
-// key/value head next to each other, so that its K and V are read once into L2.
+// another; query head h reads key/value head h / (Hq / Hkv).
+//
+// The query heads of one key/value head share its keys, so up to eight of them
+// (`heads`, the largest power of two that divides Hq / Hkv) share a tile: row r of a
+// 128-row tile is head r % heads of query r / heads, and a tile pair covers
+// 256 / heads queries. The work is the same for a long sequence, and less where tiles
+// are cut off: by the end of a short sequence and by the causal diagonal (at 16
+// sequences of 20 to 1151 rows, 32/8 heads, the products executed fall by 17 %).
+// Work items are (tile pair of a sequence, head group), from the plan's list: head
+// groups a few at a time, inside those the heaviest tiles of all sequences first, and
+// the groups of one key/value head next to each other, so that its K and V are read
+// once into L2.
 //
 // A sequence's last key block and last query tile run into the next sequence's rows
 // (or into rows of no sequence): keys past the end are masked, their V rows are
@@ -24,7 +32,9 @@ struct Packed {
     const uint8_t* plan;
     float* L;
     __nv_bfloat16* O;
+    long long off_list;           // the list's place in the plan
     int total, nseq, Hq, per_kv, causal, group, fill;
+    int list, head_shift;         // tiles of 256 >> list rows; heads = 1 << head_shift
   };
   struct View {
     const Params& p;
@@ -33,30 +43,40 @@ struct Packed {
   FA_DEV static View view(const Params& p) {
     const PlanHead* head = reinterpret_cast<const PlanHead*>(p.plan);
     const bool ok = plan_matches(head, p.total, p.nseq, status());
-    return {p, ok ? head->tiles256 : 0, ok ? head->covered : p.total};
+    return {p, ok ? (&head->tiles256)[p.list] : 0, ok ? head->covered : p.total};
   }
   struct Item {
-    PlanTile s;  // sequence start, length, 256-row tile
-    int h;
+    PlanTile s;  // sequence start, length, tile
+    int h;       // first query head
   };
   FA_DEV static unsigned int* status() { return &g_packed_status; }
   static constexpr bool kSplit = false, kAlternate = false;
   static constexpr bool kForeignTail = true;
-  FA_DEV static int items(const View& g) { return g.tiles * g.p.Hq; }
+  FA_DEV static int items(const View& g) { return g.tiles * (g.p.Hq >> g.p.head_shift); }
   FA_DEV static Item item(const View& g, int i) {
     int rank, h;
-    grouped_tile(i, g.p.Hq, g.tiles, g.p.group, rank, h);
-    return {__ldg(reinterpret_cast<const PlanTile*>(g.p.plan + sizeof(PlanHead)) + rank), h};
+    grouped_tile(i, g.p.Hq >> g.p.head_shift, g.tiles, g.p.group, rank, h);
+    return {__ldg(reinterpret_cast<const PlanTile*>(g.p.plan + g.p.off_list) + rank),
+            h << g.p.head_shift};
   }
-  FA_DEV static int first_query(const View&, const Item& it) { return it.s.z * 256; }
+  // First query of tile t, within the sequence.
+  FA_DEV static int tile_query(const View& g, const Item& it, int t) {
+    return (2 * it.s.z + t) * (128 >> g.p.head_shift);
+  }
+  FA_DEV static int query(const View& g, const Item& it, int t, int row) {
+    return tile_query(g, it, t) + (row >> g.p.head_shift);
+  }
   FA_DEV static int steps(const View& g, const Item& it, int t) {
-    return tile_steps(it.s.z * 256 + t * 128, it.s.y, it.s.y, g.p.causal);
+    const int q0 = tile_query(g, it, t), n = it.s.y;
+    if (q0 >= n) return 0;
+    const int last = min(q0 + (128 >> g.p.head_shift), n) - 1;
+    return (g.p.causal ? last : n - 1) / 64 + 1;
   }
   FA_DEV static int keys(const View&, const Item& it) { return it.s.y; }
   FA_DEV static int causal(const View& g) { return g.p.causal; }
-  FA_DEV static void load_q(void* dst, const CUtensorMap* map, uint64_t* f, int col, const View&,
-                            const Item& it, int t) {
-    tma_load_3d(dst, map, f, col, it.h, it.s.x + it.s.z * 256 + t * 128);
+  FA_DEV static void load_q(void* dst, const CUtensorMap* map, uint64_t* f, int col,
+                            const View& g, const Item& it, int t) {
+    tma_load_3d(dst, map, f, col, it.h, it.s.x + tile_query(g, it, t));
   }
   template <class C>
   FA_DEV static uint32_t tile_bytes(const View&) {
@@ -80,11 +100,13 @@ struct Packed {
   template <int D>
   FA_DEV static void store(const View& g, const Item& it, int t, int warp, int lane, uint32_t ocol,
                            float m_ref, float l, uint8_t* stage, const CUtensorMap* mo, int d) {
-    const int q0 = it.s.z * 256 + t * 128 + warp * 32;  // within the sequence
-    const int row0 = it.s.x + q0, valid = it.s.y - q0;
+    const int sh = g.p.head_shift, q0 = tile_query(g, it, t) + ((warp * 32) >> sh);
+    const int row0 = it.s.x + q0, valid = (it.s.y - q0) << sh;
     packed_rows_store<D>(ocol, 1.f / l, stage, mo, it.h, row0, valid, 0, d, g.p.O,
-                         (long long)g.p.Hq * d);
-    if (lane < valid) g.p.L[(size_t)it.h * g.p.total + row0 + lane] = (m_ref + lg2(l)) * kLn2;
+                         (long long)g.p.Hq * d, sh);
+    if (lane < valid)
+      g.p.L[(size_t)(it.h + (lane & ((1 << sh) - 1))) * g.p.total + row0 + (lane >> sh)] =
+          (m_ref + lg2(l)) * kLn2;
   }
   // Rows that no sequence covers: O = 0 and L = -inf (what attention to no key
   // gives), where the caller asked for it.
@@ -105,10 +127,13 @@ template <int D>
 cudaError_t launch_packed_d(const PackedFwdArgs& a, cudaStream_t stream) {
   using C = FwdCfg<D>;
   CUtensorMap mq, mk, mv, mo;
-  if (make_bf16_packed_map(&mq, a.Q, a.total, a.Hq, a.d, a.ldq, C::BM) != CUDA_SUCCESS ||
+  int sh = 0;  // heads that share a tile: 1 << sh
+  while (sh < 3 && a.Hq / a.Hkv % (2 << sh) == 0) ++sh;
+  if (make_bf16_packed_map(&mq, a.Q, a.total, a.Hq, a.d, a.ldq, C::BM >> sh, 1 << sh) !=
+          CUDA_SUCCESS ||
       make_bf16_packed_map(&mk, a.K, a.total, a.Hkv, a.d, a.ldk, C::BN) != CUDA_SUCCESS ||
       make_bf16_packed_map(&mv, a.V, a.total, a.Hkv, a.d, a.ldv, C::BN) != CUDA_SUCCESS ||
-      make_bf16_packed_store_map(&mo, a.O, a.total, a.Hq, a.d, (long long)a.Hq * a.d) !=
+      make_bf16_packed_store_map(&mo, a.O, a.total, a.Hq, a.d, (long long)a.Hq * a.d, 1 << sh) !=
           CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   FwdParams p;
@@ -124,17 +149,20 @@ cudaError_t launch_packed_d(const PackedFwdArgs& a, cudaStream_t stream) {
   g.per_kv = a.Hq / a.Hkv;
   g.causal = a.causal;
   g.fill = a.fill;
+  g.list = sh;
+  g.head_shift = sh;
+  const PlanLayout lay = plan_layout(a.nseq, a.total);
+  g.off_list = (long long)lay.off[sh];
   // Whole key/value heads per group. The plan's tile count is known on the device
   // only; the rows give it up to the sequences' last tiles.
-  const int tiles = ceil_div(a.total, 256);
-  g.group = round_up(heads_per_group(a.Hq, tiles), g.per_kv);
+  g.group = round_up(heads_per_group(a.Hq >> sh, ceil_div(a.total, 256 >> sh)), g.per_kv >> sh);
   cudaError_t e = cudaFuncSetAttribute(fwd_kernel<D, Packed>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess)
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const long long items = plan_layout(a.nseq, a.total).cap256 * a.Hq;
+  const long long items = lay.cap[sh] * (a.Hq >> sh);
   const unsigned grid = (unsigned)(items < sms ? items : sms);
   fwd_kernel<D, Packed><<<grid, C::THREADS, C::SMEM, stream>>>(mq, mk, mv, mo, p, g);
   return cudaGetLastError();

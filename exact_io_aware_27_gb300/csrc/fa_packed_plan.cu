@@ -1,17 +1,14 @@
 // Plans of packed batches: from cu_seqlens on the device to the work lists of the
 // forward and backward passes, without a host synchronisation.
 //
-// A sequence of length n has ceil(n / 256) forward items per head and ceil(n / 128)
-// key blocks and query blocks. The persistent kernels deal a list out in snake order,
-// which balances only a list whose heaviest entries come first, so the three lists
-// are sorted by cost: under causal masking tile t of a forward or dQ list costs
-// t + 1 and key block t of a dK/dV list costs (blocks - t); without it every tile
-// costs its sequence's length. A counting sort over at most 1024 cost classes is
-// enough (the order inside a class does not matter, and no result depends on the
-// order of a list).
+// A sequence of length n has ceil(n / rows) tiles of `rows` rows. The persistent kernels
+// deal a list out in snake order, which balances only a list whose heaviest entries
+// come first, so the lists are sorted by cost: under causal masking tile t of a query
+// list costs t + 1 and key block t costs (blocks - t); without it every tile costs its
+// sequence's length. A counting sort over at most 1024 cost classes is enough (the
+// order inside a class does not matter, and no result depends on the order of a list).
 //
-// One block of 1024 threads: the lists are short (a batch of 2^20 rows has 16384
-// entries in the longest), and a plan serves every layer that runs the batch.
+// One block of 1024 threads: a plan serves every layer that runs the batch.
 // Bounds that are not 0 = cu[0] <= cu[1] <= ... <= cu[nseq] <= total give empty
 // lists and raise kDeviceIndexBit.
 #include "fa_packed.h"
@@ -70,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const int* __restrict__ 
                                                         PlanLayout lay) {
   __shared__ int warp_sums[32];
   __shared__ int bins[kBins];
-  __shared__ int max_tiles;
+  __shared__ int longest_seq;
   const int tid = threadIdx.x;
   PlanHead* head = reinterpret_cast<PlanHead*>(plan);
 
@@ -78,64 +75,59 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const int* __restrict__ 
   for (int i = tid; i < nseq; i += kThreads) bad |= cu[i] > cu[i + 1] ? 1 : 0;
   if (tid == 0) {
     bad |= (cu[0] != 0 || cu[nseq] > total) ? 1 : 0;
-    max_tiles = 0;
+    longest_seq = 0;
   }
   if (__syncthreads_or(bad)) {
     if (tid == 0) {
-      *head = PlanHead{kPlanMagic, total, nseq, total, 0, 0, {}};
+      *head = PlanHead{kPlanMagic, total, nseq, total, 0, 0, 0, 0, {}};
       atomicOr(&g_plan_status, kDeviceIndexBit);
     }
     return;
   }
 
-  // Tiles before each sequence.
-  int* first128 = reinterpret_cast<int*>(plan + lay.off_scan);
-  int* first256 = first128 + nseq + 1;
-  int n128 = 0, n256 = 0, longest = 0;
+  // Tiles before each sequence, for the tiles of 256, 128, 64 and 32 rows.
+  int* first = reinterpret_cast<int*>(plan + lay.off_scan);  // [4][nseq + 1]
+  int tiles[4] = {0, 0, 0, 0}, longest = 0;
   for (int base = 0; base < nseq; base += kThreads) {
     const int i = base + tid;
     const int len = i < nseq ? cu[i + 1] - cu[i] : 0;
-    const int t128 = (len + 127) / 128, t256 = (len + 255) / 256;
-    longest = max(longest, t128);
-    int s128, s256;
-    const int e128 = block_scan(t128, warp_sums, s128);
-    const int e256 = block_scan(t256, warp_sums, s256);
-    if (i < nseq) {
-      first128[i] = n128 + e128;
-      first256[i] = n256 + e256;
+    longest = max(longest, len);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int rows = plan_tile_rows(k);
+      int sum;
+      const int before = block_scan((len + rows - 1) / rows, warp_sums, sum);
+      if (i < nseq) first[k * (nseq + 1) + i] = tiles[k] + before;
+      tiles[k] += sum;
     }
-    n128 += s128;
-    n256 += s256;
   }
-  atomicMax(&max_tiles, longest);
+  atomicMax(&longest_seq, longest);
   if (tid == 0) {
-    first128[nseq] = n128;
-    first256[nseq] = n256;
-    *head = PlanHead{kPlanMagic, total, nseq, cu[nseq], n256, n128, {}};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) first[k * (nseq + 1) + nseq] = tiles[k];
+    *head = PlanHead{kPlanMagic, total, nseq, cu[nseq], tiles[0], tiles[1], tiles[2], tiles[3], {}};
   }
   __syncthreads();
-  const int most = max_tiles;
-  int shift = 0;
-  while ((most >> shift) >= kBins) ++shift;
+  const int* first128 = first + (nseq + 1);
 
-  // list 0: forward items (256 rows); 1: key blocks; 2: query blocks (128 rows)
-  for (int list = 0; list < 3; ++list) {
-    const int n = list == 0 ? n256 : n128;
-    const int* first = list == 0 ? first256 : first128;
-    PlanTile* out = reinterpret_cast<PlanTile*>(
-        plan + (list == 0 ? lay.off256 : list == 1 ? lay.off_kv : lay.off_q));
+  for (int list = 0; list < kPlanLists; ++list) {
+    const int rows = plan_tile_rows(list);
+    const int* mine = list == kKeyList ? first128 : first + list * (nseq + 1);
+    const int n = mine[nseq];
+    PlanTile* out = reinterpret_cast<PlanTile*>(plan + lay.off[list]);
+    const int most = (longest_seq + rows - 1) / rows;
+    int shift = 0;
+    while ((most >> shift) >= kBins) ++shift;
     auto entry = [&](int i, int& bin) {
-      const int s = find_sequence(first, nseq, i);
-      const int start = cu[s], len = cu[s + 1] - start, tile = i - first[s];
-      const int tiles = first[s + 1] - first[s];
-      const int cost = !causal ? (len + 127) / 128
-                       : list == 0 ? min(2 * (tile + 1), (len + 127) / 128)
-                       : list == 1 ? tiles - tile
-                                   : tile + 1;  // 1 <= cost <= most, in 128-row tiles
+      const int s = find_sequence(mine, nseq, i);
+      const int start = cu[s], len = cu[s + 1] - start, tile = i - mine[s];
+      const int all = mine[s + 1] - mine[s];
+      // in tiles, 1 <= cost <= most
+      const int cost = !causal ? all : list == kKeyList ? all - tile : tile + 1;
       bin = (most - cost) >> shift;
       return make_int4(start, len, tile, first128[s] * kWorkspaceRowAlign);
     };
-    for (int b = tid; b < kBins; b += kThreads) bins[b] = 0;
+    bins[tid] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += kThreads) {
       int bin;

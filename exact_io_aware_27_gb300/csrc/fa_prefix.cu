@@ -188,7 +188,7 @@ struct Prefix {
   }
   FA_DEV static int keys(const View&, const Item& it) { return it.m; }
   FA_DEV static constexpr int causal(const View&) { return 0; }
-  FA_DEV static int first_query(const View&, const Item&) { return 0; }
+  FA_DEV static int query(const View&, const Item&, int, int) { return 0; }
   template <class C>
   FA_DEV static uint32_t tile_bytes(const View& g) {
     return (uint32_t)(g.p.s.per_tile * g.p.s.per_kv) * 128u * C::KCH;

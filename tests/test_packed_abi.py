@@ -25,8 +25,8 @@ REACHED = (api.FA_ERR_CUDA, api.FA_ERR_UNSUPPORTED_DEVICE)
 
 def test_plan(lib):
     size = lib.fa_packed_plan_bytes(5, 1000)
-    # header, one list of 256-row tiles, two of 128-row tiles, two scans
-    assert size == 64 + 16 * (3 + 5) + 2 * 16 * (7 + 5) + 6 * 2 * 4
+    # header, lists of 256-, 128- (two), 64- and 32-row tiles, four scans
+    assert size == 64 + 16 * (3 + 5 + 2 * (7 + 5) + 15 + 5 + 31 + 5) + 6 * 4 * 4
     assert lib.fa_packed_plan_bytes(0, 10) == 0
     assert lib.fa_packed_plan_bytes(70000, 10) == 0
     assert lib.fa_packed_plan_bytes(1, 0) == 0

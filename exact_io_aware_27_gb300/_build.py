@@ -4,6 +4,10 @@ Each ``csrc/*.cu`` translation unit is compiled by ``nvcc`` in parallel into
 ``_build/``, then linked into one shared library next to this file. Only one
 ``-gencode`` target is built (``compute_103a`` / ``sm_103a``). Rebuilds happen
 when a source or header is newer than the library.
+
+``csrc/fa_binding.cpp``, the marshalling of torch tensors for the packed and paged
+calls, becomes the Python module ``_fa_binding.so`` beside it, linked to the library
+and built for the torch that is installed.
 """
 from __future__ import annotations
 
@@ -11,6 +15,7 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -18,6 +23,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIBRARY = os.path.join(PKG_DIR, "libfa_gb300.so")
+BINDING = os.path.join(PKG_DIR, "_fa_binding.so")
 
 SOURCES = ["fa_api.cu", "fa_forward.cu", "fa_backward.cu", "fa_softmax.cu", "fa_selftest.cu",
            "fa_noalloc.cu", "fa_session.cu", "fa_standard.cu", "fa_packed_plan.cu",
@@ -37,16 +43,16 @@ def _nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)
-             if f.endswith((".cu", ".cuh", ".h"))]
+             if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIBRARY):
+    if not (os.path.exists(LIBRARY) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIBRARY)
+    t = min(os.path.getmtime(LIBRARY), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -69,13 +75,37 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_binding():
+        import torch  # its headers; found through the installed package
+        root = os.path.dirname(torch.__file__)
+        include = [os.path.join(root, "include"),
+                   os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                   sysconfig.get_paths()["include"], INCLUDE]
+        obj = os.path.join(BUILD_DIR, "fa_binding.o")
+        r = subprocess.run([nvcc, "-O2", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
+                            *("-I" + p for p in include), "-c",
+                            os.path.join(CSRC, "fa_binding.cpp"), "-o", obj],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"the compiler failed on fa_binding.cpp:\n{r.stdout}\n{r.stderr}")
+        return obj, os.path.join(root, "lib")
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding_obj, torch_lib = binding.result()
     tmp = LIBRARY + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIBRARY)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    r = subprocess.run([nvcc, "-shared", "-cudart", "none", "-o", tmp, binding_obj, LIBRARY,
+                        "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+                        "-Xlinker", "-rpath=$ORIGIN"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIBRARY
 
 

@@ -100,12 +100,15 @@ def test_binding_refuses(lib):
         fa.fa_packed_plan(cu, 4)  # not on a GPU
     with pytest.raises(TypeError):
         fa.fa_packed_forward(x, x, x, None)
-    meta = packed.PackedPlan(torch.zeros(8, dtype=torch.uint8, device="meta"), 1, 4, True)
-    with pytest.raises(ValueError):
-        fa.fa_packed_forward(x, x, x, meta)  # not on a GPU
+    plan = packed.PackedPlan(torch.zeros(8, dtype=torch.uint8), 1, 4, True)
+    L = torch.zeros(2, 4)
     with pytest.raises(TypeError):
-        packed._row_stride("Q", None)
+        fa.fa_packed_forward(None, x, x, plan)
     with pytest.raises(ValueError):
-        packed._int32("cu_seqlens", cu, (3,), cu.device)
+        fa.fa_packed_forward(x, x, x, plan)  # not on a GPU
     with pytest.raises(ValueError):
-        packed._int32("cu_seqlens", cu.long(), (2,), cu.device)
+        fa.fa_packed_forward(x, x, x, plan, stream=0)
+    with pytest.raises(ValueError):
+        fa.fa_packed_backward(x, x, x, x, L, x, plan)
+    with pytest.raises(TypeError):
+        fa.fa_packed_backward(x, x, x, x, L, x, None)

@@ -35,6 +35,7 @@ constexpr int kOwnWarps = 4;       // warps of a thread block of the own kernel
 constexpr int kOwnBlocksPerSm = 2;
 constexpr int kOwnChunk = 64;      // keys per step of the own keys' split
 constexpr int kMinPrefixBlocks = 2;  // 128-key blocks a prefix worker takes at least
+constexpr long long kWholeKeys = 4096, kWholeBytes = 24 << 20;  // the whole kernel's calls
 
 // `total` steps (below 2^31) dealt to at most `most` workers in contiguous pieces that
 // differ by one step at most; the longer pieces come first.
@@ -315,6 +316,136 @@ struct Prefix {
   FA_DEV static void idle_warps(const View&, int, int, int) {}
 };
 
+// ================================================================== row tiles
+// 16 query rows of one request and key/value head (rows past the group's are zeros) in
+// one warp, with their output and statistics: rows lane / 4 and lane / 4 + 8 of each
+// fragment, columns 8 n + 2 (lane % 4) + {0, 1}.
+template <int D>
+struct RowTile {
+  uint32_t q[D / 16][4];
+  float o[D / 8][4];
+  float m0, m1, l0, l1;
+
+  FA_DEV void load(const __nv_bfloat16* src, int rows, int d) {
+    const int lane = threadIdx.x & 31, qr = lane >> 2, qc = (lane & 3) * 2;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = qr + (e & 1) * 8, col = kk * 16 + (e >> 1) * 8 + qc;
+        q[kk][e] = row < rows && col < d
+                       ? __ldg(reinterpret_cast<const unsigned int*>(src + (size_t)row * d + col))
+                       : 0u;
+      }
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
+  }
+
+  // One stage of 16 keys (K at kb, V at vb in shared memory, D * 2 bytes a key, 16-byte
+  // piece j of key r at j ^ (r % 8)), of which the first `keys` count.
+  FA_DEV void step(uint32_t kb, uint32_t vb, int keys, float scale_log2) {
+    const int lane = threadIdx.x & 31, qc = (lane & 3) * 2;
+    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};  // keys 0..7, 8..15
+    {
+      const int row = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t b[4];
+        ldmatrix_x4(b, kb + row * (2 * D) + (((kk * 2 + half) ^ (row & 7)) << 4));
+        mma_16816(sa, q[kk], b[0], b[1]);
+        mma_16816(sb, q[kk], b[2], b[3]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sa[e] *= scale_log2;
+      sb[e] *= scale_log2;
+    }
+    if (keys < 16) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (qc + (e & 1) >= keys) sa[e] = -INFINITY;
+        if (8 + qc + (e & 1) >= keys) sb[e] = -INFINITY;
+      }
+    }
+    float x0 = fmaxf(fmaxf(sa[0], sa[1]), fmaxf(sb[0], sb[1]));
+    float x1 = fmaxf(fmaxf(sa[2], sa[3]), fmaxf(sb[2], sb[3]));
+    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+    // The reference maximum moves only when a row passes it by 2^8 (as in the forward
+    // kernel): most steps need no rescaling.
+    if (__any_sync(0xffffffffu, x0 > m0 + kRescaleThreshold || x1 > m1 + kRescaleThreshold)) {
+      const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+      const float c0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
+      const float c1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
+      m0 = n0;
+      m1 = n1;
+      l0 *= c0;
+      l1 *= c1;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][0] *= c0;
+        o[n][1] *= c0;
+        o[n][2] *= c1;
+        o[n][3] *= c1;
+      }
+    }
+    const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      sa[e] = ex2(sa[e] - u0);
+      sb[e] = ex2(sb[e] - u0);
+      sa[2 + e] = ex2(sa[2 + e] - u1);
+      sb[2 + e] = ex2(sb[2 + e] - u1);
+    }
+    l0 += (sa[0] + sa[1]) + (sb[0] + sb[1]);
+    l1 += (sa[2] + sa[3]) + (sb[2] + sb[3]);
+    // P in bf16 (the products' operand type), l from the values before rounding
+    const uint32_t pa[4] = {pack_bf16(sa[0], sa[1]), pack_bf16(sa[2], sa[3]),
+                            pack_bf16(sb[0], sb[1]), pack_bf16(sb[2], sb[3])};
+    const int row = (lane & 7) + (((lane >> 3) & 1) << 3), half = lane >> 4;
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) {
+      uint32_t b[4];
+      ldmatrix_x4_trans(b, vb + row * (2 * D) + (((n * 2 + half) ^ (row & 7)) << 4));
+      mma_16816(o[2 * n], pa, b[0], b[1]);
+      mma_16816(o[2 * n + 1], pa, b[2], b[3]);
+    }
+  }
+
+  // The rows' sums over the four lanes that share a row.
+  FA_DEV void finish() {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+  }
+};
+
+// Copies a stage in the background: rows [0, keys) of K and V from row `row0` of the
+// caches (rows of d values), zeros behind them and behind column d.
+template <int D>
+FA_DEV void load_stage(uint32_t dst, const __nv_bfloat16* Kc, const __nv_bfloat16* Vc, size_t row0,
+                       int keys, int d) {
+  constexpr int PPR = D / 8;  // 16-byte pieces of a row
+  const int lane = threadIdx.x & 31, first = lane / PPR, piece = lane % PPR;
+#pragma unroll
+  for (int i = 0; i < 16 * PPR / 32; ++i) {
+    const int r = first + i * (32 / PPR);
+    const bool in = r < keys && 8 * piece < d;
+    const size_t at = in ? (row0 + r) * d + 8 * piece : 0;
+    const uint32_t to = dst + r * (2 * D) + ((piece ^ (r & 7)) << 4);
+    cp_async16(to, Kc + at, in ? 16 : 0);
+    cp_async16(to + 16 * 2 * D, Vc + at, in ? 16 : 0);
+  }
+}
+
 // ================================================================== own kernel
 struct OwnParams {
   DecodeSizes s;
@@ -433,8 +564,6 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
   int i_page = 0, i_at = 32;  // pages of 32 stages, one per lane; the next of them
   bool i_more = true;
   int i_stage = 0;
-  constexpr int PPR = D / 8;  // 16-byte pieces of a row
-  const int l_row = lane / PPR, l_piece = lane % PPR;
   const size_t head_rows = (size_t)1 << p.page_shift;
   auto issue = [&]() {
     if (i_more) {
@@ -453,16 +582,7 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
       const int page = __shfl_sync(0xffffffffu, i_page, i_at);
       const int hk = ir.ht / s.row_tiles;
       const size_t row0 = ((size_t)page * s.Hkv + hk) * head_rows + (ir.key & (head_rows - 1));
-      const uint32_t dst = ring + i_stage * C::STAGE;
-#pragma unroll
-      for (int i = 0; i < C::KEYS * PPR / 32; ++i) {
-        const int r = l_row + i * (32 / PPR);
-        const bool in = ir.key + r < ir.key_end && 8 * l_piece < s.d;
-        const size_t at = in ? (row0 + r) * s.d + 8 * l_piece : 0;
-        const uint32_t to = dst + r * C::ROW + ((l_piece ^ (r & 7)) << 4);
-        cp_async16(to, p.Kc + at, in ? 16 : 0);
-        cp_async16(to + C::PART, p.Vc + at, in ? 16 : 0);
-      }
+      load_stage<D>(ring + i_stage * C::STAGE, p.Kc, p.Vc, row0, ir.key_end - ir.key, s.d);
       ++i_at;
       ir.key += C::KEYS;
       if (ir.key >= ir.key_end) {
@@ -483,111 +603,22 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
   // ---- the products
   const int qr = lane >> 2, qc = (lane & 3) * 2;  // row and first column of a fragment
   int stage = 0;
+  RowTile<D> tile;
   for (unsigned x = x_begin; x < x_end;) {
     const Run r = run_at(x);
     x = r.x1;
     const int hk = r.ht / s.row_tiles, rt = r.ht - hk * s.row_tiles;
     const int rows = min(16, s.per_kv - rt * 16);
-    const __nv_bfloat16* q = p.Q + ((size_t)r.b * s.Hq + hk * s.per_kv + rt * 16) * s.d;
-    uint32_t qa[D / 16][4];
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = qr + (e & 1) * 8, col = kk * 16 + (e >> 1) * 8 + qc;
-        qa[kk][e] = row < rows && col < s.d
-                        ? __ldg(reinterpret_cast<const unsigned int*>(q + (size_t)row * s.d + col))
-                        : 0u;
-      }
-    float o[D / 8][4];
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows qr and qr + 8
-
+    tile.load(p.Q + ((size_t)r.b * s.Hq + hk * s.per_kv + rt * 16) * s.d, rows, s.d);
     for (int key = r.key; key < r.key_end; key += C::KEYS) {
       cp_async_wait<C::STAGES - 2>();
       __syncwarp();  // the stage has landed for every lane, and the last one is read
       issue();
-      const uint32_t kb = ring + stage * C::STAGE, vb = kb + C::PART;
+      const uint32_t kb = ring + stage * C::STAGE;
       stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};  // keys 0..7, 8..15
-      {
-        const int row = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t b[4];
-          ldmatrix_x4(b, kb + row * C::ROW + (((kk * 2 + half) ^ (row & 7)) << 4));
-          mma_16816(sa, qa[kk], b[0], b[1]);
-          mma_16816(sb, qa[kk], b[2], b[3]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sa[e] *= p.scale_log2;
-        sb[e] *= p.scale_log2;
-      }
-      if (r.key_end - key < C::KEYS) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (key + qc + (e & 1) >= r.key_end) sa[e] = -INFINITY;
-          if (key + 8 + qc + (e & 1) >= r.key_end) sb[e] = -INFINITY;
-        }
-      }
-      float x0 = fmaxf(fmaxf(sa[0], sa[1]), fmaxf(sb[0], sb[1]));
-      float x1 = fmaxf(fmaxf(sa[2], sa[3]), fmaxf(sb[2], sb[3]));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-      // The reference maximum moves only when a row passes it by 2^8 (as in the forward
-      // kernel): most steps need no rescaling.
-      if (__any_sync(0xffffffffu, x0 > m0 + kRescaleThreshold || x1 > m1 + kRescaleThreshold)) {
-        const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-        const float c0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
-        const float c1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= c0;
-        l1 *= c1;
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          o[n][0] *= c0;
-          o[n][1] *= c0;
-          o[n][2] *= c1;
-          o[n][3] *= c1;
-        }
-      }
-      const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
-      sa[0] = ex2(sa[0] - u0);
-      sa[1] = ex2(sa[1] - u0);
-      sb[0] = ex2(sb[0] - u0);
-      sb[1] = ex2(sb[1] - u0);
-      sa[2] = ex2(sa[2] - u1);
-      sa[3] = ex2(sa[3] - u1);
-      sb[2] = ex2(sb[2] - u1);
-      sb[3] = ex2(sb[3] - u1);
-      l0 += (sa[0] + sa[1]) + (sb[0] + sb[1]);
-      l1 += (sa[2] + sa[3]) + (sb[2] + sb[3]);
-      // P in bf16 (the products' operand type), l from the values before rounding
-      const uint32_t pa[4] = {pack_bf16(sa[0], sa[1]), pack_bf16(sa[2], sa[3]),
-                              pack_bf16(sb[0], sb[1]), pack_bf16(sb[2], sb[3])};
-      {
-        const int row = (lane & 7) + (((lane >> 3) & 1) << 3), half = lane >> 4;
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          uint32_t b[4];
-          ldmatrix_x4_trans(b, vb + row * C::ROW + (((n * 2 + half) ^ (row & 7)) << 4));
-          mma_16816(o[2 * n], pa, b[0], b[1]);
-          mma_16816(o[2 * n + 1], pa, b[2], b[3]);
-        }
-      }
+      tile.step(kb, kb + C::PART, r.key_end - key, p.scale_log2);
     }
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    tile.finish();
     const unsigned unit = (unsigned)(r.ht * s.B + r.b);
     const unsigned slot = r.x0 == r.u0 && r.x1 == r.u1
                               ? unit
@@ -596,21 +627,160 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
     for (int e = 0; e < 2; ++e) {
       const int row = qr + 8 * e;
       if (row >= rows) continue;
-      const float inv = 1.f / (e ? l1 : l0);
+      const float inv = 1.f / (e ? tile.l1 : tile.l0);
       float* out = s.own_o + ((size_t)slot * s.own_rows + row) * s.d;
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
         if (8 * n < s.d)
           *reinterpret_cast<float2*>(out + 8 * n + qc) =
-              make_float2(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
+              make_float2(tile.o[n][2 * e] * inv, tile.o[n][2 * e + 1] * inv);
       if ((lane & 3) == 0)
-        s.own_e[(size_t)slot * s.own_rows + row] = e ? m1 + lg2(l1) : m0 + lg2(l0);
+        s.own_e[(size_t)slot * s.own_rows + row] =
+            e ? tile.m1 + lg2(tile.l1) : tile.m0 + lg2(tile.l0);
     }
   }
   cp_async_wait<0>();
   // This kernel needs nothing of the prefix kernel, beside which it may run, but it
   // completes after it: the join kernel waits for this one.
   grid_wait();
+}
+
+// ================================================================== whole kernel
+// Small calls, where three kernels' latency would be most of the time: one thread block
+// per request and row tile takes all of its keys, the prefix's and its own, 16 at a time
+// in turn by its warps, and joins the warps' parts through shared memory. The prefix is
+// read again for every request, from L2 but for the first.
+struct WholeParams {
+  DecodeSizes s;
+  const __nv_bfloat16 *Q, *Kc, *Vc;
+  const int *pages, *prefix_len, *table, *lens;
+  __nv_bfloat16* O;
+  float* L;
+  int prefix_cap, max_pages, num_pages, page_shift;  // prefix_cap: keys
+  float scale_log2;
+};
+constexpr int kWholeWarps = 8;
+template <int D>
+struct WholeCfg {
+  static constexpr int STAGES = 3;
+  static constexpr int STAGE = 2 * 16 * 2 * D;
+  static constexpr int WARP = STAGES * STAGE;
+  static constexpr int BYTES = kWholeWarps * WARP;
+  static_assert(BYTES >= kWholeWarps * 16 * D * 4, "the rings hold the warps' outputs at the end");
+};
+
+template <int D>
+__global__ void __launch_bounds__(32 * kWholeWarps)
+    whole_kernel(const __grid_constant__ WholeParams p) {
+  using C = WholeCfg<D>;
+  extern __shared__ __align__(128) uint8_t smem_whole[];
+  __shared__ float2 stats[kWholeWarps][16];  // a warp's m and l per row
+  const DecodeSizes& s = p.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.x % s.B, ht = blockIdx.x / s.B;
+  const int hk = ht / s.row_tiles, rt = ht - hk * s.row_tiles;
+  const int rows = min(16, s.per_kv - rt * 16);
+  const int own_cap = p.max_pages << p.page_shift;
+  const int len = __ldg(p.lens + b), plen = p.prefix_len ? __ldg(p.prefix_len) : 0;
+  if (len < 0 || len > own_cap || plen < 0 || plen > p.prefix_cap)
+    if (threadIdx.x == 0) atomicOr(&g_prefix_status, kDeviceIndexBit);
+  const int own = max(0, min(len, own_cap)), shared = max(0, min(plen, p.prefix_cap));
+  const int p_steps = (shared + 15) / 16, steps = p_steps + (own + 15) / 16;
+
+  // This warp's steps warp, warp + kWholeWarps, ...
+  const int mine = max(0, (steps - warp + kWholeWarps - 1) / kWholeWarps);
+  const uint32_t ring = smem_u32(smem_whole) + warp * C::WARP;
+  const size_t head_rows = (size_t)1 << p.page_shift;
+  auto keys_of = [&](int i, int& key) {  // step i's first key in its list, and its keys
+    key = i < p_steps ? 16 * i : 16 * (i - p_steps);
+    return min(16, (i < p_steps ? shared : own) - key);
+  };
+  int ids = 0;  // pages of this warp's steps 32 k .. 32 k + 31, one per lane
+  auto issue = [&](int j) {
+    if (j < mine) {
+      if ((j & 31) == 0) {
+        const int i = warp + (j + lane) * kWholeWarps;
+        ids = 0;
+        if (j + lane < mine) {
+          int key;
+          keys_of(i, key);
+          ids = __ldg(i < p_steps ? p.pages + (key >> p.page_shift)
+                                  : p.table + (size_t)b * p.max_pages + (key >> p.page_shift));
+          if ((unsigned)ids >= (unsigned)p.num_pages) {
+            atomicOr(&g_prefix_status, kDeviceIndexBit);
+            ids = 0;
+          }
+        }
+      }
+      const int page = __shfl_sync(0xffffffffu, ids, j & 31);
+      int key;
+      const int n = keys_of(warp + j * kWholeWarps, key);
+      load_stage<D>(ring + (j % C::STAGES) * C::STAGE, p.Kc, p.Vc,
+                    ((size_t)page * s.Hkv + hk) * head_rows + (key & (head_rows - 1)), n, s.d);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int j = 0; j < C::STAGES - 1; ++j) issue(j);
+  RowTile<D> tile;
+  tile.load(p.Q + ((size_t)b * s.Hq + hk * s.per_kv + rt * 16) * s.d, rows, s.d);
+  for (int j = 0; j < mine; ++j) {
+    cp_async_wait<C::STAGES - 2>();
+    __syncwarp();  // the stage has landed for every lane, and the last one is read
+    issue(j + C::STAGES - 1);
+    int key;
+    const int n = keys_of(warp + j * kWholeWarps, key);
+    const uint32_t kb = ring + (j % C::STAGES) * C::STAGE;
+    tile.step(kb, kb + C::STAGE / 2, n, p.scale_log2);
+  }
+  tile.finish();
+  cp_async_wait<0>();
+  __syncthreads();  // every ring is read: they hold the outputs now
+
+  float* part = reinterpret_cast<float*>(smem_whole);  // [warp][row][D]
+  const int qr = lane >> 2, qc = (lane & 3) * 2;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    float* out = part + (warp * 16 + qr + 8 * e) * D;
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+      *reinterpret_cast<float2*>(out + 8 * n + qc) =
+          make_float2(tile.o[n][2 * e], tile.o[n][2 * e + 1]);
+    if ((lane & 3) == 0)
+      stats[warp][qr + 8 * e] = e ? make_float2(tile.m1, tile.l1) : make_float2(tile.m0, tile.l0);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * (D / 8); i += 32 * kWholeWarps) {
+    const int r = i / (D / 8), c = (i - r * (D / 8)) * 8;
+    if (c >= s.d) continue;
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWholeWarps; ++w) m = fmaxf(m, stats[w][r].x);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f, acc[8] = {};
+#pragma unroll
+    for (int w = 0; w < kWholeWarps; ++w) {
+      if (w >= steps) break;  // a warp without keys
+      const float f = ex2(stats[w][r].x - ref);
+      l += f * stats[w][r].y;
+      const float4* src = reinterpret_cast<const float4*>(part + (w * 16 + r) * D + c);
+      const float4 x = src[0], y = src[1];
+      acc[0] += f * x.x;
+      acc[1] += f * x.y;
+      acc[2] += f * x.z;
+      acc[3] += f * x.w;
+      acc[4] += f * y.x;
+      acc[5] += f * y.y;
+      acc[6] += f * y.z;
+      acc[7] += f * y.w;
+    }
+    const float inv = steps > 0 ? 1.f / l : 0.f;
+    const size_t row = (size_t)b * s.Hq + hk * s.per_kv + rt * 16 + r;
+    *reinterpret_cast<uint4*>(p.O + row * s.d + c) =
+        make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv),
+                   pack_bf16(acc[4] * inv, acc[5] * inv), pack_bf16(acc[6] * inv, acc[7] * inv));
+    if (c == 0) p.L[row] = steps > 0 ? (ref + lg2(l)) * kLn2 : -INFINITY;
+  }
 }
 
 // ================================================================== join kernel
@@ -790,6 +960,33 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
   while ((1 << shift) < a.page) ++shift;
   cudaError_t e;
   const int cap = a.prefix_cap << shift;
+  // One launch for small calls: at most kWholeKeys keys a request, and all requests'
+  // keys, the prefix counted for each, within kWholeBytes.
+  const long long keys = (long long)cap + (long long)a.max_pages * a.page;
+  const long long blocks = (long long)s.Hkv * s.row_tiles * s.B;
+  if (keys <= kWholeKeys && blocks * keys * 4 * a.d <= kWholeBytes) {
+    WholeParams w;
+    w.s = s;
+    w.Q = static_cast<const __nv_bfloat16*>(a.Q);
+    w.Kc = static_cast<const __nv_bfloat16*>(a.Kc);
+    w.Vc = static_cast<const __nv_bfloat16*>(a.Vc);
+    w.pages = a.prefix_pages;
+    w.prefix_len = a.prefix_cap > 0 ? a.prefix_len : nullptr;
+    w.table = a.table;
+    w.lens = a.lens;
+    w.O = static_cast<__nv_bfloat16*>(a.O);
+    w.L = a.L;
+    w.prefix_cap = cap;
+    w.max_pages = a.max_pages;
+    w.num_pages = a.num_pages;
+    w.page_shift = shift;
+    w.scale_log2 = a.scale * kLog2e;
+    e = cudaFuncSetAttribute(whole_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             WholeCfg<D>::BYTES);
+    if (e != cudaSuccess) return e;
+    return launch(whole_kernel<D>, (unsigned)blocks, 32 * kWholeWarps, WholeCfg<D>::BYTES, stream,
+                  false, w);
+  }
   if (a.prefix_cap > 0) {
     PrefixParams g;
     g.s = s;

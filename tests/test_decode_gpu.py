@@ -77,13 +77,24 @@ def _reference(q, keys, hkv, scale=None):
     return out
 
 
+def _wide(args):
+    """The same call with a table for long contexts, whose capacity rules the single-kernel
+    form for small calls out."""
+    table = args[5]
+    more = torch.full((table.shape[0], 8192 // args[1].shape[2]), -9, dtype=torch.int32,
+                      device="cuda")
+    return [*args[:5], torch.cat([table, more], 1), *args[6:]]
+
+
 def _check(args, keys, hkv, scale=None, **kw):
-    O, L = fa.fa_prefix_decode(*args, scale=scale, **kw)
+    """Both forms of the call, where the small one takes it."""
     want = _reference(args[0], keys, hkv, scale)
     some = torch.tensor([k.shape[0] > 0 for k, _ in keys], device="cuda")
-    assert_close("O", O, want["O"])
-    assert_close("L", L, want["L"], mask=some[:, None].expand_as(L))
-    assert torch.all(L[~some] == -math.inf) and torch.all(O[~some] == 0)
+    for call in (args, _wide(args)):
+        O, L = fa.fa_prefix_decode(*call, scale=scale, **kw)
+        assert_close("O", O, want["O"])
+        assert_close("L", L, want["L"], mask=some[:, None].expand_as(L))
+        assert torch.all(L[~some] == -math.inf) and torch.all(O[~some] == 0)
     return O, L
 
 
@@ -109,7 +120,7 @@ def test_decode_many_requests(d):
     lens = [r.choice([0, 1, 15, 16, 17, 63, 64, 65, 200, 513]) for _ in range(150)]
     args, keys = _batch(900, lens, 16, 4, d, 16, 19)
     a = _check(args, keys, 4)
-    b = fa.fa_prefix_decode(*args)
+    b = fa.fa_prefix_decode(*_wide(args))
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
@@ -137,8 +148,10 @@ def test_decode_ignores_what_pages_held_before(value):
     _check(args, keys, 2)
 
 
-def test_decode_requests_do_not_leak():
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_requests_do_not_leak(wide):
     args, keys = _batch(40, [33, 70, 5], 4, 2, 64, 16, 43)
+    args = _wide(args) if wide else args
     clean = fa.fa_prefix_decode(*args)
     args[0][1] = math.nan
     page = int(args[5][1, 0])
@@ -149,9 +162,11 @@ def test_decode_requests_do_not_leak():
     assert torch.isnan(O[1].float()).all()
 
 
-def test_decode_reports_bad_indices():
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_reports_bad_indices(wide):
     """A bad page or length is reported, and the other requests keep their results."""
     args, keys = _batch(40, [33, 70, 5], 4, 2, 64, 16, 47)
+    args = _wide(args) if wide else args
     clean = fa.fa_prefix_decode(*args)
     for bad in (10 ** 6, -1, args[1].shape[0]):
         table = args[5].clone()
@@ -176,15 +191,17 @@ def test_decode_reports_bad_indices():
     assert fa.fa_get_device_status() == 0
 
 
-def test_decode_in_a_graph_and_on_another_stream():
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_in_a_graph_and_on_another_stream(wide):
     args, keys = _batch(300, [40, 90], 8, 2, 64, 16, 53)
+    args = _wide(args) if wide else args
     want = fa.fa_prefix_decode(*args)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     got = fa.fa_prefix_decode(*args, stream=side)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
-    ws = fa.alloc_prefix_workspace(2, 8, 2, 64, 10000, 10000, "cuda")  # more than needed
+    ws = fa.alloc_prefix_workspace(2, 8, 2, 64, 20000, 20000, "cuda")  # more than needed
     ws.fill_(255)
     O, L = torch.empty_like(args[0]), torch.empty(2, 8, device="cuda")
     torch.cuda.synchronize()

@@ -35,7 +35,6 @@ constexpr int kOwnWarps = 4;       // warps of a thread block of the own kernel
 constexpr int kOwnBlocksPerSm = 2;
 constexpr int kOwnChunk = 64;      // keys per step of the own keys' split
 constexpr int kMinPrefixBlocks = 2;  // 128-key blocks a prefix worker takes at least
-constexpr long long kWholeKeys = 4096, kWholeBytes = 24 << 20;  // the whole kernel's calls
 
 // `total` steps (below 2^31) dealt to at most `most` workers in contiguous pieces that
 // differ by one step at most; the longer pieces come first.
@@ -646,10 +645,12 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
 }
 
 // ================================================================== whole kernel
-// Small calls, where three kernels' latency would be most of the time: one thread block
-// per request and row tile takes all of its keys, the prefix's and its own, 16 at a time
-// in turn by its warps, and joins the warps' parts through shared memory. The prefix is
-// read again for every request, from L2 but for the first.
+// Small calls, where three kernels' latency would be most of the time: a cluster of one
+// to eight thread blocks per request and row tile takes all of its keys, the prefix's and
+// its own, 16 at a time in turn by the warps, and joins the warps' parts through the
+// cluster's shared memory. The prefix is read again for every request, from L2 but for
+// the first. A warp's stage takes about 0.85 us (the latency of a copy over the two in
+// flight), so that few requests want many blocks each.
 struct WholeParams {
   DecodeSizes s;
   const __nv_bfloat16 *Q, *Kc, *Vc;
@@ -657,6 +658,7 @@ struct WholeParams {
   __nv_bfloat16* O;
   float* L;
   int prefix_cap, max_pages, num_pages, page_shift;  // prefix_cap: keys
+  int cluster;                                        // blocks of a cluster
   float scale_log2;
 };
 constexpr int kWholeWarps = 8;
@@ -666,8 +668,34 @@ struct WholeCfg {
   static constexpr int STAGE = 2 * 16 * 2 * D;
   static constexpr int WARP = STAGES * STAGE;
   static constexpr int BYTES = kWholeWarps * WARP;
-  static_assert(BYTES >= kWholeWarps * 16 * D * 4, "the rings hold the warps' outputs at the end");
+  static_assert(BYTES >= (kWholeWarps + 1) * 16 * D * 4, "the rings hold the outputs at the end");
 };
+
+// Joins `n` parts of a row's four columns c .. c + 3: stat(i) gives part i's (m, l) and
+// value(i) its four columns, both relative to m. Returns the joined m and l.
+template <class S, class V>
+FA_DEV float2 join_parts(int n, float4& acc, S stat, V value) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) m = fmaxf(m, stat(i).x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (i >= n) break;
+    const float2 ml = stat(i);
+    const float4 x = value(i);
+    const float f = ex2(ml.x - ref);
+    l += f * ml.y;
+    acc.x += f * x.x;
+    acc.y += f * x.y;
+    acc.z += f * x.z;
+    acc.w += f * x.w;
+  }
+  return make_float2(ref, l);
+}
 
 template <int D>
 __global__ void __launch_bounds__(32 * kWholeWarps)
@@ -675,9 +703,11 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
   using C = WholeCfg<D>;
   extern __shared__ __align__(128) uint8_t smem_whole[];
   __shared__ float2 stats[kWholeWarps][16];  // a warp's m and l per row
+  __shared__ float2 joined[16];              // this block's
   const DecodeSizes& s = p.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x % s.B, ht = blockIdx.x / s.B;
+  const int unit = blockIdx.x / p.cluster, rank = blockIdx.x - unit * p.cluster;
+  const int b = unit % s.B, ht = unit / s.B;
   const int hk = ht / s.row_tiles, rt = ht - hk * s.row_tiles;
   const int rows = min(16, s.per_kv - rt * 16);
   const int own_cap = p.max_pages << p.page_shift;
@@ -687,8 +717,9 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
   const int own = max(0, min(len, own_cap)), shared = max(0, min(plen, p.prefix_cap));
   const int p_steps = (shared + 15) / 16, steps = p_steps + (own + 15) / 16;
 
-  // This warp's steps warp, warp + kWholeWarps, ...
-  const int mine = max(0, (steps - warp + kWholeWarps - 1) / kWholeWarps);
+  // This warp's steps me, me + all, ...
+  const int me = rank * kWholeWarps + warp, all = p.cluster * kWholeWarps;
+  const int mine = max(0, (steps - me + all - 1) / all);
   const uint32_t ring = smem_u32(smem_whole) + warp * C::WARP;
   const size_t head_rows = (size_t)1 << p.page_shift;
   auto keys_of = [&](int i, int& key) {  // step i's first key in its list, and its keys
@@ -699,7 +730,7 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
   auto issue = [&](int j) {
     if (j < mine) {
       if ((j & 31) == 0) {
-        const int i = warp + (j + lane) * kWholeWarps;
+        const int i = me + (j + lane) * all;
         ids = 0;
         if (j + lane < mine) {
           int key;
@@ -714,7 +745,7 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
       }
       const int page = __shfl_sync(0xffffffffu, ids, j & 31);
       int key;
-      const int n = keys_of(warp + j * kWholeWarps, key);
+      const int n = keys_of(me + j * all, key);
       load_stage<D>(ring + (j % C::STAGES) * C::STAGE, p.Kc, p.Vc,
                     ((size_t)page * s.Hkv + hk) * head_rows + (key & (head_rows - 1)), n, s.d);
     }
@@ -729,7 +760,7 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
     __syncwarp();  // the stage has landed for every lane, and the last one is read
     issue(j + C::STAGES - 1);
     int key;
-    const int n = keys_of(warp + j * kWholeWarps, key);
+    const int n = keys_of(me + j * all, key);
     const uint32_t kb = ring + (j % C::STAGES) * C::STAGE;
     tile.step(kb, kb + C::STAGE / 2, n, p.scale_log2);
   }
@@ -750,37 +781,43 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
       stats[warp][qr + 8 * e] = e ? make_float2(tile.m1, tile.l1) : make_float2(tile.m0, tile.l0);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * (D / 8); i += 32 * kWholeWarps) {
-    const int r = i / (D / 8), c = (i - r * (D / 8)) * 8;
-    if (c >= s.d) continue;
-    float m = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWholeWarps; ++w) m = fmaxf(m, stats[w][r].x);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f, acc[8] = {};
-#pragma unroll
-    for (int w = 0; w < kWholeWarps; ++w) {
-      if (w >= steps) break;  // a warp without keys
-      const float f = ex2(stats[w][r].x - ref);
-      l += f * stats[w][r].y;
-      const float4* src = reinterpret_cast<const float4*>(part + (w * 16 + r) * D + c);
-      const float4 x = src[0], y = src[1];
-      acc[0] += f * x.x;
-      acc[1] += f * x.y;
-      acc[2] += f * x.z;
-      acc[3] += f * x.w;
-      acc[4] += f * y.x;
-      acc[5] += f * y.y;
-      acc[6] += f * y.z;
-      acc[7] += f * y.w;
-    }
-    const float inv = steps > 0 ? 1.f / l : 0.f;
+  // The block's warps, then the cluster's blocks; those with keys come first.
+  float* const mid = part + kWholeWarps * 16 * D;  // [row][D] of this block
+  const int warps_in = min(kWholeWarps, max(0, steps - rank * kWholeWarps));
+  const int blocks_in = min(p.cluster, (steps + kWholeWarps - 1) / kWholeWarps);
+  auto write = [&](int r, int c, float4 acc, float2 ml, bool any) {
+    const float inv = any ? 1.f / ml.y : 0.f;
     const size_t row = (size_t)b * s.Hq + hk * s.per_kv + rt * 16 + r;
-    *reinterpret_cast<uint4*>(p.O + row * s.d + c) =
-        make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv),
-                   pack_bf16(acc[4] * inv, acc[5] * inv), pack_bf16(acc[6] * inv, acc[7] * inv));
-    if (c == 0) p.L[row] = steps > 0 ? (ref + lg2(l)) * kLn2 : -INFINITY;
+    *reinterpret_cast<uint2*>(p.O + row * s.d + c) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (c == 0) p.L[row] = any ? (ml.x + lg2(ml.y)) * kLn2 : -INFINITY;
+  };
+  for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * kWholeWarps) {
+    const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+    float4 acc;
+    const float2 ml = join_parts(
+        warps_in, acc, [&](int w) { return stats[w][r]; },
+        [&](int w) { return *reinterpret_cast<const float4*>(part + (w * 16 + r) * D + c); });
+    if (p.cluster == 1) {
+      if (c < s.d) write(r, c, acc, ml, steps > 0);
+    } else {
+      *reinterpret_cast<float4*>(mid + r * D + c) = acc;
+      if (c == 0) joined[r] = ml;
+    }
   }
+  if (p.cluster == 1) return;
+  cluster_sync();  // every block's rows are written
+  for (int i = rank * 32 * kWholeWarps + threadIdx.x; i < rows * (D / 4);
+       i += p.cluster * 32 * kWholeWarps) {
+    const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+    if (c >= s.d) continue;
+    float4 acc;
+    const float2 ml = join_parts(
+        blocks_in, acc, [&](int k) { return cluster_ld2(cluster_map(smem_u32(&joined[r]), k)); },
+        [&](int k) { return cluster_ld4(cluster_map(smem_u32(mid + r * D + c), k)); });
+    write(r, c, acc, ml, steps > 0);
+  }
+  cluster_sync();  // no block leaves while its rows are read
 }
 
 // ================================================================== join kernel
@@ -927,18 +964,55 @@ int decode_sms() {
 // An ordinary launch, or one that may start while the stream's previous kernel runs.
 template <class K, class P>
 cudaError_t launch(K kernel, unsigned grid, int threads, int smem, cudaStream_t stream, bool early,
-                   const P& params) {
+                   const P& params, unsigned cluster = 1) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = early ? 1 : 0;
+  cudaLaunchAttribute attr[2] = {};
+  if (early) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = cluster;
+    attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
   return cudaLaunchKernelEx(&cfg, kernel, params);
+}
+
+// Blocks per unit with which the whole kernel is expected to beat the three kernels, or
+// 0 where it is not, from the capacities (the lengths are known on the device only). Both
+// forms were timed at 72 points (8, 2 and 1 key/value heads of 4, 4 and 16 rows, 1 to 64
+// requests, 64 to 8000 shared and 64 to 2048 own keys); in ns they fit
+//   whole   1500 + waves (3000 + stages t), t = 850 (d > 64) or 460 for a warp's stage of
+//           16 keys, + 1000 for a cluster, and 1 per 9000 bytes at least
+//   three   12000 + 1 per 6000 bytes, every key read once, + 2 per row joined
+// to about 15 %. The two lie between 6.0 and 12.3 us for 16 requests of 2 x 4 heads,
+// d = 64, behind 1024 keys with 512 own, and between 58 and 26 us for 16 requests of
+// 8 x 4 heads, d = 128, behind 8000 keys with 128 own.
+unsigned whole_cluster(const DecodeSizes& s, int D, int prefix_cap, int own_cap, int sms) {
+  const long long keys = (long long)prefix_cap + own_cap;
+  const long long units = (long long)s.Hkv * s.row_tiles * s.B;
+  const long long per_block = 16 * kWholeWarps;  // keys of a stage of all warps
+  // A cluster of eight needs eight free SMs of one GPC: no more than half of the SMs.
+  int c = 1;
+  while (c < 8 && 2 * c * units <= (c == 4 ? sms / 2 : sms) && keys >= 2 * c * per_block) c *= 2;
+  const long long stages = (keys + c * per_block - 1) / (c * per_block);
+  if (stages > 64 || units * c > 0x7fffffffLL) return 0;
+  const long long slots = (long long)sms * (D == 128 ? 1 : 2);
+  const long long waves = (units * c + slots - 1) / slots;
+  const long long bytes = 4LL * s.d;  // K and V of one key
+  long long whole = 1500 + waves * (3000 + stages * (D == 128 ? 850 : 460)) + (c > 1 ? 1000 : 0);
+  if (whole < units * keys * bytes / 9000) whole = units * keys * bytes / 9000;
+  const long long three = 12000 +
+                          (long long)s.Hkv * (prefix_cap + (long long)s.B * own_cap) * bytes / 6000 +
+                          2LL * s.B * s.Hq;
+  return whole <= three ? (unsigned)c : 0;
 }
 
 template <int D>
@@ -960,11 +1034,9 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
   while ((1 << shift) < a.page) ++shift;
   cudaError_t e;
   const int cap = a.prefix_cap << shift;
-  // One launch for small calls: at most kWholeKeys keys a request, and all requests'
-  // keys, the prefix counted for each, within kWholeBytes.
-  const long long keys = (long long)cap + (long long)a.max_pages * a.page;
-  const long long blocks = (long long)s.Hkv * s.row_tiles * s.B;
-  if (keys <= kWholeKeys && blocks * keys * 4 * a.d <= kWholeBytes) {
+  // One launch where it is expected to take less time than the three kernels.
+  const unsigned cluster = whole_cluster(s, D, cap, a.max_pages * a.page, sms);
+  if (cluster > 0) {
     WholeParams w;
     w.s = s;
     w.Q = static_cast<const __nv_bfloat16*>(a.Q);
@@ -980,12 +1052,13 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
     w.max_pages = a.max_pages;
     w.num_pages = a.num_pages;
     w.page_shift = shift;
+    w.cluster = (int)cluster;
     w.scale_log2 = a.scale * kLog2e;
     e = cudaFuncSetAttribute(whole_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              WholeCfg<D>::BYTES);
     if (e != cudaSuccess) return e;
-    return launch(whole_kernel<D>, (unsigned)blocks, 32 * kWholeWarps, WholeCfg<D>::BYTES, stream,
-                  false, w);
+    return launch(whole_kernel<D>, (unsigned)(s.Hkv * s.row_tiles * s.B) * cluster,
+                  32 * kWholeWarps, WholeCfg<D>::BYTES, stream, false, w, cluster);
   }
   if (a.prefix_cap > 0) {
     PrefixParams g;

@@ -81,7 +81,7 @@ def _wide(args):
     """The same call with a table for long contexts, whose capacity rules the single-kernel
     form for small calls out."""
     table = args[5]
-    more = torch.full((table.shape[0], 8192 // args[1].shape[2]), -9, dtype=torch.int32,
+    more = torch.full((table.shape[0], 200000 // args[1].shape[2]), -9, dtype=torch.int32,
                       device="cuda")
     return [*args[:5], torch.cat([table, more], 1), *args[6:]]
 
@@ -201,7 +201,7 @@ def test_decode_in_a_graph_and_on_another_stream(wide):
     got = fa.fa_prefix_decode(*args, stream=side)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
-    ws = fa.alloc_prefix_workspace(2, 8, 2, 64, 20000, 20000, "cuda")  # more than needed
+    ws = fa.alloc_prefix_workspace(2, 8, 2, 64, 300000, 300000, "cuda")  # more than needed
     ws.fill_(255)
     O, L = torch.empty_like(args[0]), torch.empty(2, 8, device="cuda")
     torch.cuda.synchronize()

@@ -50,10 +50,12 @@ struct Dense {
   FA_DEV static uint32_t block_bytes(const Params&, const Item&, int) {
     return 2 * C::TILE;
   }
+  struct Place {};
+  FA_DEV static Place place(const Params&, const Item&, int) { return {}; }
   template <class C>
   FA_DEV static void load_kv(uint8_t* kdst, uint8_t* vdst, const CUtensorMap* mk,
                              const CUtensorMap* mv, uint64_t* f, const Params&, const Item& it,
-                             int block) {
+                             int block, Place) {
 #pragma unroll
     for (int c = 0; c < C::KCH; ++c) {
       tma_load_3d(kdst + c * C::CHUNK, mk, f, c * 64, block * C::BN, it.bh);

@@ -52,6 +52,8 @@
 //   steps(g, it, t)           64-key steps of tile t (tile 0 always has some)
 //   keys(g, it)               keys of the item; steps past them are masked
 //   causal(g), query(g, it, t, row)  the query position of a tile's row
+//   place                     what load_kv needs to know of a block from memory: read
+//                             one block ahead, so that the producer does not wait
 //   load_q, load_kv           TMA loads of a Q tile / a 128-key block
 //   tile_bytes, block_bytes   the bytes that they bring
 //   store                     the epilogue of one warp's 32 rows
@@ -237,6 +239,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         if (j + 1 < n_mine) nxt = fetch(j + 1);
         int nht[C::TILES];
         const int nkb = blocks(steps(it, nht));  // 128-key blocks
+        auto place = G::place(g, it, 0);  // where the next block's keys are
         for (int u = 0; u < C::QUSES + nkb; ++u, ++ru) {
           const int s = ru % C::STAGES;
           if (ru >= C::STAGES &&
@@ -261,7 +264,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
               if (two) G::load_q(vdst + c * C::CHUNK, &tmQ, f, c * 64, g, it, 2 * u + 1);
             }
           } else {
-            G::template load_kv<C>(kdst, vdst, &tmK, &tmV, f, g, it, u - C::QUSES);
+            const auto here = place;
+            if (u + 1 < C::QUSES + nkb) place = G::place(g, it, u + 1 - C::QUSES);
+            G::template load_kv<C>(kdst, vdst, &tmK, &tmV, f, g, it, u - C::QUSES, here);
           }
         }
       }

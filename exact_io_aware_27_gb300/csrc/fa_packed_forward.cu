@@ -86,10 +86,12 @@ struct Packed {
   FA_DEV static uint32_t block_bytes(const View&, const Item&, int) {
     return 2 * C::TILE;
   }
+  struct Place {};
+  FA_DEV static Place place(const View&, const Item&, int) { return {}; }
   template <class C>
   FA_DEV static void load_kv(uint8_t* kdst, uint8_t* vdst, const CUtensorMap* mk,
                              const CUtensorMap* mv, uint64_t* f, const View& g, const Item& it,
-                             int block) {
+                             int block, Place) {
     const int hk = it.h / g.p.per_kv, row = it.s.x + block * C::BN;
 #pragma unroll
     for (int c = 0; c < C::KCH; ++c) {

@@ -32,7 +32,9 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kMaxSms = 160;       // slots are reserved for this many thread blocks
 constexpr int kOwnWarps = 4;       // warps of a thread block of the own kernel
-constexpr int kOwnBlocksPerSm = 2;
+// Thread blocks of the own kernel per SM: 128 KB of keys in flight on each, above the
+// latency-bandwidth product of an SM's share of HBM, for either row size.
+constexpr int kOwnPerSmWide = 2, kOwnPerSmNarrow = 4;
 constexpr int kOwnChunk = 64;      // keys per step of the own keys' split
 constexpr int kMinPrefixBlocks = 2;  // 128-key blocks a prefix worker takes at least
 
@@ -68,7 +70,9 @@ struct DecodeSizes {
   int pair_rows;      // rows of a prefix slot
   int row_tiles;      // 16-row tiles of a key/value head's rows in the own kernel
   int own_rows;       // rows of an own slot
-  int prefix_workers, own_workers;
+  int own_per_sm;     // thread blocks of the own kernel per SM
+  int sms, prefix_workers, own_blocks;  // blocks launched of the prefix and own kernels
+  int prefix_step_ns, own_chunk_ns;     // see prefix_share
   float *prefix_o, *prefix_e;  // [slot][pair_rows][d], [slot][pair_rows]
   float *own_o, *own_e;        // [slot][own_rows][d], [slot][own_rows]
   int* first;                  // [B + 1] own chunks before each request
@@ -91,7 +95,7 @@ size_t lay_out(DecodeSizes* s, void* base, int prefix_cap, int own_cap) {
   const size_t pslots = slots((size_t)s->pairs * s->Hkv, ((size_t)prefix_cap + 127) / 128, kMaxSms);
   const size_t oslots = slots((size_t)s->Hkv * s->row_tiles * s->B,
                               ((size_t)own_cap + kOwnChunk - 1) / kOwnChunk,
-                              (size_t)kMaxSms * kOwnBlocksPerSm * kOwnWarps);
+                              (size_t)kMaxSms * s->own_per_sm * kOwnWarps);
   s->prefix_o = reinterpret_cast<float*>(take(pslots * s->pair_rows * s->d * 4));
   s->prefix_e = reinterpret_cast<float*>(take(pslots * s->pair_rows * 4));
   s->own_o = reinterpret_cast<float*>(take(oslots * s->own_rows * s->d * 4));
@@ -112,6 +116,7 @@ DecodeSizes sizes_of(int B, int Hq, int Hkv, int d) {
   s.pair_rows = (B < 2 * s.per_tile ? B : 2 * s.per_tile) * s.per_kv;
   s.row_tiles = ceil_div(s.per_kv, 16);
   s.own_rows = s.per_kv < 16 ? s.per_kv : 16;
+  s.own_per_sm = d > 64 ? kOwnPerSmWide : kOwnPerSmNarrow;
   return s;
 }
 
@@ -120,17 +125,51 @@ FA_DEV int prefix_keys(const int* prefix_len, int cap) {
   const int n = prefix_len ? __ldg(prefix_len) : 0;
   return max(0, min(n, cap));
 }
-FA_DEV Split prefix_split(const DecodeSizes& s, int blocks) {
+// Thread blocks of the prefix kernel that get work, for a prefix of `blocks` 128-key
+// blocks and `chunks` chunks of own keys per head and row tile. The two kernels run side
+// by side, a prefix block on an SM of its own and the own kernel's on the others, so the
+// SMs are shared out in proportion to the work: a prefix step of 128 keys takes an SM
+// 2.4 us (two row tiles) or 1.5 us (one), 0.5 us less for d <= 64, and a chunk of own keys
+// 4 d ns (its bytes at 65 GB/s). All three kernels compute this from the same integers.
+// 256 requests behind 8192 keys (32/8 heads, d = 128, up to 2048 own): 193 us, against
+// 226 us with every SM for the one kernel and then for the other.
+FA_DEV int prefix_share(const DecodeSizes& s, int blocks, int chunks) {
   const unsigned steps = (unsigned)(s.pairs * s.Hkv) * (unsigned)blocks;
-  return Split(steps, min((unsigned)s.prefix_workers,
-                          (steps + kMinPrefixBlocks - 1) / kMinPrefixBlocks));
+  if (steps == 0) return 0;
+  const int most = (int)min((unsigned)s.prefix_workers,
+                            (steps + kMinPrefixBlocks - 1) / kMinPrefixBlocks);
+  if (chunks == 0) return most;
+  const unsigned long long a = (unsigned long long)steps * (unsigned)s.prefix_step_ns;
+  const unsigned long long b = (unsigned long long)(s.Hkv * s.row_tiles) * (unsigned)chunks *
+                               (unsigned)s.own_chunk_ns;
+  // to 24 bits, for a 32-bit division
+  const int shift = max(0, 40 - __clzll((long long)(a + b)));
+  const unsigned part = (unsigned)(a >> shift), all = (unsigned)((a + b) >> shift);
+  const int n = (int)(((unsigned)s.sms * part + all / 2) / all);
+  return max(1, min(min(n, most), s.sms - 1));
+}
+FA_DEV Split prefix_split(const DecodeSizes& s, int blocks, int share) {
+  return Split((unsigned)(s.pairs * s.Hkv) * (unsigned)blocks, (unsigned)share);
+}
+// Thread blocks of the own kernel that get work.
+FA_DEV int own_share(const DecodeSizes& s, int share) {
+  return min(s.own_blocks, s.own_per_sm * (s.sms - share));
+}
+FA_DEV Split own_split(const DecodeSizes& s, int chunks, int share) {
+  return Split((unsigned)(s.Hkv * s.row_tiles) * (unsigned)chunks,
+               (unsigned)(own_share(s, share) * kOwnWarps));
+}
+// Own chunks of a request whose table row holds `cap` keys.
+FA_DEV int own_chunks(int len, int cap) {
+  return (max(0, min(len, cap)) + kOwnChunk - 1) / kOwnChunk;
 }
 
 // ================================================================== prefix kernel
 struct PrefixParams {
   DecodeSizes s;
-  const int *pages, *len;
-  int cap, page, page_shift, box, num_pages;  // cap: keys; box: rows of a TMA copy
+  const int *pages, *len, *lens;
+  int cap, own_cap;                      // keys
+  int page, page_shift, box, num_pages;  // box: rows of a TMA copy
 };
 
 // ONE_TILE: all rows of a key/value head fit one 128-row tile (so there is one pair, and
@@ -156,7 +195,11 @@ struct Prefix {
     if ((n < 0 || n > p.cap) && blockIdx.x == 0 && threadIdx.x == 0)
       atomicOr(status(), kDeviceIndexBit);
     const int keys = max(0, min(n, p.cap)), blocks = (keys + 127) / 128;
-    return {p, keys, blocks, prefix_split(p.s, blocks)};
+    int chunks = 0;  // each warp on its own
+    for (int b = threadIdx.x & 31; b < p.s.B; b += 32)
+      chunks += own_chunks(__ldg(p.lens + b), p.own_cap);
+    chunks = __reduce_add_sync(0xffffffffu, chunks);
+    return {p, keys, blocks, prefix_split(p.s, blocks, prefix_share(p.s, blocks, chunks))};
   }
   FA_DEV static int segments(const View& g, int cta, int) {
     if (cta >= g.split.workers) return 0;
@@ -208,23 +251,36 @@ struct Prefix {
   FA_DEV static uint32_t block_bytes(const View& g, const Item& it, int block) {
     return (uint32_t)(boxes(g, it, block) * g.p.box) * 256u * C::KCH;
   }
+  // The pages of a block's copies.
+  struct Place {
+    int page[8];
+  };
+  FA_DEV static Place place(const View& g, const Item& it, int block) {
+    Place at;
+    const int n = boxes(g, it, block), key0 = it.k0 + block * 128;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      at.page[i] = i < n ? __ldg(g.p.pages + ((key0 + i * g.p.box) >> g.p.page_shift)) : 0;
+    return at;
+  }
   template <class C>
   FA_DEV static void load_kv(uint8_t* kdst, uint8_t* vdst, const CUtensorMap* mk,
                              const CUtensorMap* mv, uint64_t* f, const View& g, const Item& it,
-                             int block) {
+                             int block, const Place& at) {
     const int n = boxes(g, it, block), key0 = it.k0 + block * 128;
-    for (int i = 0; i < n; ++i) {
-      const int key = key0 + i * g.p.box;
-      int page = __ldg(g.p.pages + (key >> g.p.page_shift));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= n) break;
+      int page = at.page[i];
       if ((unsigned)page >= (unsigned)g.p.num_pages) {
         atomicOr(status(), kDeviceIndexBit);
         page = 0;
       }
-      const int row = key & (g.p.page - 1), at = page * g.p.s.Hkv + it.hk;
+      const int row = (key0 + i * g.p.box) & (g.p.page - 1), plane = page * g.p.s.Hkv + it.hk;
 #pragma unroll
       for (int c = 0; c < C::KCH; ++c) {
-        tma_load_3d(kdst + c * C::CHUNK + i * g.p.box * 128, mk, f, c * 64, row, at);
-        tma_load_3d(vdst + c * C::CHUNK + i * g.p.box * 128, mv, f, c * 64, row, at);
+        tma_load_3d(kdst + c * C::CHUNK + i * g.p.box * 128, mk, f, c * 64, row, plane);
+        tma_load_3d(vdst + c * C::CHUNK + i * g.p.box * 128, mv, f, c * 64, row, plane);
       }
     }
   }
@@ -449,8 +505,8 @@ FA_DEV void load_stage(uint32_t dst, const __nv_bfloat16* Kc, const __nv_bfloat1
 struct OwnParams {
   DecodeSizes s;
   const __nv_bfloat16 *Q, *Kc, *Vc;
-  const int *table, *lens;
-  int max_pages, num_pages, page_shift;
+  const int *table, *lens, *prefix_len;
+  int prefix_cap, max_pages, num_pages, page_shift;  // prefix_cap: keys
   float scale_log2;
 };
 
@@ -472,8 +528,7 @@ FA_DEV int own_keys(const OwnParams& p, int b) {
 
 // Pages are read 16 keys at a time (a page holds a multiple of 16): per stage 16 rows of
 // K and of V, 16-byte piece j of row r at j ^ (r % 8), which ldmatrix reads without bank
-// conflicts. Three stages a warp keep two in flight: 128 KB per SM, above the
-// latency-bandwidth product of its share of HBM.
+// conflicts. Three stages a warp keep two in flight.
 template <int D>
 __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_constant__ OwnParams p) {
   using C = OwnCfg<D>;
@@ -494,7 +549,7 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
       const int len = __ldg(p.lens + b);
       if ((len < 0 || len > p.max_pages << p.page_shift) && blockIdx.x == 0)
         atomicOr(&g_prefix_status, kDeviceIndexBit);
-      n = (own_keys(p, b) + kOwnChunk - 1) / kOwnChunk;
+      n = own_chunks(len, p.max_pages << p.page_shift);
     }
     int x = n;
 #pragma unroll
@@ -521,8 +576,12 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
 
   const int chunks = run;  // of one (head, row tile)
   const unsigned units = (unsigned)(s.Hkv * s.row_tiles * s.B);
-  const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)chunks, (unsigned)s.own_workers);
-  const int me = warp * gridDim.x + blockIdx.x;  // the first workers on different SMs
+  const int share =
+      prefix_share(s, (prefix_keys(p.prefix_len, p.prefix_cap) + 127) / 128, chunks);
+  const Split sp = own_split(s, chunks, share);
+  // The first workers on different SMs; the blocks past the share get none.
+  const int active = own_share(s, share);
+  const int me = (int)blockIdx.x < active ? warp * active + (int)blockIdx.x : sp.workers;
   if (me >= sp.workers) {  // no barrier of the block follows
     grid_wait();
     return;
@@ -832,11 +891,12 @@ struct JoinParams {
 // A row (request, query head) is joined by one warp, or by kJoinWarps where there are
 // too few rows to fill the GPU and each has many parts. Lane j of a warp looks up every
 // 32nd part (its slot and e); then the warp adds the parts up, four columns a lane and
-// eight parts in flight: the kernel is bound by the latency of these loads. A row
+// four or eight parts in flight (fewer where many rows share the registers): the kernel
+// is bound by the latency of these loads. A row
 // without keys gets O = 0, L = -inf.
 constexpr int kJoinWarps = 8;
 template <int WARPS>  // of a row
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ JoinParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps, WARPS == 1 ? 4 : 1) join_kernel(const __grid_constant__ JoinParams p) {
   __shared__ float4 sums[kJoinWarps][32];
   __shared__ float2 stats[kJoinWarps];  // a warp's reference and weight sum
   const DecodeSizes& s = p.s;
@@ -851,11 +911,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   // Parts of the prefix, then of the request's own keys.
   const int blocks = (prefix_keys(p.prefix_len, p.prefix_cap) + 127) / 128;
   const int chunks = __ldg(s.first + s.B), f0 = __ldg(s.first + b), f1 = __ldg(s.first + b + 1);
+  const int share = prefix_share(s, blocks, chunks);
   int pparts = 0, pfirst = 0;
   const int pair = b / (2 * s.per_tile);
   const unsigned punit = (unsigned)(pair * s.Hkv + hk);
   if (blocks > 0) {
-    const Split sp = prefix_split(s, blocks);
+    const Split sp = prefix_split(s, blocks, share);
     pfirst = sp.owner(punit * (unsigned)blocks);
     pparts = sp.owner((punit + 1) * (unsigned)blocks - 1) - pfirst + 1;
   }
@@ -863,7 +924,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   const int ht = hk * s.row_tiles + in / 16;
   int oparts = 0, ofirst = 0;
   if (f1 > f0) {
-    const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)chunks, (unsigned)s.own_workers);
+    const Split sp = own_split(s, chunks, share);
     ofirst = sp.owner((unsigned)(ht * chunks + f0));
     oparts = sp.owner((unsigned)(ht * chunks + f1) - 1u) - ofirst + 1;
   }
@@ -901,11 +962,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     acc.z *= back;
     acc.w *= back;
     const int n = min(32, (parts - base - mine + WARPS - 1) / WARPS);  // lanes with a part
-    for (int j = 0; j < n; j += 8) {
-      float4 v[8];
-      float w[8];
+    constexpr int U = WARPS == 1 ? 4 : 8;
+    for (int j = 0; j < n; j += U) {
+      float4 v[U];
+      float w[U];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < U; ++u) {
         const float* src = reinterpret_cast<const float*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (j + u) & 31));
         w[u] = __shfl_sync(0xffffffffu, weight, (j + u) & 31);
@@ -913,7 +975,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
         if (j + u < n && 4 * lane < s.d) v[u] = reinterpret_cast<const float4*>(src)[lane];
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < U; ++u) {
         if (j + u >= n) break;
         acc.x += w[u] * v[u].x;
         acc.y += w[u] * v[u].y;
@@ -1027,9 +1089,12 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
       (long long)s.Hkv * s.row_tiles * s.B * ceil_div(a.max_pages * a.page, kOwnChunk);
   auto least = [](long long x, long long y) { return (unsigned)(x < y ? x : y); };
   const unsigned prefix_grid = least(sms, prefix_steps);
-  const unsigned own_grid = least(sms * kOwnBlocksPerSm, own_steps > 0 ? own_steps : 1);
+  const unsigned own_grid = least(sms * s.own_per_sm, own_steps > 0 ? own_steps : 1);
+  s.sms = sms;
   s.prefix_workers = (int)prefix_grid;
-  s.own_workers = (int)own_grid * kOwnWarps;
+  s.own_blocks = (int)own_grid;
+  s.prefix_step_ns = (a.B <= s.per_tile ? 1500 : 2400) - (D == 64 ? 500 : 0);
+  s.own_chunk_ns = 4 * a.d;
   int shift = 0;
   while ((1 << shift) < a.page) ++shift;
   cudaError_t e;
@@ -1065,7 +1130,9 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
     g.s = s;
     g.pages = a.prefix_pages;
     g.len = a.prefix_len;
+    g.lens = a.lens;
     g.cap = cap;
+    g.own_cap = a.max_pages << shift;
     g.page = a.page;
     g.page_shift = shift;
     g.box = a.page < 128 ? a.page : 128;
@@ -1098,6 +1165,8 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
   op.Vc = static_cast<const __nv_bfloat16*>(a.Vc);
   op.table = a.table;
   op.lens = a.lens;
+  op.prefix_len = a.prefix_cap > 0 ? a.prefix_len : nullptr;
+  op.prefix_cap = cap;
   op.max_pages = a.max_pages;
   op.num_pages = a.num_pages;
   op.page_shift = shift;

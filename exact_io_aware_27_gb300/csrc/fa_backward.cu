@@ -21,6 +21,7 @@ struct DenseBwd {
   struct QItem {
     int q0, bh;  // first query, head
   };
+  static constexpr bool kEarly = false;
   static constexpr bool kForeignTail = false;  // TMA reads zeros past a head's rows
   FA_DEV static View view(const Params& g) { return g; }
   FA_DEV static unsigned int* status() { return &g_bwd_status; }

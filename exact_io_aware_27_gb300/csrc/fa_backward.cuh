@@ -48,7 +48,7 @@
 // get), KvItem and QItem (a key block and a query block), and the functions that say
 // where an item's rows come from and go to. With kForeignTail the rows past an item's
 // last query or key hold foreign values and are replaced by zeros; without it TMA has
-// read zeros there.
+// read zeros there. With kEarly it is launched with launch_early (fa_launch.h).
 #pragma once
 
 #include "fa_internal.h"
@@ -937,6 +937,11 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // As in the forward kernel: everything above touches only this block's own state.
+  if constexpr (G::kEarly) {
+    grid_wait();
+    if (G::trigger(gp)) grid_launch_dependents();
+  }
   typename G::View g = G::view(gp);
   const int n_kv = G::kv_items(g), n_dq = G::q_items(g);
   const int P = gridDim.x, c = blockIdx.x;

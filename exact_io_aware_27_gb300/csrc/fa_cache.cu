@@ -8,6 +8,7 @@
 // chunks in flight each. A place out of range is not written and raises
 // kDeviceIndexBit.
 #include "fa_decode.h"
+#include "fa_launch.h"
 #include "sm103.cuh"
 
 namespace fa {
@@ -31,6 +32,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
   __shared__ long long place[kTokens];  // first 16-byte unit of the token's row of head 0
   const int per = p.Hkv * p.per_row;    // 16-byte units of a token
   const long long head = (long long)p.page * p.per_row;  // units from head to head
+  grid_wait();
+  grid_launch_dependents();
   for (long long t0 = (long long)blockIdx.x * kTokens; t0 < p.total;
        t0 += (long long)gridDim.x * kTokens) {
     if (threadIdx.x < kTokens) {
@@ -109,8 +112,7 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s) {
   p.page_shift = 0;
   while ((1 << p.page_shift) < a.page) ++p.page_shift;
   const unsigned blocks = (unsigned)ceil_div(a.total, kTokens);
-  append_kernel<<<blocks, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(append_kernel, blocks, kThreads, 0, s, p);
 }
 
 cudaError_t append_read_status(unsigned int* out) {

@@ -19,7 +19,7 @@ struct Dense {
     int qs, bh;  // first query, head
   };
   FA_DEV static unsigned int* status() { return &g_fwd_status; }
-  static constexpr bool kSplit = false, kAlternate = false;
+  static constexpr bool kSplit = false, kAlternate = false, kEarly = false;
   static constexpr bool kForeignTail = false;  // TMA reads zeros past a head's rows
   FA_DEV static int items(const Params& g) { return g.num_pairs * g.BH; }
   // Heads a group at a time (their K/V stay in L2 while the group runs), inside a

@@ -58,6 +58,8 @@
 //   tile_bytes, block_bytes   the bytes that they bring
 //   store                     the epilogue of one warp's 32 rows
 //   idle_warps                work of the warps that have no role
+//   kEarly, trigger           launched with launch_early (see fa_launch.h), and whether
+//                             the next kernel may start as early
 //   kAlternate                both tiles of an item hold the same rows (see half_of),
 //                             and store_joined writes the join of the two
 //   status()                  the translation unit's device status word
@@ -146,7 +148,6 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                const FwdParams p, const typename G::Params gp) {
   using Item = typename G::Item;
-  typename G::View g = G::view(gp);
   using C = FwdCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -154,10 +155,42 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + C::NBAR);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const WaitCtx wc{abort_flag, G::status()};
-  if constexpr (G::kSplit) grid_launch_dependents();
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&bar[C::B_KVF + s], 1);
+      mbar_init(&bar[C::B_KVE + s], 1);
+    }
+    mbar_init(&bar[C::B_IN], 128 * C::TILES);
+    for (int t = 0; t < C::TILES; ++t) {
+      mbar_init(&bar[C::B_SF + t], 1);
+      mbar_init(&bar[C::B_PF + t], 128);
+      mbar_init(&bar[C::B_PVD + t], 1);
+    }
+    mbar_init(&bar[C::B_DRAIN], 1);
+    mbar_init(&bar[C::B_X], 128 * C::TILES);
+    mbar_init(&bar[C::B_Y], 128 * C::TILES);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // A launch that may begin before the stream's previous kernel has ended: everything
+  // above touches only this block's own state.
+  if constexpr (G::kEarly) {
+    grid_wait();
+    if (G::trigger(gp)) grid_launch_dependents();
+  }
+  typename G::View g = G::view(gp);
   // Persistent: CTA c takes items snake_item(j, c, P), j = 0, 1, ... of the list of
   // (tile pair, head) items in launch order: heads a group at a time (their K/V
   // stay in L2 while the group runs), inside a group the heaviest tile pairs (the
@@ -195,32 +228,6 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
   // Ring uses of item j: QUSES for its Q tiles (tiles 2u and 2u + 1 in the K and V
   // buffers of use u), then one per 128-key block of K, V. Every role counts them
   // (`ru`) and the steps of each tile identically.
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&bar[C::B_KVF + s], 1);
-      mbar_init(&bar[C::B_KVE + s], 1);
-    }
-    mbar_init(&bar[C::B_IN], 128 * C::TILES);
-    for (int t = 0; t < C::TILES; ++t) {
-      mbar_init(&bar[C::B_SF + t], 1);
-      mbar_init(&bar[C::B_PF + t], 128);
-      mbar_init(&bar[C::B_PVD + t], 1);
-    }
-    mbar_init(&bar[C::B_DRAIN], 1);
-    mbar_init(&bar[C::B_X], 128 * C::TILES);
-    mbar_init(&bar[C::B_Y], 128 * C::TILES);
-    *abort_flag = 0u;
-    fence_mbar_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, C::TMEM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer

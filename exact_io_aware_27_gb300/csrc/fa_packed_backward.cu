@@ -8,6 +8,7 @@
 // 128 rows: TMA copies of fp32 rows have to start on 16-byte boundaries, which a
 // sequence's first row in the packed tensors need not do.
 #include "fa_backward.cuh"
+#include "fa_launch.h"
 #include "fa_packed.cuh"
 
 namespace fa {
@@ -24,7 +25,7 @@ struct PackedBwd {
     long long lddq, lddk, lddv;
     const float *nD, *nL2;
     long long ws_rows;
-    int total, nseq, Hq, Hkv, per_kv, causal, kgroup, qgroup, fill;
+    int total, nseq, Hq, Hkv, per_kv, causal, kgroup, qgroup, fill, trigger;
   };
   struct View {
     const Params& p;
@@ -38,8 +39,10 @@ struct PackedBwd {
     PlanTile s;
     int h;
   };
+  static constexpr bool kEarly = true;
   static constexpr bool kForeignTail = true;
   FA_DEV static unsigned int* status() { return &g_packed_bwd_status; }
+  FA_DEV static bool trigger(const Params& p) { return p.trigger; }
   FA_DEV static View view(const Params& p) {
     const PlanHead* head = reinterpret_cast<const PlanHead*>(p.plan);
     const bool ok = plan_matches(head, p.total, p.nseq, status());
@@ -135,12 +138,14 @@ __global__ void __launch_bounds__(256) packed_preprocess_kernel(
     const __nv_bfloat16* __restrict__ O, const __nv_bfloat16* __restrict__ dO,
     const float* __restrict__ L, const uint8_t* __restrict__ plan, long long off_kv,
     float* __restrict__ ws_nD, float* __restrict__ ws_nL2, long long ws_rows, int total, int nseq,
-    int Hq, int d) {
+    int Hq, int d, int trigger) {
   constexpr int LPR = D / 8;        // lanes per row
   constexpr int RPB = 256 / LPR;    // rows per block step
   constexpr int U = 4;              // steps in flight
   static_assert(128 % (RPB * U) == 0, "whole rounds of steps per tile");
   __shared__ float sums[128];
+  grid_wait();
+  if (trigger) grid_launch_dependents();
   const PlanHead* head = reinterpret_cast<const PlanHead*>(plan);
   if (!plan_matches(head, total, nseq, &g_packed_bwd_status)) return;
   const long long pairs = (long long)head->tiles128 * Hq;
@@ -198,12 +203,11 @@ cudaError_t launch_packed_bwd_d(const PackedBwdArgs& a, cudaStream_t stream) {
   const long long ws_rows = packed_ws_rows(a.nseq, a.total);
   const int sms = sm_count();
   const long long pairs = lay.cap[kKeyList] * a.Hq;
-  packed_preprocess_kernel<D><<<(unsigned)(pairs < 8LL * sms ? pairs : 8LL * sms), 256, 0,
-                                stream>>>(
+  cudaError_t e = launch_early(
+      packed_preprocess_kernel<D>, (unsigned)(pairs < 8LL * sms ? pairs : 8LL * sms), 256, 0, stream,
       static_cast<const __nv_bfloat16*>(a.O), static_cast<const __nv_bfloat16*>(a.dO), a.L,
       static_cast<const uint8_t*>(a.plan), (long long)lay.off[kKeyList], a.ws_nD, a.ws_nL2, ws_rows,
-      a.total, a.nseq, a.Hq, a.d);
-  cudaError_t e = cudaGetLastError();
+      a.total, a.nseq, a.Hq, a.d, pairs < sms ? 1 : 0);
   if (e != cudaSuccess) return e;
 
   CUtensorMap mq, mk, mv, mdo, ml2, md, mdq, mdk, mdv;
@@ -255,9 +259,9 @@ cudaError_t launch_packed_bwd_d(const PackedBwdArgs& a, cudaStream_t stream) {
                            smem);
   if (e != cudaSuccess) return e;
   const long long items = pairs + lay.cap[kKeyList] * a.Hkv;
-  bwd_kernel<D, PackedBwd><<<(unsigned)(items < sms ? items : sms), KvCfg<D>::THREADS, smem,
-                             stream>>>(mq, mk, mv, mdo, ml2, md, mdq, mdk, mdv, p, g);
-  return cudaGetLastError();
+  g.trigger = items < sms;  // see launch_as
+  return launch_early(bwd_kernel<D, PackedBwd>, (unsigned)(items < sms ? items : sms),
+                      KvCfg<D>::THREADS, smem, stream, mq, mk, mv, mdo, ml2, md, mdq, mdk, mdv, p, g);
 }
 
 }  // namespace

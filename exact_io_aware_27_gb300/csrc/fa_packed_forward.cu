@@ -19,6 +19,7 @@
 // kForeignTail), and query rows past the end stay in their own TMEM lanes and are
 // not stored.
 #include "fa_forward.cuh"
+#include "fa_launch.h"
 #include "fa_packed.cuh"
 
 namespace fa {
@@ -35,6 +36,7 @@ struct Packed {
     long long off_list;           // the list's place in the plan
     int total, nseq, Hq, per_kv, causal, group, fill;
     int list, head_shift;         // tiles of 256 >> list rows; heads = 1 << head_shift
+    int trigger;
   };
   struct View {
     const Params& p;
@@ -50,7 +52,8 @@ struct Packed {
     int h;       // first query head
   };
   FA_DEV static unsigned int* status() { return &g_packed_status; }
-  static constexpr bool kSplit = false, kAlternate = false;
+  FA_DEV static bool trigger(const Params& p) { return p.trigger; }
+  static constexpr bool kSplit = false, kAlternate = false, kEarly = true;
   static constexpr bool kForeignTail = true;
   FA_DEV static int items(const View& g) { return g.tiles * (g.p.Hq >> g.p.head_shift); }
   FA_DEV static Item item(const View& g, int i) {
@@ -166,8 +169,9 @@ cudaError_t launch_packed_d(const PackedFwdArgs& a, cudaStream_t stream) {
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const long long items = lay.cap[sh] * (a.Hq >> sh);
   const unsigned grid = (unsigned)(items < sms ? items : sms);
-  fwd_kernel<D, Packed><<<grid, C::THREADS, C::SMEM, stream>>>(mq, mk, mv, mo, p, g);
-  return cudaGetLastError();
+  g.trigger = (int)grid < sms;  // see launch_as
+  return launch_early(fwd_kernel<D, Packed>, grid, C::THREADS, C::SMEM, stream, mq, mk, mv, mo, p,
+                      g);
 }
 
 }  // namespace

@@ -11,6 +11,7 @@
 // One block of 1024 threads: a plan serves every layer that runs the batch.
 // Bounds that are not 0 = cu[0] <= cu[1] <= ... <= cu[nseq] <= total give empty
 // lists and raise kDeviceIndexBit.
+#include "fa_launch.h"
 #include "fa_packed.h"
 #include "sm103.cuh"
 
@@ -70,6 +71,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const int* __restrict__ 
   __shared__ int longest_seq;
   const int tid = threadIdx.x;
   PlanHead* head = reinterpret_cast<PlanHead*>(plan);
+  grid_wait();
+  grid_launch_dependents();
 
   int bad = 0;
   for (int i = tid; i < nseq; i += kThreads) bad |= cu[i] > cu[i + 1] ? 1 : 0;
@@ -154,9 +157,8 @@ static_assert(kWorkspaceRowAlign == 128, "workspace rows are counted in 128-row 
 
 cudaError_t launch_packed_plan(const int* cu_seqlens, int nseq, int total, int causal, void* plan,
                                cudaStream_t s) {
-  plan_kernel<<<1, kThreads, 0, s>>>(cu_seqlens, nseq, total, causal,
-                                     static_cast<uint8_t*>(plan), plan_layout(nseq, total));
-  return cudaGetLastError();
+  return launch_early(plan_kernel, 1, kThreads, 0, s, cu_seqlens, nseq, total, causal,
+                      static_cast<uint8_t*>(plan), plan_layout(nseq, total));
 }
 
 cudaError_t plan_read_status(unsigned int* out) {

@@ -22,6 +22,7 @@
 // read on the device; nothing depends on the order in which workers finish.
 #include "fa_decode.h"
 #include "fa_forward.cuh"
+#include "fa_launch.h"
 
 namespace fa {
 
@@ -187,9 +188,10 @@ struct Prefix {
     int pair, hk, k0, m;  // tile pair, head, first key, keys
     unsigned slot;
   };
-  static constexpr bool kSplit = true, kAlternate = ONE_TILE;
+  static constexpr bool kSplit = true, kAlternate = ONE_TILE, kEarly = true;
   static constexpr bool kForeignTail = true;
   FA_DEV static unsigned int* status() { return &g_prefix_status; }
+  FA_DEV static bool trigger(const Params&) { return true; }  // for the own kernel
   FA_DEV static View view(const Params& p) {
     const int n = __ldg(p.len);
     if ((n < 0 || n > p.cap) && blockIdx.x == 0 && threadIdx.x == 0)
@@ -770,6 +772,8 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
   const int hk = ht / s.row_tiles, rt = ht - hk * s.row_tiles;
   const int rows = min(16, s.per_kv - rt * 16);
   const int own_cap = p.max_pages << p.page_shift;
+  grid_wait();
+  grid_launch_dependents();
   const int len = __ldg(p.lens + b), plen = p.prefix_len ? __ldg(p.prefix_len) : 0;
   if (len < 0 || len > own_cap || plen < 0 || plen > p.prefix_cap)
     if (threadIdx.x == 0) atomicOr(&g_prefix_status, kDeviceIndexBit);
@@ -904,6 +908,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, WARPS == 1 ? 4 : 1) join_kern
   const int row = WARPS == 1 ? blockIdx.x * kJoinWarps + warp : blockIdx.x;
   const int mine = WARPS == 1 ? 0 : warp;  // this warp of the row's
   grid_wait();
+  grid_launch_dependents();
   if (row >= s.B * s.Hq) return;  // WARPS == 1 only: no barrier follows
   const int b = row / s.Hq, hq = row - b * s.Hq;
   const int hk = hq / s.per_kv, in = hq - hk * s.per_kv;
@@ -1023,30 +1028,6 @@ int decode_sms() {
   return sms < kMaxSms ? sms : kMaxSms;
 }
 
-// An ordinary launch, or one that may start while the stream's previous kernel runs.
-template <class K, class P>
-cudaError_t launch(K kernel, unsigned grid, int threads, int smem, cudaStream_t stream, bool early,
-                   const P& params, unsigned cluster = 1) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2] = {};
-  if (early) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cluster > 1) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attr[cfg.numAttrs].val.clusterDim.x = cluster;
-    attr[cfg.numAttrs].val.clusterDim.y = 1;
-    attr[cfg.numAttrs++].val.clusterDim.z = 1;
-  }
-  cfg.attrs = attr;
-  return cudaLaunchKernelEx(&cfg, kernel, params);
-}
-
 // Blocks per unit with which the whole kernel is expected to beat the three kernels, or
 // 0 where it is not, from the capacities (the lengths are known on the device only). Both
 // forms were timed at 72 points (8, 2 and 1 key/value heads of 4, 4 and 16 rows, 1 to 64
@@ -1122,8 +1103,8 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
     e = cudaFuncSetAttribute(whole_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              WholeCfg<D>::BYTES);
     if (e != cudaSuccess) return e;
-    return launch(whole_kernel<D>, (unsigned)(s.Hkv * s.row_tiles * s.B) * cluster,
-                  32 * kWholeWarps, WholeCfg<D>::BYTES, stream, false, w, cluster);
+    return launch_as(whole_kernel<D>, (unsigned)(s.Hkv * s.row_tiles * s.B) * cluster,
+                     32 * kWholeWarps, WholeCfg<D>::BYTES, stream, true, cluster, w);
   }
   if (a.prefix_cap > 0) {
     PrefixParams g;
@@ -1155,8 +1136,8 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
     auto kernel = one_tile ? fwd_kernel<D, Prefix<true>> : fwd_kernel<D, Prefix<false>>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    kernel<<<prefix_grid, C::THREADS, C::SMEM, stream>>>(mq, mk, mv, mk, p, g);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_early(kernel, prefix_grid, C::THREADS, C::SMEM, stream, mq, mk, mv, mk, p, g);
+    if (e != cudaSuccess) return e;
   }
   OwnParams op;
   op.s = s;
@@ -1175,7 +1156,8 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
   e = cudaFuncSetAttribute(own_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            OwnCfg<D>::RINGS + (kMaxBatch + 1) * 4);
   if (e != cudaSuccess) return e;
-  e = launch(own_kernel<D>, own_grid, 32 * kOwnWarps, own_smem, stream, a.prefix_cap > 0, op);
+  // Beside the prefix kernel, which has waited for what comes before it in the stream.
+  e = launch_as(own_kernel<D>, own_grid, 32 * kOwnWarps, own_smem, stream, a.prefix_cap > 0, 1, op);
   if (e != cudaSuccess) return e;
   JoinParams jp;
   jp.s = s;
@@ -1186,9 +1168,9 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
   // A warp per row once there is a row for every fourth warp slot of the GPU's SMs.
   const int rows = a.B * a.Hq;
   return rows >= sms * 4
-             ? launch(join_kernel<1>, (unsigned)ceil_div(rows, kJoinWarps), 32 * kJoinWarps, 0,
-                      stream, true, jp)
-             : launch(join_kernel<kJoinWarps>, (unsigned)rows, 32 * kJoinWarps, 0, stream, true, jp);
+             ? launch_early(join_kernel<1>, (unsigned)ceil_div(rows, kJoinWarps), 32 * kJoinWarps,
+                            0, stream, jp)
+             : launch_early(join_kernel<kJoinWarps>, (unsigned)rows, 32 * kJoinWarps, 0, stream, jp);
 }
 
 }  // namespace

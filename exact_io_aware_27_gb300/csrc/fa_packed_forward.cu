@@ -28,16 +28,22 @@ __device__ unsigned int g_packed_status;
 
 namespace {
 
+// ONE_TILE: an item is one 128-row tile instead of a pair, and both softmax groups work on
+// it, each on every other 64 keys (the forward kernel's kAlternate): for batches with
+// fewer tile pairs than SMs, whose time is that of the longest item.
+struct PackedParams {
+  const uint8_t* plan;
+  float* L;
+  __nv_bfloat16* O;
+  long long off_list;           // the list's place in the plan
+  int total, nseq, Hq, per_kv, causal, group, fill;
+  int list, head_shift;         // tiles of 256 >> list rows; heads = 1 << head_shift
+  int trigger;
+};
+
+template <bool ONE_TILE>
 struct Packed {
-  struct Params {
-    const uint8_t* plan;
-    float* L;
-    __nv_bfloat16* O;
-    long long off_list;           // the list's place in the plan
-    int total, nseq, Hq, per_kv, causal, group, fill;
-    int list, head_shift;         // tiles of 256 >> list rows; heads = 1 << head_shift
-    int trigger;
-  };
+  using Params = PackedParams;
   struct View {
     const Params& p;
     int tiles, covered;
@@ -53,7 +59,7 @@ struct Packed {
   };
   FA_DEV static unsigned int* status() { return &g_packed_status; }
   FA_DEV static bool trigger(const Params& p) { return p.trigger; }
-  static constexpr bool kSplit = false, kAlternate = false, kEarly = true;
+  static constexpr bool kSplit = false, kAlternate = ONE_TILE, kEarly = true;
   static constexpr bool kForeignTail = true;
   FA_DEV static int items(const View& g) { return g.tiles * (g.p.Hq >> g.p.head_shift); }
   FA_DEV static Item item(const View& g, int i) {
@@ -64,7 +70,7 @@ struct Packed {
   }
   // First query of tile t, within the sequence.
   FA_DEV static int tile_query(const View& g, const Item& it, int t) {
-    return (2 * it.s.z + t) * (128 >> g.p.head_shift);
+    return (ONE_TILE ? it.s.z : 2 * it.s.z + t) * (128 >> g.p.head_shift);
   }
   FA_DEV static int query(const View& g, const Item& it, int t, int row) {
     return tile_query(g, it, t) + (row >> g.p.head_shift);
@@ -73,7 +79,8 @@ struct Packed {
     const int q0 = tile_query(g, it, t), n = it.s.y;
     if (q0 >= n) return 0;
     const int last = min(q0 + (128 >> g.p.head_shift), n) - 1;
-    return (g.p.causal ? last : n - 1) / 64 + 1;
+    const int halves = (g.p.causal ? last : n - 1) / 64 + 1;
+    return ONE_TILE ? (halves + 1 - t) / 2 : halves;
   }
   FA_DEV static int keys(const View&, const Item& it) { return it.s.y; }
   FA_DEV static int causal(const View& g) { return g.p.causal; }
@@ -113,6 +120,45 @@ struct Packed {
       g.p.L[(size_t)(it.h + (lane & ((1 << sh) - 1))) * g.p.total + row0 + (lane >> sh)] =
           (m_ref + lg2(l)) * kLn2;
   }
+  // The same from the two halves of the keys: (m, l) = s0 with O in columns ocol, s1 with
+  // O in ocol + D (nothing there where `second` is false). The join is written back over
+  // group t's half of the columns [t D/2, (t + 1) D/2), which that group stores.
+  template <int D>
+  FA_DEV static void store_joined(const View& g, const Item& it, int t, int warp, int lane,
+                                  uint32_t ocol, float2 s0, float2 s1, bool second,
+                                  uint8_t* stage, const CUtensorMap* mo, int d) {
+    const int sh = g.p.head_shift, q0 = tile_query(g, it, t) + ((warp * 32) >> sh);
+    const int row0 = it.s.x + q0, valid = (it.s.y - q0) << sh;
+    const float m = second ? fmaxf(s0.x, s1.x) : s0.x;
+    const float ref = m == -INFINITY ? 0.f : m;
+    const float f0 = ex2(s0.x - ref), f1 = second ? ex2(s1.x - ref) : 0.f;
+    const float l = second ? s0.y * f0 + s1.y * f1 : s0.y * f0;
+    const uint32_t mine = ocol + t * (D / 2);
+    if (valid > 0) {  // warp-uniform
+#pragma unroll
+      for (int c = 0; c < D / 2; c += 32) {
+        uint32_t x[32], y[32];
+        tmem_ld32(mine + c, x);
+        if (second) tmem_ld32(mine + D + c, y);
+        tmem_ld_wait();
+        reg_fence32(x);
+        if (second) reg_fence32(y);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          float v = __uint_as_float(x[e]) * f0;
+          if (second) v += __uint_as_float(y[e]) * f1;
+          x[e] = __float_as_uint(v);
+        }
+        tmem_st32(mine + c, x);
+      }
+      tmem_st_wait();
+    }
+    packed_rows_store<D / 2>(mine, 1.f / l, stage, mo, it.h, row0, valid, t * (D / 2), d, g.p.O,
+                             (long long)g.p.Hq * d, sh);
+    if (t == 0 && lane < valid)
+      g.p.L[(size_t)(it.h + (lane & ((1 << sh) - 1))) * g.p.total + row0 + (lane >> sh)] =
+          (ref + lg2(l)) * kLn2;
+  }
   // Rows that no sequence covers: O = 0 and L = -inf (what attention to no key
   // gives), where the caller asked for it.
   FA_DEV static void idle_warps(const View& g, int thread, int threads, int d) {
@@ -132,8 +178,19 @@ template <int D>
 cudaError_t launch_packed_d(const PackedFwdArgs& a, cudaStream_t stream) {
   using C = FwdCfg<D>;
   CUtensorMap mq, mk, mv, mo;
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   int sh = 0;  // heads that share a tile: 1 << sh
   while (sh < 3 && a.Hq / a.Hkv % (2 << sh) == 0) ++sh;
+  // Fewer pairs than SMs (the sequences' last pairs aside): single tiles. There is no list
+  // of 16-row tiles. One sequence of 2000 rows, 8/1 heads, d = 128: 21.7 us in single tiles,
+  // 31.9 in pairs; 4000 rows, 4/1 heads: 36.2, 58.3; three of 1000, 8/2, d = 64: 11.8, 16.4.
+  // Short sequences have few keys to share out, and the join costs: one of 472 rows, 32/8,
+  // 11.1 and 11.7; eight of 100, 16/8, 8.6 and 7.8. So from a mean length of 512.
+  const bool one = (long long)ceil_div(a.total, 256 >> sh) * (a.Hq >> sh) < sms &&
+                   a.total / 512 >= a.nseq;
+  if (one && sh == 3) sh = 2;
   if (make_bf16_packed_map(&mq, a.Q, a.total, a.Hq, a.d, a.ldq, C::BM >> sh, 1 << sh) !=
           CUDA_SUCCESS ||
       make_bf16_packed_map(&mk, a.K, a.total, a.Hkv, a.d, a.ldk, C::BN) != CUDA_SUCCESS ||
@@ -144,7 +201,7 @@ cudaError_t launch_packed_d(const PackedFwdArgs& a, cudaStream_t stream) {
   FwdParams p;
   p.d = a.d;
   p.scale_log2 = a.scale * 1.44269504088896340736f;
-  Packed::Params g;
+  PackedParams g;
   g.plan = static_cast<const uint8_t*>(a.plan);
   g.L = a.L;
   g.O = static_cast<__nv_bfloat16*>(a.O);
@@ -154,24 +211,28 @@ cudaError_t launch_packed_d(const PackedFwdArgs& a, cudaStream_t stream) {
   g.per_kv = a.Hq / a.Hkv;
   g.causal = a.causal;
   g.fill = a.fill;
-  g.list = sh;
+  const int list = sh + (one ? 1 : 0);
+  g.list = list;
   g.head_shift = sh;
   const PlanLayout lay = plan_layout(a.nseq, a.total);
-  g.off_list = (long long)lay.off[sh];
-  // Whole key/value heads per group. The plan's tile count is known on the device
-  // only; the rows give it up to the sequences' last tiles.
-  g.group = round_up(heads_per_group(a.Hq >> sh, ceil_div(a.total, 256 >> sh)), g.per_kv >> sh);
-  cudaError_t e = cudaFuncSetAttribute(fwd_kernel<D, Packed>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  g.off_list = (long long)lay.off[list];
+  // Whole key/value heads per group: as many as fill eight waves (the plan's tile count is
+  // known on the device only; the rows give it up to the sequences' last tiles), or all
+  // whose K and V fit half of L2: the fewer groups, the better the deal comes out (16384
+  // rows, 32/8 heads, d = 128 in two groups: the busiest CTA had 14 % more than the mean).
+  const long long fit = (64LL << 20) / ((long long)a.total * a.d * 4);
+  const int heads = a.Hq >> sh;
+  g.group = round_up(heads_per_group(heads, ceil_div(a.total, 256 >> list)), g.per_kv >> sh);
+  if (fit * (g.per_kv >> sh) > g.group)
+    g.group = fit >= a.Hkv ? heads : (int)fit * (g.per_kv >> sh);
+  auto kernel = one ? fwd_kernel<D, Packed<true>> : fwd_kernel<D, Packed<false>>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const long long items = lay.cap[sh] * (a.Hq >> sh);
+  const long long items = lay.cap[list] * heads;
   const unsigned grid = (unsigned)(items < sms ? items : sms);
   g.trigger = (int)grid < sms;  // see launch_as
-  return launch_early(fwd_kernel<D, Packed>, grid, C::THREADS, C::SMEM, stream, mq, mk, mv, mo, p,
-                      g);
+  return launch_early(kernel, grid, C::THREADS, C::SMEM, stream, mq, mk, mv, mo, p, g);
 }
 
 }  // namespace

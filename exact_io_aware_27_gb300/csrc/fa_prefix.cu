@@ -343,7 +343,7 @@ struct Prefix {
   template <int D>
   FA_DEV static void store_joined(const View& g, const Item& it, int t, int warp, int lane,
                                   uint32_t ocol, float2 s0, float2 s1, bool second,
-                                  uint8_t* stage, int d) {
+                                  uint8_t* stage, const CUtensorMap*, int d) {
     const DecodeSizes& s = g.p.s;
     const int rows = tile_rows(g, it, 0) - warp * 32;
     if (rows <= 0) return;  // warp-uniform

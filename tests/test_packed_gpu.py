@@ -56,10 +56,20 @@ def test_forward_heads_and_dims(hq, hkv, d):
     _check(q, k, v, cu, lens, True, scale=0.3)
 
 
-def test_forward_many_items_per_cta():
+@pytest.mark.parametrize("hq,hkv,d", [(16, 4, 64), (16, 2, 128)])
+def test_forward_many_items_per_cta(hq, hkv, d):
     lens = [(37 * i) % 400 + 1 for i in range(90)]
-    q, k, v, _, cu = packed_inputs(lens, 16, 4, 64, 77)
+    q, k, v, _, cu = packed_inputs(lens, hq, hkv, d, 77)
     _check(q, k, v, cu, lens, True)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 1, 128), (2, 1, 64), (1, 1, 128)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_forward_long_sequences_of_few_heads(hq, hkv, d, causal):
+    """Fewer row tiles than SMs."""
+    lens = [1500, 1, 63, 700]
+    q, k, v, _, cu = packed_inputs(lens, hq, hkv, d, 83, rest=3)
+    _check(q, k, v, cu, lens, causal)
 
 
 def test_forward_matches_dense():

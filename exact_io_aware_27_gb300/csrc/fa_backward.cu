@@ -26,16 +26,21 @@ struct DenseBwd {
   FA_DEV static View view(const Params& g) { return g; }
   FA_DEV static unsigned int* status() { return &g_bwd_status; }
   FA_DEV static int causal(const Params& g) { return g.causal; }
-  FA_DEV static int heads(const Params&) { return 1; }
-  FA_DEV static int kv_items(const Params& g) { return g.n_kv; }
-  FA_DEV static int q_items(const Params& g) { return g.n_dq; }
+  // Each list is dealt in snake order; the query blocks in reverse CTA order, so that
+  // the CTAs left with one key block more get no query block more.
+  FA_DEV static int kv_count(const Params& g, int c, int P) { return snake_count(g.n_kv, c, P); }
+  FA_DEV static int q_count(const Params& g, int c, int P) {
+    return snake_count(g.n_dq, P - 1 - c, P);
+  }
   FA_DEV static void finish(const Params&, int) {}
 
   // Key blocks near 0 carry the most work under causal masking: the launch order puts
   // rank 0 first, heads a group at a time so that the blocks in flight share L2.
-  FA_DEV static KvItem kv_item(const Params& g, int i) {
+  FA_DEV static int kv_rank(const Params&, int, int, int) { return 0; }
+  FA_DEV static int q_rank(const Params&, int, int, int) { return 0; }
+  FA_DEV static KvItem kv_item(const Params& g, int t, int, int c, int P) {
     int ktile, bh;
-    grouped_tile(i, g.BH, g.ktiles, g.kgroup, ktile, bh);
+    grouped_tile(snake_item(t, c, P), g.BH, g.ktiles, g.kgroup, ktile, bh);
     return {ktile * 128, bh};
   }
   FA_DEV static int first_key(const KvItem& it) { return it.ks; }
@@ -46,6 +51,10 @@ struct DenseBwd {
     const int i0 = g.causal ? it.ks / 128 : 0;
     q_first = i0 * 128;
     return 2 * max(0, (g.n + 127) / 128 - i0);
+  }
+  FA_DEV static int kv_part(const Params&, const KvItem&, int per, int& first) {
+    first = 0;
+    return per;
   }
   FA_DEV static void load_keys(void* dst, const CUtensorMap* map, uint64_t* f, int col,
                                const Params&, const KvItem& it) {
@@ -75,9 +84,9 @@ struct DenseBwd {
 
   // Under causal masking the last query blocks see the most keys: the launch order
   // puts them first.
-  FA_DEV static QItem q_item(const Params& g, int i) {
+  FA_DEV static QItem q_item(const Params& g, int t, int, int c, int P) {
     int rank, bh;
-    grouped_tile(i, g.BH, g.qtiles, g.qgroup, rank, bh);
+    grouped_tile(snake_item(t, P - 1 - c, P), g.BH, g.qtiles, g.qgroup, rank, bh);
     return {(g.causal ? g.qtiles - 1 - rank : rank) * 128, bh};
   }
   FA_DEV static int first_query(const QItem& it) { return it.q0; }

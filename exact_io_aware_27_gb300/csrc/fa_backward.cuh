@@ -45,8 +45,10 @@
 //
 // The gradient kernel is shared by the dense pass and the pass over packed sequences,
 // which differ in a geometry G: Params (a kernel argument), View (what the functions
-// get), KvItem and QItem (a key block and a query block), and the functions that say
-// where an item's rows come from and go to. With kForeignTail the rows past an item's
+// get), KvItem and QItem (a key block, or a part of one's queries, and a query block),
+// kv_count and q_count (how many of each a CTA works on), kv_item and q_item (its t-th;
+// kv_rank and q_rank are read an item earlier, so that no role waits for two loads in a
+// row), and the functions that say where an item's rows come from and go to. With kForeignTail the rows past an item's
 // last query or key hold foreign values and are replaced by zeros; without it TMA has
 // read zeros there. With kEarly it is launched with launch_early (fa_launch.h).
 #pragma once
@@ -242,7 +244,7 @@ __device__ __forceinline__ void tile_row_to_tmem(const uint8_t* tile, int r, uin
   tmem_st_wait();
 }
 
-// Key blocks snake_item(t, c, P) (t < count) in launch order, by CTA c.
+// CTA c's key blocks (its items t < count).
 template <int D, class G>
 __device__ __forceinline__ void dkdv_run(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                          const CUtensorMap& tmV, const CUtensorMap& tmdO,
@@ -275,11 +277,16 @@ __device__ __forceinline__ void dkdv_run(const CUtensorMap& tmQ, const CUtensorM
   }
   __syncthreads();
   using Item = typename G::KvItem;
-  auto fetch = [&](int t) { return G::kv_item(g, snake_item(t, c, P)); };
-  // The queries of a block: `heads` query heads read its keys (more than one with
-  // grouped heads), and of each the `per` halves of 64 queries from q_first on. Half u
-  // of the block is half u % per of query head u / per.
-  const int heads = G::heads(g);
+  // Item t, and what item t + 1 needs to know from memory to be looked up in turn.
+  int ahead = G::kv_rank(g, 0, c, P);
+  auto fetch = [&](int t) {
+    const int rank = ahead;
+    if (t + 1 < count) ahead = G::kv_rank(g, t + 1, c, P);
+    return G::kv_item(g, t, rank, c, P);
+  };
+  // The queries of a block: of each query head that reads its keys (more than one with
+  // grouped heads) the `per` halves of 64 queries from q_first on. Half u of the block is
+  // half u % per of query head u / per; an item is nu of them, from half `first` on.
   // Ring uses: per block one for its K, then one per half. `ru` counts them, `hu` the
   // halves (half number v = hu + u uses S^T region v & 1) and `at` the blocks with
   // work, identically in every role.
@@ -300,6 +307,8 @@ __device__ __forceinline__ void dkdv_run(const CUtensorMap& tmQ, const CUtensorM
         int q_first;
         const int per = G::kv_halves(g, it, q_first);
         if (per == 0) continue;
+        int first;
+        const int nu = G::kv_part(g, it, per, first);
         // V into buffer at % 2, free once block at-2's products are done
         const int vb = at & 1;
         if (at >= 2 && !mbar_wait(&bar[C::B_ACC + vb], ((at >> 1) & 1) ^ 1, wc)) break;
@@ -308,8 +317,8 @@ __device__ __forceinline__ void dkdv_run(const CUtensorMap& tmQ, const CUtensorM
         for (int c = 0; c < C::KCH; ++c)
           G::load_keys(smem + C::OFF_V + vb * C::TILE + c * C::CHUNK, &tmV, &bar[C::B_VF + vb],
                        c * 64, g, it);
-        int hd = 0, uu = 0;  // query head and half of it
-        for (int u = -1; u < heads * per; ++u, ++ru) {
+        int hd = first / per, uu = first % per;  // query head and half of it
+        for (int u = -1; u < nu; ++u, ++ru) {
           const int s = ru % C::STAGES;
           if (ru >= C::STAGES &&
               !mbar_wait(&bar[C::B_QE + s], ((ru / C::STAGES) & 1) ^ 1, wc)) {
@@ -357,9 +366,10 @@ __device__ __forceinline__ void dkdv_run(const CUtensorMap& tmQ, const CUtensorM
     for (int t = 0; ok && t < count; ++t) {
       const Item it = nxt;
       if (t + 1 < count) nxt = fetch(t + 1);
-      int q_first;
-      const int nu = heads * G::kv_halves(g, it, q_first);
-      if (nu == 0) continue;
+      int q_first, first;
+      const int per = G::kv_halves(g, it, q_first);
+      if (per == 0) continue;
+      const int nu = G::kv_part(g, it, per, first);
       const int rb = ru + 1;  // ring use of half 0
       // K is in TMEM (its slot may be refilled), V landed, halves 0 and 1 landed
       if (!warp_wait(&bar[C::B_IN], at & 1, wc)) break;
@@ -470,7 +480,8 @@ __device__ __forceinline__ void dkdv_run(const CUtensorMap& tmQ, const CUtensorM
         if (t + 1 < count) nxt = fetch(t + 1);
         continue;
       }
-      const int nu = heads * per, rows = G::rows(g, it);
+      int first;
+      const int nu = G::kv_part(g, it, per, first), rows = G::rows(g, it);
       // K of this block into TMEM. The previous block's S^T products, the only
       // readers of these columns, are complete: both groups waited for all of them.
       if (w == 0) {
@@ -483,7 +494,7 @@ __device__ __forceinline__ void dkdv_run(const CUtensorMap& tmQ, const CUtensorM
       // The previous block's dK, dV leave TMEM while this block's first products run.
       if (at >= 1 && !epilogue(at - 1, prev)) { ok = false; break; }
       const int rb = ru + 1;
-      int uu = 0;  // half of the current query head
+      int uu = first % per;  // half of the current query head
       for (int u = 0; ok && u < nu; ++u) {
         const int v = hu + u, h = v & 1;           // S^T region
         const int s = (rb + u) % C::STAGES;
@@ -612,7 +623,7 @@ struct QCfg {
   static_assert(SMEM <= 232448 - 64, "shared memory budget");
 };
 
-// Query blocks snake_item(t, c, P) (t < count) in launch order, by CTA c.
+// CTA c's query blocks (its items t < count).
 template <int D, class G>
 __device__ __forceinline__ void dq_run(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                        const CUtensorMap& tmV, const CUtensorMap& tmdO,
@@ -641,7 +652,12 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmQ, const CUtensorMap
   }
   __syncthreads();
   using Item = typename G::QItem;
-  auto fetch = [&](int t) { return G::q_item(g, snake_item(t, c, P)); };
+  int ahead = G::q_rank(g, 0, c, P);
+  auto fetch = [&](int t) {
+    const int rank = ahead;
+    if (t + 1 < count) ahead = G::q_rank(g, t + 1, c, P);
+    return G::q_item(g, t, rank, c, P);
+  };
   // Ring uses: per block one for its Q and dO, then one per key block. `ru` counts
   // them, `gb` the key blocks and `at` the query blocks with work, in every role.
 
@@ -899,10 +915,9 @@ struct BwdSmem {
 };
 
 // The gradient kernel: one CTA per SM (persistent). The key blocks and then the
-// query blocks are dealt out in rounds of P = grid size items (CTA c takes
-// snake_item(r, c, P) of round r), so that each CTA runs its share of the dK/dV
-// pass and then of the dQ pass; the lists are in launch order (heaviest blocks
-// first within a group of heads).
+// query blocks are dealt out in rounds of P = grid size items, so that each CTA runs its
+// share of the dK/dV pass and then of the dQ pass; the lists are in launch order
+// (heaviest blocks first within a group of heads).
 template <int D, class G>
 __global__ void __launch_bounds__(384, 1)
     bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -943,18 +958,13 @@ __global__ void __launch_bounds__(384, 1)
     if (G::trigger(gp)) grid_launch_dependents();
   }
   typename G::View g = G::view(gp);
-  const int n_kv = G::kv_items(g), n_dq = G::q_items(g);
   const int P = gridDim.x, c = blockIdx.x;
-  // Each list is dealt separately; the query blocks in reverse CTA order, so that
-  // the CTAs left with one key block more get no query block more.
-  int kv_rounds = 0, dq_rounds = 0;
-  while (snake_item(kv_rounds, c, P) < n_kv) ++kv_rounds;
-  while (snake_item(dq_rounds, P - 1 - c, P) < n_dq) ++dq_rounds;
+  const int kv_rounds = G::kv_count(g, c, P), dq_rounds = G::q_count(g, c, P);
   if (kv_rounds > 0)
     dkdv_run<D, G>(tmQ, tmK, tmV, tmdO, tmNL2, tmND, tmdK, tmdV, p, g, smem, tmem, c, P,
                    kv_rounds, wc);
   if (dq_rounds > 0)
-    dq_run<D, G>(tmQ, tmK, tmV, tmdO, tmdQ, p, g, smem, tmem, P - 1 - c, P, dq_rounds, wc);
+    dq_run<D, G>(tmQ, tmK, tmV, tmdO, tmdQ, p, g, smem, tmem, c, P, dq_rounds, wc);
   G::finish(g, p.d);
 
   tc_fence_before();

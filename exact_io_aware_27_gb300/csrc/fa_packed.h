@@ -66,10 +66,74 @@ struct PackedFwdArgs {
   int total, nseq, Hq, Hkv, d, causal, fill;
   float scale;
 };
-// Backward workspace: -D and -L * log2(e), fp32 [Hq, packed_ws_rows] each; a
-// sequence's rows start at its tiles' PlanTile::w.
-inline long long packed_ws_rows(int nseq, int total) {
-  return plan_layout(nseq, total).cap[kKeyList] * kWorkspaceRowAlign;
+
+// The gradient kernel's work on key blocks: all queries of one, or a range of their
+// 64-query halves.
+struct BwdItem {
+  PlanTile s;
+  int head;
+  int first, halves;
+  int slot;  // a part: where its sums go; else -1
+};
+// A key block whose parts' sums, in slots [slot, slot + parts), are joined.
+struct BwdJoin {
+  PlanTile s;
+  int head, slot, parts, pad;
+};
+// How the gradient kernel's items are dealt to its CTAs where key blocks are split (see
+// fa_packed_backward.cu); split_tiles = 0 where none is. A list's item of row t for CTA c is number t P + rank, with a rank per CTA and 1 << shift
+// rows.
+constexpr int kMaxBwdCtas = 192;  // ranks are bytes
+struct BwdDealHead {
+  int parts;        // entries of the table of parts, the first items of the key blocks' list
+  int split_tiles;  // the plan's first key tiles, which they hold
+  int joins;        // split key blocks
+  int shifts;       // of the key blocks' list, and << 8 of the query blocks'
+  int4 cta[kMaxBwdCtas];  // its key blocks and query blocks, its first rank of those, and
+                          // in which row of ranks they start
+};
+// A key block is split where it has more than 5/3 hc halves, into ceil(halves / hc) parts,
+// with hc = max(kMinPart, 6/5 of the batch's halves / kPartShare): a fifth more than what
+// one of 152 SMs gets of the dK/dV pass, which takes some 60 % of the time. At most
+// 2 (the batch's halves) / hc parts exist.
+constexpr int kMinPart = 16, kPartShare = 152, kMaxParts = 256;
+static_assert(kMaxParts >= 2 * 5 * kPartShare / 6, "every part has a slot");
+// The deal and the join cost some 4 us: batches whose key blocks cannot have more halves
+// than this are not split.
+constexpr int kSplitFrom = 32;
+constexpr size_t kPartBytes128 = 2 * 128 * 128 * 4;  // dV and dK of a key block, fp32, d = 128
+
+// Backward workspace: -D and -L * log2(e), fp32 [Hq, rows] each (a sequence's rows start at
+// its tiles' PlanTile::w), the deal's head, the split key blocks, the parts, the ranks and
+// the parts' sums.
+struct PackedBwdLayout {
+  long long rows;
+  size_t nD, nL2, head, joins, items, ranks, parts, bytes;
+  int slots;
+};
+inline PackedBwdLayout packed_bwd_layout(int nseq, int total, int Hq) {
+  const long long cap = plan_layout(nseq, total).cap[kKeyList];
+  PackedBwdLayout l;
+  l.rows = cap * kWorkspaceRowAlign;
+  // A batch has at most cap key blocks of ceil(total / 64) halves per query head.
+  const long long halves = ceil_div(total, 64);
+  const long long most = cap * Hq * halves * 2 / kMinPart;
+  l.slots = halves * Hq <= kSplitFrom ? 0 : (int)(most < kMaxParts ? most : kMaxParts);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t here = at;
+    at = (at + n + 127) / 128 * 128;
+    return here;
+  };
+  l.nD = take((size_t)l.rows * Hq * 4);
+  l.nL2 = take((size_t)l.rows * Hq * 4);
+  l.head = take(sizeof(BwdDealHead));
+  l.joins = take(kMaxParts / 2 * sizeof(BwdJoin));
+  l.items = take(kMaxParts * sizeof(BwdItem));
+  l.ranks = take((size_t)cap * Hq * 2 + kMaxParts + 4 * kMaxBwdCtas);
+  l.parts = take((size_t)l.slots * kPartBytes128);
+  l.bytes = at;
+  return l;
 }
 struct PackedBwdArgs {
   const void *Q, *K, *V, *O, *dO;
@@ -77,7 +141,7 @@ struct PackedBwdArgs {
   long long ldq, ldk, ldv;
   void *dQ, *dK, *dV;
   long long lddq, lddk, lddv;
-  float *ws_nD, *ws_nL2;
+  void* workspace;
   const void* plan;
   int total, nseq, Hq, Hkv, d, causal, fill;
   float scale;

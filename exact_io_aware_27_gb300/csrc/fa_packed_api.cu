@@ -134,7 +134,7 @@ int fa_packed_forward(const void* Q, const void* K, const void* V, long long q_s
 size_t fa_packed_workspace_bytes(int nseq, int total, int Hq) {
   if (check_plan_sizes(nseq, total) != FA_OK || check_heads(nseq, total, Hq, 1, 8) != FA_OK)
     return 0;
-  return (size_t)packed_ws_rows(nseq, total) * Hq * 2 * sizeof(float);
+  return packed_bwd_layout(nseq, total, Hq).bytes;
 }
 
 int fa_packed_backward(const void* Q, const void* K, const void* V, long long q_stride,
@@ -190,8 +190,7 @@ int fa_packed_backward(const void* Q, const void* K, const void* V, long long q_
   a.lddq = dq_stride;
   a.lddk = dk_stride;
   a.lddv = dv_stride;
-  a.ws_nD = static_cast<float*>(workspace);
-  a.ws_nL2 = a.ws_nD + (size_t)packed_ws_rows(nseq, total) * Hq;
+  a.workspace = workspace;
   a.plan = plan;
   a.total = total;
   a.nseq = nseq;

@@ -113,6 +113,12 @@ FA_DEV void grouped_tile(int lin, int BH, int tiles, int group, int& rank, int& 
 // direction so that, with the items in heaviest-first order, every CTA gets about
 // the same total work.
 FA_DEV int snake_item(int r, int c, int P) { return r * P + ((r & 1) ? P - 1 - c : c); }
+// How many of n items CTA c takes.
+FA_DEV int snake_count(int n, int c, int P) {
+  int rounds = 0;
+  while (snake_item(rounds, c, P) < n) ++rounds;
+  return rounds;
+}
 
 // ---------------------------------------------------------------- TMA
 FA_DEV void tma_prefetch_map(const CUtensorMap* map) {

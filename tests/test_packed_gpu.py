@@ -211,6 +211,53 @@ def test_backward_many_items_per_cta(d):
     assert all(torch.equal(a, b) for a, b in zip(first, again))  # no order of atomics
 
 
+@pytest.mark.parametrize("lens,hq,hkv,d", [([1500, 1, 63, 700], 8, 1, 128), ([2100], 4, 2, 64),
+                                           ([700, 30, 1, 900], 6, 2, 40), ([3000], 2, 1, 96)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_backward_long_sequences_of_few_heads(lens, hq, hkv, d, causal):
+    """Few key blocks with many queries each, whose sums come from several SMs."""
+    q, k, v, do, cu = packed_inputs(lens, hq, hkv, d, 183, rest=5)
+    first = _grads(q, k, v, do, cu, lens, causal)
+    again = _grads(q, k, v, do, cu, lens, causal)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_backward_of_few_heads_in_a_graph_and_into_one_buffer():
+    """Gradients with strides, replayed for another batch of the same sizes."""
+    hq, hkv, d, total = 8, 2, 128, 1700
+    cut = [0, hq * d, (hq + hkv) * d, (hq + 2 * hkv) * d]
+    parts = lambda x: [x[:, a:b].unflatten(1, (-1, d)) for a, b in zip(cut, cut[1:])]  # noqa: E731
+    q, k, v, do, cu = packed_inputs([1100, 500], hq, hkv, d, 187, rest=100)
+    wide = torch.cat([x.flatten(1) for x in (q, k, v)], 1)
+    dwide = torch.full_like(wide, 9.0)
+    plan = fa.fa_packed_plan(cu, total)
+    ws = fa.alloc_packed_workspace(plan, hq, d)
+    O, L = torch.zeros_like(q), torch.zeros(hq, total, device="cuda")
+    dq, dk, dv = parts(dwide)
+
+    def step():
+        fa.fa_packed_plan(cu, total, plan=plan)
+        fa.fa_packed_forward(*parts(wide), plan, O=O, L=L)
+        fa.fa_packed_backward(*parts(wide), O, L, do, plan, dQ=dq, dK=dk, dV=dv, workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for lens in ([1100, 500], [20, 1600], [500, 500]):
+        cu.copy_(torch.tensor([0, lens[0], sum(lens)], dtype=torch.int32))
+        dwide.fill_(9.0)
+        ws.fill_(255)  # contents on entry do not matter
+        graph.replay()
+        torch.cuda.synchronize()
+        n = sum(lens)
+        want = packed64(q, k, v, lens, True, None, do)
+        for name, t in zip(("dQ", "dK", "dV"), (dq, dk, dv)):
+            assert_close(name, t[:n], tuple(x[:n] for x in want[name]))
+        assert torch.all(dwide[n:] == 9.0)
+
+
 def test_backward_matches_dense():
     B, n, h, d = 3, 384, 4, 128
     q, k, v, do, cu = packed_inputs([n] * B, h, h, d, 121)

@@ -48,7 +48,8 @@
 // get), KvItem and QItem (a key block, or a part of one's queries, and a query block),
 // kv_count and q_count (how many of each a CTA works on), kv_item and q_item (its t-th;
 // kv_rank and q_rank are read an item earlier, so that no role waits for two loads in a
-// row), and the functions that say where an item's rows come from and go to. With kForeignTail the rows past an item's
+// row), and the functions that say where an item's rows come from and go to. With
+// kForeignTail the rows past an item's
 // last query or key hold foreign values and are replaced by zeros; without it TMA has
 // read zeros there. With kEarly it is launched with launch_early (fa_launch.h).
 #pragma once

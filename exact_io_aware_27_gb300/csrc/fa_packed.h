@@ -81,8 +81,8 @@ struct BwdJoin {
   int head, slot, parts, pad;
 };
 // How the gradient kernel's items are dealt to its CTAs where key blocks are split (see
-// fa_packed_backward.cu); split_tiles = 0 where none is. A list's item of row t for CTA c is number t P + rank, with a rank per CTA and 1 << shift
-// rows.
+// fa_packed_backward.cu); split_tiles = 0 where none is. A list's item of row t for CTA c
+// is number t P + rank, with a rank per CTA and 1 << shift rows.
 constexpr int kMaxBwdCtas = 192;  // ranks are bytes
 struct BwdDealHead {
   int parts;        // entries of the table of parts, the first items of the key blocks' list

@@ -7,10 +7,9 @@
 // has so few key blocks that one would take longer than an SM's share of all the work.
 // Then its queries are split into parts, whose fp32 sums a last kernel joins, in order
 // (one sequence of 4000 rows, 4/1 heads, d = 128: 86 us, 209 unsplit; 2000 rows, 8/1: 54
-// and 220). The statistics
-// -D and -L * log2(e) lie in a workspace in which every sequence starts on a multiple of
-// 128 rows: TMA copies of fp32 rows have to start on 16-byte boundaries, which a
-// sequence's first row in the packed tensors need not do.
+// and 220). The statistics -D and -L * log2(e) lie in a workspace in which every sequence
+// starts on a multiple of 128 rows: TMA copies of fp32 rows have to start on 16-byte
+// boundaries, which a sequence's first row in the packed tensors need not do.
 #include "fa_backward.cuh"
 #include "fa_launch.h"
 #include "fa_packed.cuh"
@@ -159,7 +158,8 @@ struct PackedBwd {
 
   FA_DEV static QItem q_item(const View& g, int t, int rank, int c, int P) {
     int tile, h;
-    grouped_tile(ranked(g) ? t * P + rank : snake_item(t, P - 1 - c, P), g.p.Hq, g.tiles, g.p.qgroup, tile, h);
+    const int i = ranked(g) ? t * P + rank : snake_item(t, P - 1 - c, P);
+    grouped_tile(i, g.p.Hq, g.tiles, g.p.qgroup, tile, h);
     return {__ldg(reinterpret_cast<const PlanTile*>(g.p.plan + g.p.off_q) + tile), h};
   }
   FA_DEV static int first_query(const QItem& it) { return it.s.z * 128; }
@@ -573,7 +573,8 @@ cudaError_t launch_packed_bwd_d(const PackedBwdArgs& a, cudaStream_t stream) {
   deal.q_cost = D == 128 ? 11 : 10;
   cudaError_t e = launch_early(
       split ? packed_preprocess_kernel<D, true> : packed_preprocess_kernel<D, false>,
-      (unsigned)((pairs < 8LL * sms ? pairs : 8LL * sms) + split), 256, 0, stream, static_cast<const __nv_bfloat16*>(a.O), static_cast<const __nv_bfloat16*>(a.dO), a.L,
+      (unsigned)((pairs < 8LL * sms ? pairs : 8LL * sms) + split), 256, 0, stream,
+      static_cast<const __nv_bfloat16*>(a.O), static_cast<const __nv_bfloat16*>(a.dO), a.L,
       static_cast<const uint8_t*>(a.plan), (long long)lay.off[kKeyList], ws_nD, ws_nL2, ws_rows,
       a.total, a.nseq, a.Hq, a.d, pairs < sms ? 1 : 0, deal);
   if (e != cudaSuccess) return e;

@@ -243,9 +243,10 @@ FA_API int fa_online_softmax_stats(const float* x, long long rows, long long col
  * the forward's O and L and a gradient dO; dK and dV sum over the query heads of their
  * key/value head, in a fixed order. `workspace`: caller-owned device memory of at least
  * fa_packed_workspace_bytes() bytes (8 bytes per query head and row, rows counted up to
- * each sequence's next multiple of 128), 16-byte aligned, contents on entry do not
- * matter; calls that may run at the same time need one each. Two kernel launches. Both
- * return FA_OK or a negative fa_status.
+ * each sequence's next multiple of 128, and up to 34 MB for the partial sums of batches
+ * with few key blocks), 16-byte aligned, contents on entry do not matter; calls that may
+ * run at the same time need one each. Two or three kernel launches. Both return FA_OK or
+ * a negative fa_status.
  */
 FA_API size_t fa_packed_plan_bytes(int nseq, int total);
 FA_API int fa_packed_plan(const int* cu_seqlens, int nseq, int total, int causal, void* plan,

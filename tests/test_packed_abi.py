@@ -66,7 +66,9 @@ def test_forward(lib):
 
 
 def test_backward(lib):
-    assert lib.fa_packed_workspace_bytes(3, 1000, 4) == (7 + 3) * 128 * 4 * 8
+    rows = (7 + 3) * 128 * 4 * 8
+    assert rows <= lib.fa_packed_workspace_bytes(3, 1000, 4) <= rows + 34 * 10 ** 6
+    assert lib.fa_packed_workspace_bytes(3, 100, 4) <= (3 * 128 * 4 * 8) + 10 ** 5
     assert lib.fa_packed_workspace_bytes(0, 1000, 4) == 0
     ws = lib.fa_packed_workspace_bytes(3, 100, 8)
 

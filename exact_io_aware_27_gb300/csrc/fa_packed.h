@@ -94,10 +94,10 @@ struct BwdDealHead {
 };
 // A key block is split where it has more than 5/3 hc halves, into ceil(halves / hc) parts,
 // with hc = max(kMinPart, 6/5 of the batch's halves / kPartShare): a fifth more than what
-// one of 152 SMs gets of the dK/dV pass, which takes some 60 % of the time. At most
-// 2 (the batch's halves) / hc parts exist.
+// one of 152 SMs gets of the dK/dV pass, which takes some 60 % of the time. With W halves
+// in the batch, W / hc <= 5/6 kPartShare and there are at most 8/5 W / hc parts.
 constexpr int kMinPart = 16, kPartShare = 152, kMaxParts = 256;
-static_assert(kMaxParts >= 2 * 5 * kPartShare / 6, "every part has a slot");
+static_assert(kMaxParts >= 8 * kPartShare / 6, "every part has a slot");
 // The deal and the join cost some 4 us: batches whose key blocks cannot have more halves
 // than this are not split.
 constexpr int kSplitFrom = 32;

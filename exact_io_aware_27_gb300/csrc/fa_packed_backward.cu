@@ -266,11 +266,12 @@ __device__ __noinline__ void deal_items(const DealArgs& a, int tiles) {
   const int hc = (int)max((long long)kMinPart, min(share, 0x7fffffffLL));
 
   // The tiles to split are the list's first: it is in order of their 128-query blocks, so up
-  // to one half. (The ones before the last of them that have a half less are split, too,
-  // or stay whole as one part; they have more than hc / 2 halves.)
+  // to one half. (The ones before the last of them that have a half less stay whole, as one
+  // part: what is split does not depend on the order of equals, which is not fixed. They
+  // have more than 5/6 hc halves.)
   int last = 0;
   for (int e = tid; e < tiles; e += T)
-    if ((long long)(e < CACHED ? kv_work[e] : halves(__ldg(kv + e))) * per_kv > hc * 5LL / 3)
+    if ((long long)(e < CACHED ? kv_work[e] : halves(__ldg(kv + e))) * per_kv * 3 > hc * 5LL)
       last = e + 1;
   if (last > 0) atomicMax(&split_tiles, last);
   __syncthreads();
@@ -284,7 +285,7 @@ __device__ __noinline__ void deal_items(const DealArgs& a, int tiles) {
       it.head = tid % a.Hkv;
       it.s = __ldg(kv + tid / a.Hkv);
       it.halves = halves(it.s) * per_kv;
-      parts = (it.halves - 1) / hc + 1;
+      parts = it.halves * 3LL > hc * 5LL ? (it.halves - 1) / hc + 1 : 1;
     }
     // Items in bits 0..9, slots in 10..19, joins in 20..29.
     const unsigned add = parts > 1 ? (unsigned)parts * 1025u + (1u << 20) : (unsigned)parts;

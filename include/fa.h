@@ -231,7 +231,7 @@ FA_API int fa_online_softmax_stats(const float* x, long long rows, long long col
  * bytes, 16-byte aligned). One plan serves any number of calls on that batch, of any
  * head counts, until it is written again; cu_seqlens is not read after it. `causal`
  * chooses the order of the lists: a plan made for the other setting gives the same
- * results, less evenly dealt. Bounds that break the rule give an empty plan (calls
+ * results (dK and dV up to the order of their sums), less evenly dealt. Bounds that break the rule give an empty plan (calls
  * that read it write nothing) and FA_ERR_BAD_INDEX in fa_get_device_status(), and so
  * does a plan that was made for another nseq or total.
  *

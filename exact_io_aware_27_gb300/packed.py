@@ -157,6 +157,7 @@ class FlashAttentionPacked(torch.autograd.Function):
         return O
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dO):
         Q, K, V, O, L = ctx.saved_tensors
         if ctx.plan.version != ctx.version:
@@ -167,6 +168,9 @@ class FlashAttentionPacked(torch.autograd.Function):
 
 
 def flash_attention_packed(Q, K, V, plan: PackedPlan, scale: float | None = None):
-    """Attention over the plan's packed sequences, differentiable in Q, K and V. The plan
-    has to hold this batch until the backward pass has run."""
+    """Attention over the plan's packed sequences, differentiable (once) in Q, K and V. The
+    plan has to hold this batch until the backward pass has run. To capture a backward pass
+    in a CUDA graph, first drop every eager graph that reaches the same leaves (autograd ties
+    a leaf to the stream that first used it, and does not survive waiting for another stream
+    during a capture), or capture fa_packed_forward and fa_packed_backward."""
     return FlashAttentionPacked.apply(Q, K, V, plan, scale)

@@ -220,6 +220,63 @@ def test_decode_in_a_graph_and_on_another_stream(wide):
     assert_close("L", L, ref["L"])
 
 
+def test_decode_with_pages_listed_more_than_once():
+    """Requests that share pages, name one twice, and name the prefix's."""
+    args, keys = _batch(64, [32, 48], 8, 2, 64, 16, 73)
+    pages, table = args[3].tolist(), args[5]
+    table[1, :3] = torch.tensor([int(table[0, 1]), int(table[0, 1]), pages[0]], dtype=torch.int32)
+    args[3] = torch.tensor([pages[1], pages[1], pages[2], pages[2]], dtype=torch.int32,
+                           device="cuda")
+
+    def rows(i, lo, hi):
+        return keys[i][0][lo:hi], keys[i][1][lo:hi]
+
+    def cat(*parts):
+        return tuple(torch.cat(x) for x in zip(*parts))
+
+    p1, p2 = rows(0, 16, 32), rows(0, 32, 48)
+    prefix = [p1, p1, p2, p2]
+    own1 = rows(0, 80, 96)  # the second page of request 0
+    keys = [cat(*prefix, rows(0, 64, 96)), cat(*prefix, own1, own1, rows(0, 0, 16))]
+    _check(args, keys, 2)
+
+
+def test_decode_calls_on_two_streams_at_once():
+    jobs = []
+    for i, (prefix, lens) in enumerate([(3000, [70] * 40), (100, [9000, 40])]):
+        args, _ = _batch(prefix, lens, 8, 2, 128, 16, 79 + i)
+        B = len(lens)
+        ws = fa.alloc_prefix_workspace(B, 8, 2, 128, 16 * args[3].numel(),
+                                       16 * args[5].shape[1], "cuda")
+        outs = [(torch.empty_like(args[0]), torch.empty(B, 8, device="cuda")) for _ in range(8)]
+        jobs.append((torch.cuda.Stream(), args, ws, fa.fa_prefix_decode(*args), outs))
+    torch.cuda.synchronize()
+    for r in range(8):
+        for s, args, ws, want, outs in jobs:
+            fa.fa_prefix_decode(*args, O=outs[r][0], L=outs[r][1], workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for s, args, ws, want, outs in jobs:
+        assert all(torch.equal(a, b) for o in outs for a, b in zip(o, want))
+
+
+def test_cache_beyond_32_bits():
+    """Pages whose values lie more than 2^31 into the cache."""
+    hq, hkv, d, page, pages = 16, 8, 128, 1024, 2060
+    assert (pages - 8) * hkv * page * d > 2 ** 31
+    g = torch.Generator().manual_seed(83)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    mk = lambda n, h: torch.randn(n, h, d, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    kc = torch.empty(pages, hkv, page, d, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    shared, table = i32([pages - 1]), i32([[pages - 2, pages - 5], [pages - 3, 0]])
+    pk, pv, k, v = mk(900, hkv), mk(900, hkv), mk(1500 + 70, hkv), mk(1500 + 70, hkv)
+    fa.fa_cache_append(pk, pv, i32([0, 900]), i32([0]), shared[None], kc, vc)
+    fa.fa_cache_append(k, v, i32([0, 1500, 1570]), i32([0, 0]), table, kc, vc)
+    keys = [(torch.cat([pk, k[a:b]]).cpu(), torch.cat([pv, v[a:b]]).cpu())
+            for a, b in ((0, 1500), (1500, 1570))]
+    _check([mk(2, hq), kc, vc, shared, i32([900]), table, i32([1500, 70])], keys, hkv)
+
+
 @pytest.mark.parametrize("hkv,d,page", [(1, 8, 16), (2, 64, 32), (3, 72, 16), (8, 128, 64)])
 @pytest.mark.parametrize("lens,starts", [([1], [0]), ([3, 0, 40, 1], [15, 9, 16, 100]),
                                          ([1] * 33, list(range(33)))])

@@ -222,6 +222,79 @@ def test_backward_long_sequences_of_few_heads(lens, hq, hkv, d, causal):
     assert all(torch.equal(a, b) for a, b in zip(first, again))
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(8, 1, 128), (4, 2, 64)])
+def test_long_sequences_of_few_heads_do_not_leak(hq, hkv, d):
+    lens = [610, 1, 1300]
+    q, k, v, do, cu = packed_inputs(lens, hq, hkv, d, 185, rest=30)
+    plan = fa.fa_packed_plan(cu, q.shape[0])
+
+    def run():
+        O, L = fa.fa_packed_forward(q, k, v, plan)
+        return [O, L.T, *fa.fa_packed_backward(q, k, v, O, L, do, plan)]
+
+    clean = run()
+    for t in (q, k, v, do):
+        t[:610] = math.nan
+        t[1911:] = math.inf
+    for a, b in zip(run(), clean):
+        assert torch.equal(a[610:1911], b[610:1911])
+
+
+def test_calls_on_two_streams_at_once():
+    """Different batches, each with its plan and workspace, interleaved on two streams."""
+    jobs = []
+    for i, (lens, hq, hkv, d) in enumerate([([1400, 300], 8, 1, 128), ([90] * 20, 8, 4, 64)]):
+        q, k, v, do, cu = packed_inputs(lens, hq, hkv, d, 191 + i)
+        plan = fa.fa_packed_plan(cu, q.shape[0])
+        O, L = fa.fa_packed_forward(q, k, v, plan)
+        want = fa.fa_packed_backward(q, k, v, O, L, do, plan)
+        ws = fa.alloc_packed_workspace(plan, hq, d)
+        grads = [[torch.empty_like(x) for x in (q, k, v)] for _ in range(4)]
+        outs = [(torch.empty_like(O), torch.empty_like(L)) for _ in range(4)]
+        jobs.append((torch.cuda.Stream(), q, k, v, do, plan, O, L, want, ws, grads, outs))
+    torch.cuda.synchronize()
+    for r in range(4):
+        for s, q, k, v, do, plan, O, L, want, ws, grads, outs in jobs:
+            fa.fa_packed_forward(q, k, v, plan, O=outs[r][0], L=outs[r][1], stream=s)
+            fa.fa_packed_backward(q, k, v, *outs[r], do, plan, dQ=grads[r][0], dK=grads[r][1],
+                                  dV=grads[r][2], workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for s, q, k, v, do, plan, O, L, want, ws, grads, outs in jobs:
+        for r in range(4):
+            assert torch.equal(outs[r][0], O) and torch.equal(outs[r][1], L)
+            assert all(torch.equal(a, b) for a, b in zip(grads[r], want))
+
+
+def test_large_scores():
+    """Scores of some thousands: rows of one key, a moving maximum, exp far below 1."""
+    lens = [200, 700]
+    q, k, v, do, cu = packed_inputs(lens, 4, 2, 64, 193, std=20.0)
+    _check(q, k, v, cu, lens, True, scale=1.0)
+    _grads(q, k, v, do, cu, lens, True, scale=1.0)
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 values in Q and O: the last sequences against 64 bits."""
+    hq, hkv, d, n, count = 64, 1, 128, 500, 530
+    total = n * count
+    assert total * hq * d > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(197)
+    mk = lambda h: torch.randn(total, h, d, generator=g, device="cuda",  # noqa: E731
+                               dtype=torch.bfloat16)
+    q, k, v, do = mk(hq), mk(hkv), mk(hkv), mk(hq)
+    cu = (torch.arange(count + 1, device="cuda") * n).to(torch.int32)
+    plan = fa.fa_packed_plan(cu, total)
+    O, L = fa.fa_packed_forward(q, k, v, plan)
+    grads = fa.fa_packed_backward(q, k, v, O, L, do, plan)
+    for s in (0, count - 1):
+        rows = slice(s * n, (s + 1) * n)
+        want = packed64(q[rows], k[rows], v[rows], [n], True, None, do[rows])
+        assert_close("O", O[rows], want["O"])
+        assert_close("L", L[:, rows], want["L"])
+        for name, t in zip(("dQ", "dK", "dV"), grads):
+            assert_close(name, t[rows], want[name])
+
+
 def test_backward_of_few_heads_in_a_graph_and_into_one_buffer():
     """Gradients with strides, replayed for another batch of the same sizes."""
     hq, hkv, d, total = 8, 2, 128, 1700
@@ -308,6 +381,15 @@ def test_gradients_into_one_buffer_leave_the_rest():
     for a, b in zip((dq, dk, dv), want):
         assert torch.equal(a[:267], b[:267])
     assert torch.all(dwide[267:] == 9.0)
+
+
+def test_second_derivatives_are_refused():
+    q, k, v, do, cu = packed_inputs([30], 2, 1, 64, 199)
+    q.requires_grad_()
+    out = fa.flash_attention_packed(q, k, v, fa.fa_packed_plan(cu, 30))
+    (dq,) = torch.autograd.grad(out, q, do, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(dq.float().sum(), q)
 
 
 def test_autograd_and_differences():

@@ -106,8 +106,7 @@ struct FwdCfg {
   static constexpr int B_DRAIN = B_PVD + TILES;
   static constexpr int B_X = B_DRAIN + 1;        // kAlternate: both tiles' row sums written
   static constexpr int B_Y = B_DRAIN + 2;        // kAlternate: both tiles' O read out
-  static constexpr int B_Z = B_DRAIN + 3;        // kAlternate: row sums read
-  static constexpr int NBAR = B_DRAIN + 4;
+  static constexpr int NBAR = B_DRAIN + 3;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   // TMEM columns: Q_t as bf16 pairs (the A operand of S_t = Q_t K^T), S_t of one
   // 64-key step (then P_t as bf16 pairs over its first 32 columns), O_t.
@@ -173,7 +172,6 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
     mbar_init(&bar[C::B_DRAIN], 1);
     mbar_init(&bar[C::B_X], 128 * C::TILES);
     mbar_init(&bar[C::B_Y], 128 * C::TILES);
-    mbar_init(&bar[C::B_Z], 128 * C::TILES);
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -533,8 +531,8 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       // ---------------------------------------------------------- epilogue
       if constexpr (G::kAlternate) {
         // Both groups hold partial results of the same rows: they exchange the rows'
-        // (m, l) through the second half of each warp's staging area, and group t
-        // joins and writes columns [t D/2, (t + 1) D/2).
+        // (m, l) through the second half of each warp's staging area (store_joined has
+        // the first), and group t joins and writes columns [t D/2, (t + 1) D/2).
         if (!ok) break;
         if (!warp_wait(&bar[C::B_PVD], j & 1, wc) || !warp_wait(&bar[C::B_PVD + 1], j & 1, wc)) {
           ok = false;
@@ -543,15 +541,11 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         if (nh_t > 0) ++pvd_t;
         uint8_t* mine = smem + C::OFF_EPI + (warp - C::SOFT0) * kStoreStageBytes;
         uint8_t* other = smem + C::OFF_EPI + ((warp - C::SOFT0) ^ 4) * kStoreStageBytes;
-        if (lane == 0) bulk_wait_read<0>();  // copies of the last item's rows
-        __syncwarp();
         *reinterpret_cast<float2*>(mine + 2048 + lane * 8) = make_float2(m_ref, l_run);
         mbar_arrive(&bar[C::B_X]);
         if (!warp_wait(&bar[C::B_X], j & 1, wc)) { ok = false; break; }
         tc_fence_after();
         const float2 o = *reinterpret_cast<const float2*>(other + 2048 + lane * 8);
-        mbar_arrive(&bar[C::B_Z]);
-        if (!warp_wait(&bar[C::B_Z], j & 1, wc)) { ok = false; break; }
         const float2 s0 = t == 0 ? make_float2(m_ref, l_run) : o;
         const float2 s1 = t == 0 ? o : make_float2(m_ref, l_run);
         G::template store_joined<D>(g, it, t, warp & 3, lane, lane_base + C::COL_O, s0, s1,

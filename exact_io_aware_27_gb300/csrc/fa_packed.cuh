@@ -20,8 +20,9 @@ FA_DEV bool plan_matches(const PlanHead* h, int total, int nseq, unsigned int* s
 // (heads = 1 << head_shift) of row row0 + i / heads; the first `valid` lanes are stored
 // (valid may be <= 0 or above 32). A full piece leaves through the staging buffers and TMA; a
 // piece that ends inside its 32 rows, where the next row belongs to another sequence,
-// is written lane by lane (`out` is the tensor, `ld` its row stride).
-template <int NCOL>
+// is written lane by lane (`out` is the tensor, `ld` its row stride). BUFS: staging buffers
+// of 2 KB.
+template <int NCOL, int BUFS = 2>
 FA_DEV void packed_rows_store(uint32_t tcol, float mul, uint8_t* stage, const CUtensorMap* map,
                               int h, int row0, int valid, int col0, int d, __nv_bfloat16* out,
                               long long ld, int head_shift = 0) {
@@ -56,9 +57,9 @@ FA_DEV void packed_rows_store(uint32_t tcol, float mul, uint8_t* stage, const CU
       }
       continue;
     }
-    uint8_t* buf = stage + (c & 1) * 2048;
-    if (c >= 2) {  // the copy of piece c - 2 has read this buffer
-      if (lane == 0) bulk_wait_read<1>();
+    uint8_t* buf = stage + c % BUFS * 2048;
+    if (c >= BUFS) {  // the copy of piece c - BUFS has read this buffer
+      if (lane == 0) bulk_wait_read<BUFS - 1>();
       __syncwarp();
     }
     const uint32_t row = smem_u32(buf) + lane * 64;

@@ -153,7 +153,7 @@ struct Packed {
       }
       tmem_st_wait();
     }
-    packed_rows_store<D / 2>(mine, 1.f / l, stage, mo, it.h, row0, valid, t * (D / 2), d, g.p.O,
+    packed_rows_store<D / 2, 1>(mine, 1.f / l, stage, mo, it.h, row0, valid, t * (D / 2), d, g.p.O,
                              (long long)g.p.Hq * d, sh);
     if (t == 0 && lane < valid)
       g.p.L[(size_t)(it.h + (lane & ((1 << sh) - 1))) * g.p.total + row0 + (lane >> sh)] =

@@ -9,13 +9,15 @@
 //                  of one matrix product, so that K and V are read once for 256 rows.
 //                  This is the forward kernel (fa_forward.cuh, tcgen05) with rows
 //                  (request, query head), non-causal, keys from pages.
+//   shared kernel  the same for at most 16 or 32 rows, with the own kernel's products.
 //   own kernel     each request's own keys. Hq / Hkv rows share a key, far fewer than a
 //                  tcgen05 tile has: bound by reading the keys from HBM, so the
 //                  products are warp-level ones of 16 rows and every warp streams its
 //                  own keys through a private ring of shared memory.
 //   join kernel    joins the parts of each row, prefix and own.
+//   whole kernel   instead of them all, for small calls.
 //
-// Both kernels split their keys evenly, whatever the lengths: the blocks of all (row
+// These kernels split their keys evenly, whatever the lengths: the blocks of all (row
 // group, key/value head) units are laid end to end and worker c of P takes the c-th of
 // P equal pieces of that axis (Split). A worker's piece covers whole units and at most
 // two partial ones, so the parts need one slot per unit and two per worker. Lengths are
@@ -74,6 +76,7 @@ struct DecodeSizes {
   int own_per_sm;     // thread blocks of the own kernel per SM
   int sms, prefix_workers, own_blocks;  // blocks launched of the prefix and own kernels
   int prefix_step_ns, own_chunk_ns;     // see prefix_share
+  unsigned units_magic;                 // ceil(2^32 / (pairs * Hkv))
   float *prefix_o, *prefix_e;  // [slot][pair_rows][d], [slot][pair_rows]
   float *own_o, *own_e;        // [slot][own_rows][d], [slot][own_rows]
   int* first;                  // [B + 1] own chunks before each request
@@ -130,9 +133,11 @@ FA_DEV int prefix_keys(const int* prefix_len, int cap) {
 // blocks and `chunks` chunks of own keys per head and row tile. The two kernels run side
 // by side, a prefix block on an SM of its own and the own kernel's on the others, so the
 // SMs are shared out in proportion to the work: a prefix step of 128 keys takes an SM
-// 2.4 us (two row tiles) or 1.5 us (one), 0.5 us less for d <= 64, and a chunk of own keys
-// 4 d ns (its bytes at 65 GB/s). All three kernels compute this from the same integers.
-// 256 requests behind 8192 keys (32/8 heads, d = 128, up to 2048 own): 193 us, against
+// 2.4 us (two row tiles) or 1.5 us (one), 0.5 us less for d <= 64, 8 d ns in the shared
+// kernel, and a chunk of own keys 4 d ns (their bytes at 65 GB/s). All kernels compute this
+// from the same integers, in few divisions: it stands at the start of each, and one more
+// costs a call half a microsecond.
+// 256 requests behind 8192 keys (32/8 heads, d = 128, up to 2048 own): 183 us, against
 // 226 us with every SM for the one kernel and then for the other.
 FA_DEV int prefix_share(const DecodeSizes& s, int blocks, int chunks) {
   const unsigned steps = (unsigned)(s.pairs * s.Hkv) * (unsigned)blocks;
@@ -141,13 +146,20 @@ FA_DEV int prefix_share(const DecodeSizes& s, int blocks, int chunks) {
                             (steps + kMinPrefixBlocks - 1) / kMinPrefixBlocks);
   if (chunks == 0) return most;
   const unsigned long long a = (unsigned long long)steps * (unsigned)s.prefix_step_ns;
-  const unsigned long long b = (unsigned long long)(s.Hkv * s.row_tiles) * (unsigned)chunks *
-                               (unsigned)s.own_chunk_ns;
+  const unsigned long long both = a + (unsigned long long)(s.Hkv * s.row_tiles) *
+                                          (unsigned)chunks * (unsigned)s.own_chunk_ns;
   // to 24 bits, for a 32-bit division
-  const int shift = max(0, 40 - __clzll((long long)(a + b)));
-  const unsigned part = (unsigned)(a >> shift), all = (unsigned)((a + b) >> shift);
-  const int n = (int)(((unsigned)s.sms * part + all / 2) / all);
-  return max(1, min(min(n, most), s.sms - 1));
+  const int shift = max(0, 40 - __clzll((long long)both));
+  const unsigned part = (unsigned)(a >> shift), all = (unsigned)(both >> shift);
+  const int top = min(most, s.sms - 1);
+  const int n = max(1, min((int)(((unsigned)s.sms * part + all / 2) / all), top));
+  // Whole blocks a unit where that is near: fewer parts. Else an even number: SMs come in
+  // pairs, and a pair of which one half has a prefix block and the other own ones is slower
+  // (in the case above 32 blocks take 181 us, 34 187, 31 or 33 196).
+  const int units = s.pairs * s.Hkv;
+  const int m = (int)__umulhi((unsigned)(n + units / 2), s.units_magic) * units;  // n / units
+  if (m > 0 && (m & 1) == 0 && m <= top && abs(m - n) * 8 <= min(n, s.sms - n)) return m;
+  return n > 1 ? n & ~1 : n;
 }
 FA_DEV Split prefix_split(const DecodeSizes& s, int blocks, int share) {
   return Split((unsigned)(s.pairs * s.Hkv) * (unsigned)blocks, (unsigned)share);
@@ -383,15 +395,19 @@ struct RowTile {
   float o[D / 8][4];
   float m0, m1, l0, l1;
 
-  FA_DEV void load(const __nv_bfloat16* src, int rows, int d) {
+  // The first `rows` rows, row r at src + at(r).
+  template <class F>
+  FA_DEV void load(const __nv_bfloat16* src, F at, int rows, int d) {
     const int lane = threadIdx.x & 31, qr = lane >> 2, qc = (lane & 3) * 2;
+    const int last = max(rows - 1, 0);
+    const __nv_bfloat16 *row0 = src + at(min(qr, last)), *row1 = src + at(min(qr + 8, last));
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int row = qr + (e & 1) * 8, col = kk * 16 + (e >> 1) * 8 + qc;
         q[kk][e] = row < rows && col < d
-                       ? __ldg(reinterpret_cast<const unsigned int*>(src + (size_t)row * d + col))
+                       ? __ldg(reinterpret_cast<const unsigned int*>((e & 1 ? row1 : row0) + col))
                        : 0u;
       }
 #pragma unroll
@@ -669,7 +685,8 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
     x = r.x1;
     const int hk = r.ht / s.row_tiles, rt = r.ht - hk * s.row_tiles;
     const int rows = min(16, s.per_kv - rt * 16);
-    tile.load(p.Q + ((size_t)r.b * s.Hq + hk * s.per_kv + rt * 16) * s.d, rows, s.d);
+    tile.load(p.Q + ((size_t)r.b * s.Hq + hk * s.per_kv + rt * 16) * s.d,
+              [&](int row) { return row * s.d; }, rows, s.d);
     for (int key = r.key; key < r.key_end; key += C::KEYS) {
       cp_async_wait<C::STAGES - 2>();
       __syncwarp();  // the stage has landed for every lane, and the last one is read
@@ -723,13 +740,18 @@ struct WholeParams {
   float scale_log2;
 };
 constexpr int kWholeWarps = 8;
+// Floats from row to row of outputs in shared memory: eight rows' fragments, 32 bytes of
+// each, lie in different banks.
+template <int D>
+constexpr int kPartPitch = D + 8;
 template <int D>
 struct WholeCfg {
   static constexpr int STAGES = 3;
   static constexpr int STAGE = 2 * 16 * 2 * D;
   static constexpr int WARP = STAGES * STAGE;
   static constexpr int BYTES = kWholeWarps * WARP;
-  static_assert(BYTES >= (kWholeWarps + 1) * 16 * D * 4, "the rings hold the outputs at the end");
+  static_assert(BYTES >= (kWholeWarps + 1) * 16 * kPartPitch<D> * 4,
+                "the rings hold the outputs at the end");
 };
 
 // Joins `n` parts of a row's four columns c .. c + 3: stat(i) gives part i's (m, l) and
@@ -817,7 +839,8 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
 #pragma unroll
   for (int j = 0; j < C::STAGES - 1; ++j) issue(j);
   RowTile<D> tile;
-  tile.load(p.Q + ((size_t)b * s.Hq + hk * s.per_kv + rt * 16) * s.d, rows, s.d);
+  tile.load(p.Q + ((size_t)b * s.Hq + hk * s.per_kv + rt * 16) * s.d,
+            [&](int row) { return row * s.d; }, rows, s.d);
   for (int j = 0; j < mine; ++j) {
     cp_async_wait<C::STAGES - 2>();
     __syncwarp();  // the stage has landed for every lane, and the last one is read
@@ -831,11 +854,12 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
   cp_async_wait<0>();
   __syncthreads();  // every ring is read: they hold the outputs now
 
-  float* part = reinterpret_cast<float*>(smem_whole);  // [warp][row][D]
+  constexpr int PITCH = kPartPitch<D>;
+  float* part = reinterpret_cast<float*>(smem_whole);  // [warp][row][PITCH]
   const int qr = lane >> 2, qc = (lane & 3) * 2;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    float* out = part + (warp * 16 + qr + 8 * e) * D;
+    float* out = part + (warp * 16 + qr + 8 * e) * PITCH;
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
       *reinterpret_cast<float2*>(out + 8 * n + qc) =
@@ -845,7 +869,7 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
   }
   __syncthreads();
   // The block's warps, then the cluster's blocks; those with keys come first.
-  float* const mid = part + kWholeWarps * 16 * D;  // [row][D] of this block
+  float* const mid = part + kWholeWarps * 16 * PITCH;  // [row][PITCH] of this block
   const int warps_in = min(kWholeWarps, max(0, steps - rank * kWholeWarps));
   const int blocks_in = min(p.cluster, (steps + kWholeWarps - 1) / kWholeWarps);
   auto write = [&](int r, int c, float4 acc, float2 ml, bool any) {
@@ -860,11 +884,11 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
     float4 acc;
     const float2 ml = join_parts(
         warps_in, acc, [&](int w) { return stats[w][r]; },
-        [&](int w) { return *reinterpret_cast<const float4*>(part + (w * 16 + r) * D + c); });
+        [&](int w) { return *reinterpret_cast<const float4*>(part + (w * 16 + r) * PITCH + c); });
     if (p.cluster == 1) {
       if (c < s.d) write(r, c, acc, ml, steps > 0);
     } else {
-      *reinterpret_cast<float4*>(mid + r * D + c) = acc;
+      *reinterpret_cast<float4*>(mid + r * PITCH + c) = acc;
       if (c == 0) joined[r] = ml;
     }
   }
@@ -877,17 +901,165 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
     float4 acc;
     const float2 ml = join_parts(
         blocks_in, acc, [&](int k) { return cluster_ld2(cluster_map(smem_u32(&joined[r]), k)); },
-        [&](int k) { return cluster_ld4(cluster_map(smem_u32(mid + r * D + c), k)); });
+        [&](int k) { return cluster_ld4(cluster_map(smem_u32(mid + r * PITCH + c), k)); });
     write(r, c, acc, ml, steps > 0);
   }
   cluster_sync();  // no block leaves while its rows are read
 }
 
+// ================================================================== shared kernel
+// The prefix kernel's work for few rows a key/value head, where a 128-row tile
+// would be mostly empty and one SM's chain of scores, softmax and product, not the keys'
+// way from HBM, sets the time (one request, 32/8 heads, d = 128, behind 100000 keys: 66 us,
+// 6.2 TB/s, against 82 us with the tiles; 16 requests, 8/8 heads, behind 20000: 21.5 and
+// 30.1). With d = 128 it takes 16 rows only: two row tiles a warp fill the registers, and a
+// unit's start and end take 3 us longer than the 128-row tile's. Eight warps take a worker's piece, 16 keys each of every 128,
+// and each streams its keys through a ring of its own, as in the own kernel; at the end of
+// a unit they join their parts in shared memory. Same pieces, slots and parts.
+struct SharedParams {
+  DecodeSizes s;
+  const __nv_bfloat16 *Q, *Kc, *Vc;
+  const int *pages, *len, *lens;
+  int cap, own_cap, num_pages, page_shift;  // capacities in keys
+  float scale_log2;
+};
+constexpr int kSharedWarps = 8;
+template <int D>
+constexpr int kSharedTiles = D == 64 ? 2 : 1;  // row tiles of a warp at most
+template <int D>
+struct SharedCfg {
+  static constexpr int ROWS = 16 * kSharedTiles<D>;
+  static constexpr int STAGE = 2 * 16 * 2 * D;
+  static constexpr int STAGES = 192 * 1024 / (kSharedWarps * STAGE);
+  static constexpr int WARP = STAGES * STAGE;
+  static constexpr int BYTES = kSharedWarps * WARP;
+  static_assert(BYTES >= kSharedWarps * ROWS * kPartPitch<D> * 4,
+                "the rings hold the outputs");
+};
+
+template <int D, int TILES>
+__global__ void __launch_bounds__(32 * kSharedWarps, 1)
+    shared_kernel(const __grid_constant__ SharedParams p) {
+  using C = SharedCfg<D>;
+  extern __shared__ __align__(128) uint8_t smem_shared[];
+  __shared__ float2 stats[kSharedWarps][C::ROWS];  // a warp's m and l per row
+  const DecodeSizes& s = p.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_wait();
+  grid_launch_dependents();  // the own kernel
+  const int n = __ldg(p.len);
+  if ((n < 0 || n > p.cap) && blockIdx.x == 0 && threadIdx.x == 0)
+    atomicOr(&g_prefix_status, kDeviceIndexBit);
+  const int keys = max(0, min(n, p.cap)), blocks = (keys + 127) / 128;
+  int chunks = 0;  // each warp on its own
+  for (int b = lane; b < s.B; b += 32) chunks += own_chunks(__ldg(p.lens + b), p.own_cap);
+  chunks = __reduce_add_sync(0xffffffffu, chunks);
+  const Split split = prefix_split(s, blocks, prefix_share(s, blocks, chunks));
+  const int cta = (int)blockIdx.x;
+  if (cta >= split.workers) return;
+
+  const int rows = s.B * s.per_kv;  // one pair: a unit is a head
+  const uint32_t ring = smem_u32(smem_shared) + warp * C::WARP;
+  const size_t head_rows = (size_t)1 << p.page_shift;
+  const unsigned end = split.start(cta + 1);
+  for (unsigned x = split.start(cta); x < end;) {
+    const unsigned hk = x / (unsigned)blocks, u0 = hk * (unsigned)blocks;
+    const unsigned x1 = min(end, u0 + (unsigned)blocks);
+    const int k0 = (int)(x - u0) * 128, k1 = min(keys, (int)(x1 - u0) * 128);
+    const int stages = (int)(x1 - x);
+    int ids = 0;  // pages of this warp's stages 32 k .. 32 k + 31, one per lane
+    auto issue = [&](int j) {
+      if (j < stages) {
+        const int key = k0 + 128 * j + 16 * warp;
+        if ((j & 31) == 0) {
+          const int mine = key + 128 * lane;
+          ids = 0;
+          if (mine < k1) ids = __ldg(p.pages + (mine >> p.page_shift));
+          if ((unsigned)ids >= (unsigned)p.num_pages) {
+            atomicOr(&g_prefix_status, kDeviceIndexBit);
+            ids = 0;
+          }
+        }
+        const int page = __shfl_sync(0xffffffffu, ids, j & 31);
+        load_stage<D>(ring + (j % C::STAGES) * C::STAGE, p.Kc, p.Vc,
+                      ((size_t)page * s.Hkv + hk) * head_rows + (key & (head_rows - 1)), k1 - key,
+                      s.d);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int j = 0; j < C::STAGES - 1; ++j) issue(j);
+    RowTile<D> tile[TILES];
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+      tile[t].load(p.Q + (size_t)hk * s.per_kv * s.d,
+                   [&](int r) {
+                     const int b = (16 * t + r) / s.per_kv;
+                     return ((size_t)b * s.Hq + (16 * t + r - b * s.per_kv)) * s.d;
+                   },
+                   rows - 16 * t, s.d);
+    for (int j = 0; j < stages; ++j) {
+      cp_async_wait<C::STAGES - 2>();
+      __syncwarp();  // the stage has landed for every lane, and the last one is read
+      issue(j + C::STAGES - 1);
+      const int count = k1 - (k0 + 128 * j + 16 * warp);
+      if (count <= 0) break;  // the last stage
+      const uint32_t kb = ring + (j % C::STAGES) * C::STAGE;
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) tile[t].step(kb, kb + C::STAGE / 2, count, p.scale_log2);
+    }
+    cp_async_wait<0>();
+    __syncthreads();  // every ring is read: they hold the outputs now
+
+    constexpr int PITCH = kPartPitch<D>;
+    float* part = reinterpret_cast<float*>(smem_shared);  // [warp][row][PITCH]
+    const int qr = lane >> 2, qc = (lane & 3) * 2;
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      tile[t].finish();
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 16 * t + qr + 8 * e;
+        float* out = part + (warp * C::ROWS + row) * PITCH;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<float2*>(out + 8 * i + qc) =
+              make_float2(tile[t].o[i][2 * e], tile[t].o[i][2 * e + 1]);
+        if ((lane & 3) == 0)
+          stats[warp][row] = e ? make_float2(tile[t].m1, tile[t].l1)
+                               : make_float2(tile[t].m0, tile[t].l0);
+      }
+    }
+    __syncthreads();
+    const int warps_in = min(kSharedWarps, (k1 - k0 + 15) / 16);
+    const unsigned slot = x == u0 && x1 == u0 + (unsigned)blocks
+                              ? hk
+                              : (unsigned)s.Hkv + 2u * (unsigned)cta + (x == u0 ? 1u : 0u);
+    for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * kSharedWarps) {
+      const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+      float4 acc;
+      const float2 ml = join_parts(
+          warps_in, acc, [&](int w) { return stats[w][r]; },
+          [&](int w) {
+            return *reinterpret_cast<const float4*>(part + (w * C::ROWS + r) * PITCH + c);
+          });
+      const float inv = 1.f / ml.y;
+      const size_t at = (size_t)slot * s.pair_rows + r;
+      if (c < s.d)
+        *reinterpret_cast<float4*>(s.prefix_o + at * s.d + c) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      if (c == 0) s.prefix_e[at] = ml.x + lg2(ml.y);
+    }
+    x = x1;
+    if (x < end) __syncthreads();  // the outputs are read: the rings may be filled again
+  }
+}
+
 // ================================================================== join kernel
 struct JoinParams {
   DecodeSizes s;
-  const int* prefix_len;
-  int prefix_cap;  // keys
+  const int *prefix_len, *lens;
+  int prefix_cap, own_cap;  // keys
   __nv_bfloat16* O;
   float* L;
 };
@@ -900,22 +1072,39 @@ struct JoinParams {
 // without keys gets O = 0, L = -inf.
 constexpr int kJoinWarps = 8;
 template <int WARPS>  // of a row
-__global__ void __launch_bounds__(32 * kJoinWarps, WARPS == 1 ? 4 : 1) join_kernel(const __grid_constant__ JoinParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps, WARPS == 1 ? 4 : 1)
+    join_kernel(const __grid_constant__ JoinParams p) {
   __shared__ float4 sums[kJoinWarps][32];
   __shared__ float2 stats[kJoinWarps];  // a warp's reference and weight sum
   const DecodeSizes& s = p.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = WARPS == 1 ? blockIdx.x * kJoinWarps + warp : blockIdx.x;
   const int mine = WARPS == 1 ? 0 : warp;  // this warp of the row's
-  grid_wait();
-  grid_launch_dependents();
-  if (row >= s.B * s.Hq) return;  // WARPS == 1 only: no barrier follows
-  const int b = row / s.Hq, hq = row - b * s.Hq;
+  const int b = min(row / s.Hq, s.B - 1), hq = min(row - b * s.Hq, s.Hq - 1);
   const int hk = hq / s.per_kv, in = hq - hk * s.per_kv;
 
-  // Parts of the prefix, then of the request's own keys.
+  // Parts of the prefix, then of the request's own keys. The lengths are the call's inputs:
+  // they were written before the own kernel started, which launched this one, so that the
+  // parts are found while that kernel runs (1.2 us). Many requests' lengths take longer
+  // to sum up than to read from where the own kernel puts their sums.
   const int blocks = (prefix_keys(p.prefix_len, p.prefix_cap) + 127) / 128;
-  const int chunks = __ldg(s.first + s.B), f0 = __ldg(s.first + b), f1 = __ldg(s.first + b + 1);
+  int f0 = 0, f1 = 0, chunks = 0;
+  if (s.B <= 256) {
+    for (int i = lane; i < s.B; i += 32) {
+      const int n = own_chunks(__ldg(p.lens + i), p.own_cap);
+      chunks += n;
+      if (i < b) f0 += n;
+      if (i == b) f1 = n;
+    }
+    chunks = __reduce_add_sync(0xffffffffu, chunks);
+    f0 = __reduce_add_sync(0xffffffffu, f0);
+    f1 = __reduce_add_sync(0xffffffffu, f1) + f0;
+  } else {
+    grid_wait();
+    chunks = s.first[s.B];
+    f0 = s.first[b];
+    f1 = s.first[b + 1];
+  }
   const int share = prefix_share(s, blocks, chunks);
   int pparts = 0, pfirst = 0;
   const int pair = b / (2 * s.per_tile);
@@ -936,6 +1125,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps, WARPS == 1 ? 4 : 1) join_kern
   const unsigned punits = (unsigned)(s.pairs * s.Hkv);
   const unsigned ounits = (unsigned)(s.Hkv * s.row_tiles * s.B);
   const int parts = pparts + oparts;
+  grid_wait();
+  grid_launch_dependents();
+  if (row >= s.B * s.Hq) return;  // WARPS == 1 only: no barrier follows
 
   float ref = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1074,7 +1266,10 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
   s.sms = sms;
   s.prefix_workers = (int)prefix_grid;
   s.own_blocks = (int)own_grid;
-  s.prefix_step_ns = (a.B <= s.per_tile ? 1500 : 2400) - (D == 64 ? 500 : 0);
+  const int rows = a.B * s.per_kv;  // of a key/value head
+  const bool few = rows <= SharedCfg<D>::ROWS;
+  s.prefix_step_ns = few ? 8 * a.d : (a.B <= s.per_tile ? 1500 : 2400) - (D == 64 ? 500 : 0);
+  s.units_magic = (unsigned)((0x100000000ull + s.pairs * s.Hkv - 1) / (unsigned)(s.pairs * s.Hkv));
   s.own_chunk_ns = 4 * a.d;
   int shift = 0;
   while ((1 << shift) < a.page) ++shift;
@@ -1106,7 +1301,27 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
     return launch_as(whole_kernel<D>, (unsigned)(s.Hkv * s.row_tiles * s.B) * cluster,
                      32 * kWholeWarps, WholeCfg<D>::BYTES, stream, true, cluster, w);
   }
-  if (a.prefix_cap > 0) {
+  if (a.prefix_cap > 0 && few) {
+    SharedParams h;
+    h.s = s;
+    h.Q = static_cast<const __nv_bfloat16*>(a.Q);
+    h.Kc = static_cast<const __nv_bfloat16*>(a.Kc);
+    h.Vc = static_cast<const __nv_bfloat16*>(a.Vc);
+    h.pages = a.prefix_pages;
+    h.len = a.prefix_len;
+    h.lens = a.lens;
+    h.cap = cap;
+    h.own_cap = a.max_pages << shift;
+    h.num_pages = a.num_pages;
+    h.page_shift = shift;
+    h.scale_log2 = a.scale * kLog2e;
+    auto kernel = rows <= 16 ? shared_kernel<D, 1> : shared_kernel<D, kSharedTiles<D>>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             SharedCfg<D>::BYTES);
+    if (e != cudaSuccess) return e;
+    e = launch_early(kernel, prefix_grid, 32 * kSharedWarps, SharedCfg<D>::BYTES, stream, h);
+    if (e != cudaSuccess) return e;
+  } else if (a.prefix_cap > 0) {
     PrefixParams g;
     g.s = s;
     g.pages = a.prefix_pages;
@@ -1163,14 +1378,17 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
   jp.s = s;
   jp.prefix_len = a.prefix_cap > 0 ? a.prefix_len : nullptr;
   jp.prefix_cap = cap;
+  jp.lens = a.lens;
+  jp.own_cap = a.max_pages << shift;
   jp.O = static_cast<__nv_bfloat16*>(a.O);
   jp.L = a.L;
   // A warp per row once there is a row for every fourth warp slot of the GPU's SMs.
-  const int rows = a.B * a.Hq;
-  return rows >= sms * 4
-             ? launch_early(join_kernel<1>, (unsigned)ceil_div(rows, kJoinWarps), 32 * kJoinWarps,
-                            0, stream, jp)
-             : launch_early(join_kernel<kJoinWarps>, (unsigned)rows, 32 * kJoinWarps, 0, stream, jp);
+  const int joined = a.B * a.Hq;
+  return joined >= sms * 4
+             ? launch_early(join_kernel<1>, (unsigned)ceil_div(joined, kJoinWarps),
+                            32 * kJoinWarps, 0, stream, jp)
+             : launch_early(join_kernel<kJoinWarps>, (unsigned)joined, 32 * kJoinWarps, 0, stream,
+                            jp);
 }
 
 }  // namespace

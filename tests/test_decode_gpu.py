@@ -129,6 +129,18 @@ def test_decode_long_keys_of_few_requests():
     _check(args, keys, 1)
 
 
+@pytest.mark.parametrize("B,hq,hkv,d,page", [(4, 16, 2, 128, 32), (3, 10, 1, 64, 16),
+                                             (2, 64, 8, 40, 16), (1, 8, 8, 128, 64),
+                                             (32, 8, 8, 96, 16), (33, 4, 4, 128, 16)])
+@pytest.mark.parametrize("prefix", [1, 129, 9000])
+def test_decode_few_rows_behind_a_long_prefix(B, hq, hkv, d, page, prefix):
+    """Up to 32 rows a key/value head and one more, pieces of one unit and of several."""
+    args, keys = _batch(prefix, [(7 * i) % 90 for i in range(B)], hq, hkv, d, page, 27 + B)
+    a = _check(args, keys, hkv)
+    b = fa.fa_prefix_decode(*_wide(args))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_decode_without_prefix_or_own():
     args, keys = _batch(0, [30, 0, 200], 4, 2, 64, 16, 29)
     args[3] = args[4] = None

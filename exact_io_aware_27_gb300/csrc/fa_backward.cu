@@ -22,6 +22,7 @@ struct DenseBwd {
     int q0, bh;  // first query, head
   };
   static constexpr bool kEarly = false;
+  static constexpr bool kHeads = false, kListed = false;
   static constexpr bool kForeignTail = false;  // TMA reads zeros past a head's rows
   FA_DEV static View view(const Params& g) { return g; }
   FA_DEV static unsigned int* status() { return &g_bwd_status; }

@@ -14,7 +14,8 @@
 // The reference maximum is moved only when a row maximum exceeds it by more
 // than 8 (base 2): until then P stays below 2^8 and O, l keep their common
 // reference, so the result is the same up to rounding while most blocks need
-// no rescaling of O.
+// no rescaling of O. P is rounded to bf16 (2^-8 of a weight at most), the operand
+// type of the full-rate products; l is summed in fp32 before that rounding.
 //
 // GB300 mapping (one persistent CTA per SM, 384 threads). The work items are
 // (pair of 128-row query tiles, head); CTA c takes items c, 2P - 1 - c, 2P + c, ...

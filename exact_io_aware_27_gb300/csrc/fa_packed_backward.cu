@@ -50,7 +50,7 @@ struct PackedBwd {
     int h;
   };
   static constexpr bool kEarly = true;
-  static constexpr bool kForeignTail = true;
+  static constexpr bool kHeads = true, kListed = true, kForeignTail = true;
   FA_DEV static unsigned int* status() { return &g_packed_bwd_status; }
   FA_DEV static bool trigger(const Params& p) { return p.trigger; }
   FA_DEV static View view(const Params& p) {

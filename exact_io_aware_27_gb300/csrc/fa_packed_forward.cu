@@ -184,8 +184,8 @@ cudaError_t launch_packed_d(const PackedFwdArgs& a, cudaStream_t stream) {
   int sh = 0;  // heads that share a tile: 1 << sh
   while (sh < 3 && a.Hq / a.Hkv % (2 << sh) == 0) ++sh;
   // Fewer pairs than SMs (the sequences' last pairs aside): single tiles. There is no list
-  // of 16-row tiles. One sequence of 2000 rows, 8/1 heads, d = 128: 21.7 us in single tiles,
-  // 31.9 in pairs; 4000 rows, 4/1 heads: 36.2, 58.3; three of 1000, 8/2, d = 64: 11.8, 16.4.
+  // of 16-row tiles. One sequence of 2000 rows, 8/1 heads, d = 128: 19.6 us in single tiles,
+  // 31.9 in pairs; 4000 rows, 4/1 heads: 33.1, 58.3; three of 1000, 8/2, d = 64: 11.6, 16.4.
   // Short sequences have few keys to share out, and the join costs: one of 472 rows, 32/8,
   // 11.1 and 11.7; eight of 100, 16/8, 8.6 and 7.8. So from a mean length of 512.
   const bool one = (long long)ceil_div(a.total, 256 >> sh) * (a.Hq >> sh) < sms &&

@@ -913,9 +913,10 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
 // way from HBM, sets the time (one request, 32/8 heads, d = 128, behind 100000 keys: 66 us,
 // 6.2 TB/s, against 82 us with the tiles; 16 requests, 8/8 heads, behind 20000: 21.5 and
 // 30.1). With d = 128 it takes 16 rows only: two row tiles a warp fill the registers, and a
-// unit's start and end take 3 us longer than the 128-row tile's. Eight warps take a worker's piece, 16 keys each of every 128,
-// and each streams its keys through a ring of its own, as in the own kernel; at the end of
-// a unit they join their parts in shared memory. Same pieces, slots and parts.
+// unit's start and end take 3 us longer than the 128-row tile's. Eight warps take a worker's
+// piece, 16 keys each of every 128, and each streams its keys through a ring of its own, as
+// in the own kernel; at the end of a unit they join their parts in shared memory. Same
+// pieces, slots and parts.
 struct SharedParams {
   DecodeSizes s;
   const __nv_bfloat16 *Q, *Kc, *Vc;
@@ -1226,11 +1227,14 @@ int decode_sms() {
 // requests, 64 to 8000 shared and 64 to 2048 own keys); in ns they fit
 //   whole   1500 + waves (3000 + stages t), t = 850 (d > 64) or 460 for a warp's stage of
 //           16 keys, + 1000 for a cluster, and 1 per 9000 bytes at least
-//   three   12000 + 1 per 6000 bytes, every key read once, + 2 per row joined
-// to about 15 %. The two lie between 6.0 and 12.3 us for 16 requests of 2 x 4 heads,
-// d = 64, behind 1024 keys with 512 own, and between 58 and 26 us for 16 requests of
-// 8 x 4 heads, d = 128, behind 8000 keys with 128 own.
-unsigned whole_cluster(const DecodeSizes& s, int D, int prefix_cap, int own_cap, int sms) {
+//   three   11000 (9000 with the shared kernel) + 1 per 6000 bytes, every key read once,
+//           + 2 per row joined
+// to about 15 %; over 64 other points the form taken was 0.5 % slower than the better one.
+// The two take 6.0 and 12.3 us for 16 requests of 2 x 4 heads, d = 64, behind 1024 keys
+// with 512 own, and 58 and 26 us for 16 requests of 8 x 4 heads, d = 128, behind 8000 keys
+// with 128 own.
+template <int D>
+unsigned whole_cluster(const DecodeSizes& s, int prefix_cap, int own_cap, int sms) {
   const long long keys = (long long)prefix_cap + own_cap;
   const long long units = (long long)s.Hkv * s.row_tiles * s.B;
   const long long per_block = 16 * kWholeWarps;  // keys of a stage of all warps
@@ -1244,7 +1248,8 @@ unsigned whole_cluster(const DecodeSizes& s, int D, int prefix_cap, int own_cap,
   const long long bytes = 4LL * s.d;  // K and V of one key
   long long whole = 1500 + waves * (3000 + stages * (D == 128 ? 850 : 460)) + (c > 1 ? 1000 : 0);
   if (whole < units * keys * bytes / 9000) whole = units * keys * bytes / 9000;
-  const long long three = 12000 +
+  const bool few = s.B * s.per_kv <= SharedCfg<D>::ROWS;
+  const long long three = (few ? 9000 : 11000) +
                           (long long)s.Hkv * (prefix_cap + (long long)s.B * own_cap) * bytes / 6000 +
                           2LL * s.B * s.Hq;
   return whole <= three ? (unsigned)c : 0;
@@ -1276,7 +1281,7 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t stream) {
   cudaError_t e;
   const int cap = a.prefix_cap << shift;
   // One launch where it is expected to take less time than the three kernels.
-  const unsigned cluster = whole_cluster(s, D, cap, a.max_pages * a.page, sms);
+  const unsigned cluster = whole_cluster<D>(s, cap, a.max_pages * a.page, sms);
   if (cluster > 0) {
     WholeParams w;
     w.s = s;

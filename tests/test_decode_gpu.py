@@ -141,6 +141,34 @@ def test_decode_few_rows_behind_a_long_prefix(B, hq, hkv, d, page, prefix):
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+@pytest.mark.parametrize("B,hq,hkv", [(3, 4, 2), (40, 4, 2), (40, 32, 2)])
+def test_decode_lengths_of_zero_within_capacities(B, hq, hkv):
+    """Pages are listed, but the lengths on the device are 0: the prefix's, everyone's own,
+    and both."""
+    args, keys = _batch(700, [30 + i for i in range(B)], hq, hkv, 64, 16, 31)
+    own = [(k[700:], v[700:]) for k, v in keys]
+    shared = [(k[:700], v[:700]) for k, v in keys]
+    zero = torch.zeros_like
+    _check([*args[:4], zero(args[4]), *args[5:]], own, hkv)
+    _check([*args[:6], zero(args[6])], shared, hkv)
+    for call in (args, _wide(args)):
+        O, L = fa.fa_prefix_decode(*call[:4], zero(args[4]), call[5], zero(args[6]))
+        assert torch.all(O == 0) and torch.all(L == -math.inf)
+
+
+@pytest.mark.parametrize("prefix", [0, 300])
+def test_decode_the_largest_batch(prefix):
+    B, hq, hkv, d = 8192, 2, 1, 32
+    args, keys = _batch(prefix, [i % 3 for i in range(B)], hq, hkv, d, 16, 33)
+    some = list(range(0, B, 431)) + [B - 1]
+    want = _reference(args[0][some], [keys[i] for i in some], hkv)
+    has = torch.tensor([keys[i][0].shape[0] > 0 for i in some], device="cuda")
+    for call in (args, _wide(args)):
+        O, L = fa.fa_prefix_decode(*call)
+        assert_close("O", O[some], want["O"])
+        assert_close("L", L[some], want["L"], mask=has[:, None].expand(-1, hq))
+
+
 def test_decode_without_prefix_or_own():
     args, keys = _batch(0, [30, 0, 200], 4, 2, 64, 16, 29)
     args[3] = args[4] = None

@@ -273,6 +273,30 @@ def test_large_scores():
     _grads(q, k, v, do, cu, lens, True, scale=1.0)
 
 
+def test_the_most_sequences():
+    """65535 of them, nearly all empty, and one of the others the last."""
+    nseq = 65535
+    lens = [0] * nseq
+    lens[100], lens[40000], lens[nseq - 1] = 70, 1, 130
+    q, k, v, do, cu = packed_inputs(lens, 4, 2, 64, 195, rest=3)
+    plan = fa.fa_packed_plan(cu, q.shape[0])
+    O, L = fa.fa_packed_forward(q, k, v, plan)
+    grads = fa.fa_packed_backward(q, k, v, O, L, do, plan)
+    want = packed64(q, k, v, [70, 1, 130], True, None, do)
+    assert_close("O", O[:201], tuple(x[:201] for x in want["O"]))
+    for name, t in zip(("dQ", "dK", "dV"), grads):
+        assert_close(name, t[:201], tuple(x[:201] for x in want[name]))
+        assert torch.all(t[201:] == 0)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(64, 1, 8), (48, 1, 128), (24, 8, 16)])
+def test_many_heads_of_one_key_head(hq, hkv, d):
+    lens = [150, 3, 64]
+    q, k, v, do, cu = packed_inputs(lens, hq, hkv, d, 196, rest=1)
+    _check(q, k, v, cu, lens, True)
+    _grads(q, k, v, do, cu, lens, False)
+
+
 def test_offsets_beyond_32_bits():
     """More than 2^31 values in Q and O: the last sequences against 64 bits."""
     hq, hkv, d, n, count = 64, 1, 128, 500, 530
@@ -443,3 +467,35 @@ def test_backward_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_autograd_in_a_graph():
+    """Forward and backward pass through autograd, captured after a warm-up on a side stream
+    whose graph is gone, replayed for other values and another batch of the same sizes."""
+    lens, total = [40, 260], 310
+    q, k, v, do, cu = packed_inputs(lens, 4, 2, 64, 163, rest=10)
+    leaves = [x.detach().clone().requires_grad_() for x in (q, k, v)]
+    plan = fa.fa_packed_plan(cu, total)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fa.flash_attention_packed(*leaves, plan).backward(do)
+    torch.cuda.current_stream().wait_stream(side)
+    for x in leaves:
+        x.grad = None
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fa.flash_attention_packed(*leaves, plan).backward(do)
+    lens = [300, 5]
+    cu.copy_(torch.tensor([0, 300, 305], dtype=torch.int32))
+    fa.fa_packed_plan(cu, total, plan=plan)
+    with torch.no_grad():
+        for x, y in zip(leaves, (q, k, v)):
+            x.copy_(y.flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    want = packed64(*(x.detach() for x in leaves), lens, True, None, do)
+    for name, x in zip(("dQ", "dK", "dV"), leaves):
+        assert_close(name, x.grad[:305], tuple(t[:305] for t in want[name]))
+        assert torch.all(x.grad[305:] == 0)

@@ -98,8 +98,8 @@ struct BwdDealHead {
 // in the batch, W / hc <= 5/6 kPartShare and there are at most 8/5 W / hc parts.
 constexpr int kMinPart = 16, kPartShare = 152, kMaxParts = 256;
 static_assert(kMaxParts >= 8 * kPartShare / 6, "every part has a slot");
-// The deal and the join cost some 4 us: batches whose key blocks cannot have more halves
-// than this are not split.
+// The deal and the join cost some 5 us: batches whose key blocks are not likely to have
+// more halves than this are not split.
 constexpr int kSplitFrom = 32;
 constexpr size_t kPartBytes128 = 2 * 128 * 128 * 4;  // dV and dK of a key block, fp32, d = 128
 

@@ -6,7 +6,7 @@
 // that dK and dV are summed on chip, in a fixed order, and written once; unless the batch
 // has so few key blocks that one would take longer than an SM's share of all the work.
 // Then its queries are split into parts, whose fp32 sums a last kernel joins, in order
-// (one sequence of 4000 rows, 4/1 heads, d = 128: 86 us, 209 unsplit; 2000 rows, 8/1: 54
+// (one sequence of 4000 rows, 4/1 heads, d = 128: 82 us, 209 unsplit; 2000 rows, 8/1: 54
 // and 220). The statistics -D and -L * log2(e) lie in a workspace in which every sequence
 // starts on a multiple of 128 rows: TMA copies of fp32 rows have to start on 16-byte
 // boundaries, which a sequence's first row in the packed tensors need not do.
@@ -414,10 +414,12 @@ __device__ __noinline__ void deal_items(const DealArgs& a, int tiles) {
 // -D = -rowsum(dO o O) and -L * log2(e) of one 128-row tile and head per block step;
 // rows past the sequence's end get 0 and -inf, so that P is exactly 0 there. Bound by
 // reading O and dO from HBM: D / 8 lanes per row, 16 bytes of each per lane, four rows
-// in flight per lane before any arithmetic.
+// in flight per lane before any arithmetic. The launch bound asks for the registers of
+// that; without one the compiler kept fewer in flight (16384 rows, 32 heads, d = 128: 52 us,
+// 59 without; 2048 rows in 16, 32/8 heads, the whole pass: 33.3 and 36.9).
 // With DEAL, block 0 deals the gradient kernel's items meanwhile.
 template <int D, bool DEAL>
-__global__ void __launch_bounds__(256) packed_preprocess_kernel(
+__global__ void __launch_bounds__(256, DEAL ? 3 : 4) packed_preprocess_kernel(
     const __nv_bfloat16* __restrict__ O, const __nv_bfloat16* __restrict__ dO,
     const float* __restrict__ L, const uint8_t* __restrict__ plan, long long off_kv,
     float* __restrict__ ws_nD, float* __restrict__ ws_nL2, long long ws_rows, int total, int nseq,
@@ -521,12 +523,18 @@ __global__ void __launch_bounds__(256) packed_join_kernel(
   }
 }
 
-// Where a key block may have more than kSplitFrom halves, and there are fewer of them than
-// SMs (the sequences' last tiles aside). Where none is split after all, the look is what it
-// costs: eight sequences of 500, 16/4 heads, d = 128: 65.8 us, 59.8 without.
-bool may_split(int total, int Hq, int Hkv, int sms) {
-  return (long long)ceil_div(total, 64) * (Hq / Hkv) > kSplitFrom &&
-         (long long)ceil_div(total, 128) * Hkv < sms;
+// Whether key blocks may be split: where there are fewer of them than SMs (the sequences'
+// last tiles aside), and one may have many halves. The lengths are on the device only; so
+// that is where one of a sequence of four times the mean length has more than kSplitFrom,
+// or one of a sequence that is nearly the whole batch eight times as many. Where none is
+// split after all, the look costs some 5 us (eight sequences of 500, 16/4 heads, d = 128: 65
+// us, 60 without).
+bool may_split(int total, int nseq, int Hq, int Hkv, int sms) {
+  const long long most = ceil_div(total, 64), per_kv = Hq / Hkv;
+  const long long likely = (4LL * ceil_div(total, nseq) + 63) / 64;
+  return (long long)ceil_div(total, 128) * Hkv < sms &&
+         ((likely < most ? likely : most) * per_kv > kSplitFrom ||
+          most * per_kv > 8 * kSplitFrom);
 }
 
 int sm_count() {
@@ -547,7 +555,7 @@ cudaError_t launch_packed_bwd_d(const PackedBwdArgs& a, cudaStream_t stream) {
   float* const parts = reinterpret_cast<float*>(base + ws.parts);
   const int sms = min(sm_count(), kMaxBwdCtas), per_kv = a.Hq / a.Hkv;
   const long long pairs = lay.cap[kKeyList] * a.Hq;
-  const bool split = may_split(a.total, a.Hq, a.Hkv, sms);
+  const bool split = may_split(a.total, a.nseq, a.Hq, a.Hkv, sms);
   const long long items = pairs + lay.cap[kKeyList] * a.Hkv + (split ? ws.slots : 0);
   const unsigned ctas = (unsigned)(items < sms ? items : sms);
   DealArgs deal;

@@ -29,8 +29,8 @@ __device__ unsigned int g_packed_status;
 namespace {
 
 // ONE_TILE: an item is one 128-row tile instead of a pair, and both softmax groups work on
-// it, each on every other 64 keys (the forward kernel's kAlternate): for batches with
-// fewer tile pairs than SMs, whose time is that of the longest item.
+// it, each on every other 64 keys (the forward kernel's kAlternate): for batches with few
+// tile pairs, whose time is that of the longest item.
 struct PackedParams {
   const uint8_t* plan;
   float* L;
@@ -187,9 +187,13 @@ cudaError_t launch_packed_d(const PackedFwdArgs& a, cudaStream_t stream) {
   // of 16-row tiles. One sequence of 2000 rows, 8/1 heads, d = 128: 19.6 us in single tiles,
   // 31.9 in pairs; 4000 rows, 4/1 heads: 33.1, 58.3; three of 1000, 8/2, d = 64: 11.6, 16.4.
   // Short sequences have few keys to share out, and the join costs: one of 472 rows, 32/8,
-  // 11.1 and 11.7; eight of 100, 16/8, 8.6 and 7.8. So from a mean length of 512.
-  const bool one = (long long)ceil_div(a.total, 256 >> sh) * (a.Hq >> sh) < sms &&
-                   a.total / 512 >= a.nseq;
+  // 11.1 and 11.7; eight of 100, 16/8, 8.6 and 7.8. So from a mean length of 512. With one
+  // to two pairs an SM their number comes out uneven, and single tiles win from about 1024:
+  // five of 9000 rows in all, 8/8, 60.9 and 70.3; six of 3312, 24/8, 35.1 and 32.4; one of
+  // 4096, 32/8 (3.4 pairs), 124 and 112.
+  const long long pairs = (long long)ceil_div(a.total, 256 >> sh) * (a.Hq >> sh);
+  const bool one = pairs < sms ? a.total / 512 >= a.nseq
+                               : pairs < 2LL * sms && a.total / 1024 >= a.nseq;
   if (one && sh == 3) sh = 2;
   if (make_bf16_packed_map(&mq, a.Q, a.total, a.Hq, a.d, a.ldq, C::BM >> sh, 1 << sh) !=
           CUDA_SUCCESS ||

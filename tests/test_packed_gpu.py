@@ -63,7 +63,7 @@ def test_forward_many_items_per_cta(hq, hkv, d):
     _check(q, k, v, cu, lens, True)
 
 
-@pytest.mark.parametrize("hq,hkv,d", [(8, 1, 128), (2, 1, 64), (1, 1, 128)])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 1, 128), (2, 1, 64), (1, 1, 128), (16, 8, 40)])
 @pytest.mark.parametrize("causal", [True, False])
 def test_forward_long_sequences_of_few_heads(hq, hkv, d, causal):
     """Fewer row tiles than SMs."""

@@ -2,7 +2,9 @@
 // keys are the prefix that all of them share and then their own, both in pages of a
 // cache. Per query row the keys are split into parts, each part gives
 //   o = softmax over its keys times V,   e = log2 sum 2^(s * scale * log2(e))
-// and the parts are joined exactly: O = sum 2^(e - M) o / sum 2^(e - M), M = max e.
+// and the parts are joined exactly: O = sum 2^(e - M) o / sum 2^(e - M), M = max e. A part
+// whose scores are all minus infinity (a key with an infinite entry, or a product that
+// overflows) has e = -inf and o = 0: it adds nothing to the others.
 //
 //   prefix kernel  the shared keys, once for all requests: the query rows of all
 //                  requests and of the query heads of one key/value head are the rows
@@ -172,6 +174,8 @@ FA_DEV Split own_split(const DecodeSizes& s, int chunks, int share) {
   return Split((unsigned)(s.Hkv * s.row_tiles) * (unsigned)chunks,
                (unsigned)(own_share(s, share) * kOwnWarps));
 }
+// 1 / l for a part's sum l of weights, 0 for a part without a finite score.
+FA_DEV float part_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 // Own chunks of a request whose table row holds `cap` keys.
 FA_DEV int own_chunks(int len, int cap) {
   return (max(0, min(len, cap)) + kOwnChunk - 1) / kOwnChunk;
@@ -338,7 +342,7 @@ struct Prefix {
     const int rows = tile_rows(g, it, t) - warp * 32;
     if (rows <= 0) return;  // warp-uniform
     const size_t at = (size_t)it.slot * s.pair_rows + t * s.per_tile * s.per_kv + warp * 32;
-    const float inv = 1.f / l;
+    const float inv = part_inverse(l);
     write_part<D>(s.prefix_o + at * d, rows, 0, d, lane, stage, [&](int c, float (&v)[16]) {
       uint32_t x[16];
       tmem_ld16(ocol + c, x);
@@ -364,8 +368,10 @@ struct Prefix {
     const float ref = top == -INFINITY ? 0.f : top;
     float f0 = ex2(s0.x - ref), f1 = second ? ex2(s1.x - ref) : 0.f;
     const float l = second ? s0.y * f0 + s1.y * f1 : s0.y * f0;
-    f0 /= l;
-    f1 /= l;
+    if (l != 0.f) {  // else both are 0
+      f0 /= l;
+      f1 /= l;
+    }
     write_part<D / 2>(s.prefix_o + at * d, rows, t * (D / 2), d, lane, stage,
                       [&](int c, float (&v)[16]) {
                         uint32_t x[16], y[16];
@@ -704,7 +710,7 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
     for (int e = 0; e < 2; ++e) {
       const int row = qr + 8 * e;
       if (row >= rows) continue;
-      const float inv = 1.f / (e ? tile.l1 : tile.l0);
+      const float inv = part_inverse(e ? tile.l1 : tile.l0);
       float* out = s.own_o + ((size_t)slot * s.own_rows + row) * s.d;
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
@@ -1044,7 +1050,7 @@ __global__ void __launch_bounds__(32 * kSharedWarps, 1)
           [&](int w) {
             return *reinterpret_cast<const float4*>(part + (w * C::ROWS + r) * PITCH + c);
           });
-      const float inv = 1.f / ml.y;
+      const float inv = part_inverse(ml.y);
       const size_t at = (size_t)slot * s.pair_rows + r;
       if (c < s.d)
         *reinterpret_cast<float4*>(s.prefix_o + at * s.d + c) =

@@ -761,7 +761,8 @@ struct WholeCfg {
 };
 
 // Joins `n` parts of a row's four columns c .. c + 3: stat(i) gives part i's (m, l) and
-// value(i) its four columns, both relative to m. Returns the joined m and l.
+// value(i) its four columns, both relative to m. Returns the joined m and l: (-inf, 0)
+// where no part has a finite score, so that a further join gives them no say in its maximum.
 template <class S, class V>
 FA_DEV float2 join_parts(int n, float4& acc, S stat, V value) {
   float m = -INFINITY;
@@ -783,7 +784,7 @@ FA_DEV float2 join_parts(int n, float4& acc, S stat, V value) {
     acc.z += f * x.z;
     acc.w += f * x.w;
   }
-  return make_float2(ref, l);
+  return make_float2(m, l);
 }
 
 template <int D>

@@ -91,3 +91,17 @@ def test_forward_steps_without_a_finite_score(n, hq, hkv, d, hidden):
                            v[:n][keep, h].double(), False, d ** -0.5)
         assert_close("O", O[:n, hs], tuple(x.transpose(0, 1) for x in want["O"]))
         assert_close("L", L[hs, :n], want["L"])
+
+
+@pytest.mark.parametrize("hidden", [(128, 256), (0, 128), (896, 1024)])
+def test_decode_in_one_launch_joins_far_below_zero(hidden):
+    """A block of the cluster without a finite score, beside blocks whose scores lie far below
+    0: it adds nothing to their sums."""
+    args, keys = _batch(1024, [20, 24], 8, 2, 64, 16, 11)
+    keys = _hide(args, keys, 1024, range(*hidden), range(0), offset=2048.0)
+    want = _reference(args[0], keys, 2)
+    assert float(want["L"][0].max()) < -200.0
+    for call in (args, _wide(args)):
+        O, L = fa.fa_prefix_decode(*call)
+        assert_close("O", O, want["O"])
+        assert_close("L", L, want["L"])

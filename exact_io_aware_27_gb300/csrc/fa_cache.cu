@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
         if (to[u] >= 0) {
           const int h = c / p.per_row;
           to[u] += h * head + (c - h * p.per_row);
-          k[u] = __ldcs(p.K + (t0 + tok) * p.ldk + c);
-          v[u] = __ldcs(p.V + (t0 + tok) * p.ldv + c);
+          k[u] = ld_stream16(p.K + (t0 + tok) * p.ldk + c);
+          v[u] = ld_stream16(p.V + (t0 + tok) * p.ldv + c);
         }
       }
 #pragma unroll

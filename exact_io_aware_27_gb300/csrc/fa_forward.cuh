@@ -297,7 +297,6 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       Item nxt = fetch(0);
       for (int j = 0; ok && j < n_mine; ++j) {
         const Item it = nxt;
-        if (j + 1 < n_mine) nxt = fetch(j + 1);
         int nht[C::TILES];
         const int nh = steps(it, nht), nkb = blocks(nh);
         // ring use of the block that holds half `u` of the item's keys
@@ -337,6 +336,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
 #pragma unroll
         for (int t = 0; t < C::TILES; ++t)
           if (nht[t] > 0) scores(t, 0);
+        if (j + 1 < n_mine) nxt = fetch(j + 1);
         for (int k = 0; ok && k < nh; ++k) {
           // step k + 1 opens a block
           if (k + 1 < nh && (half_of(0, k + 1) & 1) == 0) {
@@ -518,7 +518,6 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         l_run = l_run * corr + (((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7)));
       }
 
-      if (j + 1 < n_mine) nxt = fetch(j + 1);
       // A tile with no steps waits for the end of the item's products first: only
       // then has the earlier fill of the next item's Q slot surely landed, so that
       // the slot's barrier is at most one phase behind the wait in move_q.
@@ -529,6 +528,10 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       // The next item's Q_t goes in before this item's O_t comes out, so that the
       // next item's first S products run while the O rows are written.
       if (ok && j + 1 < n_mine && !move_q(ru + C::QUSES + nkb)) ok = false;
+      // The item after is read behind that barrier's arrival, which is a release and waits
+      // for loads before it (8192 rows in 23 sequences, 16/16 heads, d = 64: 44.3 us; read
+      // before it 46.0).
+      if (j + 1 < n_mine) nxt = fetch(j + 1);
       // ---------------------------------------------------------- epilogue
       if constexpr (G::kAlternate) {
         // Both groups hold partial results of the same rows: they exchange the rows'

@@ -57,8 +57,8 @@ struct PackedBwd {
     const PlanHead* head = reinterpret_cast<const PlanHead*>(p.plan);
     int4 mine = make_int4(0, 0, 0, 0), deal = mine;
     if constexpr (SPLIT) {
-      mine = __ldg(&p.deal->cta[blockIdx.x]);
-      deal = __ldg(reinterpret_cast<const int4*>(p.deal));
+      mine = p.deal->cta[blockIdx.x];
+      deal = *reinterpret_cast<const int4*>(p.deal);
     }
     const bool ok = plan_matches(head, p.total, p.nseq, status());
     return {p, ok ? head->tiles128 : 0, ok ? head->covered : p.total, deal, mine};
@@ -77,25 +77,25 @@ struct PackedBwd {
   FA_DEV static int kv_rank(const View& g, int t, int c, int P) {
     if (!ranked(g)) return 0;
     const int row = t >> (g.deal.w & 255);
-    return row == 0 ? c : __ldg(g.p.ranks + (size_t)row * P + c);
+    return row == 0 ? c : g.p.ranks[(size_t)row * P + c];
   }
   FA_DEV static int q_rank(const View& g, int t, int c, int P) {
     if (!ranked(g)) return 0;
     const int row = t >> (g.deal.w >> 8);
-    return row == 0 ? g.mine.z : __ldg(g.p.ranks + (size_t)(g.mine.w + row) * P + c);
+    return row == 0 ? g.mine.z : g.p.ranks[(size_t)(g.mine.w + row) * P + c];
   }
   FA_DEV static KvItem kv_item(const View& g, int t, int rank, int c, int P) {
     const int i = ranked(g) ? t * P + rank : snake_item(t, c, P);
     if (SPLIT && i < g.deal.x) {
       const int4* e = reinterpret_cast<const int4*>(g.p.items + i);
-      const int4 s = __ldg(e), r = __ldg(e + 1);
+      const int4 s = e[0], r = e[1];
       return {s, r.x, r.y, r.z, r.w};
     }
     int tile, hk;
     const int from = SPLIT ? g.deal.y : 0;
     grouped_tile(i - (SPLIT ? g.deal.x : 0), g.p.Hkv, g.tiles - from, g.p.kgroup, tile, hk);
     KvItem it;
-    it.s = __ldg(reinterpret_cast<const PlanTile*>(g.p.plan + g.p.off_kv) + from + tile);
+    it.s = reinterpret_cast<const PlanTile*>(g.p.plan + g.p.off_kv)[from + tile];
     it.head = hk;
     it.first = it.halves = 0;
     it.slot = -1;
@@ -160,7 +160,7 @@ struct PackedBwd {
     int tile, h;
     const int i = ranked(g) ? t * P + rank : snake_item(t, P - 1 - c, P);
     grouped_tile(i, g.p.Hq, g.tiles, g.p.qgroup, tile, h);
-    return {__ldg(reinterpret_cast<const PlanTile*>(g.p.plan + g.p.off_q) + tile), h};
+    return {reinterpret_cast<const PlanTile*>(g.p.plan + g.p.off_q)[tile], h};
   }
   FA_DEV static int first_query(const QItem& it) { return it.s.z * 128; }
   FA_DEV static int keys(const View&, const QItem& it) { return it.s.y; }
@@ -246,13 +246,24 @@ __device__ __noinline__ void deal_items(const DealArgs& a, int tiles) {
   bins[tid] = 0;
   if (tid == 0) split_tiles = 0;
   long long sum = 0;
-#pragma unroll 4
-  for (int e = tid; e < tiles; e += T) {
-    const int h = halves(__ldg(kv + e)), b = blocks(__ldg(qs + e));
-    sum += h;
-    if (e < CACHED) {
-      kv_work[e] = h;
-      q_work[e] = b;
+  for (int e0 = tid; e0 < tiles; e0 += 4 * T) {
+    PlanTile k[4], q[4];  // loads of four rounds before the first store
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = min(e0 + u * T, tiles - 1);
+      k[u] = kv[e];
+      q[u] = qs[e];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = e0 + u * T;
+      if (e >= tiles) break;
+      const int h = halves(k[u]);
+      sum += h;
+      if (e < CACHED) {
+        kv_work[e] = h;
+        q_work[e] = blocks(q[u]);
+      }
     }
   }
 #pragma unroll
@@ -271,7 +282,7 @@ __device__ __noinline__ void deal_items(const DealArgs& a, int tiles) {
   // have more than 5/6 hc halves.)
   int last = 0;
   for (int e = tid; e < tiles; e += T)
-    if ((long long)(e < CACHED ? kv_work[e] : halves(__ldg(kv + e))) * per_kv * 3 > hc * 5LL)
+    if ((long long)(e < CACHED ? kv_work[e] : halves(kv[e])) * per_kv * 3 > hc * 5LL)
       last = e + 1;
   if (last > 0) atomicMax(&split_tiles, last);
   __syncthreads();
@@ -283,7 +294,7 @@ __device__ __noinline__ void deal_items(const DealArgs& a, int tiles) {
     int parts = 0;
     if (tid < n_split * a.Hkv) {
       it.head = tid % a.Hkv;
-      it.s = __ldg(kv + tid / a.Hkv);
+      it.s = kv[tid / a.Hkv];
       it.halves = halves(it.s) * per_kv;
       parts = it.halves * 3LL > hc * 5LL ? (it.halves - 1) / hc + 1 : 1;
     }
@@ -393,8 +404,8 @@ __device__ __noinline__ void deal_items(const DealArgs& a, int tiles) {
             const unsigned x = (unsigned)i - (unsigned)head_items, at = per_group(x);
             const unsigned in = x - at * per_group.d;  // see grouped_tile
             const int e = from + (int)((int)at == groups - 1 ? per_last(in) : per_tile(in));
-            work = pass == 0 ? (e < CACHED ? kv_work[e] : halves(__ldg(kv + e))) * per_kv
-                             : (e < CACHED ? q_work[e] : blocks(__ldg(qs + e)));
+            work = pass == 0 ? (e < CACHED ? kv_work[e] : halves(kv[e])) * per_kv
+                             : (e < CACHED ? q_work[e] : blocks(qs[e]));
           }
           load += pass == 0 ? work * a.half_cost + a.kv_cost : work * a.block_cost + a.q_cost;
           ++taken;
@@ -420,10 +431,9 @@ __device__ __noinline__ void deal_items(const DealArgs& a, int tiles) {
 // With DEAL, block 0 deals the gradient kernel's items meanwhile.
 template <int D, bool DEAL>
 __global__ void __launch_bounds__(256, DEAL ? 3 : 4) packed_preprocess_kernel(
-    const __nv_bfloat16* __restrict__ O, const __nv_bfloat16* __restrict__ dO,
-    const float* __restrict__ L, const uint8_t* __restrict__ plan, long long off_kv,
-    float* __restrict__ ws_nD, float* __restrict__ ws_nL2, long long ws_rows, int total, int nseq,
-    int Hq, int d, int trigger, const DealArgs deal) {
+    const __nv_bfloat16* O, const __nv_bfloat16* dO, const float* L, const uint8_t* plan,
+    long long off_kv, float* ws_nD, float* ws_nL2, long long ws_rows, int total, int nseq, int Hq,
+    int d, int trigger, const DealArgs deal) {
   constexpr int LPR = D / 8;        // lanes per row
   constexpr int RPB = 256 / LPR;    // rows per block step
   constexpr int U = 4;              // steps in flight
@@ -442,7 +452,7 @@ __global__ void __launch_bounds__(256, DEAL ? 3 : 4) packed_preprocess_kernel(
   const int sub = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
   for (long long i = blockIdx.x - DEAL; i < pairs; i += gridDim.x - DEAL) {
     const int e = (int)(i / Hq), h = (int)(i - (long long)e * Hq);
-    const PlanTile s = __ldg(reinterpret_cast<const PlanTile*>(plan + off_kv) + e);
+    const PlanTile s = reinterpret_cast<const PlanTile*>(plan + off_kv)[e];
     const int valid = s.y - s.z * 128;  // rows of this tile
     const size_t row0 = (size_t)s.x + (size_t)s.z * 128;
 #pragma unroll
@@ -469,12 +479,14 @@ __global__ void __launch_bounds__(256, DEAL ? 3 : 4) packed_preprocess_kernel(
         if (sub == 0) sums[base + u * RPB + r0] = acc;
       }
     }
+    float lse = 0.f;  // of row threadIdx.x; read before the barrier
+    if ((int)threadIdx.x < min(valid, 128)) lse = L[(size_t)h * total + row0 + threadIdx.x];
     __syncthreads();
     if (threadIdx.x < 128) {
       const int r = threadIdx.x;
       const size_t w = (size_t)h * ws_rows + s.w + s.z * 128 + r;
       ws_nD[w] = -sums[r];
-      ws_nL2[w] = r < valid ? -L[(size_t)h * total + row0 + r] * kLog2e : -INFINITY;
+      ws_nL2[w] = r < valid ? -lse * kLog2e : -INFINITY;
     }
     __syncthreads();
   }
@@ -484,14 +496,13 @@ __global__ void __launch_bounds__(256, DEAL ? 3 : 4) packed_preprocess_kernel(
 // and eight columns; bound by the parts' way through L2 and, for few of them, by latency.
 template <int D>
 __global__ void __launch_bounds__(256) packed_join_kernel(
-    const BwdDealHead* __restrict__ head, const BwdJoin* __restrict__ joins,
-    const float* __restrict__ parts, __nv_bfloat16* __restrict__ dK, __nv_bfloat16* __restrict__ dV,
-    long long lddk, long long lddv, float scale, int d) {
+    const BwdDealHead* head, const BwdJoin* joins, const float* parts, __nv_bfloat16* dK,
+    __nv_bfloat16* dV, long long lddk, long long lddv, float scale, int d) {
   constexpr int UNIT = 2 * 4 * (D / 8) * 32;  // threads of a key block
   constexpr size_t STRIDE = 2 * 128 * D;      // floats of a part
   grid_wait();
   grid_launch_dependents();
-  const int n = __ldg(&head->joins) * UNIT;
+  const int n = head->joins * UNIT;
   for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
     const int lane = i & 31, c8 = (i >> 5) % (D / 8), warp = (i / (32 * (D / 8))) & 3;
     const int w = (i / (UNIT / 2)) & 1;

@@ -65,7 +65,7 @@ struct Packed {
   FA_DEV static Item item(const View& g, int i) {
     int rank, h;
     grouped_tile(i, g.p.Hq >> g.p.head_shift, g.tiles, g.p.group, rank, h);
-    return {__ldg(reinterpret_cast<const PlanTile*>(g.p.plan + g.p.off_list) + rank),
+    return {reinterpret_cast<const PlanTile*>(g.p.plan + g.p.off_list)[rank],
             h << g.p.head_shift};
   }
   // First query of tile t, within the sequence.

@@ -63,7 +63,7 @@ __device__ int find_sequence(const int* first, int n, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) plan_kernel(const int* __restrict__ cu, int nseq,
+__global__ void __launch_bounds__(kThreads) plan_kernel(const int* cu, int nseq,
                                                         int total, int causal, uint8_t* plan,
                                                         PlanLayout lay) {
   __shared__ int warp_sums[32];

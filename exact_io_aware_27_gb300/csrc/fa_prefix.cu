@@ -128,7 +128,7 @@ DecodeSizes sizes_of(int B, int Hq, int Hkv, int d) {
 
 // The prefix's length, at most what the listed pages hold.
 FA_DEV int prefix_keys(const int* prefix_len, int cap) {
-  const int n = prefix_len ? __ldg(prefix_len) : 0;
+  const int n = prefix_len ? *prefix_len : 0;
   return max(0, min(n, cap));
 }
 // Thread blocks of the prefix kernel that get work, for a prefix of `blocks` 128-key
@@ -209,14 +209,14 @@ struct Prefix {
   FA_DEV static unsigned int* status() { return &g_prefix_status; }
   FA_DEV static bool trigger(const Params&) { return true; }  // for the own kernel
   FA_DEV static View view(const Params& p) {
-    const int n = __ldg(p.len);
+    const int n = *p.len;
+    int chunks = 0;  // each warp on its own; read beside n
+    for (int b = threadIdx.x & 31; b < p.s.B; b += 32)
+      chunks += own_chunks(p.lens[b], p.own_cap);
+    chunks = __reduce_add_sync(0xffffffffu, chunks);
     if ((n < 0 || n > p.cap) && blockIdx.x == 0 && threadIdx.x == 0)
       atomicOr(status(), kDeviceIndexBit);
     const int keys = max(0, min(n, p.cap)), blocks = (keys + 127) / 128;
-    int chunks = 0;  // each warp on its own
-    for (int b = threadIdx.x & 31; b < p.s.B; b += 32)
-      chunks += own_chunks(__ldg(p.lens + b), p.own_cap);
-    chunks = __reduce_add_sync(0xffffffffu, chunks);
     return {p, keys, blocks, prefix_split(p.s, blocks, prefix_share(p.s, blocks, chunks))};
   }
   FA_DEV static int segments(const View& g, int cta, int) {
@@ -278,7 +278,7 @@ struct Prefix {
     const int n = boxes(g, it, block), key0 = it.k0 + block * 128;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      at.page[i] = i < n ? __ldg(g.p.pages + ((key0 + i * g.p.box) >> g.p.page_shift)) : 0;
+      at.page[i] = i < n ? g.p.pages[(key0 + i * g.p.box) >> g.p.page_shift] : 0;
     return at;
   }
   template <class C>
@@ -413,7 +413,7 @@ struct RowTile {
       for (int e = 0; e < 4; ++e) {
         const int row = qr + (e & 1) * 8, col = kk * 16 + (e >> 1) * 8 + qc;
         q[kk][e] = row < rows && col < d
-                       ? __ldg(reinterpret_cast<const unsigned int*>((e & 1 ? row1 : row0) + col))
+                       ? *reinterpret_cast<const unsigned int*>((e & 1 ? row1 : row0) + col)
                        : 0u;
       }
 #pragma unroll
@@ -547,7 +547,7 @@ struct OwnCfg {
 
 // Length of request b's own keys, at most what its table row holds.
 FA_DEV int own_keys(const OwnParams& p, int b) {
-  return max(0, min(__ldg(p.lens + b), p.max_pages << p.page_shift));
+  return max(0, min(p.lens[b], p.max_pages << p.page_shift));
 }
 
 // Pages are read 16 keys at a time (a page holds a multiple of 16): per stage 16 rows of
@@ -565,12 +565,13 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
   constexpr int kThreads = 32 * kOwnWarps;
 
   // Chunks before each request (exclusive scan of the lengths).
+  const int shared_keys = prefix_keys(p.prefix_len, p.prefix_cap);  // in flight with them
   int run = 0;
   for (int b0 = 0; b0 < s.B; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
     int n = 0;
     if (b < s.B) {
-      const int len = __ldg(p.lens + b);
+      const int len = p.lens[b];
       if ((len < 0 || len > p.max_pages << p.page_shift) && blockIdx.x == 0)
         atomicOr(&g_prefix_status, kDeviceIndexBit);
       n = own_chunks(len, p.max_pages << p.page_shift);
@@ -600,8 +601,7 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
 
   const int chunks = run;  // of one (head, row tile)
   const unsigned units = (unsigned)(s.Hkv * s.row_tiles * s.B);
-  const int share =
-      prefix_share(s, (prefix_keys(p.prefix_len, p.prefix_cap) + 127) / 128, chunks);
+  const int share = prefix_share(s, (shared_keys + 127) / 128, chunks);
   const Split sp = own_split(s, chunks, share);
   // The first workers on different SMs; the blocks past the share get none.
   const int active = own_share(s, share);
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(32 * kOwnWarps) own_kernel(const __grid_consta
         const int key = ir.key + lane * C::KEYS;
         int page = 0;
         if (key < ir.key_end)
-          page = __ldg(p.table + (size_t)ir.b * p.max_pages + (key >> p.page_shift));
+          page = p.table[(size_t)ir.b * p.max_pages + (key >> p.page_shift)];
         if ((unsigned)page >= (unsigned)p.num_pages) {
           atomicOr(&g_prefix_status, kDeviceIndexBit);
           page = 0;
@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
   const int own_cap = p.max_pages << p.page_shift;
   grid_wait();
   grid_launch_dependents();
-  const int len = __ldg(p.lens + b), plen = p.prefix_len ? __ldg(p.prefix_len) : 0;
+  const int len = p.lens[b], plen = p.prefix_len ? *p.prefix_len : 0;
   if (len < 0 || len > own_cap || plen < 0 || plen > p.prefix_cap)
     if (threadIdx.x == 0) atomicOr(&g_prefix_status, kDeviceIndexBit);
   const int own = max(0, min(len, own_cap)), shared = max(0, min(plen, p.prefix_cap));
@@ -827,8 +827,8 @@ __global__ void __launch_bounds__(32 * kWholeWarps)
         if (j + lane < mine) {
           int key;
           keys_of(i, key);
-          ids = __ldg(i < p_steps ? p.pages + (key >> p.page_shift)
-                                  : p.table + (size_t)b * p.max_pages + (key >> p.page_shift));
+          ids = *(i < p_steps ? p.pages + (key >> p.page_shift)
+                              : p.table + (size_t)b * p.max_pages + (key >> p.page_shift));
           if ((unsigned)ids >= (unsigned)p.num_pages) {
             atomicOr(&g_prefix_status, kDeviceIndexBit);
             ids = 0;
@@ -955,13 +955,13 @@ __global__ void __launch_bounds__(32 * kSharedWarps, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_wait();
   grid_launch_dependents();  // the own kernel
-  const int n = __ldg(p.len);
+  const int n = *p.len;
+  int chunks = 0;  // each warp on its own; read beside n
+  for (int b = lane; b < s.B; b += 32) chunks += own_chunks(p.lens[b], p.own_cap);
+  chunks = __reduce_add_sync(0xffffffffu, chunks);
   if ((n < 0 || n > p.cap) && blockIdx.x == 0 && threadIdx.x == 0)
     atomicOr(&g_prefix_status, kDeviceIndexBit);
   const int keys = max(0, min(n, p.cap)), blocks = (keys + 127) / 128;
-  int chunks = 0;  // each warp on its own
-  for (int b = lane; b < s.B; b += 32) chunks += own_chunks(__ldg(p.lens + b), p.own_cap);
-  chunks = __reduce_add_sync(0xffffffffu, chunks);
   const Split split = prefix_split(s, blocks, prefix_share(s, blocks, chunks));
   const int cta = (int)blockIdx.x;
   if (cta >= split.workers) return;
@@ -982,7 +982,7 @@ __global__ void __launch_bounds__(32 * kSharedWarps, 1)
         if ((j & 31) == 0) {
           const int mine = key + 128 * lane;
           ids = 0;
-          if (mine < k1) ids = __ldg(p.pages + (mine >> p.page_shift));
+          if (mine < k1) ids = p.pages[mine >> p.page_shift];
           if ((unsigned)ids >= (unsigned)p.num_pages) {
             atomicOr(&g_prefix_status, kDeviceIndexBit);
             ids = 0;
@@ -1099,7 +1099,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, WARPS == 1 ? 4 : 1)
   int f0 = 0, f1 = 0, chunks = 0;
   if (s.B <= 256) {
     for (int i = lane; i < s.B; i += 32) {
-      const int n = own_chunks(__ldg(p.lens + i), p.own_cap);
+      const int n = own_chunks(p.lens[i], p.own_cap);
       chunks += n;
       if (i < b) f0 += n;
       if (i == b) f1 = n;

@@ -208,6 +208,16 @@ FA_DEV float2 cluster_ld2(uint32_t addr) {
   return v;
 }
 
+// 16 bytes that are read once.
+FA_DEV uint4 ld_stream16(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // ------------------------------------------------- programmatic dependent launch
 // Lets the next kernel of the stream, if it was launched for it, start now.
 FA_DEV void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -6,7 +6,9 @@
 // takes kTokens tokens: its first threads look the tokens' places up (a binary search
 // over the bounds, then the table), then all threads copy, K and V of up to four
 // chunks in flight each. A place out of range is not written and raises
-// kDeviceIndexBit.
+// kDeviceIndexBit; so do bounds that are not 0 = cu[0] <= ... <= cu[nseq] <= total, which
+// the other threads look at meanwhile, each block at its share. Whatever the bounds are, a
+// row goes only to a request in whose bounds it lies.
 #include "fa_decode.h"
 #include "fa_launch.h"
 #include "sm103.cuh"
@@ -34,13 +36,22 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
   const long long head = (long long)p.page * p.per_row;  // units from head to head
   grid_wait();
   grid_launch_dependents();
+  if (threadIdx.x >= 32) {  // the threads that have no token to look up
+    constexpr int n = kThreads - 32;
+    const int me = threadIdx.x - 32;
+    bool bad = false;
+    for (long long i = (long long)blockIdx.x * n + me; i < p.nseq; i += (long long)gridDim.x * n)
+      bad |= p.cu[i] > p.cu[i + 1];
+    if (blockIdx.x == 0 && me == 0) bad |= p.cu[0] != 0 || p.cu[p.nseq] > p.total;
+    if (bad) atomicOr(&g_append_status, kDeviceIndexBit);
+  }
   for (long long t0 = (long long)blockIdx.x * kTokens; t0 < p.total;
        t0 += (long long)gridDim.x * kTokens) {
     if (threadIdx.x < kTokens) {
       const int t = (int)t0 + threadIdx.x;
       long long at = -1;
       if (t < p.total && t < p.cu[p.nseq]) {  // rows behind the last request are skipped
-        int lo = 0, hi = p.nseq;  // cu[lo] <= t < cu[hi] for bounds that do not decrease
+        int lo = 0, hi = p.nseq;  // t < cu[hi]; cu[lo] <= t, or lo = 0
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
           if (p.cu[mid] <= t)

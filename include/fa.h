@@ -282,8 +282,10 @@ FA_API int fa_packed_backward(const void* Q, const void* K, const void* V, long 
  * rows [cu_seqlens[i], cu_seqlens[i + 1]) go to positions starts[i], starts[i] + 1, ...
  * of request i. cu_seqlens is int32 [nseq + 1] and starts int32 [nseq] in device memory,
  * with 0 = cu_seqlens[0] <= ... <= cu_seqlens[nseq] <= total; rows behind the last are
- * not written. Two rows for one place leave one of the two there, in 16-byte pieces.
- * total <= 2^24, nseq <= 65535. One kernel launch.
+ * not written. Bounds that break the rule give FA_ERR_BAD_INDEX in fa_get_device_status();
+ * a row is then written for one request in whose bounds it lies, or not at all. Two rows
+ * for one place leave one of the two there, in 16-byte pieces. 1 <= total <= 2^24,
+ * 1 <= nseq <= 65535. One kernel launch.
  */
 FA_API int fa_cache_append(const void* K, const void* V, long long k_stride, long long v_stride,
                            int total, const int* cu_seqlens, const int* starts, int nseq,

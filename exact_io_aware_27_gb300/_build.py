@@ -95,7 +95,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs = list(ex.map(compile_one, SOURCES))
         binding_obj, torch_lib = binding.result()
     tmp = LIBRARY + f".tmp{os.getpid()}"
-    r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
+    # The name under which the binding asks for it, and finds it beside itself ($ORIGIN).
+    r = subprocess.run([nvcc, *ARCH, "-shared", "-Xlinker",
+                        "-soname=" + os.path.basename(LIBRARY), "-o", tmp, *objs],
+                       capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIBRARY)

@@ -6,8 +6,9 @@ Each ``csrc/*.cu`` translation unit is compiled by ``nvcc`` in parallel into
 when a source or header is newer than the library.
 
 ``csrc/fa_binding.cpp``, the marshalling of torch tensors for the packed and paged
-calls, becomes the Python module ``_fa_binding.so`` beside it, linked to the library
-and built for the torch that is installed.
+calls, becomes the Python module ``_fa_binding.<abi>.so`` beside it, linked to the
+library and built for the Python and the torch that are installed, which its name states:
+with another torch it is not found, and build() makes that one's.
 """
 from __future__ import annotations
 
@@ -17,13 +18,16 @@ import shutil
 import subprocess
 import sysconfig
 
+import torch
+
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIBRARY = os.path.join(PKG_DIR, "libfa_gb300.so")
-BINDING = os.path.join(PKG_DIR, "_fa_binding.so")
+BINDING = os.path.join(
+    PKG_DIR, f"_fa_binding.{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}.so")
 
 SOURCES = ["fa_api.cu", "fa_forward.cu", "fa_backward.cu", "fa_softmax.cu", "fa_selftest.cu",
            "fa_noalloc.cu", "fa_session.cu", "fa_standard.cu", "fa_packed_plan.cu",
@@ -76,8 +80,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     def compile_binding():
-        import torch  # its headers; found through the installed package
-        root = os.path.dirname(torch.__file__)
+        root = os.path.dirname(torch.__file__)  # its headers and libraries
         include = [os.path.join(root, "include"),
                    os.path.join(root, "include", "torch", "csrc", "api", "include"),
                    sysconfig.get_paths()["include"], INCLUDE]

@@ -33,3 +33,22 @@ def test_a_copied_package_uses_its_own_library(tmp_path):
     assert r.returncode == 0, r.stderr
     assert sorted(r.stdout.split()) == sorted(str(copy / os.path.basename(f))
                                               for f in (_build.BINDING, _build.LIBRARY))
+
+
+def test_the_binding_of_another_torch_is_not_used():
+    """The module is built against one torch and one Python; with another torch it is not
+    loaded, and build() has work to do."""
+    name = os.path.basename(_build.PKG_DIR)
+    code = ("import torch\n"
+            "torch.__version__ = '0.0.1'\n"
+            f"from {name} import _build, packed\n"
+            "assert not _build.up_to_date()\n"
+            "try:\n"
+            "    packed._binding()\n"
+            "except RuntimeError as e:\n"
+            "    assert 'is not built' in str(e), e\n"
+            "    print('refused')\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=_build.ROOT, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["refused"], r.stdout + r.stderr
+    assert _build.up_to_date()

@@ -386,6 +386,9 @@ int fa_standard_forward(const void* Q, const void* K, const void* V, int B, int 
 
 int fa_get_device_status(int* status_out) {
   if (!status_out) return FA_ERR_INVALID_ARG;
+  // The copies below wait for the default stream alone, not for streams created without
+  // that dependence (torch's are).
+  if (cudaDeviceSynchronize() != cudaSuccess) return FA_ERR_CUDA;
   unsigned int f = 0, b = 0, t = 0, sd = 0, pl = 0, pk = 0, pb = 0, ap = 0, px = 0;
   if (forward_read_status(&f) != cudaSuccess || bwd_read_status(&b) != cudaSuccess ||
       selftest_read_status(&t) != cudaSuccess || standard_read_status(&sd) != cudaSuccess ||

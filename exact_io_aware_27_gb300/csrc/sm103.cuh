@@ -174,11 +174,6 @@ FA_DEV void fence_proxy_async_smem() {
 }
 
 // ---------------------------------------------------------------- clusters
-FA_DEV uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 // Barrier of all threads of the cluster; orders their shared-memory accesses.
 FA_DEV void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::

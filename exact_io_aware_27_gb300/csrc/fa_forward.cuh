@@ -101,10 +101,13 @@ struct FwdCfg {
   static constexpr int B_IN = 2 * STAGES;        // Q tiles in TMEM (256 arrivals)
   static constexpr int B_SF = B_IN + 1;          // + tile: S_t of the current step done
   static constexpr int B_PF = B_SF + TILES;      // + tile: P_t written (128 arrivals)
-  static constexpr int B_PVD = B_PF + TILES;     // + tile: the tile's last O += P V done
-                                                 // (for a tile with no steps: the item's
-                                                 // products done)
-  static constexpr int B_DRAIN = B_PVD + TILES;
+  // + tile + TILES * (item & 1): the tile's last O += P V done (for a tile with no steps:
+  // the item's products done). Two slots: a softmax group signals the next item's Q before
+  // it waits for this, and where its tile has no steps in the next item that item's
+  // products finish without the group. One barrier could complete twice before the wait
+  // and hide its phase; the item after the next needs the group first.
+  static constexpr int B_PVD = B_PF + TILES;
+  static constexpr int B_DRAIN = B_PVD + 2 * TILES;
   static constexpr int B_X = B_DRAIN + 1;        // kAlternate: both tiles' row sums written
   static constexpr int B_Y = B_DRAIN + 2;        // kAlternate: both tiles' O read out
   static constexpr int NBAR = B_DRAIN + 3;
@@ -169,6 +172,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       mbar_init(&bar[C::B_SF + t], 1);
       mbar_init(&bar[C::B_PF + t], 128);
       mbar_init(&bar[C::B_PVD + t], 1);
+      mbar_init(&bar[C::B_PVD + C::TILES + t], 1);
     }
     mbar_init(&bar[C::B_DRAIN], 1);
     mbar_init(&bar[C::B_X], 128 * C::TILES);
@@ -352,7 +356,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
             if (k + 1 < nht[t])
               scores(t, k + 1);
             else
-              umma_commit_w(&bar[C::B_PVD + t]);
+              umma_commit_w(&bar[C::B_PVD + C::TILES * (j & 1) + t]);
           }
           // both tiles are done with a block once its second half's step is issued
           if (ok && (G::kAlternate || (k & 1) || k + 1 == nh))
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         // for the next item's Q slot (whose earlier fill is one of those blocks).
 #pragma unroll
         for (int t = 0; t < C::TILES; ++t)
-          if (ok && nht[t] == 0) umma_commit_w(&bar[C::B_PVD + t]);
+          if (ok && nht[t] == 0) umma_commit_w(&bar[C::B_PVD + C::TILES * (j & 1) + t]);
         ru += C::QUSES + nkb;
 #pragma unroll
         for (int t = 0; t < C::TILES; ++t) base[t] += nht[t];
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
     const uint32_t scol = lane_base + C::COL_S + 64 * t;
     const uint32_t ocol = lane_base + C::COL_O + D * t;
     const float sl2 = p.scale_log2;
-    int ru = 0, base_t = 0, pvd_t = 0;  // ring uses, steps and finished items of tile t
+    int ru = 0, base_t = 0;  // ring uses and steps of tile t in earlier items
     // Row `row` of Q_t of the item whose Q tiles are ring use `rq` into TMEM: the
     // row's 16-byte pieces in the 128-byte-swizzled tile (piece j of a chunk row at
     // j ^ (row % 8)). The previous item's S_t products, the only readers of these
@@ -521,16 +525,13 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
       // A tile with no steps waits for the end of the item's products first: only
       // then has the earlier fill of the next item's Q slot surely landed, so that
       // the slot's barrier is at most one phase behind the wait in move_q.
-      if (ok && nh_t == 0) {
-        if (!warp_wait(&bar[C::B_PVD + t], pvd_t & 1, wc)) { ok = false; break; }
-        ++pvd_t;
-      }
+      uint64_t* const pvd = &bar[C::B_PVD + C::TILES * (j & 1)];
+      if (ok && nh_t == 0 && !warp_wait(pvd + t, (j >> 1) & 1, wc)) { ok = false; break; }
       // The next item's Q_t goes in before this item's O_t comes out, so that the
       // next item's first S products run while the O rows are written.
       if (ok && j + 1 < n_mine && !move_q(ru + C::QUSES + nkb)) ok = false;
-      // The item after is read behind that barrier's arrival, which is a release and waits
-      // for loads before it (8192 rows in 23 sequences, 16/16 heads, d = 64: 44.3 us; read
-      // before it 46.0).
+      // The item after is read behind that barrier's arrival, which is a release and would
+      // wait for loads before it.
       if (j + 1 < n_mine) nxt = fetch(j + 1);
       // ---------------------------------------------------------- epilogue
       if constexpr (G::kAlternate) {
@@ -538,11 +539,10 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         // (m, l) through the second half of each warp's staging area (store_joined has
         // the first), and group t joins and writes columns [t D/2, (t + 1) D/2).
         if (!ok) break;
-        if (!warp_wait(&bar[C::B_PVD], j & 1, wc) || !warp_wait(&bar[C::B_PVD + 1], j & 1, wc)) {
+        if (!warp_wait(pvd, (j >> 1) & 1, wc) || !warp_wait(pvd + 1, (j >> 1) & 1, wc)) {
           ok = false;
           break;
         }
-        if (nh_t > 0) ++pvd_t;
         uint8_t* mine = smem + C::OFF_EPI + (warp - C::SOFT0) * kStoreStageBytes;
         uint8_t* other = smem + C::OFF_EPI + ((warp - C::SOFT0) ^ 4) * kStoreStageBytes;
         *reinterpret_cast<float2*>(mine + 2048 + lane * 8) = make_float2(m_ref, l_run);
@@ -559,12 +559,11 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         // the next item's products overwrite both accumulators
         if (!warp_wait(&bar[C::B_Y], j & 1, wc)) { ok = false; break; }
       } else if (ok && nh_t > 0) {
-        if (!warp_wait(&bar[C::B_PVD + t], pvd_t & 1, wc)) { ok = false; break; }
+        if (!warp_wait(pvd + t, (j >> 1) & 1, wc)) { ok = false; break; }
         tc_fence_after();
         G::template store<D>(g, it, t, warp & 3, lane, ocol, m_ref, l_run,
                              smem + C::OFF_EPI + (warp - C::SOFT0) * kStoreStageBytes, &tmO, p.d);
         tc_fence_before();  // O_t read out before the next item's products overwrite it
-        ++pvd_t;
       }
       ru += C::QUSES + nkb;
       base_t += nh_t;

@@ -21,7 +21,8 @@ from .packed import _binding, _on_stream
 def fa_cache_append(K, V, cu_seqlens, starts, block_table, K_cache, V_cache, stream=None):
     """Writes rows [cu_seqlens[i], cu_seqlens[i + 1]) of K and V [total, Hkv, d] to the
     cache positions starts[i], starts[i] + 1, ... of request i, in place. K and V may be
-    slices of one projection (any row stride)."""
+    slices of one projection (any row stride). Bounds that decrease or leave the rows, and
+    places out of range, are reported by fa_get_device_status()."""
     if stream is not None:
         with _on_stream(K_cache, stream):
             return fa_cache_append(K, V, cu_seqlens, starts, block_table, K_cache, V_cache)

@@ -77,8 +77,8 @@ def fa_packed_plan(cu_seqlens, total: int, causal: bool = True, plan: PackedPlan
                    stream=None) -> PackedPlan:
     """Plan of the batch with sequence bounds `cu_seqlens` (int32 [nseq + 1] on the
     device, 0 = cu[0] <= ... <= cu[nseq] <= total) in tensors of `total` rows, for causal
-    attention or not. `plan`: an earlier plan of the same sizes to write over, for example
-    where the call is captured in a graph."""
+    attention or not; at least one sequence and one row. `plan`: an earlier plan of the same
+    sizes to write over, for example where the call is captured in a graph."""
     if (not isinstance(cu_seqlens, torch.Tensor) or not cu_seqlens.is_cuda
             or cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1
             or not cu_seqlens.is_contiguous()):
@@ -169,7 +169,9 @@ class FlashAttentionPacked(torch.autograd.Function):
 
 def flash_attention_packed(Q, K, V, plan: PackedPlan, scale: float | None = None):
     """Attention over the plan's packed sequences, differentiable (once) in Q, K and V. The
-    plan has to hold this batch until the backward pass has run. To capture a backward pass
+    plan has to hold this batch until the backward pass has run: writing it over in between
+    is refused, but for the replay of a captured fa_packed_plan, which Python does not see
+    and which gives the gradients of the other batch's bounds. To capture a backward pass
     in a CUDA graph, first drop every eager graph that reaches the same leaves (autograd ties
     a leaf to the stream that first used it, and does not survive waiting for another stream
     during a capture), or capture fa_packed_forward and fa_packed_backward."""

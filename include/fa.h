@@ -221,9 +221,9 @@ FA_API int fa_online_softmax_stats(const float* x, long long rows, long long col
  * L: fp32 [Hq, total]. Heads and columns are dense; Q, K, V and dQ, dK, dV have a row
  * stride of their own (elements from row to row: at least heads * d, a multiple of 8,
  * at most 2^30), so that they may be slices of one [total, (Hq + 2 Hkv) d] projection.
- * O, dO and L are dense. Hq a multiple of Hkv, d as in fa_forward, total <= 2^24,
- * nseq <= 65535, (total / 128 + nseq) * Hq < 2^31. Sequences may be empty. No value of
- * one sequence reaches another's results, NaN included.
+ * O, dO and L are dense. Hq a multiple of Hkv, d as in fa_forward, 1 <= total <= 2^24,
+ * 1 <= nseq <= 65535, (total / 128 + nseq) * Hq < 2^31. Sequences may be empty. No value
+ * of one sequence reaches another's results, NaN included.
  *
  * fa_packed_plan reads cu_seqlens, int32 [nseq + 1] in device memory with
  * 0 = cu_seqlens[0] <= ... <= cu_seqlens[nseq] <= total, and writes the work lists that
@@ -231,9 +231,9 @@ FA_API int fa_online_softmax_stats(const float* x, long long rows, long long col
  * bytes, 16-byte aligned). One plan serves any number of calls on that batch, of any
  * head counts, until it is written again; cu_seqlens is not read after it. `causal`
  * chooses the order of the lists: a plan made for the other setting gives the same
- * results (dK and dV up to the order of their sums), less evenly dealt. Bounds that break the rule give an empty plan (calls
- * that read it write nothing) and FA_ERR_BAD_INDEX in fa_get_device_status(), and so
- * does a plan that was made for another nseq or total.
+ * results (dK and dV up to the order of their sums), less evenly dealt. Bounds that break
+ * the rule give an empty plan (calls that read it write nothing) and FA_ERR_BAD_INDEX in
+ * fa_get_device_status(), and so does a plan that was made for another nseq or total.
  *
  * Rows behind the last sequence (cu_seqlens[nseq] < total) are left as they were.
  * `fill` asks for values there instead: in fa_packed_forward 1 sets them to 0 in O and
@@ -301,10 +301,11 @@ FA_API int fa_cache_append(const void* K, const void* V, long long k_stride, lon
  *   O[b, h] = softmax(scale Q[b, h] K^T) V     L[b, h] = logsumexp of the scores
  * Q, O: bf16 [B, Hq, d], dense; L: fp32 [B, Hq]. prefix_len (int32 [1]) and lens
  * (int32 [B]) are in device memory, so that a captured call follows them. A request
- * without keys gets O = 0 and L = -inf. num_prefix_pages and max_pages may be 0, and the
- * pointers that they size are then not read. Hq a multiple of Hkv, Hq / Hkv <= 128,
- * B <= 8192, ceil(Hq / Hkv / 16) * Hkv * B * max_pages * page < 2^37, d as in
- * fa_forward. `workspace`: caller-owned device memory of at least
+ * without keys gets O = 0 and L = -inf; keys whose scores are -inf (an infinite entry, a
+ * product that overflows) have weight 0 beside others, and alone give O = NaN, L = -inf.
+ * num_prefix_pages and max_pages may be 0, and the pointers that they size are then not
+ * read. Hq a multiple of Hkv, Hq / Hkv <= 128, 1 <= B <= 8192,
+ * ceil(Hq / Hkv / 16) * Hkv * B * max_pages * page < 2^37, d as in fa_forward. `workspace`: caller-owned device memory of at least
  * fa_prefix_workspace_bytes() bytes for num_prefix_pages * page and max_pages * page keys
  * (more for larger capacities), 16-byte aligned, contents on entry do not matter; calls
  * that may run at the same time need one each. Up to three kernel launches on

@@ -32,7 +32,8 @@ BINDING = os.path.join(
 SOURCES = ["fa_api.cu", "fa_forward.cu", "fa_backward.cu", "fa_softmax.cu", "fa_selftest.cu",
            "fa_noalloc.cu", "fa_session.cu", "fa_standard.cu", "fa_packed_plan.cu",
            "fa_packed_forward.cu", "fa_packed_backward.cu", "fa_packed_api.cu",
-           "fa_cache.cu", "fa_prefix.cu", "fa_decode_api.cu"]
+           "fa_cache.cu", "fa_prefix.cu", "fa_decode_api.cu", "fa_rope.cu", "fa_rope_append.cu",
+           "fa_cache4_decode.cu", "fa_rope_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-fvisibility=hidden", "-I" + INCLUDE, "-I" + CSRC]

@@ -68,6 +68,18 @@ SIGNATURES = {
     "fa_prefix_workspace_bytes": (_S, [_I, _I, _I, _I, _I, _I]),
     "fa_prefix_decode": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _P,
                               _P, _P, _S, _P]),
+    "fa_qk_norm_rope": (_I, [_P, _P, _LL, _LL, _I, _I, _I, _I, _P, _P, _P, _P, _LL, _LL, _P]),
+    "fa_qk_norm_rope_workspace_bytes": (_S, [_I, _I, _I]),
+    "fa_qk_norm_rope_backward": (_I, [_P, _P, _LL, _LL, _P, _P, _LL, _LL, _I, _I, _I, _I, _P, _P,
+                                      _P, _P, _LL, _LL, _P, _P, _P, _S, _P]),
+    "fa_rope_append": (_I, [_P, _P, _P, _LL, _LL, _LL, _I, _I, _P, _P, _I, _P, _I, _P, _P, _I, _P,
+                            _P, _I, _I, _I, _I, _P]),
+    "fa_cache4_row_bytes": (_S, [_I]),
+    "fa_cache4_append": (_I, [_P, _P, _P, _LL, _LL, _LL, _I, _I, _P, _P, _I, _P, _I, _P, _P, _I,
+                              _P, _I, _I, _I, _I, _P]),
+    "fa_cache4_read": (_I, [_P, _I, _I, _I, _I, _P, _P, _I, _P, _I, _I, _P, _P, _I, _P]),
+    "fa_cache4_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
+    "fa_cache4_decode": (_I, [_P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _S, _P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_get_device_status": (_I, [ctypes.POINTER(_I)]),
     "fa_version": (_I, []),

@@ -9,6 +9,7 @@
 #include "fa_decode.h"
 #include "fa_internal.h"
 #include "fa_packed.h"
+#include "fa_rope.h"
 #include "sm103.cuh"
 
 namespace fa {
@@ -389,14 +390,16 @@ int fa_get_device_status(int* status_out) {
   // The copies below wait for the default stream alone, not for streams created without
   // that dependence (torch's are).
   if (cudaDeviceSynchronize() != cudaSuccess) return FA_ERR_CUDA;
-  unsigned int f = 0, b = 0, t = 0, sd = 0, pl = 0, pk = 0, pb = 0, ap = 0, px = 0;
+  unsigned int f = 0, b = 0, t = 0, sd = 0, pl = 0, pk = 0, pb = 0, ap = 0, px = 0, ro = 0,
+               ra = 0, d4 = 0;
   if (forward_read_status(&f) != cudaSuccess || bwd_read_status(&b) != cudaSuccess ||
       selftest_read_status(&t) != cudaSuccess || standard_read_status(&sd) != cudaSuccess ||
       plan_read_status(&pl) != cudaSuccess || packed_read_status(&pk) != cudaSuccess ||
       packed_bwd_read_status(&pb) != cudaSuccess || append_read_status(&ap) != cudaSuccess ||
-      prefix_read_status(&px) != cudaSuccess)
+      prefix_read_status(&px) != cudaSuccess || rope_read_status(&ro) != cudaSuccess ||
+      rope_append_read_status(&ra) != cudaSuccess || decode4_read_status(&d4) != cudaSuccess)
     return FA_ERR_CUDA;
-  const unsigned int bits = f | b | t | sd | pl | pk | pb | ap | px;
+  const unsigned int bits = f | b | t | sd | pl | pk | pb | ap | px | ro | ra | d4;
   *status_out = (bits & kDeviceTimeoutBit)  ? FA_ERR_DEVICE_TIMEOUT
                 : (bits & kDeviceLayoutBit) ? FA_ERR_UNSUPPORTED_DEVICE
                 : (bits & kDeviceIndexBit)  ? FA_ERR_BAD_INDEX

@@ -1,0 +1,797 @@
+// Decode attention over the paged cache in 4 bits (fa_cache4.cuh): one new token for each of B
+// requests over its own keys.
+//
+//   split kernel  the keys of all (row tile, key/value head, request) units lie end to end in
+//                 chunks of 64, and every block takes an even piece of that axis (Split),
+//                 whatever the lengths, 16 keys of each chunk per warp. A unit that lies in
+//                 one piece is finished there; else each piece gives a part (o, e) as in
+//                 fa_prefix.cu.
+//   join kernel   joins the parts, and fills the rows of requests without keys.
+//
+// Warp-level products (16 x 8 x 16) with the keys as the 16 rows and the queries of a
+// key/value head as the 8 columns, so that the few queries of grouped heads fill them:
+//   S = K Q^T      K's codes become 128 + code by one logical operation on two codes (bf16 with
+//                  the code as the lowest bits): S = sum over groups of
+//                  scale (sum q (128 + code)) + (min - 128 scale) sum q, in fp32
+//   O^T = V^T P^T  V's as code - 8, exact in bf16, and P times the rows' scales in bf16: the
+//                  offset that is left, min + 8 scale, is about 0 for most data and its
+//                  product with P is summed in fp32. (With 128 + code the sums would be 30
+//                  times larger than what stays of them.)
+// Each warp has a ring of stages of 16 keys, a bulk copy each.
+#include "fa_cache4.cuh"
+#include "fa_launch.h"
+#include "fa_rope.h"
+#include "fa_split.cuh"
+
+namespace fa {
+
+__device__ unsigned int g_decode4_status;
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kRescale = 8.f;  // the reference maximum moves when passed by 2^8
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kChunk = 16 * kWarps;  // keys per step of the split
+constexpr int kMaxSms = 160;         // slots are reserved for this many SMs
+
+// Blocks of the split kernel per SM at most, by the registers: 16 warps of 128, or 12 of 168
+// for two tiles of queries.
+constexpr int per_sm(int NT) { return NT == 1 ? 4 : 3; }
+
+struct Sizes {
+  int B, Hq, Hkv, per_kv, d;
+  int row_tiles;   // tiles of up to 16 queries of a key/value head
+  int slot_rows;
+  int blocks;      // launched
+  float *o, *e;    // [slot][slot_rows][d], [slot][slot_rows]
+  int* first;      // [B + 1] chunks before each request
+};
+
+Sizes sizes_of(int B, int Hq, int Hkv, int d) {
+  Sizes s{};
+  s.B = B;
+  s.Hq = Hq;
+  s.Hkv = Hkv;
+  s.per_kv = Hq / Hkv;
+  s.d = d;
+  s.row_tiles = ceil_div(s.per_kv, 16);
+  s.slot_rows = s.per_kv < 16 ? s.per_kv : 16;
+  return s;
+}
+size_t lay_out(Sizes* s, void* base, int capacity) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* q = p + at;
+    at += (bytes + 255) / 256 * 256;
+    return q;
+  };
+  const size_t units = (size_t)s->Hkv * s->row_tiles * s->B;
+  const size_t steps = units * (((size_t)capacity + kChunk - 1) / kChunk);
+  const size_t workers = (size_t)kMaxSms * per_sm(1);
+  const size_t slots = 2 * (steps < workers ? steps : workers);
+  s->o = reinterpret_cast<float*>(take(slots * s->slot_rows * s->d * 4));
+  s->e = reinterpret_cast<float*>(take(slots * s->slot_rows * 4));
+  s->first = reinterpret_cast<int*>(take(((size_t)s->B + 1) * 4));
+  return at;
+}
+
+struct DecodeParams {
+  Sizes s;
+  const __nv_bfloat16* Q;
+  const uint8_t* cache;
+  const int *table, *lens;
+  __nv_bfloat16* O;
+  float* L;
+  int max_pages, num_pages, page_shift;
+  float scale_log2;
+};
+
+FA_DEV int keys_of(const DecodeParams& p, int b) {
+  return max(0, min(p.lens[b], p.max_pages << p.page_shift));
+}
+
+template <int G, int NT>
+struct Cfg {
+  static constexpr int STAGE = G * kBlock4;
+  static constexpr int STAGES = NT == 1 ? 4 : 3;
+  static constexpr int ROWS = 8 * NT;      // queries of a tile
+  static constexpr int D = 64 * G;
+  static constexpr int RINGS = kWarps * STAGES * STAGE;
+  static constexpr int PARTS = kWarps * ROWS * D * 4;
+  static constexpr int BYTES = RINGS + PARTS;  // then first[B + 1]
+};
+
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned, counted on `bar`.
+FA_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+FA_DEV uint4 ld_shared16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+FA_DEV uint2 ld_shared8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+// Codes e (low half) and e + 4 of a word, or codes e of two rows, as 128 + code in bf16.
+FA_DEV uint32_t codes128(uint32_t w, int e) { return ((w >> (4 * e)) & 0x000f000fu) | 0x43004300u; }
+FA_DEV uint32_t codes0(uint32_t w, int e) {  // as code - 8
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(codes128(w, e)), "r"(0x43084308u));
+  return r;
+}
+// An 8 x 8 matrix of 16-bit values, a row of it in four lanes, transposed.
+FA_DEV uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// A stage's words of one lane: 16 keys of K (rows g and g + 8), of V (rows 2 t, 2 t + 1, 2 t + 8,
+// 2 t + 9), and the pairs of rows g and g + 8.
+template <int G>
+struct Words {
+  uint32_t k[2][2 * G], v[G][4], pair[2][2 * G];
+  FA_DEV void load(uint32_t stage, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = g + 8 * h;
+      if constexpr (G == 2) {
+        const uint4 a = ld_shared16(stage + 4 * k_word4(G, r, 0, 2 * t));
+        const uint4 b = ld_shared16(stage + 4 * pair_word4(G, r, 0, 0));
+        k[h][0] = a.x, k[h][1] = a.y, k[h][2] = a.z, k[h][3] = a.w;
+        pair[h][0] = b.x, pair[h][1] = b.y, pair[h][2] = b.z, pair[h][3] = b.w;
+      } else {
+        const uint2 a = ld_shared8(stage + 4 * k_word4(G, r, 0, 2 * t));
+        const uint2 b = ld_shared8(stage + 4 * pair_word4(G, r, 0, 0));
+        k[h][0] = a.x, k[h][1] = a.y;
+        pair[h][0] = b.x, pair[h][1] = b.y;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      const uint4 a = ld_shared16(stage + 4 * v_word4(G, 2 * t, j, g));
+      v[j][0] = a.x, v[j][1] = a.y, v[j][2] = a.z, v[j][3] = a.w;
+    }
+  }
+};
+
+// The queries of a tile and their running softmax over the keys that a warp has seen. Lane
+// (g, t) has columns (queries) 2 t and 2 t + 1 of every 8 x 8 accumulator.
+template <int G, int NT>
+struct Tile {
+  uint32_t q[NT][G][4][2];
+  float qs[NT][G][2];       // sums of a query over a group
+  float o[NT][G][4][4];     // channels 64 j + 8 g + 2 i + (e / 2), query 2 t + e % 2
+  float z[NT][G][2];        // sums of P (min + 8 scale), of this lane's keys
+  float m[NT][2], l[NT][2], top[NT][2];  // reference, weight sum of this lane's keys, limit
+
+  FA_DEV void load(const __nv_bfloat16* Q, int rows, int d, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        float sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          const int c = 64 * j + 16 * t + 8 * u, row = 8 * n + g;
+          if (row < rows && c < d) w = *reinterpret_cast<const uint4*>(Q + row * d + c);
+          sum += (bf16_lo(w.x) + bf16_hi(w.x)) + (bf16_lo(w.y) + bf16_hi(w.y)) +
+                 ((bf16_lo(w.z) + bf16_hi(w.z)) + (bf16_lo(w.w) + bf16_hi(w.w)));
+          q[n][j][2 * u][0] = __byte_perm(w.x, w.z, 0x5410);
+          q[n][j][2 * u][1] = __byte_perm(w.x, w.z, 0x7632);
+          q[n][j][2 * u + 1][0] = __byte_perm(w.y, w.w, 0x5410);
+          q[n][j][2 * u + 1][1] = __byte_perm(w.y, w.w, 0x7632);
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        qs[n][j][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
+        qs[n][j][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][j][i][e] = 0.f;
+        z[n][j][0] = z[n][j][1] = 0.f;
+      }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[n][e] = top[n][e] = -INFINITY, l[n][e] = 0.f;
+  }
+
+  // The first `keys` of a stage's 16 keys.
+  FA_DEV void step(const Words<G>& w, int keys, float c, float room, int lane) {
+    const int g = lane >> 2;
+    float sk[2][G], zk[2][G], sv[2][G], zv[2][G];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        sk[h][j] = bf16_lo(w.pair[h][j]);
+        zk[h][j] = fmaf(-128.f, sk[h][j], bf16_hi(w.pair[h][j]));
+        sv[h][j] = bf16_lo(w.pair[h][G + j]);
+        zv[h][j] = fmaf(8.f, sv[h][j], bf16_hi(w.pair[h][G + j]));
+      }
+    float s[NT][4];
+    {
+      float acc[NT][G][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][j][i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t w0 = w.k[0][2 * j + x / 2], w1 = w.k[1][2 * j + x / 2];
+          const int e = 2 * (x & 1);
+          const uint32_t a[4] = {codes128(w0, e), codes128(w1, e), codes128(w0, e + 1),
+                                 codes128(w1, e + 1)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_16816(acc[n][j], a, q[n][j][x][0], q[n][j][x][1]);
+        }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[n][i] = 0.f;
+#pragma unroll
+          for (int j = 0; j < G; ++j)
+            s[n][i] = fmaf(sk[i >> 1][j], acc[n][j][i],
+                           fmaf(zk[i >> 1][j], qs[n][j][i & 1], s[n][i]));
+        }
+    }
+    if (keys < 16) {  // what lies behind the keys may be anything
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (g + 8 * h >= keys) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) s[n][2 * h] = s[n][2 * h + 1] = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < G; ++j) sv[h][j] = zv[h][j] = 0.f;
+        }
+    }
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) over |= fmaxf(s[n][e], s[n][2 + e]) > top[n][e];
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(s[n][e], s[n][2 + e]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          x = fmaxf(x, m[n][e]);
+          const float f = x == -INFINITY ? 1.f : ex2((m[n][e] - x) * c);
+          m[n][e] = x;
+          top[n][e] = x + room;
+          l[n][e] *= f;
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            z[n][j][e] *= f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              o[n][j][i][e] *= f;
+              o[n][j][i][2 + e] *= f;
+            }
+          }
+        }
+    }
+    uint32_t b[NT][G][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ref = m[n][e] == -INFINITY ? 0.f : -m[n][e] * c;
+        p[e] = ex2(fmaf(s[n][e], c, ref));
+        p[2 + e] = ex2(fmaf(s[n][2 + e], c, ref));
+        l[n][e] += p[e] + p[2 + e];
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+          z[n][j][e] = fmaf(p[e], zv[0][j], fmaf(p[2 + e], zv[1][j], z[n][j][e]));
+      }
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          b[n][j][h] =
+              transpose8(pack_bf16(p[2 * h] * sv[h][j], p[2 * h + 1] * sv[h][j]));
+    }
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      const uint32_t two[2][2] = {
+          {__byte_perm(w.v[j][0], w.v[j][1], 0x5410), __byte_perm(w.v[j][2], w.v[j][3], 0x5410)},
+          {__byte_perm(w.v[j][0], w.v[j][1], 0x7632), __byte_perm(w.v[j][2], w.v[j][3], 0x7632)}};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w0 = two[i / 2][0], w1 = two[i / 2][1];
+        const int e = 2 * (i & 1);
+        const uint32_t a[4] = {codes0(w0, e), codes0(w0, e + 1), codes0(w1, e), codes0(w1, e + 1)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_16816(o[n][j][i], a, b[n][j][0], b[n][j][1]);
+      }
+    }
+  }
+
+  // The sums over the lanes that share a query.
+  FA_DEV void finish() {
+    auto all = [](float v) {
+      v += __shfl_xor_sync(0xffffffffu, v, 4);
+      v += __shfl_xor_sync(0xffffffffu, v, 8);
+      return v + __shfl_xor_sync(0xffffffffu, v, 16);
+    };
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[n][e] = all(l[n][e]);
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          const float add = all(z[n][j][e]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[n][j][i][e] += add;
+            o[n][j][i][2 + e] += add;
+          }
+        }
+      }
+  }
+
+  // Rows [0, 8 NT) of o as floats [row][64 G]: two channels at a time, pair x of every four
+  // at x ^ (row % 8 / 2), which puts a half warp's stores into different banks.
+  FA_DEV void store(float* part, int lane) const {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float2*>(part + (8 * n + 2 * t + e) * 64 * G + 64 * j + 8 * g +
+                                       2 * (i ^ t)) =
+                make_float2(o[n][j][i][e], o[n][j][i][2 + e]);
+  }
+  // Columns c .. c + 3 (c a multiple of 4) of a row that store() wrote.
+  FA_DEV static float4 fetch(const float* part, int row, int c) {
+    const int t = (row & 7) >> 1, x = (c & 7) / 2;
+    const float* at = part + row * 64 * G + (c & ~7);
+    const float2 a = *reinterpret_cast<const float2*>(at + 2 * (x ^ t));
+    const float2 b = *reinterpret_cast<const float2*>(at + 2 * ((x + 1) ^ t));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+};
+
+FA_DEV float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }  // of a part
+
+template <int G, int NT>
+__global__ void __launch_bounds__(kThreads, per_sm(NT))
+    decode4_kernel(const __grid_constant__ DecodeParams p) {
+  using C = Cfg<G, NT>;
+  extern __shared__ __align__(128) uint8_t smem4[];
+  __shared__ uint64_t full[kWarps][C::STAGES];
+  __shared__ float2 stats[kWarps][C::ROWS];  // a warp's reference and weight sum
+  __shared__ int warp_sums[kWarps];
+  __shared__ uint32_t abort_flag, never;
+  const Sizes& s = p.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* const parts = reinterpret_cast<float*>(smem4 + C::RINGS);
+  int* const first = reinterpret_cast<int*>(smem4 + C::BYTES);
+
+  if (lane == 0) {
+    for (int i = 0; i < C::STAGES; ++i) mbar_init(&full[warp][i], 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) abort_flag = never = 0;
+  grid_wait();
+  grid_launch_dependents();
+
+  // Chunks before each request (exclusive scan of the lengths).
+  int run = 0;
+  for (int b0 = 0; b0 < s.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int n = 0;
+    if (b < s.B) {
+      const int len = p.lens[b];
+      if ((len < 0 || len > p.max_pages << p.page_shift) && blockIdx.x == 0)
+        atomicOr(&g_decode4_status, kDeviceIndexBit);
+      n = (max(0, min(len, p.max_pages << p.page_shift)) + kChunk - 1) / kChunk;
+    }
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int before = run, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += warp_sums[w];
+      sum += warp_sums[w];
+    }
+    if (b < s.B) first[b] = before + x - n;
+    run += sum;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) first[s.B] = run;
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b <= s.B; b += kThreads) s.first[b] = first[b];
+
+  const int chunks = run;  // of one (head, row tile)
+  const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)chunks, (unsigned)s.blocks);
+  const int me = (int)blockIdx.x;
+  if (me >= sp.workers) return;
+  const unsigned x_begin = sp.start(me), x_end = sp.start(me + 1);
+
+  // A run of chunks of one unit.
+  struct Run {
+    int b, ht, len;
+    unsigned x0, x1, u0, u1;  // this run's chunks, the unit's chunks
+  };
+  auto run_at = [&](unsigned x) {
+    Run r;
+    r.ht = (int)(x / (unsigned)chunks);
+    const int in = (int)(x - (unsigned)(r.ht * chunks));
+    int lo = 0, hi = s.B;  // first[lo] <= in < first[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= in)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    r.b = lo;
+    r.u0 = (unsigned)(r.ht * chunks + first[lo]);
+    r.u1 = (unsigned)(r.ht * chunks + first[lo + 1]);
+    r.x0 = x;
+    r.x1 = min(r.u1, x_end);
+    r.len = keys_of(p, lo);
+    return r;
+  };
+
+  const uint32_t ring = smem_u32(smem4) + warp * C::STAGES * C::STAGE;
+  const WaitCtx wait{&abort_flag, &g_decode4_status};
+  // ---- the issuing side, up to STAGES stages ahead of the products
+  Run ir = run_at(x_begin);
+  unsigned ix = x_begin;      // its chunk
+  int ids = 0, i_at = 32;     // pages of 32 chunks from ix - i_at on, one per lane
+  int i_stage = 0, issued = 0;
+  bool more = true;
+  // Moves on to a chunk in which this warp has keys.
+  auto settle = [&]() {
+    for (;;) {
+      if (ix == ir.x1) {
+        if (ix == x_end) {
+          more = false;
+          return;
+        }
+        ir = run_at(ix);
+        i_at = 32;
+      }
+      if ((int)(ix - ir.u0) * kChunk + 16 * warp < ir.len) return;
+      ++ix;  // the unit's last chunk
+    }
+  };
+  settle();
+  auto issue = [&]() {
+    if (!more) return;
+    const int key = (int)(ix - ir.u0) * kChunk + 16 * warp;
+    if (i_at == 32) {
+      const int mine = key + lane * kChunk;
+      ids = 0;
+      if (ix + lane < ir.x1 && mine < ir.len)
+        ids = p.table[(size_t)ir.b * p.max_pages + (mine >> p.page_shift)];
+      if ((unsigned)ids >= (unsigned)p.num_pages) {
+        atomicOr(&g_decode4_status, kDeviceIndexBit);
+        ids = 0;
+      }
+      i_at = 0;
+    }
+    const int page = __shfl_sync(0xffffffffu, ids, i_at);
+    if (lane == 0) {
+      const int hk = ir.ht / s.row_tiles, in = key & ((1 << p.page_shift) - 1);
+      const uint8_t* src =
+          p.cache + ((((size_t)page * s.Hkv + hk) << p.page_shift) + in) * (C::STAGE / 16);
+      uint64_t* bar = &full[warp][i_stage];
+      mbar_arrive_expect_tx(bar, C::STAGE);
+      bulk_load(ring + i_stage * C::STAGE, src, C::STAGE, bar);
+    }
+    i_stage = i_stage + 1 == C::STAGES ? 0 : i_stage + 1;
+    ++issued;
+    ++i_at;
+    ++ix;
+    settle();
+  };
+  __syncwarp();  // the barriers are initialised
+#pragma unroll
+  for (int i = 0; i < C::STAGES; ++i) issue();
+
+  // ---- the products
+  const float room = kRescale / p.scale_log2;
+  int stage = 0, used = 0;
+  uint32_t phase = 0;
+  bool alive = true;
+  Tile<G, NT> tile;
+  for (unsigned x = x_begin; x < x_end;) {
+    const Run r = run_at(x);
+    x = r.x1;
+    const int hk = r.ht / s.row_tiles, rt = r.ht - hk * s.row_tiles;
+    const int rows = min(16, s.per_kv - rt * 16);
+    const size_t row0 = (size_t)r.b * s.Hq + hk * s.per_kv + rt * 16;
+    tile.load(p.Q + row0 * s.d, rows, s.d, lane);
+    for (unsigned c = r.x0; c < r.x1; ++c) {
+      const int n = r.len - ((int)(c - r.u0) * kChunk + 16 * warp);
+      if (n <= 0) break;
+      if (alive) alive = warp_wait(&full[warp][stage], phase, wait);
+      if (!alive) break;
+      Words<G> w;
+      w.load(ring + stage * C::STAGE, lane);
+      ++used;
+      if (++stage == C::STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      __syncwarp();  // every lane has read the stage: it may be filled again
+      issue();
+      tile.step(w, n, p.scale_log2, room, lane);
+    }
+    tile.finish();
+    tile.store(parts + warp * C::ROWS * C::D, lane);
+    if (lane < 4) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          stats[warp][8 * n + 2 * lane + e] =
+              make_float2(tile.m[n][e] * p.scale_log2, tile.l[n][e]);
+    }
+    __syncthreads();
+    const bool whole = r.x0 == r.u0 && r.x1 == r.u1;
+    const unsigned slot = 2u * (unsigned)me + (r.x0 == r.u0 ? 1u : 0u);  // Split::slot
+    for (int i = threadIdx.x; i < rows * (C::D / 4); i += kThreads) {
+      const int row = i / (C::D / 4), c = (i - row * (C::D / 4)) * 4;
+      if (c >= s.d) continue;
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) top = fmaxf(top, stats[k][row].x);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float2 ml = stats[k][row];
+        const float f = ex2(ml.x - ref);
+        const float4 v = Tile<G, NT>::fetch(parts + k * C::ROWS * C::D, row, c);
+        sum += f * ml.y;
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+      }
+      if (whole) {
+        const float inv = 1.f / sum;
+        *reinterpret_cast<uint2*>(p.O + (row0 + row) * s.d + c) = make_uint2(
+            pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        if (c == 0) p.L[row0 + row] = (top + lg2(sum)) * kLn2;
+      } else {
+        const float inv = inverse(sum);
+        const size_t at = (size_t)slot * s.slot_rows + row;
+        *reinterpret_cast<float4*>(s.o + at * s.d + c) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (c == 0) s.e[at] = top + lg2(sum);
+      }
+    }
+    __syncthreads();  // the parts are read
+  }
+  // After a wait that ran out: the copies in flight land before the block's memory is given up.
+  const WaitCtx drain{&never, &g_decode4_status};
+  while (used < issued) {
+    warp_wait(&full[warp][stage], phase, drain);
+    ++used;
+    if (++stage == C::STAGES) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+}
+
+// A row (request, query head) is joined by one warp, or by kJoinWarps where there are few rows:
+// lane i looks up part i's slot and e, then the warp adds the parts up, four columns a lane.
+// Rows that the split kernel has finished are left alone.
+constexpr int kJoinWarps = 8;
+template <int WARPS>  // of a row
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    join4_kernel(const __grid_constant__ DecodeParams p) {
+  __shared__ float4 sums[kJoinWarps][32];
+  __shared__ float2 stats[kJoinWarps];
+  const Sizes& s = p.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = WARPS == 1 ? blockIdx.x * kJoinWarps + warp : blockIdx.x;
+  const int mine = WARPS == 1 ? 0 : warp;
+  grid_wait();
+  grid_launch_dependents();
+  if (row >= s.B * s.Hq) return;  // WARPS == 1 only: no barrier follows
+  const int b = row / s.Hq, hq = row - b * s.Hq;
+  const int hk = hq / s.per_kv, in = hq - hk * s.per_kv, ht = hk * s.row_tiles + in / 16;
+  const int chunks = s.first[s.B], f0 = s.first[b], f1 = s.first[b + 1];
+  if (f0 == f1) {
+    if (mine == 0 && 4 * lane < s.d)
+      reinterpret_cast<uint2*>(p.O + (size_t)row * s.d)[lane] = make_uint2(0, 0);
+    if (mine == 0 && lane == 0) p.L[row] = -INFINITY;
+    return;
+  }
+  const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)chunks, (unsigned)s.blocks);
+  const int w0 = sp.owner((unsigned)(ht * chunks + f0));
+  const int parts = sp.owner((unsigned)(ht * chunks + f1) - 1u) - w0 + 1;
+  if (parts == 1) return;
+
+  float ref = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int base = 0; base < parts; base += 32 * WARPS) {
+    const int i = base + lane * WARPS + mine;
+    unsigned long long at = 0;
+    float e = -INFINITY;
+    if (i < parts) {
+      at = (unsigned long long)Split::slot(0, 0, parts, w0, i) * s.slot_rows + in % 16;
+      e = s.e[at];
+    }
+    float top = e;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float next = fmaxf(ref, top);
+    const float back = ref == next ? 1.f : ex2(ref - next);  // 0 on the first round
+    ref = next;
+    const float weight = i < parts ? ex2(e - (ref == -INFINITY ? 0.f : ref)) : 0.f;
+    sum = sum * back + weight;  // this lane's parts
+    acc.x *= back;
+    acc.y *= back;
+    acc.z *= back;
+    acc.w *= back;
+    const int n = min(32, (parts - base - mine + WARPS - 1) / WARPS);  // lanes with a part
+    constexpr int U = 4;
+    for (int j = 0; j < n; j += U) {
+      float4 v[U];
+      float w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const unsigned long long from = __shfl_sync(0xffffffffu, at, (j + u) & 31);
+        w[u] = __shfl_sync(0xffffffffu, weight, (j + u) & 31);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j + u < n && 4 * lane < s.d)
+          v[u] = reinterpret_cast<const float4*>(s.o + from * s.d)[lane];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (j + u >= n) break;
+        acc.x += w[u] * v[u].x;
+        acc.y += w[u] * v[u].y;
+        acc.z += w[u] * v[u].z;
+        acc.w += w[u] * v[u].w;
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  if (WARPS > 1) {
+    sums[warp][lane] = acc;
+    if (lane == 0) stats[warp] = make_float2(ref, sum);
+    __syncthreads();
+    if (warp != 0) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, stats[w].x);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      // a warp without parts has reference -inf and adds nothing
+      const float f = w < parts ? ex2(stats[w].x - (top == -INFINITY ? 0.f : top)) : 0.f;
+      const float4 v = sums[w][lane];
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+      sum += f * stats[w].y;
+    }
+    ref = top;
+  }
+  const float inv = 1.f / sum;
+  if (4 * lane < s.d)
+    reinterpret_cast<uint2*>(p.O + (size_t)row * s.d)[lane] =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (lane == 0) p.L[row] = (ref + lg2(sum)) * kLn2;
+}
+
+int sm_count() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms < kMaxSms ? sms : kMaxSms;
+}
+
+template <int G, int NT>
+cudaError_t launch(const Decode4Args& a, cudaStream_t stream) {
+  using C = Cfg<G, NT>;
+  DecodeParams p;
+  p.s = sizes_of(a.B, a.Hq, a.Hkv, a.d);
+  lay_out(&p.s, a.workspace, a.max_pages * a.page);
+  const int sms = sm_count(), smem = C::BYTES + (a.B + 1) * 4;
+  // As many blocks as fit (an SM has 227 KB for them, and 1 KB of each is the system's), and no
+  // more than the capacities can keep busy.
+  const int fit = 227 * 1024 / (smem + 1024 + 1024), most = fit < per_sm(NT) ? fit : per_sm(NT);
+  const long long steps =
+      (long long)a.Hkv * p.s.row_tiles * a.B * ceil_div(a.max_pages * a.page, kChunk);
+  const long long blocks = (long long)sms * most;
+  p.s.blocks = (int)(blocks < steps ? blocks : steps > 0 ? steps : 1);
+  p.Q = static_cast<const __nv_bfloat16*>(a.Q);
+  p.cache = static_cast<const uint8_t*>(a.cache);
+  p.table = a.table;
+  p.lens = a.lens;
+  p.O = static_cast<__nv_bfloat16*>(a.O);
+  p.L = a.L;
+  p.max_pages = a.max_pages;
+  p.num_pages = a.num_pages;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < a.page) ++p.page_shift;
+  p.scale_log2 = a.scale * kLog2e;
+  cudaError_t e =
+      cudaFuncSetAttribute(decode4_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           C::BYTES + (8192 + 1) * 4);
+  if (e != cudaSuccess) return e;
+  e = launch_early(decode4_kernel<G, NT>, dim3((unsigned)p.s.blocks), kThreads, smem, stream, p);
+  if (e != cudaSuccess) return e;
+  const int rows = a.B * a.Hq;
+  // A warp per row once there is a row for every fourth warp slot of the GPU's SMs.
+  return rows >= sms * 4
+             ? launch_early(join4_kernel<1>, dim3((unsigned)ceil_div(rows, kJoinWarps)),
+                            32 * kJoinWarps, 0, stream, p)
+             : launch_early(join4_kernel<kJoinWarps>, dim3((unsigned)rows), 32 * kJoinWarps, 0,
+                            stream, p);
+}
+
+}  // namespace
+
+size_t decode4_workspace_bytes(int B, int Hq, int Hkv, int d, int capacity) {
+  Sizes s = sizes_of(B, Hq, Hkv, d);
+  return lay_out(&s, nullptr, capacity);
+}
+
+cudaError_t launch_decode4(const Decode4Args& a, cudaStream_t s) {
+  const bool two = a.Hq / a.Hkv > 8;
+  if (a.d > 64) return two ? launch<2, 2>(a, s) : launch<2, 1>(a, s);
+  return two ? launch<1, 2>(a, s) : launch<1, 1>(a, s);
+}
+
+cudaError_t decode4_read_status(unsigned int* out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_decode4_status, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_decode4_status, &zero, sizeof(unsigned int));
+}
+
+}  // namespace fa

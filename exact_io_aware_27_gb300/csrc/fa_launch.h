@@ -18,10 +18,10 @@ namespace fa {
 // when it ends: with the blocks of the next one placed as SMs came free, packed training of
 // 16384 rows took 4 % longer.
 template <class... P, class... A>
-cudaError_t launch_as(void (*kernel)(P...), unsigned grid, int threads, int smem,
+cudaError_t launch_as(void (*kernel)(P...), dim3 grid, int threads, int smem,
                       cudaStream_t stream, bool early, unsigned cluster, A... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
@@ -40,7 +40,7 @@ cudaError_t launch_as(void (*kernel)(P...), unsigned grid, int threads, int smem
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 template <class... P, class... A>
-cudaError_t launch_early(void (*kernel)(P...), unsigned grid, int threads, int smem,
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem,
                          cudaStream_t stream, A... args) {
   return launch_as(kernel, grid, threads, smem, stream, true, 1, args...);
 }

@@ -320,6 +320,129 @@ FA_API int fa_prefix_decode(const void* Q, const void* K_cache, const void* V_ca
                             float* L, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Between projection and attention: queries and keys, each head's row of d channels
+ * divided by its root mean square and times a weight (the norm), and its first `rot`
+ * channels turned by the angles of the row's position (the rotation).
+ *   n = x / sqrt(mean(x^2) + eps),  u = n o weight,
+ *   (a, b) -> (a cos - b sin, b cos + a sin)   for the pairs of u's first rot channels:
+ *   (i, i + rot / 2), or with `interleaved` (2 i, 2 i + 1), turned by angle i.
+ * q_weight and k_weight: bf16 [d], NULL for no norm of that tensor. cos_sin: fp32
+ * [positions, rot], the cosines of a position's rot / 2 angles, then the sines; NULL for no
+ * rotation (positions, rot and interleaved are then not read). rot: a multiple of 8, at most d.
+ * eps: finite, at least 0. The weights 8-byte, cos_sin 16-byte aligned. All of it is computed
+ * in fp32 and rounded once.
+ */
+typedef struct fa_rope {
+  const void* q_weight;
+  const void* k_weight;
+  const float* cos_sin;
+  int positions, rot, interleaved;
+  float eps;
+} fa_rope;
+
+/*
+ * fa_qk_norm_rope: Qo = norm and rotation of Q, bf16 [total, Hq, d], and Ko of K, bf16
+ * [total, Hkv, d], all with row strides of their own (as in fa_packed_forward), row t at
+ * position positions[t] (int32 [total] in device memory; may be NULL without rotation). Qo may
+ * be Q (with its stride) and Ko K: the rows are then changed in place. Otherwise outputs must
+ * not overlap inputs. A position outside [0, how->positions) gives FA_ERR_BAD_INDEX in
+ * fa_get_device_status(); that row is not written. 1 <= total <= 2^24, 1 <= Hq, Hkv <= 65535,
+ * d as in fa_forward. One kernel launch.
+ *
+ * fa_qk_norm_rope_backward: for gradients dQo and dKo of the outputs, dQ and dK of the inputs,
+ * and the gradients dq_weight and dk_weight, fp32 [d], of the weights that there are (summed
+ * over all rows and heads in an order that depends on the sizes alone; rows whose position is
+ * out of range add nothing). Q and K are the forward's inputs; each may be NULL if it has no
+ * weight. `workspace`: caller-owned device memory of fa_qk_norm_rope_workspace_bytes() bytes,
+ * 16-byte aligned, contents on entry do not matter; calls that may run at the same time need
+ * one each; may be NULL without weights. One or two kernel launches.
+ */
+FA_API int fa_qk_norm_rope(const void* Q, const void* K, long long q_stride, long long k_stride,
+                           int total, int Hq, int Hkv, int d, const int* positions,
+                           const fa_rope* how, void* Qo, void* Ko, long long qo_stride,
+                           long long ko_stride, void* stream);
+FA_API size_t fa_qk_norm_rope_workspace_bytes(int Hq, int Hkv, int d);
+FA_API int fa_qk_norm_rope_backward(const void* dQo, const void* dKo, long long dqo_stride,
+                                    long long dko_stride, const void* Q, const void* K,
+                                    long long q_stride, long long k_stride, int total, int Hq,
+                                    int Hkv, int d, const int* positions, const fa_rope* how,
+                                    void* dQ, void* dK, long long dq_stride, long long dk_stride,
+                                    float* dq_weight, float* dk_weight, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
+ * fa_rope_append: fa_cache_append with the norm and rotation on the way: K's rows are normed,
+ * turned by the angles of the cache positions that they go to, and written, V's are written as
+ * they are, and the queries Q, bf16 [total, Hq, d] with a row stride of their own, come back
+ * normed and turned in Qo, bf16 [total, Hq, d], dense (Q and Qo may be NULL with Hq = 0: keys
+ * and values only). Sizes, tables, and what happens to indices out of range, as in
+ * fa_cache_append; a position that cos_sin has no row for counts as out of range too. Rows of
+ * Qo behind the last request, or without a position, are left as they were, or set to 0 where
+ * `fill` is 1. One kernel launch.
+ */
+FA_API int fa_rope_append(const void* Q, const void* K, const void* V, long long q_stride,
+                          long long k_stride, long long v_stride, int total, int Hq,
+                          const int* cu_seqlens, const int* starts, int nseq,
+                          const int* block_table, int max_pages, const fa_rope* how, void* Qo,
+                          int fill, void* K_cache, void* V_cache, int num_pages, int Hkv, int page,
+                          int d, void* stream);
+
+/*
+ * Paged cache in 4 bits: keys and values of G = 1 (d <= 64) or 2 groups of 64 channels in
+ * 72 G bytes a row (256 G for bf16), in one tensor uint8 [num_pages, Hkv, page / 16, 1152 G],
+ * 16-byte aligned; pages and tables as in the bf16 cache. Each row and group of K and of V has
+ * a pair in bf16,
+ *   min = bf16(min x),  scale = bf16(max(max x - min, 0) / 15),
+ * and a code of 0 .. 15 for each channel, the nearest (of a tie the even one) to
+ * (x - min) / scale, 0 where scale is 0; it stands for min + scale * code. Values are off by at
+ * most half a scale where min and scale are exact, and by 2^-8 of the group's largest
+ * magnitude more where they are rounded. A group with a value that is not finite, or whose
+ * range is not, is held as NaN. A block of 16 rows of a head is 288 G 32-bit words:
+ *   codes of 8 channels, 8 w .. 8 w + 7 of group j, the lowest in the lowest four bits, of row r
+ *     K   at word 8 G r + 2 G (w / 2) + 2 j + w % 2
+ *     V   at word 128 G + 128 j + 16 w + 4 (r % 8 / 2) + r % 2 + 2 (r / 8)
+ *   pairs, scale in the lower half, min in the upper, of row r and group j
+ *     K   at word 256 G + 2 G r + j        V   at word 256 G + 2 G r + G + j
+ * fa_cache4_row_bytes(d): 72 G, 0 for a d that is not supported.
+ *
+ * fa_cache4_append: fa_rope_append into such a cache, K in 4 bits from its normed and turned
+ * values in fp32. One kernel launch.
+ *
+ * fa_cache4_read: rows back in bf16, for attention of more than one token to what the cache
+ * holds: rows [cu_seqlens[i], cu_seqlens[i + 1]) of K and V, bf16 [total, Hkv, d], dense, are
+ * positions starts[i], starts[i] + 1, ... of request i. Bounds as in fa_cache_append. Rows
+ * behind the last request, and rows whose place is out of range (FA_ERR_BAD_INDEX in
+ * fa_get_device_status()), are left as they were, or set to 0 where `fill` is 1. One launch.
+ *
+ * fa_cache4_decode: one new token for each of B requests over the first lens[b] positions of
+ * its row of block_table, as in fa_prefix_decode without a prefix: Q, O bf16 [B, Hq, d], dense;
+ * L fp32 [B, Hq]; lens int32 [B] in device memory; O = 0 and L = -inf for a request without
+ * keys. The products take the codes as they are and the scores and sums in fp32; the weights
+ * times the scales are rounded to bf16. Entries of Q above 2^96 in magnitude may give NaN.
+ * Hq a multiple of Hkv, Hq / Hkv <= 128, 1 <= B <= 8192, ceil(Hq / Hkv / 16) * Hkv * B *
+ * max_pages * page < 2^37. `workspace`: caller-owned device memory of at least
+ * fa_cache4_workspace_bytes() bytes for `capacity` = max_pages * page keys a request (more for
+ * larger capacities), 16-byte aligned, contents on entry do not matter; calls that may run at
+ * the same time need one each. Up to two kernel launches.
+ */
+FA_API size_t fa_cache4_row_bytes(int d);
+FA_API int fa_cache4_append(const void* Q, const void* K, const void* V, long long q_stride,
+                            long long k_stride, long long v_stride, int total, int Hq,
+                            const int* cu_seqlens, const int* starts, int nseq,
+                            const int* block_table, int max_pages, const fa_rope* how, void* Qo,
+                            int fill, void* cache, int num_pages, int Hkv, int page, int d,
+                            void* stream);
+FA_API int fa_cache4_read(const void* cache, int num_pages, int Hkv, int page, int d,
+                          const int* cu_seqlens, const int* starts, int nseq,
+                          const int* block_table, int max_pages, int total, void* K, void* V,
+                          int fill, void* stream);
+FA_API size_t fa_cache4_workspace_bytes(int B, int Hq, int Hkv, int d, int capacity);
+FA_API int fa_cache4_decode(const void* Q, const void* cache, const int* block_table,
+                            int max_pages, const int* lens, int B, int Hq, int Hkv, int d,
+                            int num_pages, int page, float scale, void* O, float* L,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Host-buffer sessions: one forward + backward step whose inputs and outputs are
  * in host memory, for callers that keep their tensors on the host. A session owns
  * device buffers for `chunk_heads` heads at a time (four sets), a backward

@@ -2,22 +2,22 @@
 // requests over its own keys.
 //
 //   split kernel  the keys of all (row tile, key/value head, request) units lie end to end in
-//                 chunks of 64, and every block takes an even piece of that axis (Split),
-//                 whatever the lengths, 16 keys of each chunk per warp. A unit that lies in
+//                 chunks of 128, and every block takes an even piece of that axis (Split),
+//                 whatever the lengths, 32 keys of each chunk per warp. A unit that lies in
 //                 one piece is finished there; else each piece gives a part (o, e) as in
 //                 fa_prefix.cu.
 //   join kernel   joins the parts, and fills the rows of requests without keys.
 //
 // Warp-level products (16 x 8 x 16) with the keys as the 16 rows and the queries of a
 // key/value head as the 8 columns, so that the few queries of grouped heads fill them:
-//   S = K Q^T      K's codes become 128 + code by one logical operation on two codes (bf16 with
-//                  the code as the lowest bits): S = sum over groups of
-//                  scale (sum q (128 + code)) + (min - 128 scale) sum q, in fp32
-//   O^T = V^T P^T  V's as code - 8, exact in bf16, and P times the rows' scales in bf16: the
-//                  offset that is left, min + 8 scale, is about 0 for most data and its
-//                  product with P is summed in fp32. (With 128 + code the sums would be 30
-//                  times larger than what stays of them.)
-// Each warp has a ring of stages of 16 keys, a bulk copy each.
+//   S = K Q^T      = sum over groups of scale (q . code) + min (sum q), in fp32
+//   O^T = V^T P^T  = (P scale) . code, and P min, summed in fp32
+// A code alone in the lowest four bits of a 16-bit number is, read as fp16, code 2^-24, and in
+// the next four code 2^-20: two logical operations and half a shift turn two codes into
+// operands, exactly, without an addition. Q is brought to a largest value of 256 to 512 by a
+// power of two for each query, and P scale, rounded to fp16, by one for each warp that
+// follows the largest scale it has met: values below 2^-24 of that lose bits.
+// Each warp has a ring of two stages of 32 keys, two bulk copies each.
 #include "fa_cache4.cuh"
 #include "fa_launch.h"
 #include "fa_rope.h"
@@ -33,7 +33,8 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 constexpr float kRescale = 8.f;  // the reference maximum moves when passed by 2^8
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kChunk = 16 * kWarps;  // keys per step of the split
+constexpr int kKeys = 32;              // keys of a warp's stage: two blocks of the cache
+constexpr int kChunk = kKeys * kWarps;  // keys per step of the split
 constexpr int kMaxSms = 160;         // slots are reserved for this many SMs
 
 // Blocks of the split kernel per SM at most, by the registers: 16 warps of 128, or 12 of 168
@@ -95,8 +96,9 @@ FA_DEV int keys_of(const DecodeParams& p, int b) {
 
 template <int G, int NT>
 struct Cfg {
-  static constexpr int STAGE = G * kBlock4;
-  static constexpr int STAGES = NT == 1 ? 4 : 3;
+  static constexpr int BLOCK = G * kBlock4;
+  static constexpr int STAGE = 2 * BLOCK;
+  static constexpr int STAGES = 2;
   static constexpr int ROWS = 8 * NT;      // queries of a tile
   static constexpr int D = 64 * G;
   static constexpr int RINGS = kWarps * STAGES * STAGE;
@@ -125,12 +127,32 @@ FA_DEV uint2 ld_shared8(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
-// Codes e (low half) and e + 4 of a word, or codes e of two rows, as 128 + code in bf16.
-FA_DEV uint32_t codes128(uint32_t w, int e) { return ((w >> (4 * e)) & 0x000f000fu) | 0x43004300u; }
-FA_DEV uint32_t codes0(uint32_t w, int e) {  // as code - 8
+// Codes e of the halves of a word in fp16, times 2^-24 (e even) or 2^-20.
+FA_DEV uint32_t codes(uint32_t w, int e) {
+  return (e < 2 ? w : w >> 8) & (e & 1 ? 0x00f000f0u : 0x000f000fu);
+}
+FA_DEV uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(codes128(w, e)), "r"(0x43084308u));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+FA_DEV void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+FA_DEV void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// The power of two at or below x, at least 2^-100.
+FA_DEV float power_of_two(float x) {
+  return fmaxf(__uint_as_float(__float_as_uint(x) & 0x7f800000u), 0x1p-100f);
 }
 // An 8 x 8 matrix of 16-bit values, a row of it in four lanes, transposed.
 FA_DEV uint32_t transpose8(uint32_t v) {
@@ -170,36 +192,60 @@ struct Words {
 };
 
 // The queries of a tile and their running softmax over the keys that a warp has seen. Lane
-// (g, t) has columns (queries) 2 t and 2 t + 1 of every 8 x 8 accumulator.
+// (g, t) has columns (queries) 2 t and 2 t + 1 of every 8 x 8 accumulator. Scores are in units
+// of a query's own: c is what makes them exponents of 2.
 template <int G, int NT>
 struct Tile {
-  uint32_t q[NT][G][4][2];
-  float qs[NT][G][2];       // sums of a query over a group
+  uint32_t q[NT][G][4][2];  // every second pair divided by 16
+  float qs[NT][G][2];       // sums of a query over a group, times 2^-24
+  float c[NT][2];
   float o[NT][G][4][4];     // channels 64 j + 8 g + 2 i + (e / 2), query 2 t + e % 2
-  float z[NT][G][2];        // sums of P (min + 8 scale), of this lane's keys
-  float m[NT][2], l[NT][2], top[NT][2];  // reference, weight sum of this lane's keys, limit
+  float z[NT][G][2];        // sums of P min, of this lane's keys
+  // reference, -c times it (0 if there is none yet), weight sum of this lane's keys, and the
+  // score that moves the reference
+  float m[NT][2], ref[NT][2], l[NT][2], top[NT][2];
+  float v_ref, v_inv, v_top;  // o is in units of v_ref; the scale that moves it
 
-  FA_DEV void load(const __nv_bfloat16* Q, int rows, int d, int lane) {
+  FA_DEV void load(const __nv_bfloat16* Q, int rows, int d, float scale_log2, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      uint4 w[G][2];
+      float most = 0.f;
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int c0 = 64 * j + 16 * t + 8 * u, row = 8 * n + g;
+          w[j][u] = make_uint4(0, 0, 0, 0);
+          if (row < rows && c0 < d) w[j][u] = *reinterpret_cast<const uint4*>(Q + row * d + c0);
+          for (uint32_t x : {w[j][u].x, w[j][u].y, w[j][u].z, w[j][u].w})
+            most = fmaxf(most, fmaxf(fabsf(bf16_lo(x)), fabsf(bf16_hi(x))));
+        }
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      // 2^-8 of the query's power of two; an infinite entry stays one
+      const float unit = most < INFINITY ? power_of_two(most) * 0x1p-8f : 1.f, inv = 1.f / unit;
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         float sum = 0.f;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          const int c = 64 * j + 16 * t + 8 * u, row = 8 * n + g;
-          if (row < rows && c < d) w = *reinterpret_cast<const uint4*>(Q + row * d + c);
-          sum += (bf16_lo(w.x) + bf16_hi(w.x)) + (bf16_lo(w.y) + bf16_hi(w.y)) +
-                 ((bf16_lo(w.z) + bf16_hi(w.z)) + (bf16_lo(w.w) + bf16_hi(w.w)));
-          q[n][j][2 * u][0] = __byte_perm(w.x, w.z, 0x5410);
-          q[n][j][2 * u][1] = __byte_perm(w.x, w.z, 0x7632);
-          q[n][j][2 * u + 1][0] = __byte_perm(w.y, w.w, 0x5410);
-          q[n][j][2 * u + 1][1] = __byte_perm(w.y, w.w, 0x7632);
+          const uint32_t x[4] = {w[j][u].x, w[j][u].y, w[j][u].z, w[j][u].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // channels e and e + 4
+            float a = e & 1 ? bf16_hi(x[e / 2]) : bf16_lo(x[e / 2]);
+            float b = e & 1 ? bf16_hi(x[2 + e / 2]) : bf16_lo(x[2 + e / 2]);
+            a *= inv;
+            b *= inv;
+            sum += a + b;
+            q[n][j][2 * u + e / 2][e & 1] =
+                e & 1 ? pack_f16(a * 0.0625f, b * 0.0625f) : pack_f16(a, b);
+          }
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum *= 0x1p-24f;
         qs[n][j][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
         qs[n][j][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
 #pragma unroll
@@ -209,53 +255,56 @@ struct Tile {
         z[n][j][0] = z[n][j][1] = 0.f;
       }
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) m[n][e] = top[n][e] = -INFINITY, l[n][e] = 0.f;
+      for (int e = 0; e < 2; ++e) {
+        c[n][e] = __shfl_sync(0xffffffffu, unit, 8 * t + 4 * e) * 0x1p24f * scale_log2;
+        m[n][e] = top[n][e] = -INFINITY;
+        ref[n][e] = l[n][e] = 0.f;
+      }
+    }
+    v_ref = v_inv = 0.f;
+    v_top = -1.f;
   }
 
   // The first `keys` of a stage's 16 keys.
-  FA_DEV void step(const Words<G>& w, int keys, float c, float room, int lane) {
+  FA_DEV void step(const Words<G>& w, int keys, int lane) {
     const int g = lane >> 2;
-    float sk[2][G], zk[2][G], sv[2][G], zv[2][G];
+    float sk[2][G], mk[2][G], sv[2][G], mv[2][G];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         sk[h][j] = bf16_lo(w.pair[h][j]);
-        zk[h][j] = fmaf(-128.f, sk[h][j], bf16_hi(w.pair[h][j]));
+        mk[h][j] = bf16_hi(w.pair[h][j]);
         sv[h][j] = bf16_lo(w.pair[h][G + j]);
-        zv[h][j] = fmaf(8.f, sv[h][j], bf16_hi(w.pair[h][G + j]));
+        mv[h][j] = bf16_hi(w.pair[h][G + j]);
       }
     float s[NT][4];
     {
       float acc[NT][G][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < G; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[n][j][i] = 0.f;
 #pragma unroll
       for (int j = 0; j < G; ++j)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const uint32_t w0 = w.k[0][2 * j + x / 2], w1 = w.k[1][2 * j + x / 2];
           const int e = 2 * (x & 1);
-          const uint32_t a[4] = {codes128(w0, e), codes128(w1, e), codes128(w0, e + 1),
-                                 codes128(w1, e + 1)};
+          const uint32_t a[4] = {codes(w0, e), codes(w1, e), codes(w0, e + 1), codes(w1, e + 1)};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_16816(acc[n][j], a, q[n][j][x][0], q[n][j][x][1]);
+          for (int n = 0; n < NT; ++n) {
+            if (x == 0)
+              mma_f16_first(acc[n][j], a, q[n][j][x][0], q[n][j][x][1]);
+            else
+              mma_f16(acc[n][j], a, q[n][j][x][0], q[n][j][x][1]);
+          }
         }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s[n][i] = 0.f;
+          s[n][i] = fmaf(sk[i >> 1][0], acc[n][0][i], mk[i >> 1][0] * qs[n][0][i & 1]);
 #pragma unroll
-          for (int j = 0; j < G; ++j)
+          for (int j = 1; j < G; ++j)
             s[n][i] = fmaf(sk[i >> 1][j], acc[n][j][i],
-                           fmaf(zk[i >> 1][j], qs[n][j][i & 1], s[n][i]));
+                           fmaf(mk[i >> 1][j], qs[n][j][i & 1], s[n][i]));
         }
     }
     if (keys < 16) {  // what lies behind the keys may be anything
@@ -265,15 +314,28 @@ struct Tile {
 #pragma unroll
           for (int n = 0; n < NT; ++n) s[n][2 * h] = s[n][2 * h + 1] = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < G; ++j) sv[h][j] = zv[h][j] = 0.f;
+          for (int j = 0; j < G; ++j) sv[h][j] = mv[h][j] = 0.f;
         }
     }
-    bool over = false;
+    float most = fmaxf(sv[0][0], sv[1][0]);
+#pragma unroll
+    for (int j = 1; j < G; ++j) most = fmaxf(most, fmaxf(sv[0][j], sv[1][j]));
+    bool over = most > v_top;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) over |= fmaxf(s[n][e], s[n][2 + e]) > top[n][e];
     if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int x = 4; x < 32; x *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+      float back = 1.f;
+      if (most > v_top) {
+        const float next = power_of_two(most);
+        back = v_ref / next;
+        v_ref = next;
+        v_inv = 1.f / next;
+        v_top = 16.f * next;  // with weights up to 2^8, P scale stays below 2^13
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -283,41 +345,44 @@ struct Tile {
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
           x = fmaxf(x, m[n][e]);
-          const float f = x == -INFINITY ? 1.f : ex2((m[n][e] - x) * c);
+          const float f = x == -INFINITY ? 1.f : ex2((m[n][e] - x) * c[n][e]);
           m[n][e] = x;
-          top[n][e] = x + room;
+          ref[n][e] = x == -INFINITY ? 0.f : -x * c[n][e];
+          top[n][e] = x + kRescale / c[n][e];
           l[n][e] *= f;
 #pragma unroll
           for (int j = 0; j < G; ++j) {
             z[n][j][e] *= f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              o[n][j][i][e] *= f;
-              o[n][j][i][2 + e] *= f;
+              o[n][j][i][e] *= f * back;
+              o[n][j][i][2 + e] *= f * back;
             }
           }
         }
     }
     uint32_t b[NT][G][2];
 #pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < G; ++j) sv[h][j] *= v_inv;
+#pragma unroll
     for (int n = 0; n < NT; ++n) {
       float p[4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float ref = m[n][e] == -INFINITY ? 0.f : -m[n][e] * c;
-        p[e] = ex2(fmaf(s[n][e], c, ref));
-        p[2 + e] = ex2(fmaf(s[n][2 + e], c, ref));
+        p[e] = ex2(fmaf(s[n][e], c[n][e], ref[n][e]));
+        p[2 + e] = ex2(fmaf(s[n][2 + e], c[n][e], ref[n][e]));
         l[n][e] += p[e] + p[2 + e];
 #pragma unroll
         for (int j = 0; j < G; ++j)
-          z[n][j][e] = fmaf(p[e], zv[0][j], fmaf(p[2 + e], zv[1][j], z[n][j][e]));
+          z[n][j][e] = fmaf(p[e], mv[0][j], fmaf(p[2 + e], mv[1][j], z[n][j][e]));
       }
 #pragma unroll
       for (int j = 0; j < G; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          b[n][j][h] =
-              transpose8(pack_bf16(p[2 * h] * sv[h][j], p[2 * h + 1] * sv[h][j]));
+          b[n][j][h] = transpose8(pack_f16(p[2 * h] * sv[h][j], p[2 * h + 1] * sv[h][j]));
     }
 #pragma unroll
     for (int j = 0; j < G; ++j) {
@@ -328,14 +393,14 @@ struct Tile {
       for (int i = 0; i < 4; ++i) {
         const uint32_t w0 = two[i / 2][0], w1 = two[i / 2][1];
         const int e = 2 * (i & 1);
-        const uint32_t a[4] = {codes0(w0, e), codes0(w0, e + 1), codes0(w1, e), codes0(w1, e + 1)};
+        const uint32_t a[4] = {codes(w0, e), codes(w0, e + 1), codes(w1, e), codes(w1, e + 1)};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_16816(o[n][j][i], a, b[n][j][0], b[n][j][1]);
+        for (int n = 0; n < NT; ++n) mma_f16(o[n][j][i], a, b[n][j][0], b[n][j][1]);
       }
     }
   }
 
-  // The sums over the lanes that share a query.
+  // The sums over the lanes that share a query, in plain units.
   FA_DEV void finish() {
     auto all = [](float v) {
       v += __shfl_xor_sync(0xffffffffu, v, 4);
@@ -351,9 +416,9 @@ struct Tile {
         for (int j = 0; j < G; ++j) {
           const float add = all(z[n][j][e]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            o[n][j][i][e] += add;
-            o[n][j][i][2 + e] += add;
+          for (int i = 0; i < 4; ++i) {  // even channels came times 2^-24, odd ones 2^-20
+            o[n][j][i][e] = fmaf(o[n][j][i][e] * 0x1p24f, v_ref, add);
+            o[n][j][i][2 + e] = fmaf(o[n][j][i][2 + e] * 0x1p20f, v_ref, add);
           }
         }
       }
@@ -402,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   int* const first = reinterpret_cast<int*>(smem4 + C::BYTES);
 
   if (lane == 0) {
-    for (int i = 0; i < C::STAGES; ++i) mbar_init(&full[warp][i], 1);
+    for (int i = 0; i < C::STAGES; ++i) mbar_init(&full[warp][i], 2);
     fence_mbar_init();
   }
   if (threadIdx.x == 0) abort_flag = never = 0;
@@ -475,65 +540,69 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
     return r;
   };
 
+  // Stages of a run in which this warp has keys.
+  auto stages_of = [&](const Run& r) {
+    const int key = (int)(r.x0 - r.u0) * kChunk + kKeys * warp;
+    return min((int)(r.x1 - r.x0), max(0, r.len - key + kChunk - 1) / kChunk);
+  };
+
   const uint32_t ring = smem_u32(smem4) + warp * C::STAGES * C::STAGE;
   const WaitCtx wait{&abort_flag, &g_decode4_status};
-  // ---- the issuing side, up to STAGES stages ahead of the products
+  // ---- the issuing side, up to STAGES stages ahead of the products: lanes 2 i and 2 i + 1 have
+  // the addresses of the two blocks of stage i of the next 16, and issue their copies.
   Run ir = run_at(x_begin);
-  unsigned ix = x_begin;      // its chunk
-  int ids = 0, i_at = 32;     // pages of 32 chunks from ix - i_at on, one per lane
+  int ij = 0, i_stages = stages_of(ir);  // stages of the run that lanes have had, and all
+  int i_at = 0, i_end = 0;               // of the 16
   int i_stage = 0, issued = 0;
   bool more = true;
-  // Moves on to a chunk in which this warp has keys.
-  auto settle = [&]() {
-    for (;;) {
-      if (ix == ir.x1) {
-        if (ix == x_end) {
-          more = false;
-          return;
-        }
-        ir = run_at(ix);
-        i_at = 32;
+  const uint8_t* src = nullptr;
+  auto refill = [&]() {
+    while (ij == i_stages) {
+      if (ir.x1 == x_end) {
+        more = false;
+        return;
       }
-      if ((int)(ix - ir.u0) * kChunk + 16 * warp < ir.len) return;
-      ++ix;  // the unit's last chunk
+      ir = run_at(ir.x1);
+      i_stages = stages_of(ir);
+      ij = 0;
     }
-  };
-  settle();
-  auto issue = [&]() {
-    if (!more) return;
-    const int key = (int)(ix - ir.u0) * kChunk + 16 * warp;
-    if (i_at == 32) {
-      const int mine = key + lane * kChunk;
-      ids = 0;
-      if (ix + lane < ir.x1 && mine < ir.len)
-        ids = p.table[(size_t)ir.b * p.max_pages + (mine >> p.page_shift)];
-      if ((unsigned)ids >= (unsigned)p.num_pages) {
+    const int key = ((int)(ir.x0 - ir.u0) + ij + (lane >> 1)) * kChunk + kKeys * warp +
+                    kRows4 * (lane & 1);
+    src = nullptr;
+    if (ij + (lane >> 1) < i_stages && key < ir.len) {
+      int page = p.table[(size_t)ir.b * p.max_pages + (key >> p.page_shift)];
+      if ((unsigned)page >= (unsigned)p.num_pages) {
         atomicOr(&g_decode4_status, kDeviceIndexBit);
-        ids = 0;
+        page = 0;
       }
-      i_at = 0;
-    }
-    const int page = __shfl_sync(0xffffffffu, ids, i_at);
-    if (lane == 0) {
       const int hk = ir.ht / s.row_tiles, in = key & ((1 << p.page_shift) - 1);
-      const uint8_t* src =
-          p.cache + ((((size_t)page * s.Hkv + hk) << p.page_shift) + in) * (C::STAGE / 16);
+      src = p.cache + ((((size_t)page * s.Hkv + hk) << p.page_shift) + in) * (C::BLOCK / kRows4);
+    }
+    i_at = 0;
+    i_end = min(16, i_stages - ij);
+    ij += i_end;
+  };
+  auto issue = [&]() {
+    if (i_at == i_end) refill();
+    if (!more) return;
+    if (lane >> 1 == i_at) {
       uint64_t* bar = &full[warp][i_stage];
-      mbar_arrive_expect_tx(bar, C::STAGE);
-      bulk_load(ring + i_stage * C::STAGE, src, C::STAGE, bar);
+      if (src) {
+        mbar_arrive_expect_tx(bar, C::BLOCK);
+        bulk_load(ring + i_stage * C::STAGE + (lane & 1) * C::BLOCK, src, C::BLOCK, bar);
+      } else {
+        mbar_arrive(bar);
+      }
     }
     i_stage = i_stage + 1 == C::STAGES ? 0 : i_stage + 1;
     ++issued;
     ++i_at;
-    ++ix;
-    settle();
   };
   __syncwarp();  // the barriers are initialised
 #pragma unroll
   for (int i = 0; i < C::STAGES; ++i) issue();
 
   // ---- the products
-  const float room = kRescale / p.scale_log2;
   int stage = 0, used = 0;
   uint32_t phase = 0;
   bool alive = true;
@@ -544,22 +613,24 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
     const int hk = r.ht / s.row_tiles, rt = r.ht - hk * s.row_tiles;
     const int rows = min(16, s.per_kv - rt * 16);
     const size_t row0 = (size_t)r.b * s.Hq + hk * s.per_kv + rt * 16;
-    tile.load(p.Q + row0 * s.d, rows, s.d, lane);
-    for (unsigned c = r.x0; c < r.x1; ++c) {
-      const int n = r.len - ((int)(c - r.u0) * kChunk + 16 * warp);
-      if (n <= 0) break;
+    tile.load(p.Q + row0 * s.d, rows, s.d, p.scale_log2, lane);
+    int keys = r.len - ((int)(r.x0 - r.u0) * kChunk + kKeys * warp);  // from the stage on
+    for (int j = stages_of(r); j > 0; --j, keys -= kChunk) {
       if (alive) alive = warp_wait(&full[warp][stage], phase, wait);
       if (!alive) break;
-      Words<G> w;
-      w.load(ring + stage * C::STAGE, lane);
+      const uint32_t at = ring + stage * C::STAGE;
       ++used;
       if (++stage == C::STAGES) {
         stage = 0;
         phase ^= 1u;
       }
+      Words<G> w;
+      w.load(at, lane);
+      tile.step(w, keys, lane);
+      if (keys > kRows4) w.load(at + C::BLOCK, lane);
       __syncwarp();  // every lane has read the stage: it may be filled again
       issue();
-      tile.step(w, n, p.scale_log2, room, lane);
+      if (keys > kRows4) tile.step(w, keys - kRows4, lane);
     }
     tile.finish();
     tile.store(parts + warp * C::ROWS * C::D, lane);
@@ -569,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           stats[warp][8 * n + 2 * lane + e] =
-              make_float2(tile.m[n][e] * p.scale_log2, tile.l[n][e]);
+              make_float2(tile.m[n][e] * tile.c[n][e], tile.l[n][e]);
     }
     __syncthreads();
     const bool whole = r.x0 == r.u0 && r.x1 == r.u1;

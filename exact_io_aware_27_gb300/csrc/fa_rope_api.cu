@@ -327,7 +327,7 @@ int fa_cache4_decode(const void* Q, const void* cache, const int* block_table, i
   if ((rc = check_decode4(B, Hq, Hkv, d)) != FA_OK) return rc;
   if ((rc = check_scale_value(scale)) != FA_OK) return rc;
   if (max_pages < 0 || (long long)max_pages * page > kMaxKeys) return FA_ERR_INVALID_ARG;
-  // the kernels count steps of 64 keys in 32 bits
+  // the kernels count chunks of keys in 32 bits
   if ((long long)Hkv * ((Hq / Hkv + 15) / 16) * B * (((long long)max_pages * page + 63) / 64) >
       0x7fffffffLL)
     return FA_ERR_INVALID_ARG;

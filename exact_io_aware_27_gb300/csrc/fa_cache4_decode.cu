@@ -20,7 +20,7 @@
 // Each warp has a ring of two stages of 32 keys, two bulk copies each.
 #include "fa_cache4.cuh"
 #include "fa_launch.h"
-#include "fa_rope.h"
+#include "fa_rope.cuh"
 #include "fa_split.cuh"
 
 namespace fa {
@@ -120,11 +120,6 @@ FA_DEV uint4 ld_shared16(uint32_t a) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(a)
                : "memory");
-  return v;
-}
-FA_DEV uint2 ld_shared8(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
 // Codes e of the halves of a word in fp16, times 2^-24 (e even) or 2^-20.
@@ -798,20 +793,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   if (lane == 0) p.L[row] = (ref + lg2(sum)) * kLn2;
 }
 
-int sm_count() {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms < kMaxSms ? sms : kMaxSms;
-}
-
 template <int G, int NT>
 cudaError_t launch(const Decode4Args& a, cudaStream_t stream) {
   using C = Cfg<G, NT>;
   DecodeParams p;
   p.s = sizes_of(a.B, a.Hq, a.Hkv, a.d);
   lay_out(&p.s, a.workspace, a.max_pages * a.page);
-  const int sms = sm_count(), smem = C::BYTES + (a.B + 1) * 4;
+  const int sms = sm_count() < kMaxSms ? sm_count() : kMaxSms, smem = C::BYTES + (a.B + 1) * 4;
   // As many blocks as fit (an SM has 227 KB for them, and 1 KB of each is the system's), and no
   // more than the capacities can keep busy.
   const int fit = 227 * 1024 / (smem + 1024 + 1024), most = fit < per_sm(NT) ? fit : per_sm(NT);

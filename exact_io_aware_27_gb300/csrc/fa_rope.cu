@@ -17,171 +17,235 @@ __device__ unsigned int g_rope_status;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;  // rows of a lane in flight
+// Passes of a warp's lanes over the rows of an item, and stages of a warp's ring: four KB a warp
+// are on their way, 96 or 80 KB on an SM.
+constexpr int kPasses = 4, kForwardStages = 3, kBackwardStages = 2;
+constexpr int kForwardStage = 512 * kPasses + kAngleBytes;
+constexpr int kBackwardStage = 2 * 512 * kPasses + kAngleBytes;  // dy's rows, x's, angles
+// Blocks: as many as the registers allow to be resident, six or five on an SM.
+constexpr int kMaxSms = 160;  // partial sums are reserved for this many
+constexpr int kForwardPerSm = 6, kBackwardPerSm = 5;
 
 // One of the two tensors, Q or K.
 struct Side {
   const __nv_bfloat16 *x, *dy, *w;
-  __nv_bfloat16* y;       // y, or dx
+  __nv_bfloat16* y;  // y, or dx
   long long ldx, lddy, ldy;
-  int heads, chunks;      // chunks of kUnroll * 32 / W heads
+  int heads;
+  Deal deal;
 };
 
 struct RopeParams {
   Side q, k;
   RopeHow how;
   const int* positions;
-  int total;
-  float* partial;  // backward: [2][blocks][d]
+  float* partial;  // backward: [blocks][d], Q's blocks first
 };
 
-// The position of row t, or -1 (reported) where the table has none.
-FA_DEV int position_of(const RopeParams& p, int t) {
-  if (p.how.rot == 0) return 0;
-  const int pos = p.positions[t];
-  if ((unsigned)pos < (unsigned)p.how.positions) return pos;
-  atomicOr(&g_rope_status, kDeviceIndexBit);
-  return -1;
+// The position of a row, as it stands in `positions`; 0 where nothing is turned.
+FA_DEV int position_of(const RopeParams& p, int t) { return p.how.rot ? p.positions[t] : 0; }
+// Whether the table has it (else it is reported).
+FA_DEV bool position_ok(const RopeParams& p, int pos, int lane) {
+  if (p.how.rot == 0 || (unsigned)pos < (unsigned)p.how.positions) return true;
+  if (lane == 0) atomicOr(&g_rope_status, kDeviceIndexBit);
+  return false;
+}
+FA_DEV void load_angles(const RopeParams& p, uint32_t to, int pos, int lane) {
+  if (p.how.rot && (unsigned)pos < (unsigned)p.how.positions)
+    copy_async<1>(to, p.how.cos_sin + (size_t)pos * p.how.rot, 4 * p.how.rot, lane);
 }
 
-// A warp takes kUnroll * 32 / W heads of one row t; blockIdx.y counts Q's chunks of heads, then
-// K's.
-template <int W>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int R = 32 / W;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % W;
-  const bool is_q = (int)blockIdx.y < p.q.chunks;
+// An item is kPasses * 32 / W heads of one row; the first blocks take Q's, the others K's.
+// Positions are read an item before the angles that they choose are copied. The stream's next
+// kernel may start once all rows are on their way: earlier, its blocks take SMs from this one's
+// (training 16384 rows, 32/8 heads, d = 128: 236 us against 145), at the end it comes 4 us later.
+template <int W, bool INTER>
+__global__ void __launch_bounds__(kThreads, kForwardPerSm)
+    rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int R = 32 / W, U = kPasses, S = kForwardStages;
+  __shared__ __align__(16) uint8_t rings[kWarps * S * kForwardStage];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % W, seg = lane / W;
+  const bool is_q = (int)blockIdx.x < p.q.deal.blocks;
   const Side& s = is_q ? p.q : p.k;
-  const int h0 = ((int)blockIdx.y - (is_q ? 0 : p.q.chunks)) * kUnroll * R + lane / W;
+  const int d = p.how.d, heads = s.heads;
+  const Piece mine =
+      piece_of(s.deal, ((int)blockIdx.x - (is_q ? 0 : p.q.deal.blocks)) * kWarps + warp);
+  const uint32_t ring = smem_u32(rings) + warp * S * kForwardStage, row = 2 * d;
   const RopeLane at = rope_lane(p.how, l, true);
   grid_wait();
-  grid_launch_dependents();
-  float w[8];
-  load_weight(w, s.w, at);
-  for (int t = (int)blockIdx.x * kWarps + warp; t < p.total; t += (int)gridDim.x * kWarps) {
-    const int pos = position_of(p, t);
-    uint2 a[kUnroll], b[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      a[u] = b[u] = make_uint2(0, 0);
-      const int h = h0 + u * R;
-      if (h < s.heads && at.in) {
-        const __nv_bfloat16* row = s.x + (long long)t * s.ldx + h * p.how.d;
-        a[u] = ld_stream8(row + at.a);
-        b[u] = ld_stream8(row + at.b);
+  if (mine.items > 0) {
+    Item in = mine.first;
+    int put = 0;                  // items whose copies are issued
+    int pos[S];                   // of the items from the one worked on
+    int ahead = position_of(p, in.token);
+    uint32_t to = ring;
+    auto issue = [&]() {
+      pos[S - 1] = ahead;
+      if (put < mine.items) {
+        const int h = in.chunk * U * R;
+        copy_async<U>(to, s.x + (long long)in.token * s.ldx + h * d, min(U * R, heads - h) * 2 * d,
+                      lane);
+        load_angles(p, to + 512 * U, ahead, lane);
+        in.advance(s.deal);
+        if (++put < mine.items)
+          ahead = position_of(p, in.token);
+        else
+          grid_launch_dependents();
       }
+      cp_async_commit();
+      to = to == ring + (S - 1) * kForwardStage ? ring : to + kForwardStage;
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+#pragma unroll
+      for (int k = 0; k + 1 < S; ++k) pos[k] = pos[k + 1];
+      issue();
     }
-    if (pos < 0) continue;
-    const Angles g = rope_angles(p.how, at, l, pos);
+    const bool norm = s.w != nullptr;
+    const Pairs w = load_weight<INTER>(s.w, at);
+    Item it = mine.first;
+    uint32_t stage = ring;
+    for (int i = 0; i < mine.items; ++i, it.advance(s.deal)) {
+      cp_async_wait<S - 2>();
+      __syncwarp();  // the stage has landed for every lane, and the last one is read
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * R;
-      if (h - lane / W >= s.heads) break;  // warp-uniform
-      float x[8];
-      unpack8(x, a[u], b[u]);
-      if (s.w) norm8<W>(x, w, p.how);
-      turn8(x, p.how, at, g, 1.f);
-      if (h < s.heads && at.in) {
-        __nv_bfloat16* row = s.y + (long long)t * s.ldy + h * p.how.d;
-        *reinterpret_cast<uint2*>(row + at.a) = pack4(x);
-        *reinterpret_cast<uint2*>(row + at.b) = pack4(x + 4);
+      for (int k = 0; k + 1 < S; ++k) pos[k] = pos[k + 1];
+      issue();
+      if (position_ok(p, pos[0], lane)) {
+        const uint32_t rows = stage + seg * row;
+        const Turn turn = rope_turn(rope_angles(stage + 512 * U, p.how, at, l), w);
+        const int h0 = it.chunk * U * R + seg;
+        __nv_bfloat16* const out = s.y + (long long)it.token * s.ldy + h0 * d;
+#pragma unroll
+        for (int u = 0; u < U; u += 2) {
+          if (h0 - seg + u * R >= heads) break;  // warp-uniform
+          Pairs y[2];
+          norm_and_turn<W, INTER, 2>(y, rows + u * R * row, R * row, turn, norm, p.how, at);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (h0 + (u + k) * R < heads && at.in)
+              store_row<INTER>(out + (u + k) * R * d, y[k], at);
+        }
       }
+      stage = stage == ring + (S - 1) * kForwardStage ? ring : stage + kForwardStage;
     }
   }
 }
 
-// The same division of the work, by persistent blocks: a lane sums its channels' part of dw over
-// all its rows, a block over its lanes, in a fixed order, and reduce_kernel over the blocks.
-template <int W>
-__global__ void __launch_bounds__(kThreads)
+// The same division of the work: a lane sums its channels' part of dw over all its rows, a block
+// over its lanes, in a fixed order, and reduce_kernel over the blocks.
+template <int W, bool INTER>
+__global__ void __launch_bounds__(kThreads, kBackwardPerSm)
     rope_backward_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int R = 32 / W;
+  constexpr int R = 32 / W, U = kPasses;
+  static_assert(kBackwardStages == 2, "one stage is worked on, one is on its way");
+  __shared__ __align__(16) uint8_t rings[kWarps * 2 * kBackwardStage];
   __shared__ float sums[kWarps][8 * W];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % W;
-  const bool is_q = (int)blockIdx.y < p.q.chunks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % W, seg = lane / W;
+  const bool is_q = (int)blockIdx.x < p.q.deal.blocks;
   const Side& s = is_q ? p.q : p.k;
-  const int h0 = ((int)blockIdx.y - (is_q ? 0 : p.q.chunks)) * kUnroll * R + lane / W;
+  const int d = p.how.d, heads = s.heads;
+  const Piece mine =
+      piece_of(s.deal, ((int)blockIdx.x - (is_q ? 0 : p.q.deal.blocks)) * kWarps + warp);
+  const uint32_t ring = smem_u32(rings) + warp * 2 * kBackwardStage, row = 2 * d;
   const RopeLane at = rope_lane(p.how, l, true);
+  const bool norm = s.w != nullptr;
   grid_wait();
-  grid_launch_dependents();
-  float w[8], dw[8];
-  load_weight(w, s.w, at);
+  const Pairs w = load_weight<INTER>(s.w, at);
+  Pairs dw = {{0, 0}, {0, 0}};
+  if (mine.items > 0) {
+    Item in = mine.first;
+    int put = 0;  // items whose copies are issued
+    int ahead = position_of(p, in.token), next = 0;
+    uint32_t stage = ring, other = ring + kBackwardStage;
+    auto issue = [&](uint32_t to) {
+      next = ahead;
+      if (put < mine.items) {
+        const int h = in.chunk * U * R, bytes = min(U * R, heads - h) * 2 * d;
+        copy_async<U>(to, s.dy + (long long)in.token * s.lddy + h * d, bytes, lane);
+        if (norm)
+          copy_async<U>(to + 512 * U, s.x + (long long)in.token * s.ldx + h * d, bytes, lane);
+        load_angles(p, to + 1024 * U, ahead, lane);
+        in.advance(s.deal);
+        if (++put < mine.items)
+          ahead = position_of(p, in.token);
+        else
+          grid_launch_dependents();
+      }
+      cp_async_commit();
+    };
+    issue(stage);
+    Item it = mine.first;
+    for (int i = 0; i < mine.items; ++i, it.advance(s.deal)) {
+      const int pos = next;
+      cp_async_wait<0>();
+      __syncwarp();  // the stage has landed for every lane, and the other one is read
+      issue(other);
+      if (position_ok(p, pos, lane)) {
+        const uint32_t rows = stage + seg * row;
+        const Angles g = rope_angles(stage + 1024 * U, p.how, at, l);
+        const int h0 = it.chunk * U * R + seg;
+        __nv_bfloat16* const out = s.y + (long long)it.token * s.ldy + h0 * d;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dw[i] = 0.f;
-  for (int t = (int)blockIdx.x * kWarps + warp; t < p.total; t += (int)gridDim.x * kWarps) {
-    const int pos = position_of(p, t);
-    uint2 a[kUnroll], b[kUnroll], xa[kUnroll], xb[kUnroll];
+        for (int u0 = 0; u0 < U; u0 += 2) {
+          if (h0 - seg + u0 * R >= heads) break;  // warp-uniform
+          Pairs y[2], x[2];
+          float sum[4];  // of x^2, then of g o w o x
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      a[u] = b[u] = xa[u] = xb[u] = make_uint2(0, 0);
-      const int h = h0 + u * R;
-      if (h < s.heads && at.in) {
-        const __nv_bfloat16* row = s.dy + (long long)t * s.lddy + h * p.how.d;
-        a[u] = ld_stream8(row + at.a);
-        b[u] = ld_stream8(row + at.b);
-        if (s.w) {
-          row = s.x + (long long)t * s.ldx + h * p.how.d;
-          xa[u] = ld_stream8(row + at.a);
-          xb[u] = ld_stream8(row + at.b);
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t from = rows + (u0 + k) * R * row;
+            y[k] = turned_back(row_of<INTER>(from, at), g, at.turns);
+            if (norm) {
+              x[k] = row_of<INTER>(from + 512 * U, at);
+              sum[k] = dot(x[k], x[k]);
+              sum[2 + k] = dot(times(y[k], w), x[k]);
+            }
+          }
+          if (norm) {
+            row_sums<W, 4>(sum);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float r = inverse_root(sum[k] * p.how.inv_d + p.how.eps);
+              const Pairs n = times(x[k], both(r));
+              if (h0 + (u0 + k) * R < heads) dw = plus(y[k], n, dw);  // else it is anything
+              y[k] = plus(times(y[k], w), {{both(r), both(r)}, {both(r), both(r)}},
+                          times(n, both(-sum[2 + k] * r * r * p.how.inv_d)));
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (h0 + (u0 + k) * R < heads && at.in)
+              store_row<INTER>(out + (u0 + k) * R * d, y[k], at);
         }
       }
-    }
-    if (pos < 0) continue;
-    const Angles g = rope_angles(p.how, at, l, pos);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * R;
-      if (h - lane / W >= s.heads) break;  // warp-uniform
-      float y[8];
-      unpack8(y, a[u], b[u]);
-      turn8(y, p.how, at, g, -1.f);
-      if (s.w) {
-        float x[8];
-        unpack8(x, xa[u], xb[u]);
-        float xx = 0.f, dot = 0.f;  // sums of x^2 and of g o w o x
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          xx += x[i] * x[i];
-          dot += y[i] * w[i] * x[i];
-        }
-        xx = row_sum<W>(xx);
-        dot = row_sum<W>(dot);
-        const float r = rsqrtf(xx * p.how.inv_d + p.how.eps);
-        const float back = dot * r * r * p.how.inv_d;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dw[i] += y[i] * (x[i] * r);
-          y[i] = r * (y[i] * w[i] - x[i] * back);
-        }
-      }
-      if (h < s.heads && at.in) {
-        __nv_bfloat16* row = s.y + (long long)t * s.ldy + h * p.how.d;
-        *reinterpret_cast<uint2*>(row + at.a) = pack4(y);
-        *reinterpret_cast<uint2*>(row + at.b) = pack4(y + 4);
-      }
+      const uint32_t swap = stage;
+      stage = other;
+      other = swap;
     }
   }
-  if (!s.w) return;
+  if (!norm) return;
+  float mine_dw[8];
+  channels<INTER>(dw, mine_dw);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int o = W; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
+    for (int o = W; o < 32; o <<= 1) mine_dw[i] += __shfl_xor_sync(0xffffffffu, mine_dw[i], o);
   if (lane < W && at.in) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      sums[warp][at.a + i] = dw[i];
-      sums[warp][at.b + i] = dw[4 + i];
+      sums[warp][at.a + i] = mine_dw[i];
+      sums[warp][at.b + i] = mine_dw[4 + i];
     }
   }
   __syncthreads();
   const int c = threadIdx.x;
-  if (c < p.how.d) {
+  if (c < d) {
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) v += sums[i][c];
-    p.partial[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * p.how.d + c] = v;
+    p.partial[(size_t)blockIdx.x * d + c] = v;
   }
 }
 
@@ -203,7 +267,7 @@ __global__ void __launch_bounds__(1024) reduce_kernel(const __grid_constant__ Re
   if (!out) return;
   float v = 0.f;
   if (c < p.d) {
-#pragma unroll 4
+#pragma unroll 8
     for (int r = row; r < rows; r += 32) v += from[(size_t)r * p.d + c];
   }
   sums[row][lane] = v;
@@ -215,10 +279,8 @@ __global__ void __launch_bounds__(1024) reduce_kernel(const __grid_constant__ Re
   if (lane == 0 && mine < p.d) out[mine] = v;
 }
 
-int chunks_of(int heads, int d) { return ceil_div(heads, kUnroll * (32 / rope_lanes(d))); }
-
 Side side(const void* x, const void* dy, const void* w, void* y, long long ldx, long long lddy,
-          long long ldy, int heads, int d) {
+          long long ldy, int heads) {
   Side s;
   s.x = static_cast<const __nv_bfloat16*>(x);
   s.dy = static_cast<const __nv_bfloat16*>(dy);
@@ -228,36 +290,37 @@ Side side(const void* x, const void* dy, const void* w, void* y, long long ldx, 
   s.lddy = lddy;
   s.ldy = ldy;
   s.heads = heads;
-  s.chunks = chunks_of(heads, d);
   return s;
 }
 
-// Blocks per chunk of the backward kernel: six on each SM in all, so that every warp has rows
-// in flight while its neighbours reduce.
-constexpr int kBackwardBlocks = 6 * 152;
-int backward_blocks(int Hq, int Hkv, int d) {
-  const int n = chunks_of(Hq, d) + chunks_of(Hkv, d);
-  return n < kBackwardBlocks ? kBackwardBlocks / n : 1;
+// Deals both sides' items; returns the blocks of both.
+int deal_sides(RopeParams& p, int total, int d, int per_sm) {
+  const int sms = sm_count(), per = kPasses * (32 / rope_lanes(d));
+  const int cq = ceil_div(p.q.heads, per), ck = ceil_div(p.k.heads, per);
+  int blocks[2];
+  share_blocks<2>(blocks, {(long long)total * cq, (long long)total * ck}, {1, 1},
+                  (sms < kMaxSms ? sms : kMaxSms) * per_sm, kWarps);
+  p.q.deal = deal(total, cq, blocks[0], kWarps);
+  p.k.deal = deal(total, ck, blocks[1], kWarps);
+  return blocks[0] + blocks[1];
 }
 
 struct Forward {
   const RopeParams& p;
+  int blocks;
   cudaStream_t stream;
-  template <int W>
+  template <int W, bool INTER>
   cudaError_t run() const {
-    const int blocks = ceil_div(p.total, kWarps);
-    return launch_early(rope_kernel<W>, dim3((unsigned)blocks, (unsigned)(p.q.chunks + p.k.chunks)),
-                        kThreads, 0, stream, p);
+    return launch_early(rope_kernel<W, INTER>, dim3((unsigned)blocks), kThreads, 0, stream, p);
   }
 };
 struct Backward {
   const RopeParams& p;
   int blocks;
   cudaStream_t stream;
-  template <int W>
+  template <int W, bool INTER>
   cudaError_t run() const {
-    return launch_early(rope_backward_kernel<W>,
-                        dim3((unsigned)blocks, (unsigned)(p.q.chunks + p.k.chunks)), kThreads, 0,
+    return launch_early(rope_backward_kernel<W, INTER>, dim3((unsigned)blocks), kThreads, 0,
                         stream, p);
   }
 };
@@ -266,38 +329,35 @@ struct Backward {
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   RopeParams p{};
-  p.q = side(a.Q, nullptr, a.how.q_weight, a.Qo, a.ldq, 0, a.ldqo, a.Hq, a.d);
-  p.k = side(a.K, nullptr, a.how.k_weight, a.Ko, a.ldk, 0, a.ldko, a.Hkv, a.d);
+  p.q = side(a.Q, nullptr, a.how.q_weight, a.Qo, a.ldq, 0, a.ldqo, a.Hq);
+  p.k = side(a.K, nullptr, a.how.k_weight, a.Ko, a.ldk, 0, a.ldko, a.Hkv);
   p.how = rope_how(a.how, a.d);
   p.positions = a.positions;
-  p.total = a.total;
-  return with_lanes(a.d, Forward{p, s});
+  const int blocks = deal_sides(p, a.total, a.d, kForwardPerSm);
+  return with_lanes(p.how, Forward{p, blocks, s});
 }
 
-size_t rope_workspace_bytes(int Hq, int Hkv, int d) {
-  const size_t n = (size_t)chunks_of(Hq, d) + chunks_of(Hkv, d);
-  return n * backward_blocks(Hq, Hkv, d) * d * sizeof(float);
+size_t rope_workspace_bytes(int d) {
+  return (size_t)(kMaxSms * kBackwardPerSm + 2) * d * sizeof(float);
 }
 
 cudaError_t launch_rope_backward(const RopeBackwardArgs& a, cudaStream_t s) {
   RopeParams p{};
-  p.q = side(a.Q, a.dQo, a.how.q_weight, a.dQ, a.ldq, a.lddqo, a.lddq, a.Hq, a.d);
-  p.k = side(a.K, a.dKo, a.how.k_weight, a.dK, a.ldk, a.lddko, a.lddk, a.Hkv, a.d);
+  p.q = side(a.Q, a.dQo, a.how.q_weight, a.dQ, a.ldq, a.lddqo, a.lddq, a.Hq);
+  p.k = side(a.K, a.dKo, a.how.k_weight, a.dK, a.ldk, a.lddko, a.lddk, a.Hkv);
   p.how = rope_how(a.how, a.d);
   p.positions = a.positions;
-  p.total = a.total;
   p.partial = a.partial;
-  const int most = backward_blocks(a.Hq, a.Hkv, a.d), need = ceil_div(a.total, kWarps);
-  const int blocks = need < most ? need : most;
-  cudaError_t e = with_lanes(a.d, Backward{p, blocks, s});
+  const int blocks = deal_sides(p, a.total, a.d, kBackwardPerSm);
+  cudaError_t e = with_lanes(p.how, Backward{p, blocks, s});
   if (e != cudaSuccess || (!a.how.q_weight && !a.how.k_weight)) return e;
   ReduceParams r;
   r.partial = a.partial;
   r.dwq = a.how.q_weight ? a.dwq : nullptr;
   r.dwk = a.how.k_weight ? a.dwk : nullptr;
   r.d = a.d;
-  r.q_rows = p.q.chunks * blocks;
-  r.k_rows = p.k.chunks * blocks;
+  r.q_rows = p.q.deal.blocks;
+  r.k_rows = p.k.deal.blocks;
   return launch_early(reduce_kernel, dim3((unsigned)ceil_div(a.d, 32), 2), 1024, 0, s, r);
 }
 

@@ -26,6 +26,12 @@ struct RopeHow {
   int positions, rot, interleaved, d;
   float eps, inv_d;
 };
+inline int sm_count() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
 inline RopeHow rope_how(const fa_rope& h, int d) {
   RopeHow r;
   r.cos_sin = h.cos_sin;
@@ -53,100 +59,294 @@ FA_DEV RopeLane rope_lane(const RopeHow& h, int l, bool turned) {
   return r;
 }
 
-FA_DEV uint2 ld_stream8(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
-               : "l"(p)
-               : "memory");
-  return v;
+// A lane's eight channels in fp32 as four packed pairs: a[i] and b[i] hold the first and second
+// channels of the pairs 2 i and 2 i + 1 that are turned together. INTER: those are neighbours.
+struct Pairs {
+  uint64_t a[2], b[2];
+};
+template <bool INTER>
+FA_DEV Pairs unpack_pairs(uint2 A, uint2 B) {
+  Pairs p;
+  if (INTER) {
+    p.a[0] = f2pack(bf16_lo(A.x), bf16_lo(A.y));
+    p.b[0] = f2pack(bf16_hi(A.x), bf16_hi(A.y));
+    p.a[1] = f2pack(bf16_lo(B.x), bf16_lo(B.y));
+    p.b[1] = f2pack(bf16_hi(B.x), bf16_hi(B.y));
+  } else {
+    p.a[0] = f2pack(bf16_lo(A.x), bf16_hi(A.x));
+    p.a[1] = f2pack(bf16_lo(A.y), bf16_hi(A.y));
+    p.b[0] = f2pack(bf16_lo(B.x), bf16_hi(B.x));
+    p.b[1] = f2pack(bf16_lo(B.y), bf16_hi(B.y));
+  }
+  return p;
 }
-// Channels A (x[0..3]) and B (x[4..7]) of a row.
-FA_DEV void unpack8(float (&x)[8], uint2 a, uint2 b) {
-  x[0] = bf16_lo(a.x);
-  x[1] = bf16_hi(a.x);
-  x[2] = bf16_lo(a.y);
-  x[3] = bf16_hi(a.y);
-  x[4] = bf16_lo(b.x);
-  x[5] = bf16_hi(b.x);
-  x[6] = bf16_lo(b.y);
-  x[7] = bf16_hi(b.y);
+// The channels of pieces A (x[0 .. 3]) and B.
+template <bool INTER>
+FA_DEV void channels(const Pairs& p, float (&x)[8]) {
+  if (INTER) {
+    f2unpack(p.a[0], x[0], x[2]);
+    f2unpack(p.b[0], x[1], x[3]);
+    f2unpack(p.a[1], x[4], x[6]);
+    f2unpack(p.b[1], x[5], x[7]);
+  } else {
+    f2unpack(p.a[0], x[0], x[1]);
+    f2unpack(p.a[1], x[2], x[3]);
+    f2unpack(p.b[0], x[4], x[5]);
+    f2unpack(p.b[1], x[6], x[7]);
+  }
 }
 FA_DEV uint2 pack4(const float* x) {
   return make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
 }
+FA_DEV Pairs times(const Pairs& x, uint64_t f) {
+  return {{fmul2(x.a[0], f), fmul2(x.a[1], f)}, {fmul2(x.b[0], f), fmul2(x.b[1], f)}};
+}
+FA_DEV Pairs times(const Pairs& x, const Pairs& y) {
+  return {{fmul2(x.a[0], y.a[0]), fmul2(x.a[1], y.a[1])},
+          {fmul2(x.b[0], y.b[0]), fmul2(x.b[1], y.b[1])}};
+}
+FA_DEV Pairs plus(const Pairs& x, const Pairs& y, const Pairs& z) {  // x y + z
+  return {{ffma2(x.a[0], y.a[0], z.a[0]), ffma2(x.a[1], y.a[1], z.a[1])},
+          {ffma2(x.b[0], y.b[0], z.b[0]), ffma2(x.b[1], y.b[1], z.b[1])}};
+}
+FA_DEV float dot(const Pairs& x, const Pairs& y) {
+  uint64_t v = fmul2(x.a[0], y.a[0]);
+  v = ffma2(x.a[1], y.a[1], v);
+  v = ffma2(x.b[0], y.b[0], v);
+  v = ffma2(x.b[1], y.b[1], v);
+  float lo, hi;
+  f2unpack(v, lo, hi);
+  return lo + hi;
+}
+FA_DEV uint64_t both(float x) { return f2pack(x, x); }
+// 1 / sqrt(x), 2^-22 off at most.
+FA_DEV float inverse_root(float x) {
+  float r;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
-template <int W>
-FA_DEV float row_sum(float v) {
+// A warp's rows on their way through shared memory: a ring of stages, each a token's chunk of
+// heads, 512 bytes for every pass of the warp's lanes over 32 / W rows, and the angles of its
+// position. Rows that are behind the heads hold anything.
+constexpr int kAngleBytes = 512;
+// Copies `bytes` (at most 512 N) from src to shared memory in the background.
+template <int N>
+FA_DEV void copy_async(uint32_t to, const void* src, int bytes, int lane) {
 #pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int i = 0; i < N; ++i) {
+    const int at = 16 * lane + 512 * i;
+    if (at < bytes) cp_async16(to + at, static_cast<const uint8_t*>(src) + at, 16);
+  }
+}
+FA_DEV float4 ld_shared16f(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+FA_DEV uint2 ld_shared8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
 
-// The lane's angles at position `pos`: cosines and sines of its four pairs.
+template <bool INTER>
+FA_DEV void store_row(__nv_bfloat16* row, const Pairs& p, const RopeLane& at) {
+  float x[8];
+  channels<INTER>(p, x);
+  *reinterpret_cast<uint2*>(row + at.a) = pack4(x);
+  *reinterpret_cast<uint2*>(row + at.b) = pack4(x + 4);
+}
+
+template <bool INTER>
+FA_DEV Pairs row_of(uint32_t row, const RopeLane& at) {
+  uint2 a = make_uint2(0, 0), b = a;  // a lane without channels adds nothing to its row's sums
+  if (at.in) {
+    a = ld_shared8(row + 2 * at.a);
+    b = ld_shared8(row + 2 * at.b);
+  }
+  return unpack_pairs<INTER>(a, b);
+}
+
+// Sums over the W lanes of a row, of N rows side by side.
+template <int W, int N>
+FA_DEV void row_sums(float (&v)[N]) {
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+}
+
+// The lane's angles: cosines and sines of its four pairs, from a position's row of the table in
+// shared memory.
 struct Angles {
-  float4 c, s;
+  uint64_t c[2], s[2];
 };
-FA_DEV Angles rope_angles(const RopeHow& h, const RopeLane& at, int l, int pos) {
+FA_DEV Angles rope_angles(uint32_t row, const RopeHow& h, const RopeLane& at, int l) {
   Angles g;
-  g.c = make_float4(1.f, 1.f, 1.f, 1.f);
-  g.s = make_float4(0.f, 0.f, 0.f, 0.f);
+  g.c[0] = g.c[1] = both(1.f);
+  g.s[0] = g.s[1] = both(0.f);
   if (at.turns) {
-    const float* row = h.cos_sin + (size_t)pos * h.rot;
-    g.c = *reinterpret_cast<const float4*>(row + 4 * l);
-    g.s = *reinterpret_cast<const float4*>(row + h.rot / 2 + 4 * l);
+    const float4 c = ld_shared16f(row + 16 * l), s = ld_shared16f(row + 2 * h.rot + 16 * l);
+    g.c[0] = f2pack(c.x, c.y);
+    g.c[1] = f2pack(c.z, c.w);
+    g.s[0] = f2pack(s.x, s.y);
+    g.s[1] = f2pack(s.z, s.w);
   }
   return g;
 }
-FA_DEV void turn(float& a, float& b, float c, float s) {
-  const float x = a * c - b * s;
-  b = b * c + a * s;
-  a = x;
-}
-// The lane's pairs turned (sign = -1: back).
-FA_DEV void turn8(float (&x)[8], const RopeHow& h, const RopeLane& at, const Angles& g,
-                  float sign) {
-  if (!at.turns) return;
-  if (h.interleaved) {
-    turn(x[0], x[1], g.c.x, sign * g.s.x);
-    turn(x[2], x[3], g.c.y, sign * g.s.y);
-    turn(x[4], x[5], g.c.z, sign * g.s.z);
-    turn(x[6], x[7], g.c.w, sign * g.s.w);
-  } else {
-    turn(x[0], x[4], g.c.x, sign * g.s.x);
-    turn(x[1], x[5], g.c.y, sign * g.s.y);
-    turn(x[2], x[6], g.c.z, sign * g.s.z);
-    turn(x[3], x[7], g.c.w, sign * g.s.w);
+// Weight and rotation in one: a' = a ca + b sb, b' = b cb + a sa.
+struct Turn {
+  uint64_t ca[2], sb[2], cb[2], sa[2];
+};
+FA_DEV Turn rope_turn(const Angles& g, const Pairs& w) {
+  Turn t;
+  const uint64_t minus = both(-1.f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    t.ca[i] = fmul2(w.a[i], g.c[i]);
+    t.sa[i] = fmul2(w.a[i], g.s[i]);
+    t.cb[i] = fmul2(w.b[i], g.c[i]);
+    t.sb[i] = fmul2(fmul2(w.b[i], g.s[i]), minus);
   }
+  return t;
 }
-// x / root mean square, times the weight w; every lane of a row takes part.
-template <int W>
-FA_DEV void norm8(float (&x)[8], const float (&w)[8], const RopeHow& h) {
-  float s = 0.f;
+FA_DEV Pairs turned(const Pairs& x, const Turn& t, bool turns) {
+  Pairs y;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s += x[i] * x[i];
-  const float r = rsqrtf(row_sum<W>(s) * h.inv_d + h.eps);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
+  for (int i = 0; i < 2; ++i) {
+    y.a[i] = fmul2(x.a[i], t.ca[i]);
+    y.b[i] = fmul2(x.b[i], t.cb[i]);
+    if (turns) {
+      y.a[i] = ffma2(x.b[i], t.sb[i], y.a[i]);
+      y.b[i] = ffma2(x.a[i], t.sa[i], y.b[i]);
+    }
+  }
+  return y;
 }
-FA_DEV void load_weight(float (&w)[8], const __nv_bfloat16* weight, const RopeLane& at) {
-  uint2 a = make_uint2(0, 0), b = a;
+// The rotation back, by the angles alone.
+FA_DEV Pairs turned_back(const Pairs& y, const Angles& g, bool turns) {
+  if (!turns) return y;
+  Pairs x;
+  const uint64_t minus = both(-1.f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x.a[i] = ffma2(y.b[i], g.s[i], fmul2(y.a[i], g.c[i]));
+    x.b[i] = ffma2(y.a[i], fmul2(g.s[i], minus), fmul2(y.b[i], g.c[i]));
+  }
+  return x;
+}
+// N rows of a stage, `step` bytes from row to row, normed (if so; the weight is in `t`) and turned.
+template <int W, bool INTER, int N>
+FA_DEV void norm_and_turn(Pairs (&y)[N], uint32_t row, uint32_t step, const Turn& t, bool norm,
+                          const RopeHow& h, const RopeLane& at) {
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const Pairs x = row_of<INTER>(row + i * step, at);
+    if (norm) v[i] = dot(x, x);
+    y[i] = turned(x, t, at.turns);
+  }
+  if (!norm) return;
+  row_sums<W, N>(v);
+#pragma unroll
+  for (int i = 0; i < N; ++i) y[i] = times(y[i], both(inverse_root(v[i] * h.inv_d + h.eps)));
+}
+// The lane's weights, ones without a weight.
+template <bool INTER>
+FA_DEV Pairs load_weight(const __nv_bfloat16* weight, const RopeLane& at) {
+  const uint32_t one = weight ? 0u : 0x3f803f80u;
+  uint2 a = make_uint2(one, one), b = a;
   if (weight && at.in) {
     a = *reinterpret_cast<const uint2*>(weight + at.a);
     b = *reinterpret_cast<const uint2*>(weight + at.b);
   }
-  unpack8(w, a, b);
+  return unpack_pairs<INTER>(a, b);
 }
 
-// f.run<W>() for the lanes of a row of d channels.
+// Items (chunks of heads of a token, in order) dealt to the warps of `blocks` thread blocks in
+// turn, so that neighbouring warps work on neighbouring rows: pieces of the items' axis, a
+// token's chunks in one warp, took 20 % longer. The warps that take part are a number without a
+// common divisor with a token's chunks, so that each meets all of a token's chunks, which
+// may cost more or less, in turn.
+struct Deal {
+  int blocks, workers, chunks;  // chunks of a token
+  long long items;
+  int tokens, rest;             // a round's items: whole tokens, and chunks
+};
+inline Deal deal(long long tokens, int chunks, int blocks, int warps) {
+  Deal d;
+  d.blocks = blocks;
+  d.chunks = chunks;
+  d.items = tokens * chunks;
+  d.workers = blocks * warps;
+  auto divisor = [](int a, int b) {
+    while (b) {
+      const int r = a % b;
+      a = b;
+      b = r;
+    }
+    return a;
+  };
+  if (d.items > d.workers)
+    while (d.workers > 1 && divisor(d.workers, chunks) != 1) --d.workers;
+  d.tokens = d.workers / chunks;
+  d.rest = d.workers % chunks;
+  return d;
+}
+// An item, and the same warp's next.
+struct Item {
+  int token, chunk;
+  FA_DEV void advance(const Deal& d) {
+    token += d.tokens;
+    chunk += d.rest;
+    if (chunk >= d.chunks) {
+      chunk -= d.chunks;
+      ++token;
+    }
+  }
+};
+struct Piece {
+  Item first;
+  int items;
+};
+// The share of warp `me` of all.
+FA_DEV Piece piece_of(const Deal& d, int me) {
+  Piece p;
+  p.first.token = me / d.chunks;
+  p.first.chunk = me - p.first.token * d.chunks;
+  p.items = me < d.workers && me < d.items ? (int)((d.items - me - 1) / d.workers) + 1 : 0;
+  return p;
+}
+
+// Thread blocks of each of N kinds: `most` in all, shared out by items times cost, one at least
+// where there is an item, and no more than there are items for.
+template <int N>
+void share_blocks(int (&blocks)[N], const long long (&items)[N], const int (&cost)[N], int most,
+                  int warps) {
+  long long all = 0;
+  for (int i = 0; i < N; ++i) all += items[i] * cost[i];
+  for (int i = 0; i < N; ++i) {
+    const long long need = (items[i] + warps - 1) / warps;
+    long long b = all > 0 ? (long long)((double)most * items[i] * cost[i] / all) : 0;
+    if (b < 1) b = 1;
+    blocks[i] = (int)(b < need ? b : need);
+  }
+}
+
+// f.run<W, INTER>() for the lanes of a row of d channels.
 template <class F>
-cudaError_t with_lanes(int d, const F& f) {
-  switch (rope_lanes(d)) {
-    case 1: return f.template run<1>();
-    case 2: return f.template run<2>();
-    case 4: return f.template run<4>();
-    case 8: return f.template run<8>();
-    default: return f.template run<16>();
+cudaError_t with_lanes(const RopeHow& h, const F& f) {
+  const bool inter = h.rot > 0 && h.interleaved;
+  switch (rope_lanes(h.d)) {
+    case 1: return inter ? f.template run<1, true>() : f.template run<1, false>();
+    case 2: return inter ? f.template run<2, true>() : f.template run<2, false>();
+    case 4: return inter ? f.template run<4, true>() : f.template run<4, false>();
+    case 8: return inter ? f.template run<8, true>() : f.template run<8, false>();
+    default: return inter ? f.template run<16, true>() : f.template run<16, false>();
   }
 }
 

@@ -27,7 +27,7 @@ struct RopeBackwardArgs {
   fa_rope how;
 };
 // Bytes of partial sums of the weights' gradients.
-size_t rope_workspace_bytes(int Hq, int Hkv, int d);
+size_t rope_workspace_bytes(int d);
 cudaError_t launch_rope_backward(const RopeBackwardArgs& a, cudaStream_t s);
 cudaError_t rope_read_status(unsigned int* out);
 

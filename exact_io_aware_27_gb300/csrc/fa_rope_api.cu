@@ -187,7 +187,7 @@ int fa_qk_norm_rope(const void* Q, const void* K, long long q_stride, long long 
 
 size_t fa_qk_norm_rope_workspace_bytes(int Hq, int Hkv, int d) {
   if (check_heads(Hq, d) != FA_OK || check_heads(Hkv, d) != FA_OK) return 0;
-  return rope_workspace_bytes(Hq, Hkv, d);
+  return rope_workspace_bytes(d);
 }
 
 int fa_qk_norm_rope_backward(const void* dQo, const void* dKo, long long dqo_stride,
@@ -217,7 +217,7 @@ int fa_qk_norm_rope_backward(const void* dQo, const void* dKo, long long dqo_str
        {static_cast<const void*>(positions), static_cast<const void*>(wq ? dq_weight : nullptr),
         static_cast<const void*>(wk ? dk_weight : nullptr)})
     if (!is_aligned(p, 4)) return FA_ERR_MISALIGNED;
-  const size_t need = wq || wk ? rope_workspace_bytes(Hq, Hkv, d) : 0;
+  const size_t need = wq || wk ? rope_workspace_bytes(d) : 0;
   if (workspace_bytes < need) return FA_ERR_WORKSPACE_TOO_SMALL;
   const size_t qw = (size_t)Hq * d * 2, kw = (size_t)Hkv * d * 2;
   const HowRows h = rows_of_how(how, d);

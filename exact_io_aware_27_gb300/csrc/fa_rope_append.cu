@@ -3,10 +3,10 @@
 //
 // Token t of request i goes to cache position starts[i] + t - cu_seqlens[i], which is row
 // (position mod page) of page table[i, position / page] and turns by that position's angles.
-// Bound by memory: every row is read once and written once. A warp takes a few heads of one
-// token; Q's heads, K's and V's are chunks of one grid, so that a decode step's tokens are
-// one short launch. Indices are checked as in fa_cache.cu: a place out of range is not written
-// and raises kDeviceIndexBit, and so do bounds that break the rule.
+// Bound by memory: every row is read once and written once. A warp takes a few heads of Q, K or
+// V of one token after another, all warps side by side, and looks a request up only where
+// another one begins. Indices are checked as in fa_cache.cu: a place out of range is not written and
+// raises kDeviceIndexBit, and so do bounds that break the rule.
 #include "fa_cache4.cuh"
 #include "fa_launch.h"
 #include "fa_rope.cuh"
@@ -17,9 +17,13 @@ __device__ unsigned int g_rope_append_status;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;  // rows of a lane in flight
+// Passes of a warp's lanes over the rows of an item, stages of a warp's ring.
+constexpr int kPasses = 4, kStages = 3;
+constexpr int kStage = 512 * kPasses + kAngleBytes;
+// Blocks on an SM, as many as the registers allow; 4 bits want 120.
+constexpr int kPerSm = 6, kPerSm4 = 4;
 
 struct Place {
   const int *cu, *starts, *table;
@@ -36,207 +40,290 @@ FA_DEV void check_bounds(const Place& p, long long me, long long all) {
   if (bad) bad_index();
 }
 
-// The request in whose bounds row t lies and the row's position; request -1 behind the last
-// one, -2 (reported) where it has no position. The warp searches 32 bounds at a time.
-struct Token {
-  int request;
-  long long pos;
+// Where rows go. A warp meets them in order, so that most lie in the request of the one before.
+struct Cursor {
+  int request = -1;    // of the row: -1 behind the last request, -2 without a place (reported)
+  int end = 0;         // of the request's rows
+  long long shift = 0; // from row to position
+
+  // Moves on to row t. The search looks at 32 bounds at a time.
+  FA_DEV void to(const Place& p, int t) {
+    if (request >= 0 && t < end) return;
+    const int lane = threadIdx.x & 31;
+    request = -1;
+    if (t >= p.cu[p.nseq]) return;
+    int lo = 0, hi = p.nseq;  // the last i of [lo, hi) with cu[i] <= t
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+      const unsigned under = __ballot_sync(0xffffffffu, i < hi && p.cu[i] <= t);
+      if (under == 0) break;  // bounds that break the rule
+      lo += (31 - __clz(under)) * step;
+      hi = min(hi, lo + step);
+    }
+    const int from = p.cu[lo], start = p.starts[lo];
+    end = p.cu[lo + 1];
+    request = lo;
+    shift = (long long)start - from;
+    if (from < 0 || from > t || t >= end || start < 0) {
+      if (lane == 0) bad_index();
+      request = -2;
+    }
+  }
 };
-FA_DEV Token token_of(const Place& p, int t) {
-  const int lane = threadIdx.x & 31;
-  if (t >= p.cu[p.nseq]) return {-1, 0};
-  int lo = 0, hi = p.nseq;  // the last i of [lo, hi) with cu[i] <= t
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-    const unsigned under = __ballot_sync(0xffffffffu, i < hi && p.cu[i] <= t);
-    if (under == 0) break;  // bounds that break the rule
-    lo += (31 - __clz(under)) * step;
-    hi = min(hi, lo + step);
-  }
-  const int from = p.cu[lo], start = p.starts[lo];
-  const long long pos = (long long)start + t - from;
-  if (from < 0 || from > t || t >= p.cu[lo + 1] || start < 0) {
-    if (lane == 0) bad_index();
-    return {-2, 0};
-  }
-  return {lo, pos};
+// The page that holds position pos of a request, as the table has it, or -1.
+FA_DEV int table_page(const Place& p, int request, long long pos) {
+  const long long index = pos >> p.page_shift;
+  return index < p.max_pages ? p.table[(long long)request * p.max_pages + index] : -1;
 }
-// The page that holds the token's position, or -1 (reported).
-FA_DEV int page_of(const Place& p, const Token& k) {
-  if (k.pos < (long long)p.max_pages << p.page_shift) {
-    const int page = p.table[(long long)k.request * p.max_pages + (k.pos >> p.page_shift)];
-    if ((unsigned)page < (unsigned)p.num_pages) return page;
-  }
+FA_DEV bool page_ok(const Place& p, int page) {
+  if ((unsigned)page < (unsigned)p.num_pages) return true;
   if ((threadIdx.x & 31) == 0) bad_index();
-  return -1;
+  return false;
 }
 
+struct AppendSide {  // Q, K or V
+  const __nv_bfloat16 *x, *w;
+  __nv_bfloat16* y;  // Qo or a bf16 cache
+  long long ld;
+  int heads, chunks;
+};
 struct AppendParams {
   Place at;
-  const __nv_bfloat16 *Q, *K, *V, *wq, *wk;
-  __nv_bfloat16 *Qo, *Kc, *Vc;
+  AppendSide side[3];
+  Deal deal;  // of the chunks of Q's heads, K's and V's of each token
   uint8_t* cache4;
-  long long ldq, ldk, ldv;
   RopeHow how;
-  int Hq, q_chunks, kv_chunks, fill;
+  int fill;
 };
 
-// A row's group of up to 64 channels in 4 bits: the pair, and the codes of the lane's eight
-// channels (A in bits 0 .. 15, B above). Every lane of the row takes part. A group with a value
-// that is not finite, or whose range is not, is held as NaN.
+// Chunks of a token: Q's, then K's, then V's (kinds 0, 1, 2).
+FA_DEV int kind_of(const AppendParams& p, int c) {
+  return c < p.side[0].chunks ? 0 : c < p.side[0].chunks + p.side[1].chunks ? 1 : 2;
+}
+FA_DEV int chunk_of(const AppendParams& p, int c) {  // within the kind
+  if (c >= p.side[0].chunks) c -= p.side[0].chunks;
+  else return c;
+  return c >= p.side[1].chunks ? c - p.side[1].chunks : c;
+}
+
+FA_DEV float min_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+FA_DEV float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Eight neighbouring channels of a group in 4 bits, of N rows side by side; SAME lanes have the
+// group. A group with a value that is not finite, or whose range is not, is held as NaN.
 struct Codes {
-  uint32_t pair[2];  // of each group
-  uint32_t code;
+  uint32_t pair, code;
 };
-// x to the nearest of the 16 values, of a tie to the even one. The quotient is off by 2^-23
-// at most; a remainder on the other side of half a step says so, and exactly half is a tie.
-// `up`: a power of two that a very small scale, whose inverse would be infinite, is times.
-FA_DEV uint32_t code_of(float x, float lo, float up, float scale, float inv) {
-  const float a = (x - lo) * up;
-  float c = fminf(fmaxf(rintf(a * inv), 0.f), 15.f);
-  const float r2 = 2.f * fmaf(-c, scale, a);
-  const bool odd = ((int)c & 1) != 0;
-  if (c < 15.f && (r2 > scale || (odd && r2 == scale))) c += 1.f;
-  if (c > 0.f && (r2 < -scale || (odd && r2 == -scale))) c -= 1.f;
-  return (uint32_t)c;
-}
-template <int W, int G>
-FA_DEV Codes quantize8(const float (&x)[8], const RopeLane& at) {
-  Codes out;
-  out.code = 0;
-  float lo[2], scale[2], up[2], inv[2];
+template <int SAME, int N>
+FA_DEV void quantize8(Codes (&out)[N], const float (&x)[N][8], bool in) {
+  float lo[N], hi[N];
 #pragma unroll
-  for (int j = 0; j < G; ++j) {
-    const bool a = at.in && at.a / 64 == j, b = at.in && at.b / 64 == j;
-    float mn = INFINITY, mx = -INFINITY, zero = 0.f;
+  for (int n = 0; n < N; ++n) {
+    lo[n] = in ? x[n][0] : INFINITY;
+    hi[n] = in ? x[n][0] : -INFINITY;
+    if (in) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i < 4 ? !a : !b) continue;
-      mn = fminf(mn, x[i]);
-      mx = fmaxf(mx, x[i]);
-      zero += x[i] * 0.f;  // NaN where x is not finite
+      for (int i = 1; i < 8; ++i) {
+        lo[n] = min_nan(lo[n], x[n][i]);
+        hi[n] = max_nan(hi[n], x[n][i]);
+      }
     }
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) {
-      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      zero += __shfl_xor_sync(0xffffffffu, zero, o);
-    }
-    lo[j] = __bfloat162float(__float2bfloat16_rn(mn)) + zero;
-    const float range = mx - lo[j];
-    scale[j] = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(fmaxf(range, 0.f), 15.f)));
-    if (!(range < INFINITY) || !(fabsf(lo[j]) < INFINITY)) scale[j] = lo[j] = NAN;
-    out.pair[j] = pack_bf16(scale[j], lo[j]);
-    up[j] = scale[j] < 0x1p-100f ? 0x1p100f : 1.f;
-    scale[j] *= up[j];
-    inv[j] = __fdiv_rn(1.f, scale[j]);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int j = G == 1 ? 0 : (i < 4 ? at.a : at.b) >> 6;
-    const float s = j ? scale[G - 1] : scale[0];
-    if (s > 0.f)
-      out.code |= code_of(x[i], j ? lo[G - 1] : lo[0], j ? up[G - 1] : up[0], s,
-                          j ? inv[G - 1] : inv[0])
-                  << (4 * i);
+  for (int o = SAME / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      lo[n] = min_nan(lo[n], __shfl_xor_sync(0xffffffffu, lo[n], o));
+      hi[n] = max_nan(hi[n], __shfl_xor_sync(0xffffffffu, hi[n], o));
+    }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    float least = __bfloat162float(__float2bfloat16_rn(lo[n]));
+    const float range = hi[n] - least;
+    float scale = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(max_nan(range, 0.f), 15.f)));
+    if (!(range < INFINITY) || !(fabsf(least) < INFINITY)) scale = least = NAN;
+    out[n].pair = pack_bf16(scale, least);
+    // The nearest code, of a tie the even one: the quotient by one correction of the product
+    // with the inverse, which is the quotient rounded to fp32 and so exact for a tie. A power
+    // of two keeps the inverse of a very small scale finite. Codes are 0 where the scale is.
+    const float up = scale < 0x1p-100f ? 0x1p100f : 1.f;
+    scale *= up;
+    const float inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
+    float half[2] = {0.f, 0.f};  // four codes each
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+      const float a = (x[n][i] - least) * up, q = a * inv;
+      const float e = fmaf(fmaf(-q, scale, a), inv, q);
+      half[i / 4] = fmaf(half[i / 4], 16.f, rintf(fminf(fmaxf(e, 0.f), 15.f)));
+    }
+    out[n].code = (uint32_t)half[0] | (uint32_t)half[1] << 16;
   }
-  return out;
 }
 
-// FOUR: the cache in 4 bits.
-template <int W, bool FOUR>
-__global__ void __launch_bounds__(kThreads)
+// FOUR: the cache in 4 bits. An item is kPasses * 32 / W heads of one token;
+// requests and pages are looked up and angles copied two items ahead.
+template <int W, bool INTER, bool FOUR>
+__global__ void __launch_bounds__(kThreads, FOUR ? kPerSm4 : kPerSm)
     rope_append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int R = 32 / W, G = W == 16 ? 2 : 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % W;
-  const int y = (int)blockIdx.y;
-  const int kind = y < p.q_chunks ? 0 : y < p.q_chunks + p.kv_chunks ? 1 : 2;  // Q, K, V
-  const int chunk = y - (kind > 0 ? p.q_chunks : 0) - (kind > 1 ? p.kv_chunks : 0);
-  const int h0 = chunk * kUnroll * R + lane / W;
-  const int heads = kind == 0 ? p.Hq : p.at.Hkv, d = p.how.d;
-  const __nv_bfloat16* const x_of = kind == 0 ? p.Q : kind == 1 ? p.K : p.V;
-  const __nv_bfloat16* const weight = kind == 0 ? p.wq : kind == 1 ? p.wk : nullptr;
-  const long long ld = kind == 0 ? p.ldq : kind == 1 ? p.ldk : p.ldv;
-  const RopeLane at = rope_lane(p.how, l, kind < 2);
+  constexpr int R = 32 / W, U = kPasses, S = kStages, G = W == 16 ? 2 : 1;
+  __shared__ __align__(16) uint8_t rings[kWarps * S * kStage];
+  __shared__ float4 natural[FOUR ? kWarps : 1][128];  // 2 R rows in fp32, channels in order
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % W, seg = lane / W;
+  const int d = p.how.d;
+  const Piece mine = piece_of(p.deal, (int)blockIdx.x * kWarps + warp);
+  const uint32_t ring = smem_u32(rings) + warp * S * kStage, row = 2 * d;
+  // where a lane's channels lie in a row that is turned and in one that is not
+  const RopeLane at_turned = rope_lane(p.how, l, true), at_plain = rope_lane(p.how, l, false);
   grid_wait();
-  grid_launch_dependents();
-  if (kind == 1 && chunk == 0)
-    check_bounds(p.at, (long long)blockIdx.x * kThreads + threadIdx.x,
-                 (long long)gridDim.x * kThreads);
-  float w[8];
-  load_weight(w, weight, at);
-  for (int t = (int)blockIdx.x * kWarps + warp; t < p.at.total; t += (int)gridDim.x * kWarps) {
-    uint2 a[kUnroll], b[kUnroll];
+  Item next = mine.first, it = next;
+  Cursor cur;
+  struct Where {
+    int pos, page;  // pos -1: no place; page as the table has it
+  } where[S];       // of the items from the one worked on
+  int put = 0;      // items whose copies are issued
+  uint32_t to = ring;
+  auto issue = [&]() {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      a[u] = b[u] = make_uint2(0, 0);
-      const int h = h0 + u * R;
-      if (h < heads && at.in) {
-        const __nv_bfloat16* row = x_of + (long long)t * ld + h * d;
-        a[u] = ld_stream8(row + at.a);
-        b[u] = ld_stream8(row + at.b);
+    for (int k = 0; k + 1 < S; ++k) where[k] = where[k + 1];
+    if (put < mine.items) {
+      const int kind = kind_of(p, next.chunk);
+      const AppendSide& s = p.side[kind];
+      const int t = next.token, h = chunk_of(p, next.chunk) * U * R;
+      copy_async<U>(to, s.x + (long long)t * s.ld + h * d, min(U * R, s.heads - h) * 2 * d, lane);
+      cur.to(p.at, t);
+      Where& w = where[S - 1];
+      const long long pos = t + cur.shift;
+      w.pos = cur.request >= 0 && pos < 0x7fffffffLL ? (int)pos : -1;
+      w.page = w.pos >= 0 && kind > 0 ? table_page(p.at, cur.request, pos) : 0;
+      if (p.how.rot && w.pos >= p.how.positions) {
+        if (lane == 0) bad_index();
+        w.pos = -1;
       }
+      if (p.how.rot && kind < 2 && w.pos >= 0)
+        copy_async<1>(to + 512 * U, p.how.cos_sin + (size_t)w.pos * p.how.rot, 4 * p.how.rot, lane);
+      next.advance(p.deal);
+      if (++put == mine.items) grid_launch_dependents();
     }
-    const Token token = token_of(p.at, t);
-    bool ok = token.request >= 0;
-    int page = 0;
-    if (ok && kind > 0) {
-      page = page_of(p.at, token);
-      ok = page >= 0;
-    }
-    if (ok && p.how.rot > 0 && token.pos >= p.how.positions) {
-      if (lane == 0) bad_index();
-      ok = false;
-    }
-    if (!ok) {
-      if (kind != 0 || !p.fill) continue;
+    cp_async_commit();
+    to = to == ring + (S - 1) * kStage ? ring : to + kStage;
+  };
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int h = h0 + u * R;
-        if (h >= heads || !at.in) continue;
-        __nv_bfloat16* row = p.Qo + ((long long)t * heads + h) * d;
-        *reinterpret_cast<uint2*>(row + at.a) = make_uint2(0, 0);
-        *reinterpret_cast<uint2*>(row + at.b) = make_uint2(0, 0);
+  for (int i = 0; i < S - 1; ++i) issue();
+  check_bounds(p.at, (long long)blockIdx.x * kThreads + threadIdx.x,
+               (long long)gridDim.x * kThreads);
+  uint32_t stage = ring;
+  for (int i = 0; i < mine.items; ++i, it.advance(p.deal)) {
+    cp_async_wait<S - 2>();
+    __syncwarp();  // the stage has landed for every lane, and the last one is read
+    issue();
+    const int kind = kind_of(p, it.chunk);
+    const AppendSide& s = p.side[kind];
+    const int heads = s.heads, t = it.token, h0 = chunk_of(p, it.chunk) * U * R + seg;
+    const int pos = where[0].pos, page = where[0].page;
+    const bool norm = s.w != nullptr;
+    const RopeLane at = kind < 2 ? at_turned : at_plain;
+    const uint32_t rows = stage + seg * row;
+    Turn turn{};
+    if (kind < 2)
+      turn = rope_turn(rope_angles(stage + 512 * U, p.how, at, l), load_weight<INTER>(s.w, at));
+    stage = stage == ring + (S - 1) * kStage ? ring : stage + kStage;
+    if (pos < 0 || (kind > 0 && !page_ok(p.at, page))) {
+      if (kind == 0 && p.fill) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (h0 + u * R < heads && at.in) {
+            __nv_bfloat16* const out = s.y + ((long long)t * heads + h0 + u * R) * d;
+            *reinterpret_cast<uint2*>(out + at.a) = make_uint2(0, 0);
+            *reinterpret_cast<uint2*>(out + at.b) = make_uint2(0, 0);
+          }
       }
-      continue;
-    }
-    const int pos = (int)token.pos, in_page = pos & (p.at.page - 1);
-    Angles g{};
-    if (kind < 2) g = rope_angles(p.how, at, l, pos);
+    } else if (kind == 0 || !FOUR) {
+      // of head h0, and from head to head of this token
+      __nv_bfloat16* const out =
+          kind == 0 ? s.y + ((long long)t * heads + h0) * d
+                    : s.y + ((((long long)page * heads + h0) << p.at.page_shift) +
+                             (pos & (p.at.page - 1))) * d;
+      const long long step = kind == 0 ? d : (long long)d << p.at.page_shift;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * R;
-      if (h - lane / W >= heads) break;  // warp-uniform
-      float x[8];
-      unpack8(x, a[u], b[u]);
-      if (weight) norm8<W>(x, w, p.how);
-      if (kind < 2) turn8(x, p.how, at, g, 1.f);
-      const bool in = h < heads && at.in;
-      if (kind == 0 || !FOUR) {
-        if (!in) continue;
-        __nv_bfloat16* row =
-            kind == 0 ? p.Qo + ((long long)t * heads + h) * d
-                      : (kind == 1 ? p.Kc : p.Vc) +
-                            ((((long long)page * heads + h) << p.at.page_shift) + in_page) * d;
-        *reinterpret_cast<uint2*>(row + at.a) = pack4(x);
-        *reinterpret_cast<uint2*>(row + at.b) = pack4(x + 4);
-      } else {
-        const Codes c = quantize8<W, G>(x, at);
-        if (!in) continue;
-        uint32_t* const block = reinterpret_cast<uint32_t*>(
-            p.cache4 + ((((long long)page * heads + h) << p.at.page_shift) + (in_page & ~15)) *
-                           (G * kBlock4 / kRows4));
-        const int r = in_page & 15;
-        if (kind == 1) {
-          uint16_t* const half = reinterpret_cast<uint16_t*>(block);
-          half[2 * k_word4(G, r, at.a >> 6, (at.a >> 3) & 7) + ((at.a >> 2) & 1)] =
-              (uint16_t)c.code;
-          half[2 * k_word4(G, r, at.b >> 6, (at.b >> 3) & 7) + ((at.b >> 2) & 1)] =
-              (uint16_t)(c.code >> 16);
+      for (int u = 0; u < U; u += 2) {
+        if (h0 - seg + u * R >= heads) break;  // warp-uniform
+        if (kind < 2) {
+          Pairs y[2];
+          norm_and_turn<W, INTER, 2>(y, rows + u * R * row, R * row, turn, norm, p.how, at);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (h0 + (u + k) * R < heads && at.in)
+              store_row<INTER>(out + (u + k) * R * step, y[k], at);
         } else {
-          block[v_word4(G, r, at.a >> 6, (at.a >> 3) & 7)] = c.code;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (h0 + (u + k) * R < heads && at.in) {
+              const uint32_t from = rows + (u + k) * R * row;
+              *reinterpret_cast<uint2*>(out + (u + k) * R * step + at.a) =
+                  ld_shared8(from + 2 * at.a);
+              *reinterpret_cast<uint2*>(out + (u + k) * R * step + at.b) =
+                  ld_shared8(from + 2 * at.b);
+            }
         }
-        if (l < G) block[pair_word4(G, r, kind - 1, l)] = c.pair[G == 2 && l ? 1 : 0];
+      }
+    } else {
+      const int in_page = pos & (p.at.page - 1), r = in_page & 15, j = l >> 3;
+      uint8_t* const block =
+          p.cache4 + ((((long long)page * heads + h0) << p.at.page_shift) + (in_page & ~15)) *
+                         (G * kBlock4 / kRows4);
+      const long long step = (long long)(G * kBlock4 / kRows4) << p.at.page_shift;
+      const int word = kind == 1 ? k_word4(G, r, j, l & 7) : v_word4(G, r, j, l & 7);
+#pragma unroll
+      for (int u = 0; u < U; u += 2) {
+        if (h0 - seg + u * R >= heads) break;  // warp-uniform
+        float x[2][8];
+        if (kind == 1) {
+          Pairs y[2];
+          norm_and_turn<W, INTER, 2>(y, rows + u * R * row, R * row, turn, norm, p.how, at);
+          channels<INTER>(y[0], x[0]);
+          channels<INTER>(y[1], x[1]);
+          if (!INTER && p.how.rot > 0) {  // channels 8 l .. 8 l + 7 from the lanes that have them
+            float* const to = reinterpret_cast<float*>(natural[warp]) + seg * 8 * W;
+            __syncwarp();
+            if (at.in) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                *reinterpret_cast<float4*>(to + 256 * k + at.a) =
+                    make_float4(x[k][0], x[k][1], x[k][2], x[k][3]);
+                *reinterpret_cast<float4*>(to + 256 * k + at.b) =
+                    make_float4(x[k][4], x[k][5], x[k][6], x[k][7]);
+              }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float4 a = *reinterpret_cast<const float4*>(to + 256 * k + 8 * l);
+              const float4 b = *reinterpret_cast<const float4*>(to + 256 * k + 8 * l + 4);
+              x[k][0] = a.x, x[k][1] = a.y, x[k][2] = a.z, x[k][3] = a.w;
+              x[k][4] = b.x, x[k][5] = b.y, x[k][6] = b.z, x[k][7] = b.w;
+            }
+          }
+        } else {
+          channels<false>(row_of<false>(rows + u * R * row, at), x[0]);
+          channels<false>(row_of<false>(rows + (u + 1) * R * row, at), x[1]);
+        }
+        Codes code[2];
+        quantize8<(W < 8 ? W : 8), 2>(code, x, at.in);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (h0 + (u + k) * R < heads && at.in) {
+            uint32_t* const words = reinterpret_cast<uint32_t*>(block + (u + k) * R * step);
+            words[word] = code[k].code;
+            if ((l & 7) == 0) words[pair_word4(G, r, kind - 1, j)] = code[k].pair;
+          }
       }
     }
   }
@@ -249,44 +336,86 @@ struct ReadParams {
   int d, fill;
 };
 
-// A lane turns one word of eight codes into 16 bytes: 16 lanes take K and V of a row of G = 1,
-// 32 of G = 2. Sixteen tokens a block, so that most of a cache block's sectors, which the rows
-// of V share, are used from L1.
+// A word of eight codes as eight values in bf16.
+FA_DEV uint4 values8(uint32_t code, uint32_t pair) {
+  const float scale = bf16_lo(pair), lo = bf16_hi(pair);
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = pack_bf16(fmaf((float)(code >> (8 * i) & 15), scale, lo),
+                     fmaf((float)(code >> (8 * i + 4) & 15), scale, lo));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// A warp takes 16 rows of `total`, and of those the runs that lie in one block of the cache: it
+// reads the block's words in their order and writes eight channels a lane, 128 bytes of four
+// rows at a time. blockIdx.y: the heads y, y + gridDim.y, ...
 template <int G>
-__global__ void __launch_bounds__(512) cache4_read_kernel(const __grid_constant__ ReadParams p) {
-  constexpr int LANES = 16 * G, R = 32 / LANES;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LANES;
-  const int kv = l / (8 * G), j = l / 8 % G, word = l % 8, c0 = 64 * j + 8 * word;
+__global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_constant__ ReadParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = lane & 7, q = lane >> 3;  // word of a group; row of four
   grid_wait();
   grid_launch_dependents();
-  check_bounds(p.at, (long long)blockIdx.x * 512 + threadIdx.x, (long long)gridDim.x * 512);
-  const int t = (int)blockIdx.x * 16 + warp;
-  if (t >= p.at.total) return;
-  __nv_bfloat16* const out = (kv ? p.V : p.K) + (long long)t * p.at.Hkv * p.d + c0;
-  const Token token = token_of(p.at, t);
-  const int page = token.request >= 0 ? page_of(p.at, token) : -1;
-  if (page < 0) {
-    if (p.fill && c0 < p.d)
-      for (int h = lane / LANES; h < p.at.Hkv; h += R)
-        *reinterpret_cast<uint4*>(out + h * p.d) = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const int in_page = (int)token.pos & (p.at.page - 1), r = in_page & 15;
-  const int at = kv ? v_word4(G, r, j, word) : k_word4(G, r, j, word);
-  const int pair_at = pair_word4(G, r, kv, j);
-#pragma unroll 4
-  for (int h = lane / LANES; h < p.at.Hkv; h += R) {
-    const uint32_t* block = reinterpret_cast<const uint32_t*>(
-        p.cache + ((((long long)page * p.at.Hkv + h) << p.at.page_shift) + (in_page & ~15)) *
-                      (G * kBlock4 / kRows4));
-    const uint32_t code = block[at], pair = block[pair_at];
-    const float scale = bf16_lo(pair), lo = bf16_hi(pair);
-    uint32_t v[4];
+  if (blockIdx.y == 0)
+    check_bounds(p.at, (long long)blockIdx.x * kThreads + threadIdx.x,
+                 (long long)gridDim.x * kThreads);
+  const int t0 = ((int)blockIdx.x * kWarps + warp) * 16, t1 = min(t0 + 16, p.at.total);
+  Cursor cur;
+  for (int t = t0; t < t1;) {
+    cur.to(p.at, t);
+    const long long pos = t + cur.shift;
+    const int page = cur.request >= 0 ? table_page(p.at, cur.request, pos) : -1;
+    const bool ok = cur.request >= 0 && page_ok(p.at, page);
+    const int in_page = (int)pos & (p.at.page - 1), r0 = in_page & 15;
+    int n = ok ? min(16 - r0, cur.end - t) : 1;  // rows r0 .. r0 + n - 1 of the block
+    n = min(n, t1 - t);
+    if (!ok) {
+      if (p.fill)
+        for (int h = blockIdx.y; h < p.at.Hkv; h += gridDim.y)
+          for (int c = 8 * lane; c < p.d; c += 256) {
+            const long long to = ((long long)t * p.at.Hkv + h) * p.d + c;
+            *reinterpret_cast<uint4*>(p.K + to) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(p.V + to) = make_uint4(0, 0, 0, 0);
+          }
+      ++t;
+      continue;
+    }
+    for (int h = blockIdx.y; h < p.at.Hkv; h += gridDim.y) {
+      const uint32_t* const block = reinterpret_cast<const uint32_t*>(
+          p.cache +
+          ((((long long)page * p.at.Hkv + h) << p.at.page_shift) + (in_page & ~15)) *
+              (G * kBlock4 / kRows4));
+      uint32_t k[4][G], kp[4][G], vp[4][G];
+      uint4 v[G];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = pack_bf16(fmaf((float)(code >> (8 * i) & 15), scale, lo),
-                       fmaf((float)(code >> (8 * i + 4) & 15), scale, lo));
-    if (c0 < p.d) *reinterpret_cast<uint4*>(out + h * p.d) = make_uint4(v[0], v[1], v[2], v[3]);
+      for (int j = 0; j < G; ++j) {
+        v[j] = *reinterpret_cast<const uint4*>(block + v_word4(G, 2 * q, j, w));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          k[i][j] = block[k_word4(G, 4 * i + q, j, w)];
+          kp[i][j] = block[pair_word4(G, 4 * i + q, 0, j)];
+          // V's four words are of rows 2 q, 2 q + 1, 2 q + 8, 2 q + 9
+          vp[i][j] = block[pair_word4(G, 2 * q + (i & 1) + 8 * (i >> 1), 1, j)];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const int c = 64 * j + 8 * w;
+        const uint32_t words[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+        if (c >= p.d) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rk = 4 * i + q - r0, rv = 2 * q + (i & 1) + 8 * (i >> 1) - r0;
+          if (rk >= 0 && rk < n)
+            *reinterpret_cast<uint4*>(p.K + ((long long)(t + rk) * p.at.Hkv + h) * p.d + c) =
+                values8(k[i][j], kp[i][j]);
+          if (rv >= 0 && rv < n)
+            *reinterpret_cast<uint4*>(p.V + ((long long)(t + rv) * p.at.Hkv + h) * p.d + c) =
+                values8(words[i], vp[i][j]);
+        }
+      }
+    }
+    t += n;
   }
 }
 
@@ -310,15 +439,19 @@ struct Append {
   AppendParams& p;
   bool four;
   cudaStream_t stream;
-  template <int W>
+  template <int W, bool INTER>
   cudaError_t run() const {
-    const int per = kUnroll * (32 / W);
-    p.q_chunks = p.Q ? ceil_div(p.Hq, per) : 0;
-    p.kv_chunks = ceil_div(p.at.Hkv, per);
-    return launch_early(four ? rope_append_kernel<W, true> : rope_append_kernel<W, false>,
-                        dim3((unsigned)ceil_div(p.at.total, kWarps),
-                             (unsigned)(p.q_chunks + 2 * p.kv_chunks)),
-                        kThreads, 0, stream, p);
+    const int per = kPasses * (32 / W);
+    int chunks = 0;
+    for (int i = 0; i < 3; ++i) {
+      p.side[i].chunks = ceil_div(p.side[i].heads, per);
+      chunks += p.side[i].chunks;
+    }
+    const long long need = ((long long)p.at.total * chunks + kWarps - 1) / kWarps;
+    const int most = sm_count() * (four ? kPerSm4 : kPerSm), blocks = (int)(need < most ? need : most);
+    p.deal = deal(p.at.total, chunks, blocks, kWarps);
+    return launch_early(four ? rope_append_kernel<W, INTER, true> : rope_append_kernel<W, INTER, false>,
+                        dim3((unsigned)blocks), kThreads, 0, stream, p);
   }
 };
 
@@ -327,22 +460,20 @@ struct Append {
 cudaError_t launch_rope_append(const RopeAppendArgs& a, cudaStream_t s) {
   AppendParams p{};
   p.at = place_of(a.at);
-  p.Q = static_cast<const __nv_bfloat16*>(a.Q);
-  p.K = static_cast<const __nv_bfloat16*>(a.K);
-  p.V = static_cast<const __nv_bfloat16*>(a.V);
-  p.wq = static_cast<const __nv_bfloat16*>(a.how.q_weight);
-  p.wk = static_cast<const __nv_bfloat16*>(a.how.k_weight);
-  p.Qo = static_cast<__nv_bfloat16*>(a.Qo);
-  p.Kc = static_cast<__nv_bfloat16*>(a.Kc);
-  p.Vc = static_cast<__nv_bfloat16*>(a.Vc);
+  const void *const x[3] = {a.Q, a.K, a.V}, *const w[3] = {a.how.q_weight, a.how.k_weight, nullptr};
+  void* const y[3] = {a.Qo, a.Kc, a.Vc};
+  const long long ld[3] = {a.ldq, a.ldk, a.ldv};
+  for (int i = 0; i < 3; ++i) {
+    p.side[i].x = static_cast<const __nv_bfloat16*>(x[i]);
+    p.side[i].w = static_cast<const __nv_bfloat16*>(w[i]);
+    p.side[i].y = static_cast<__nv_bfloat16*>(y[i]);
+    p.side[i].ld = ld[i];
+    p.side[i].heads = i == 0 ? a.Hq : a.at.Hkv;
+  }
   p.cache4 = static_cast<uint8_t*>(a.cache4);
-  p.ldq = a.ldq;
-  p.ldk = a.ldk;
-  p.ldv = a.ldv;
   p.how = rope_how(a.how, a.at.d);
-  p.Hq = a.Hq;
   p.fill = a.fill;
-  return with_lanes(a.at.d, Append{p, a.cache4 != nullptr, s});
+  return with_lanes(p.how, Append{p, a.cache4 != nullptr, s});
 }
 
 cudaError_t launch_cache4_read(const Cache4ReadArgs& a, cudaStream_t s) {
@@ -353,8 +484,11 @@ cudaError_t launch_cache4_read(const Cache4ReadArgs& a, cudaStream_t s) {
   p.V = static_cast<__nv_bfloat16*>(a.V);
   p.d = a.at.d;
   p.fill = a.fill;
+  // A head a warp until there are enough of them.
+  const int blocks = ceil_div(p.at.total, 16 * kWarps), want = ceil_div(sm_count() * 8, blocks);
   return launch_early(groups4(p.d) == 2 ? cache4_read_kernel<2> : cache4_read_kernel<1>,
-                      dim3((unsigned)ceil_div(p.at.total, 16)), 512, 0, s, p);
+                      dim3((unsigned)blocks, (unsigned)(want < p.at.Hkv ? want : p.at.Hkv)),
+                      kThreads, 0, s, p);
 }
 
 cudaError_t rope_append_read_status(unsigned int* out) {

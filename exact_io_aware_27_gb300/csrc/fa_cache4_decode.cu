@@ -37,9 +37,12 @@ constexpr int kKeys = 32;              // keys of a warp's stage: two blocks of 
 constexpr int kChunk = kKeys * kWarps;  // keys per step of the split
 constexpr int kMaxSms = 160;         // slots are reserved for this many SMs
 
-// Blocks of the split kernel per SM at most, by the registers: 16 warps of 128, or 12 of 168
-// for two tiles of queries.
-constexpr int per_sm(int NT) { return NT == 1 ? 4 : 3; }
+// Blocks of the split kernel per SM at most, by the registers: 12 warps of 168, or 8 of more for
+// two tiles of queries.
+constexpr int per_sm(int NT) { return NT == 1 ? 3 : 2; }
+// A unit of at most so many chunks is one block's, where all units find a block at once: then
+// nothing is joined, and a call is one launch.
+constexpr int kWholeChunks = 8;
 
 struct Sizes {
   int B, Hq, Hkv, per_kv, d;
@@ -201,22 +204,35 @@ struct Tile {
   float m[NT][2], ref[NT][2], l[NT][2], top[NT][2];
   float v_ref, v_inv, v_top;  // o is in units of v_ref; the scale that moves it
 
-  FA_DEV void load(const __nv_bfloat16* Q, int rows, int d, float scale_log2, int lane) {
-    const int g = lane >> 2, t = lane & 3;
+  // The lane's part of the queries' rows.
+  struct Raw {
+    uint4 w[NT][G][2];
+    FA_DEV void load(const __nv_bfloat16* Q, int rows, int d, int lane) {
+      const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int c0 = 64 * j + 16 * t + 8 * u, row = 8 * n + g;
+            w[n][j][u] = make_uint4(0, 0, 0, 0);
+            if (row < rows && c0 < d) w[n][j][u] = *reinterpret_cast<const uint4*>(Q + row * d + c0);
+          }
+    }
+  };
+  FA_DEV void start(const Raw& raw, float scale_log2, int lane) {
+    const int t = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      uint4 w[G][2];
+      const uint4 (&w)[G][2] = raw.w[n];
       float most = 0.f;
 #pragma unroll
       for (int j = 0; j < G; ++j)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int c0 = 64 * j + 16 * t + 8 * u, row = 8 * n + g;
-          w[j][u] = make_uint4(0, 0, 0, 0);
-          if (row < rows && c0 < d) w[j][u] = *reinterpret_cast<const uint4*>(Q + row * d + c0);
+        for (int u = 0; u < 2; ++u)
           for (uint32_t x : {w[j][u].x, w[j][u].y, w[j][u].z, w[j][u].w})
             most = fmaxf(most, fmaxf(fabsf(bf16_lo(x)), fabsf(bf16_hi(x))));
-        }
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
       // 2^-8 of the query's power of two; an infinite entry stays one
@@ -260,66 +276,77 @@ struct Tile {
     v_top = -1.f;
   }
 
-  // The first `keys` of a stage's 16 keys.
-  FA_DEV void step(const Words<G>& w, int keys, int lane) {
+  // The first `keys` of a stage's two blocks, side by side: one block's chain of products,
+  // weights and products leaves half of the issue slots empty.
+  FA_DEV void step(const Words<G> (&w)[2], int keys, int lane) {
     const int g = lane >> 2;
-    float sk[2][G], mk[2][G], sv[2][G], mv[2][G];
+    float s[2][NT][4], sv[2][2][G], mv[2][2][G], acc[2][NT][G][4];
+    // The products of a sum one after another wait for each other: four sums in turn.
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int x = 0; x < 4; ++x)
 #pragma unroll
-      for (int j = 0; j < G; ++j) {
-        sk[h][j] = bf16_lo(w.pair[h][j]);
-        mk[h][j] = bf16_hi(w.pair[h][j]);
-        sv[h][j] = bf16_lo(w.pair[h][G + j]);
-        mv[h][j] = bf16_hi(w.pair[h][G + j]);
-      }
-    float s[NT][4];
-    {
-      float acc[NT][G][4];
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int j = 0; j < G; ++j)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t w0 = w.k[0][2 * j + x / 2], w1 = w.k[1][2 * j + x / 2];
+        for (int j = 0; j < G; ++j) {
+          const uint32_t w0 = w[k].k[0][2 * j + x / 2], w1 = w[k].k[1][2 * j + x / 2];
           const int e = 2 * (x & 1);
           const uint32_t a[4] = {codes(w0, e), codes(w1, e), codes(w0, e + 1), codes(w1, e + 1)};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             if (x == 0)
-              mma_f16_first(acc[n][j], a, q[n][j][x][0], q[n][j][x][1]);
+              mma_f16_first(acc[k][n][j], a, q[n][j][x][0], q[n][j][x][1]);
             else
-              mma_f16(acc[n][j], a, q[n][j][x][0], q[n][j][x][1]);
+              mma_f16(acc[k][n][j], a, q[n][j][x][0], q[n][j][x][1]);
           }
         }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s[n][i] = fmaf(sk[i >> 1][0], acc[n][0][i], mk[i >> 1][0] * qs[n][0][i & 1]);
+          const int h = i >> 1;
+          s[k][n][i] = fmaf(bf16_lo(w[k].pair[h][0]), acc[k][n][0][i],
+                            bf16_hi(w[k].pair[h][0]) * qs[n][0][i & 1]);
 #pragma unroll
           for (int j = 1; j < G; ++j)
-            s[n][i] = fmaf(sk[i >> 1][j], acc[n][j][i],
-                           fmaf(mk[i >> 1][j], qs[n][j][i & 1], s[n][i]));
+            s[k][n][i] = fmaf(bf16_lo(w[k].pair[h][j]), acc[k][n][j][i],
+                              fmaf(bf16_hi(w[k].pair[h][j]), qs[n][j][i & 1], s[k][n][i]));
         }
-    }
-    if (keys < 16) {  // what lies behind the keys may be anything
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        if (g + 8 * h >= keys) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) s[n][2 * h] = s[n][2 * h + 1] = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < G; ++j) sv[h][j] = mv[h][j] = 0.f;
+        for (int j = 0; j < G; ++j) {
+          sv[k][h][j] = bf16_lo(w[k].pair[h][G + j]);
+          mv[k][h][j] = bf16_hi(w[k].pair[h][G + j]);
         }
     }
-    float most = fmaxf(sv[0][0], sv[1][0]);
+    if (keys < kKeys) {  // what lies behind the keys may be anything
 #pragma unroll
-    for (int j = 1; j < G; ++j) most = fmaxf(most, fmaxf(sv[0][j], sv[1][j]));
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (g + 8 * h + 16 * k >= keys) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[k][n][2 * h] = s[k][n][2 * h + 1] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < G; ++j) sv[k][h][j] = mv[k][h][j] = 0.f;
+          }
+    }
+    float most = -1.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < G; ++j) most = max3f(most, sv[k][0][j], sv[k][1][j]);
     bool over = most > v_top;
+    float high[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) over |= fmaxf(s[n][e], s[n][2 + e]) > top[n][e];
+      for (int e = 0; e < 2; ++e) {
+        high[n][e] = max3f(fmaxf(s[0][n][e], s[0][n][2 + e]), s[1][n][e], s[1][n][2 + e]);
+        over |= high[n][e] > top[n][e];
+      }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int x = 4; x < 32; x *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
@@ -335,7 +362,7 @@ struct Tile {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(s[n][e], s[n][2 + e]);
+          float x = high[n][e];
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -356,43 +383,46 @@ struct Tile {
           }
         }
     }
-    uint32_t b[NT][G][2];
+    uint32_t b[2][NT][G][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int j = 0; j < G; ++j) sv[h][j] *= v_inv;
+      for (int n = 0; n < NT; ++n) {
+        float p[4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float p[4];
+        for (int e = 0; e < 2; ++e) {
+          p[e] = ex2(fmaf(s[k][n][e], c[n][e], ref[n][e]));
+          p[2 + e] = ex2(fmaf(s[k][n][2 + e], c[n][e], ref[n][e]));
+          l[n][e] += p[e] + p[2 + e];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        p[e] = ex2(fmaf(s[n][e], c[n][e], ref[n][e]));
-        p[2 + e] = ex2(fmaf(s[n][2 + e], c[n][e], ref[n][e]));
-        l[n][e] += p[e] + p[2 + e];
+          for (int j = 0; j < G; ++j)
+            z[n][j][e] = fmaf(p[e], mv[k][0][j], fmaf(p[2 + e], mv[k][1][j], z[n][j][e]));
+        }
 #pragma unroll
         for (int j = 0; j < G; ++j)
-          z[n][j][e] = fmaf(p[e], mv[0][j], fmaf(p[2 + e], mv[1][j], z[n][j][e]));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float f = sv[k][h][j] * v_inv;
+            b[k][n][j][h] = transpose8(pack_f16(p[2 * h] * f, p[2 * h + 1] * f));
+          }
       }
 #pragma unroll
-      for (int j = 0; j < G; ++j)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          b[n][j][h] = transpose8(pack_f16(p[2 * h] * sv[h][j], p[2 * h + 1] * sv[h][j]));
-    }
+      for (int j = 0; j < G; ++j) {
+        const uint32_t (&v)[4] = w[k].v[j];
+        const uint32_t two[2][2] = {
+            {__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410)},
+            {__byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632)}};
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-      const uint32_t two[2][2] = {
-          {__byte_perm(w.v[j][0], w.v[j][1], 0x5410), __byte_perm(w.v[j][2], w.v[j][3], 0x5410)},
-          {__byte_perm(w.v[j][0], w.v[j][1], 0x7632), __byte_perm(w.v[j][2], w.v[j][3], 0x7632)}};
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w0 = two[i / 2][0], w1 = two[i / 2][1];
+          const int e = 2 * (i & 1);
+          const uint32_t a[4] = {codes(w0, e), codes(w0, e + 1), codes(w1, e), codes(w1, e + 1)};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w0 = two[i / 2][0], w1 = two[i / 2][1];
-        const int e = 2 * (i & 1);
-        const uint32_t a[4] = {codes(w0, e), codes(w0, e + 1), codes(w1, e), codes(w1, e + 1)};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma_f16(o[n][j][i], a, b[n][j][0], b[n][j][1]);
+          for (int n = 0; n < NT; ++n) mma_f16(o[n][j][i], a, b[k][n][j][0], b[k][n][j][1]);
+        }
       }
-    }
   }
 
   // The sums over the lanes that share a query, in plain units.
@@ -447,7 +477,8 @@ struct Tile {
 
 FA_DEV float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }  // of a part
 
-template <int G, int NT>
+// WHOLE: a block per unit.
+template <int G, int NT, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, per_sm(NT))
     decode4_kernel(const __grid_constant__ DecodeParams p) {
   using C = Cfg<G, NT>;
@@ -457,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   __shared__ int warp_sums[kWarps];
   __shared__ uint32_t abort_flag, never;
   const Sizes& s = p.s;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   float* const parts = reinterpret_cast<float*>(smem4 + C::RINGS);
   int* const first = reinterpret_cast<int*>(smem4 + C::BYTES);
 
@@ -469,45 +500,49 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   grid_wait();
   grid_launch_dependents();
 
-  // Chunks before each request (exclusive scan of the lengths).
-  int run = 0;
-  for (int b0 = 0; b0 < s.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    int n = 0;
-    if (b < s.B) {
-      const int len = p.lens[b];
-      if ((len < 0 || len > p.max_pages << p.page_shift) && blockIdx.x == 0)
-        atomicOr(&g_decode4_status, kDeviceIndexBit);
-      n = (max(0, min(len, p.max_pages << p.page_shift)) + kChunk - 1) / kChunk;
-    }
-    int x = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    int before = run, sum = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += warp_sums[w];
-      sum += warp_sums[w];
-    }
-    if (b < s.B) first[b] = before + x - n;
-    run += sum;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) first[s.B] = run;
-  __syncthreads();
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b <= s.B; b += kThreads) s.first[b] = first[b];
-
-  const int chunks = run;  // of one (head, row tile)
-  const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)chunks, (unsigned)s.blocks);
   const int me = (int)blockIdx.x;
-  if (me >= sp.workers) return;
-  const unsigned x_begin = sp.start(me), x_end = sp.start(me + 1);
+  int chunks = 0;  // of one (head, row tile)
+  unsigned x_begin = 0, x_end = 0;
+  if constexpr (!WHOLE) {
+    // Chunks before each request (exclusive scan of the lengths).
+    int run = 0;
+    for (int b0 = 0; b0 < s.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      int n = 0;
+      if (b < s.B) {
+        const int len = p.lens[b];
+        if ((len < 0 || len > p.max_pages << p.page_shift) && blockIdx.x == 0)
+          atomicOr(&g_decode4_status, kDeviceIndexBit);
+        n = (max(0, min(len, p.max_pages << p.page_shift)) + kChunk - 1) / kChunk;
+      }
+      int x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) warp_sums[warp] = x;
+      __syncthreads();
+      int before = run, sum = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += warp_sums[w];
+        sum += warp_sums[w];
+      }
+      if (b < s.B) first[b] = before + x - n;
+      run += sum;
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) first[s.B] = run;
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int b = threadIdx.x; b <= s.B; b += kThreads) s.first[b] = first[b];
+    chunks = uniform(run);
+    const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)chunks, (unsigned)s.blocks);
+    if (me >= sp.workers) return;
+    x_begin = sp.start(me);
+    x_end = sp.start(me + 1);
+  }
 
   // A run of chunks of one unit.
   struct Run {
@@ -516,6 +551,14 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   };
   auto run_at = [&](unsigned x) {
     Run r;
+    if constexpr (WHOLE) {
+      r.ht = me / s.B;
+      r.b = me - r.ht * s.B;
+      r.len = uniform(keys_of(p, r.b));
+      r.x0 = r.u0 = 0;
+      r.x1 = r.u1 = (unsigned)((r.len + kChunk - 1) / kChunk);
+      return r;
+    }
     r.ht = (int)(x / (unsigned)chunks);
     const int in = (int)(x - (unsigned)(r.ht * chunks));
     int lo = 0, hi = s.B;  // first[lo] <= in < first[hi]
@@ -526,12 +569,12 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
       else
         hi = mid;
     }
-    r.b = lo;
-    r.u0 = (unsigned)(r.ht * chunks + first[lo]);
-    r.u1 = (unsigned)(r.ht * chunks + first[lo + 1]);
+    r.b = uniform(lo);
+    r.u0 = (unsigned)(r.ht * chunks + uniform(first[lo]));
+    r.u1 = (unsigned)(r.ht * chunks + uniform(first[lo + 1]));
     r.x0 = x;
     r.x1 = min(r.u1, x_end);
-    r.len = keys_of(p, lo);
+    r.len = uniform(keys_of(p, lo));
     return r;
   };
 
@@ -546,6 +589,12 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   // ---- the issuing side, up to STAGES stages ahead of the products: lanes 2 i and 2 i + 1 have
   // the addresses of the two blocks of stage i of the next 16, and issue their copies.
   Run ir = run_at(x_begin);
+  if constexpr (WHOLE) {
+    const int len = p.lens[ir.b];
+    if ((len < 0 || len > p.max_pages << p.page_shift) && threadIdx.x == 0)
+      atomicOr(&g_decode4_status, kDeviceIndexBit);
+    x_end = ir.x1;
+  }
   int ij = 0, i_stages = stages_of(ir);  // stages of the run that lanes have had, and all
   int i_at = 0, i_end = 0;               // of the 16
   int i_stage = 0, issued = 0;
@@ -602,13 +651,27 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   uint32_t phase = 0;
   bool alive = true;
   Tile<G, NT> tile;
-  for (unsigned x = x_begin; x < x_end;) {
-    const Run r = run_at(x);
-    x = r.x1;
+  typename Tile<G, NT>::Raw raw;
+  Run r = WHOLE ? ir : run_at(x_begin);
+  int rows;
+  size_t row0;
+  auto load_queries = [&]() {  // of run r
     const int hk = r.ht / s.row_tiles, rt = r.ht - hk * s.row_tiles;
-    const int rows = min(16, s.per_kv - rt * 16);
-    const size_t row0 = (size_t)r.b * s.Hq + hk * s.per_kv + rt * 16;
-    tile.load(p.Q + row0 * s.d, rows, s.d, p.scale_log2, lane);
+    rows = min(16, s.per_kv - rt * 16);
+    row0 = (size_t)r.b * s.Hq + hk * s.per_kv + rt * 16;
+    raw.load(p.Q + row0 * s.d, rows, s.d, lane);
+  };
+  load_queries();
+  if constexpr (WHOLE) {
+    if (r.len == 0) {
+      for (int i = threadIdx.x; i < rows * (s.d / 8); i += kThreads)
+        reinterpret_cast<uint4*>(p.O + row0 * s.d)[i] = make_uint4(0, 0, 0, 0);
+      if (threadIdx.x < rows) p.L[row0 + threadIdx.x] = -INFINITY;
+      return;
+    }
+  }
+  for (;;) {
+    tile.start(raw, p.scale_log2, lane);
     int keys = r.len - ((int)(r.x0 - r.u0) * kChunk + kKeys * warp);  // from the stage on
     for (int j = stages_of(r); j > 0; --j, keys -= kChunk) {
       if (alive) alive = warp_wait(&full[warp][stage], phase, wait);
@@ -619,13 +682,12 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
         stage = 0;
         phase ^= 1u;
       }
-      Words<G> w;
-      w.load(at, lane);
-      tile.step(w, keys, lane);
-      if (keys > kRows4) w.load(at + C::BLOCK, lane);
+      Words<G> w[2];
+      w[0].load(at, lane);
+      w[1].load(at + C::BLOCK, lane);
       __syncwarp();  // every lane has read the stage: it may be filled again
       issue();
-      if (keys > kRows4) tile.step(w, keys - kRows4, lane);
+      tile.step(w, keys, lane);
     }
     tile.finish();
     tile.store(parts + warp * C::ROWS * C::D, lane);
@@ -637,10 +699,16 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
           stats[warp][8 * n + 2 * lane + e] =
               make_float2(tile.m[n][e] * tile.c[n][e], tile.l[n][e]);
     }
-    __syncthreads();
-    const bool whole = r.x0 == r.u0 && r.x1 == r.u1;
+    const bool whole = r.x0 == r.u0 && r.x1 == r.u1, last = r.x1 == x_end;
     const unsigned slot = 2u * (unsigned)me + (r.x0 == r.u0 ? 1u : 0u);  // Split::slot
-    for (int i = threadIdx.x; i < rows * (C::D / 4); i += kThreads) {
+    const int done_rows = rows;
+    const size_t done_row0 = row0;
+    if (!last) {  // the next run's queries come while this one's parts are joined
+      r = run_at(r.x1);
+      load_queries();
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < done_rows * (C::D / 4); i += kThreads) {
       const int row = i / (C::D / 4), c = (i - row * (C::D / 4)) * 4;
       if (c >= s.d) continue;
       float top = -INFINITY, sum = 0.f;
@@ -661,9 +729,9 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
       }
       if (whole) {
         const float inv = 1.f / sum;
-        *reinterpret_cast<uint2*>(p.O + (row0 + row) * s.d + c) = make_uint2(
+        *reinterpret_cast<uint2*>(p.O + (done_row0 + row) * s.d + c) = make_uint2(
             pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-        if (c == 0) p.L[row0 + row] = (top + lg2(sum)) * kLn2;
+        if (c == 0) p.L[done_row0 + row] = (top + lg2(sum)) * kLn2;
       } else {
         const float inv = inverse(sum);
         const size_t at = (size_t)slot * s.slot_rows + row;
@@ -672,6 +740,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
         if (c == 0) s.e[at] = top + lg2(sum);
       }
     }
+    if (last) break;
     __syncthreads();  // the parts are read
   }
   // After a wait that ran out: the copies in flight land before the block's memory is given up.
@@ -699,12 +768,31 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = WARPS == 1 ? blockIdx.x * kJoinWarps + warp : blockIdx.x;
   const int mine = WARPS == 1 ? 0 : warp;
-  grid_wait();
+  const int b = min(row / s.Hq, s.B - 1), hq = min(row - b * s.Hq, s.Hq - 1);
+  const int hk = hq / s.per_kv, in = hq - hk * s.per_kv, ht = hk * s.row_tiles + in / 16;
+  // The lengths are the call's inputs: they were written before the split kernel, which launched
+  // this one, had started, so that the parts are found while that kernel runs. Many requests'
+  // lengths take longer to sum up than to read from where the split kernel puts their sums.
+  int f0 = 0, f1 = 0, chunks = 0;
+  if (s.B <= 256) {
+    for (int i = lane; i < s.B; i += 32) {
+      const int n = (keys_of(p, i) + kChunk - 1) / kChunk;
+      chunks += n;
+      if (i < b) f0 += n;
+      if (i == b) f1 = n;
+    }
+    chunks = __reduce_add_sync(0xffffffffu, chunks);
+    f0 = __reduce_add_sync(0xffffffffu, f0);
+    f1 = __reduce_add_sync(0xffffffffu, f1) + f0;
+    grid_wait();
+  } else {
+    grid_wait();
+    chunks = s.first[s.B];
+    f0 = s.first[b];
+    f1 = s.first[b + 1];
+  }
   grid_launch_dependents();
   if (row >= s.B * s.Hq) return;  // WARPS == 1 only: no barrier follows
-  const int b = row / s.Hq, hq = row - b * s.Hq;
-  const int hk = hq / s.per_kv, in = hq - hk * s.per_kv, ht = hk * s.row_tiles + in / 16;
-  const int chunks = s.first[s.B], f0 = s.first[b], f1 = s.first[b + 1];
   if (f0 == f1) {
     if (mine == 0 && 4 * lane < s.d)
       reinterpret_cast<uint2*>(p.O + (size_t)row * s.d)[lane] = make_uint2(0, 0);
@@ -739,7 +827,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     acc.z *= back;
     acc.w *= back;
     const int n = min(32, (parts - base - mine + WARPS - 1) / WARPS);  // lanes with a part
-    constexpr int U = 4;
+    constexpr int U = WARPS == 1 ? 4 : 5;
     for (int j = 0; j < n; j += U) {
       float4 v[U];
       float w[U];
@@ -818,12 +906,16 @@ cudaError_t launch(const Decode4Args& a, cudaStream_t stream) {
   p.page_shift = 0;
   while ((1 << p.page_shift) < a.page) ++p.page_shift;
   p.scale_log2 = a.scale * kLog2e;
-  cudaError_t e =
-      cudaFuncSetAttribute(decode4_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           C::BYTES + (8192 + 1) * 4);
+  const long long units = (long long)a.Hkv * p.s.row_tiles * a.B;
+  const bool whole =
+      ceil_div(a.max_pages * a.page, kChunk) <= kWholeChunks && units <= (long long)sms * per_sm(NT);
+  auto kernel = whole ? decode4_kernel<G, NT, true> : decode4_kernel<G, NT, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::BYTES + (8192 + 1) * 4);
   if (e != cudaSuccess) return e;
-  e = launch_early(decode4_kernel<G, NT>, dim3((unsigned)p.s.blocks), kThreads, smem, stream, p);
-  if (e != cudaSuccess) return e;
+  e = launch_early(kernel, dim3((unsigned)(whole ? units : p.s.blocks)), kThreads,
+                   whole ? C::BYTES : smem, stream, p);
+  if (e != cudaSuccess || whole) return e;
   const int rows = a.B * a.Hq;
   // A warp per row once there is a row for every fourth warp slot of the GPU's SMs.
   return rows >= sms * 4

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm)
     rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int R = 32 / W, U = kPasses, S = kForwardStages;
   __shared__ __align__(16) uint8_t rings[kWarps * S * kForwardStage];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % W, seg = lane / W;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, l = lane % W, seg = lane / W;
   const bool is_q = (int)blockIdx.x < p.q.deal.blocks;
   const Side& s = is_q ? p.q : p.k;
   const int d = p.how.d, heads = s.heads;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardPerSm)
   static_assert(kBackwardStages == 2, "one stage is worked on, one is on its way");
   __shared__ __align__(16) uint8_t rings[kWarps * 2 * kBackwardStage];
   __shared__ float sums[kWarps][8 * W];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % W, seg = lane / W;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, l = lane % W, seg = lane / W;
   const bool is_q = (int)blockIdx.x < p.q.deal.blocks;
   const Side& s = is_q ? p.q : p.k;
   const int d = p.how.d, heads = s.heads;

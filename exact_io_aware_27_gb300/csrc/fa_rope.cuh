@@ -26,6 +26,10 @@ struct RopeHow {
   int positions, rot, interleaved, d;
   float eps, inv_d;
 };
+// A value that is the same in all lanes, as one that the compiler knows to be: it then takes
+// uniform registers for it and what follows from it.
+FA_DEV int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 inline int sm_count() {
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess)

@@ -60,9 +60,9 @@ struct Cursor {
       lo += (31 - __clz(under)) * step;
       hi = min(hi, lo + step);
     }
-    const int from = p.cu[lo], start = p.starts[lo];
-    end = p.cu[lo + 1];
-    request = lo;
+    const int from = uniform(p.cu[lo]), start = uniform(p.starts[lo]);
+    end = uniform(p.cu[lo + 1]);
+    request = uniform(lo);
     shift = (long long)start - from;
     if (from < 0 || from > t || t >= end || start < 0) {
       if (lane == 0) bad_index();
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, FOUR ? kPerSm4 : kPerSm)
   constexpr int R = 32 / W, U = kPasses, S = kStages, G = W == 16 ? 2 : 1;
   __shared__ __align__(16) uint8_t rings[kWarps * S * kStage];
   __shared__ float4 natural[FOUR ? kWarps : 1][128];  // 2 R rows in fp32, channels in order
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % W, seg = lane / W;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, l = lane % W, seg = lane / W;
   const int d = p.how.d;
   const Piece mine = piece_of(p.deal, (int)blockIdx.x * kWarps + warp);
   const uint32_t ring = smem_u32(rings) + warp * S * kStage, row = 2 * d;
@@ -352,7 +352,7 @@ FA_DEV uint4 values8(uint32_t code, uint32_t pair) {
 // rows at a time. blockIdx.y: the heads y, y + gridDim.y, ...
 template <int G>
 __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_constant__ ReadParams p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int w = lane & 7, q = lane >> 3;  // word of a group; row of four
   grid_wait();
   grid_launch_dependents();

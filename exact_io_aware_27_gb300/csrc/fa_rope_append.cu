@@ -106,19 +106,23 @@ FA_DEV int chunk_of(const AppendParams& p, int c) {  // within the kind
   return c >= p.side[1].chunks ? c - p.side[1].chunks : c;
 }
 
-FA_DEV float min_nan(float a, float b) {  // NaN if either is
+FA_DEV float min_nan(float a, float b, float c) {  // NaN if one is
   float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-FA_DEV float max_nan(float a, float b) {
+FA_DEV float max_nan(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
 // Eight neighbouring channels of a group in 4 bits, of N rows side by side; SAME lanes have the
 // group. A group with a value that is not finite, or whose range is not, is held as NaN.
+//
+// Quotients are a product with an inverse, and one correction by the remainder: off by far
+// less than half a step of fp32, so that they round as the exact quotients do, and a tie
+// between two codes, which is a number of few bits, comes out exactly.
 struct Codes {
   uint32_t pair, code;
 };
@@ -127,44 +131,52 @@ FA_DEV void quantize8(Codes (&out)[N], const float (&x)[N][8], bool in) {
   float lo[N], hi[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    lo[n] = in ? x[n][0] : INFINITY;
-    hi[n] = in ? x[n][0] : -INFINITY;
-    if (in) {
-#pragma unroll
-      for (int i = 1; i < 8; ++i) {
-        lo[n] = min_nan(lo[n], x[n][i]);
-        hi[n] = max_nan(hi[n], x[n][i]);
-      }
+    lo[n] = min_nan(min_nan(x[n][0], x[n][1], x[n][2]), x[n][3], x[n][4]);
+    hi[n] = max_nan(max_nan(x[n][0], x[n][1], x[n][2]), x[n][3], x[n][4]);
+    lo[n] = min_nan(min_nan(lo[n], x[n][5], x[n][6]), x[n][7], x[n][7]);
+    hi[n] = max_nan(max_nan(hi[n], x[n][5], x[n][6]), x[n][7], x[n][7]);
+    if (!in) {
+      lo[n] = INFINITY;
+      hi[n] = -INFINITY;
     }
   }
 #pragma unroll
   for (int o = SAME / 2; o > 0; o >>= 1)
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      lo[n] = min_nan(lo[n], __shfl_xor_sync(0xffffffffu, lo[n], o));
-      hi[n] = max_nan(hi[n], __shfl_xor_sync(0xffffffffu, hi[n], o));
+      lo[n] = min_nan(lo[n], lo[n], __shfl_xor_sync(0xffffffffu, lo[n], o));
+      hi[n] = max_nan(hi[n], hi[n], __shfl_xor_sync(0xffffffffu, hi[n], o));
     }
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     float least = __bfloat162float(__float2bfloat16_rn(lo[n]));
-    const float range = hi[n] - least;
-    float scale = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(max_nan(range, 0.f), 15.f)));
+    const float range = hi[n] - least, span = max_nan(range, 0.f, 0.f);
+    constexpr float k15 = 1.f / 15.f;
+    const float fifteenth = fmaf(fmaf(-15.f, span * k15, span), k15, span * k15);
+    float scale = __bfloat162float(__float2bfloat16_rn(fifteenth));
     if (!(range < INFINITY) || !(fabsf(least) < INFINITY)) scale = least = NAN;
     out[n].pair = pack_bf16(scale, least);
-    // The nearest code, of a tie the even one: the quotient by one correction of the product
-    // with the inverse, which is the quotient rounded to fp32 and so exact for a tie. A power
-    // of two keeps the inverse of a very small scale finite. Codes are 0 where the scale is.
+    // A power of two keeps the inverse of a very small scale finite; codes are 0 where it is 0.
     const float up = scale < 0x1p-100f ? 0x1p100f : 1.f;
     scale *= up;
-    const float inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
-    float half[2] = {0.f, 0.f};  // four codes each
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+    if (!(scale > 0.f)) inv = 0.f;
+    const uint64_t up2 = both(up), from = both(-least * up), inv2 = both(inv), down = both(-scale);
+    // 1.5 2^23 + e is a number whose lowest bits are e's nearest integer; sixteen times the sum
+    // of those before and it are the codes so far, and a constant that wraps around.
+    uint32_t code = 0;
 #pragma unroll
-    for (int i = 7; i >= 0; --i) {
-      const float a = (x[n][i] - least) * up, q = a * inv;
-      const float e = fmaf(fmaf(-q, scale, a), inv, q);
-      half[i / 4] = fmaf(half[i / 4], 16.f, rintf(fminf(fmaxf(e, 0.f), 15.f)));
+    for (int i = 6; i >= 0; i -= 2) {
+      const uint64_t a = ffma2(f2pack(x[n][i], x[n][i + 1]), up2, from), q = fmul2(a, inv2);
+      float e0, e1;
+      f2unpack(ffma2(ffma2(q, down, a), inv2, q), e0, e1);
+      e0 = fminf(fmaxf(e0, 0.f), 15.f) + 12582912.f;
+      e1 = fminf(fmaxf(e1, 0.f), 15.f) + 12582912.f;
+      code = (code * 16u + __float_as_uint(e1)) * 16u + __float_as_uint(e0);
     }
-    out[n].code = (uint32_t)half[0] | (uint32_t)half[1] << 16;
+    // 0x4b400000 (1.5 2^23) times 1 + 16 + ... + 16^7 modulo 2^32
+    out[n].code = code - 0x4b400000u * 0x11111111u;
   }
 }
 
@@ -347,44 +359,42 @@ FA_DEV uint4 values8(uint32_t code, uint32_t pair) {
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// A warp takes 16 rows of `total`, and of those the runs that lie in one block of the cache: it
-// reads the block's words in their order and writes eight channels a lane, 128 bytes of four
-// rows at a time. blockIdx.y: the heads y, y + gridDim.y, ...
+// A warp takes a head of 16 rows of `total`, and of those the runs that lie in one block of the
+// cache: it reads the block's words in their order and writes eight channels a lane, 128 bytes
+// of four rows at a time. Neighbouring warps take the heads of the same rows, so that whole
+// rows leave together.
 template <int G>
 __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_constant__ ReadParams p) {
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int w = lane & 7, q = lane >> 3;  // word of a group; row of four
   grid_wait();
   grid_launch_dependents();
-  if (blockIdx.y == 0)
-    check_bounds(p.at, (long long)blockIdx.x * kThreads + threadIdx.x,
-                 (long long)gridDim.x * kThreads);
-  const int t0 = ((int)blockIdx.x * kWarps + warp) * 16, t1 = min(t0 + 16, p.at.total);
-  Cursor cur;
-  for (int t = t0; t < t1;) {
-    cur.to(p.at, t);
-    const long long pos = t + cur.shift;
-    const int page = cur.request >= 0 ? table_page(p.at, cur.request, pos) : -1;
-    const bool ok = cur.request >= 0 && page_ok(p.at, page);
-    const int in_page = (int)pos & (p.at.page - 1), r0 = in_page & 15;
-    int n = ok ? min(16 - r0, cur.end - t) : 1;  // rows r0 .. r0 + n - 1 of the block
-    n = min(n, t1 - t);
-    if (!ok) {
-      if (p.fill)
-        for (int h = blockIdx.y; h < p.at.Hkv; h += gridDim.y)
-          for (int c = 8 * lane; c < p.d; c += 256) {
-            const long long to = ((long long)t * p.at.Hkv + h) * p.d + c;
-            *reinterpret_cast<uint4*>(p.K + to) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(p.V + to) = make_uint4(0, 0, 0, 0);
-          }
-      ++t;
-      continue;
-    }
-    for (int h = blockIdx.y; h < p.at.Hkv; h += gridDim.y) {
+  check_bounds(p.at, (long long)blockIdx.x * kThreads + threadIdx.x,
+               (long long)gridDim.x * kThreads);
+  const long long all = (long long)((p.at.total + 15) / 16) * p.at.Hkv;
+  for (long long i = (long long)blockIdx.x * kWarps + warp; i < all;
+       i += (long long)gridDim.x * kWarps) {
+    const int t0 = (int)(i / p.at.Hkv) * 16, t1 = min(t0 + 16, p.at.total);
+    const int h = (int)(i % p.at.Hkv);
+    Cursor cur;
+    for (int t = t0; t < t1;) {
+      cur.to(p.at, t);
+      const long long pos = t + cur.shift;
+      const int page = cur.request >= 0 ? table_page(p.at, cur.request, pos) : -1;
+      if (cur.request < 0 || !page_ok(p.at, page)) {
+        if (p.fill && 8 * lane < p.d) {
+          const long long to = ((long long)t * p.at.Hkv + h) * p.d + 8 * lane;
+          *reinterpret_cast<uint4*>(p.K + to) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(p.V + to) = make_uint4(0, 0, 0, 0);
+        }
+        ++t;
+        continue;
+      }
+      const int in_page = (int)pos & (p.at.page - 1), r0 = in_page & 15;
+      const int n = min(min(16 - r0, cur.end - t), t1 - t);  // rows r0 .. r0 + n - 1 of the block
       const uint32_t* const block = reinterpret_cast<const uint32_t*>(
-          p.cache +
-          ((((long long)page * p.at.Hkv + h) << p.at.page_shift) + (in_page & ~15)) *
-              (G * kBlock4 / kRows4));
+          p.cache + ((((long long)page * p.at.Hkv + h) << p.at.page_shift) + (in_page & ~15)) *
+                        (G * kBlock4 / kRows4));
       uint32_t k[4][G], kp[4][G], vp[4][G];
       uint4 v[G];
 #pragma unroll
@@ -414,8 +424,8 @@ __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_cons
                 values8(words[i], vp[i][j]);
         }
       }
+      t += n;
     }
-    t += n;
   }
 }
 
@@ -484,11 +494,10 @@ cudaError_t launch_cache4_read(const Cache4ReadArgs& a, cudaStream_t s) {
   p.V = static_cast<__nv_bfloat16*>(a.V);
   p.d = a.at.d;
   p.fill = a.fill;
-  // A head a warp until there are enough of them.
-  const int blocks = ceil_div(p.at.total, 16 * kWarps), want = ceil_div(sm_count() * 8, blocks);
+  const long long warps = (long long)ceil_div(p.at.total, 16) * p.at.Hkv;
+  const long long blocks = (warps + kWarps - 1) / kWarps;
   return launch_early(groups4(p.d) == 2 ? cache4_read_kernel<2> : cache4_read_kernel<1>,
-                      dim3((unsigned)blocks, (unsigned)(want < p.at.Hkv ? want : p.at.Hkv)),
-                      kThreads, 0, s, p);
+                      dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), kThreads, 0, s, p);
 }
 
 cudaError_t rope_append_read_status(unsigned int* out) {

@@ -23,7 +23,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPasses = 4, kStages = 3;
 constexpr int kStage = 512 * kPasses + kAngleBytes;
 // Blocks on an SM, as many as the registers allow; 4 bits want 120.
-constexpr int kPerSm = 6, kPerSm4 = 4;
+constexpr int kPerSm = 6, kPerSm4 = 5;
 
 struct Place {
   const int *cu, *starts, *table;

@@ -497,21 +497,22 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
     fence_mbar_init();
   }
   if (threadIdx.x == 0) abort_flag = never = 0;
+  __syncthreads();
   grid_wait();
   grid_launch_dependents();
 
   const int me = (int)blockIdx.x;
   int chunks = 0;  // of one (head, row tile)
+  int mine = 0;    // up to 32 requests: chunks before request `lane`, in every warp by itself
+  const bool few = s.B <= 32;
   unsigned x_begin = 0, x_end = 0;
   if constexpr (!WHOLE) {
-    // Chunks before each request (exclusive scan of the lengths).
     int run = 0;
-    for (int b0 = 0; b0 < s.B; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
+    if (few) {
       int n = 0;
-      if (b < s.B) {
-        const int len = p.lens[b];
-        if ((len < 0 || len > p.max_pages << p.page_shift) && blockIdx.x == 0)
+      if (lane < s.B) {
+        const int len = p.lens[lane];
+        if ((len < 0 || len > p.max_pages << p.page_shift) && blockIdx.x == 0 && warp == 0)
           atomicOr(&g_decode4_status, kDeviceIndexBit);
         n = (max(0, min(len, p.max_pages << p.page_shift)) + kChunk - 1) / kChunk;
       }
@@ -521,22 +522,42 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
-      if (lane == 31) warp_sums[warp] = x;
-      __syncthreads();
-      int before = run, sum = 0;
+      run = __shfl_sync(0xffffffffu, x, 31);
+      mine = x - n;
+    } else {
+      // Chunks before each request (exclusive scan of the lengths).
+      for (int b0 = 0; b0 < s.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        int n = 0;
+        if (b < s.B) {
+          const int len = p.lens[b];
+          if ((len < 0 || len > p.max_pages << p.page_shift) && blockIdx.x == 0)
+            atomicOr(&g_decode4_status, kDeviceIndexBit);
+          n = (max(0, min(len, p.max_pages << p.page_shift)) + kChunk - 1) / kChunk;
+        }
+        int x = n;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += warp_sums[w];
-        sum += warp_sums[w];
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (lane == 31) warp_sums[warp] = x;
+        __syncthreads();
+        int before = run, sum = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) before += warp_sums[w];
+          sum += warp_sums[w];
+        }
+        if (b < s.B) first[b] = before + x - n;
+        run += sum;
+        __syncthreads();
       }
-      if (b < s.B) first[b] = before + x - n;
-      run += sum;
+      if (threadIdx.x == 0) first[s.B] = run;
       __syncthreads();
+      if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b <= s.B; b += kThreads) s.first[b] = first[b];
     }
-    if (threadIdx.x == 0) first[s.B] = run;
-    __syncthreads();
-    if (blockIdx.x == 0)
-      for (int b = threadIdx.x; b <= s.B; b += kThreads) s.first[b] = first[b];
     chunks = uniform(run);
     const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)chunks, (unsigned)s.blocks);
     if (me >= sp.workers) return;
@@ -561,6 +582,17 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
     }
     r.ht = (int)(x / (unsigned)chunks);
     const int in = (int)(x - (unsigned)(r.ht * chunks));
+    if (few) {  // the last request with chunks before it that are no more than `in`
+      const unsigned under = __ballot_sync(0xffffffffu, lane < s.B && mine <= in);
+      r.b = 31 - __clz(under);
+      r.u0 = (unsigned)(r.ht * chunks + __shfl_sync(0xffffffffu, mine, r.b));
+      r.u1 = (unsigned)(r.ht * chunks +
+                        (r.b + 1 < s.B ? __shfl_sync(0xffffffffu, mine, r.b + 1) : chunks));
+      r.x0 = x;
+      r.x1 = min(r.u1, x_end);
+      r.len = uniform(keys_of(p, r.b));
+      return r;
+    }
     int lo = 0, hi = s.B;  // first[lo] <= in < first[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -804,16 +836,28 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   const int parts = sp.owner((unsigned)(ht * chunks + f1) - 1u) - w0 + 1;
   if (parts == 1) return;
 
+  // Part i of the row in s.o and s.e.
+  auto place = [&](int i) {
+    return (size_t)Split::slot(0, 0, parts, w0, i) * s.slot_rows + in % 16;
+  };
+  const bool has = 4 * lane < s.d;
   float ref = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int base = 0; base < parts; base += 32 * WARPS) {
-    const int i = base + lane * WARPS + mine;
-    unsigned long long at = 0;
-    float e = -INFINITY;
-    if (i < parts) {
-      at = (unsigned long long)Split::slot(0, 0, parts, w0, i) * s.slot_rows + in % 16;
-      e = s.e[at];
-    }
+  for (int base = mine; base < parts; base += 32 * WARPS) {
+    const int i = base + lane * WARPS;
+    const float e = i < parts ? s.e[place(i)] : -INFINITY;
+    const int n = min(32, (parts - base + WARPS - 1) / WARPS);  // lanes with a part
+    constexpr int U = WARPS == 1 ? 6 : 16;
+    float4 v[U];
+    auto load = [&](int j) {  // the first ones on their way beside e
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j + u < n && has)
+          v[u] = reinterpret_cast<const float4*>(s.o + place(base + (j + u) * WARPS) * s.d)[lane];
+      }
+    };
+    load(0);
     float top = e;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -826,26 +870,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     acc.y *= back;
     acc.z *= back;
     acc.w *= back;
-    const int n = min(32, (parts - base - mine + WARPS - 1) / WARPS);  // lanes with a part
-    constexpr int U = WARPS == 1 ? 4 : 5;
     for (int j = 0; j < n; j += U) {
-      float4 v[U];
-      float w[U];
+      if (j > 0) load(j);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const unsigned long long from = __shfl_sync(0xffffffffu, at, (j + u) & 31);
-        w[u] = __shfl_sync(0xffffffffu, weight, (j + u) & 31);
-        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j + u < n && 4 * lane < s.d)
-          v[u] = reinterpret_cast<const float4*>(s.o + from * s.d)[lane];
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
+        const float w = __shfl_sync(0xffffffffu, weight, (j + u) & 31);
         if (j + u >= n) break;
-        acc.x += w[u] * v[u].x;
-        acc.y += w[u] * v[u].y;
-        acc.z += w[u] * v[u].z;
-        acc.w += w[u] * v[u].w;
+        acc.x += w * v[u].x;
+        acc.y += w * v[u].y;
+        acc.z += w * v[u].z;
+        acc.w += w * v[u].w;
       }
     }
   }

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(1024) reduce_kernel(const __grid_constant__ Re
   if (!out) return;
   float v = 0.f;
   if (c < p.d) {
-#pragma unroll 8
+#pragma unroll 16
     for (int r = row; r < rows; r += 32) v += from[(size_t)r * p.d + c];
   }
   sums[row][lane] = v;

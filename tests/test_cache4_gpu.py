@@ -205,8 +205,14 @@ def _check_decode(q, cache, table, lens, codes, pairs, place, scale=None, O=None
     ([130, 64], 16, 1, 128, 16), ([77, 400], 20, 1, 128, 64), ([90], 128, 1, 64, 16),
     ([257, 0, 31], 40, 2, 120, 16), ([5000], 32, 8, 128, 64), ([1, 9000], 3, 3, 40, 1024),
     ([i % 37 for i in range(300)], 4, 2, 64, 16), ([40000], 16, 2, 128, 32)])
-def test_decode(lens, hq, hkv, d, page):
-    _check_decode(*_decode_inputs(lens, hq, hkv, d, page, sum(lens) + d))
+@pytest.mark.parametrize("capacity", ["as needed", "wide"])
+def test_decode(lens, hq, hkv, d, page, capacity):
+    """Short tables take a block for each key/value head and request, others even pieces."""
+    args = _decode_inputs(lens, hq, hkv, d, page, sum(lens) + d)
+    if capacity == "wide":
+        more = torch.full((len(lens), 4096 // page), -9, dtype=torch.int32, device="cuda")
+        args = (*args[:2], torch.cat([args[2], more], 1), *args[3:])
+    _check_decode(*args)
 
 
 @pytest.mark.parametrize("std,scale", [(4.0, None), (0.0, None), (1.0, 1e-6), (1.0, 3.0),

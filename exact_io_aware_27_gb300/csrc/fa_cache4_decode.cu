@@ -109,12 +109,18 @@ struct Cfg {
   static constexpr int BYTES = RINGS + PARTS;  // then first[B + 1]
 };
 
-// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned, counted on `bar`.
-FA_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+// A lane's part of a stage, where `mine`: `bytes` (a multiple of 16) from global to shared memory,
+// both 16-byte aligned, counted on `bar`, or an arrival alone where there is no source.
+// Predicated, without branches.
+FA_DEV void bulk_load(bool mine, uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      "{\n\t.reg .pred p, q, r;\n\tsetp.ne.u32 p, %0, 0;\n\tsetp.ne.and.u64 q, %2, 0, p;\n\t"
+      "setp.eq.and.u64 r, %2, 0, p;\n\t"
+      "@r mbarrier.arrive.shared::cta.b64 _, [%4];\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%4], %3;\n\t"
+      "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%2], %3, [%4];"
+      "\n\t}" ::"r"((uint32_t)mine),
+      "r"(dst), "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
 FA_DEV uint4 ld_shared16(uint32_t a) {
@@ -617,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   };
 
   const uint32_t ring = smem_u32(smem4) + warp * C::STAGES * C::STAGE;
+  const uint32_t bars = smem_u32(&full[warp][0]);
   const WaitCtx wait{&abort_flag, &g_decode4_status};
   // ---- the issuing side, up to STAGES stages ahead of the products: lanes 2 i and 2 i + 1 have
   // the addresses of the two blocks of stage i of the next 16, and issue their copies.
@@ -661,15 +668,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   auto issue = [&]() {
     if (i_at == i_end) refill();
     if (!more) return;
-    if (lane >> 1 == i_at) {
-      uint64_t* bar = &full[warp][i_stage];
-      if (src) {
-        mbar_arrive_expect_tx(bar, C::BLOCK);
-        bulk_load(ring + i_stage * C::STAGE + (lane & 1) * C::BLOCK, src, C::BLOCK, bar);
-      } else {
-        mbar_arrive(bar);
-      }
-    }
+    bulk_load(lane >> 1 == i_at, ring + i_stage * C::STAGE + (lane & 1) * C::BLOCK, src, C::BLOCK,
+              bars + 8 * i_stage);
     i_stage = i_stage + 1 == C::STAGES ? 0 : i_stage + 1;
     ++issued;
     ++i_at;
@@ -921,7 +921,7 @@ cudaError_t launch(const Decode4Args& a, cudaStream_t stream) {
   DecodeParams p;
   p.s = sizes_of(a.B, a.Hq, a.Hkv, a.d);
   lay_out(&p.s, a.workspace, a.max_pages * a.page);
-  const int sms = sm_count() < kMaxSms ? sm_count() : kMaxSms, smem = C::BYTES + (a.B + 1) * 4;
+  const int count = sm_count(), sms = count < kMaxSms ? count : kMaxSms, smem = C::BYTES + (a.B + 1) * 4;
   // As many blocks as fit (an SM has 227 KB for them, and 1 KB of each is the system's), and no
   // more than the capacities can keep busy.
   const int fit = 227 * 1024 / (smem + 1024 + 1024), most = fit < per_sm(NT) ? fit : per_sm(NT);
@@ -944,8 +944,10 @@ cudaError_t launch(const Decode4Args& a, cudaStream_t stream) {
   const bool whole =
       ceil_div(a.max_pages * a.page, kChunk) <= kWholeChunks && units <= (long long)sms * per_sm(NT);
   auto kernel = whole ? decode4_kernel<G, NT, true> : decode4_kernel<G, NT, false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::BYTES + (8192 + 1) * 4);
+  cudaError_t e = cudaSuccess;
+  if (C::BYTES + (8192 + 1) * 4 > 48 * 1024 && !(whole && C::BYTES <= 48 * 1024))
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::BYTES + (8192 + 1) * 4);
   if (e != cudaSuccess) return e;
   e = launch_early(kernel, dim3((unsigned)(whole ? units : p.s.blocks)), kThreads,
                    whole ? C::BYTES : smem, stream, p);

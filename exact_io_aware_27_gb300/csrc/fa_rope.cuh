@@ -9,6 +9,8 @@
 // 4 l .. 4 l + 3. Only the sums over a row go through shuffles.
 #pragma once
 
+#include <atomic>
+
 #include "fa_rope.h"
 #include "sm103.cuh"
 
@@ -30,10 +32,16 @@ struct RopeHow {
 // uniform registers for it and what follows from it.
 FA_DEV int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
+// SMs of the current device, asked for once.
 inline int sm_count() {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  static std::atomic<int> known[64];
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  sms = known[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    known[dev].store(sms, std::memory_order_relaxed);
+  }
   return sms;
 }
 inline RopeHow rope_how(const fa_rope& h, int d) {

@@ -213,9 +213,9 @@ __global__ void __launch_bounds__(kThreads, FOUR ? kPerSm4 : kPerSm)
       cur.to(p.at, t);
       Where& w = where[S - 1];
       const long long pos = t + cur.shift;
-      w.pos = cur.request >= 0 && pos < 0x7fffffffLL ? (int)pos : -1;
+      w.pos = cur.request >= 0 ? (int)min(pos, 0x7fffffffLL) : -1;
       w.page = w.pos >= 0 && kind > 0 ? table_page(p.at, cur.request, pos) : 0;
-      if (p.how.rot && w.pos >= p.how.positions) {
+      if (w.pos == 0x7fffffff || (p.how.rot && w.pos >= p.how.positions)) {
         if (lane == 0) bad_index();
         w.pos = -1;
       }

@@ -417,8 +417,10 @@ FA_API int fa_rope_append(const void* Q, const void* K, const void* V, long long
  * fa_cache4_decode: one new token for each of B requests over the first lens[b] positions of
  * its row of block_table, as in fa_prefix_decode without a prefix: Q, O bf16 [B, Hq, d], dense;
  * L fp32 [B, Hq]; lens int32 [B] in device memory; O = 0 and L = -inf for a request without
- * keys. The products take the codes as they are and the scores and sums in fp32; the weights
- * times the scales are rounded to bf16. Entries of Q above 2^96 in magnitude may give NaN.
+ * keys. The products take the codes as they are; scores, softmax and sums are fp32. Q is held in
+ * fp16 times a power of two for each row, whose largest magnitude becomes 256 to 512 (entries
+ * 2^-18 of it and larger keep all their bits), and the weights times V's scales in fp16 times
+ * one that follows the largest scale met (11 bits, and none below 2^-24 of that scale).
  * Hq a multiple of Hkv, Hq / Hkv <= 128, 1 <= B <= 8192, ceil(Hq / Hkv / 16) * Hkv * B *
  * max_pages * page < 2^37. `workspace`: caller-owned device memory of at least
  * fa_cache4_workspace_bytes() bytes for `capacity` = max_pages * page keys a request (more for

@@ -281,6 +281,33 @@ def test_decode_a_wide_table_and_more_capacity_than_keys():
     _check_decode(q, cache, wide, lens, codes, pairs, place)
 
 
+@pytest.mark.parametrize("B", [1, 40, 700])
+def test_decode_without_any_page(B):
+    cache = fa.alloc_cache4(1, 2, 16, 64, "cuda")
+    q = torch.ones(B, 4, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(B, 0, dtype=torch.int32, device="cuda")
+    O, L = fa.fa_cache4_decode(q, cache, table, _i32([0] * B))
+    assert not bool(O.any()) and bool((L == -math.inf).all())
+    O, L = fa.fa_cache4_decode(q, cache, table, _i32([0] * (B - 1) + [1]))
+    assert fa.fa_get_device_status() == -8
+    assert not bool(O.any()) and bool((L == -math.inf).all())
+
+
+def test_decode_the_largest_batch():
+    """8192 requests: the lengths' sums take shared memory of the blocks'."""
+    lens = [(7 * i) % 50 for i in range(8192)]
+    q, cache, table, n, codes, pairs, place = _decode_inputs(lens, 2, 1, 8, 16, 83)
+    wide = torch.full((8192, 4096), -9, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    for t in (table, wide):
+        O, L = fa.fa_cache4_decode(q, cache, t, n)
+        for b in (0, 1, 2, 31, 32, 33, 4000, 4001, 8190, 8191):
+            pick = slice(b, b + 1)
+            _check_decode(q[pick], cache, t, n, codes, pairs, place[pick], O=O[pick], L=L[pick])
+        near = O if t is table else near
+    assert bool(((O.float() - near.float()).abs() <= 2 * ref.U * 4).all())
+
+
 def test_decode_reports_bad_lengths_and_pages():
     q, cache, table, lens, *_ = _decode_inputs([40, 40], 4, 2, 64, 16, 77)
     want = fa.fa_cache4_decode(q, cache, table, lens)

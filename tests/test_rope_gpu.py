@@ -354,7 +354,8 @@ def test_append_reports_bad_bounds(bounds, four):
 
 
 @pytest.mark.parametrize("four", [False, True])
-@pytest.mark.parametrize("what", ["page", "negative page", "position", "start", "angles"])
+@pytest.mark.parametrize("what", ["page", "negative page", "position", "start", "angles",
+                                  "far start", "far start, nothing turned"])
 def test_append_reports_bad_places(what, four):
     """The row concerned is not written, the others are."""
     total, page, d = 6, 16, 64
@@ -371,9 +372,13 @@ def test_append_reports_bad_places(what, four):
         ok = 5
     elif what == "start":
         st[1] = -1
-    else:
+    elif what == "angles":
         table = table[:15].contiguous()
         ok = 5
+    else:
+        st[1] = 2 ** 31 - 1
+        if "nothing" in what:
+            table = None
     if four:
         cache = fa.alloc_cache4(pages, 2, page, d, "cuda")
         Qo = fa.fa_cache4_append(q, k, k, cu, st, bt, cache, table, wq, wk)

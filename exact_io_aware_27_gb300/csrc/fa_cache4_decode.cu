@@ -15,8 +15,9 @@
 // A code alone in the lowest four bits of a 16-bit number is, read as fp16, code 2^-24, and in
 // the next four code 2^-20: two logical operations and half a shift turn two codes into
 // operands, exactly, without an addition. Q is brought to a largest value of 256 to 512 by a
-// power of two for each query, and P scale, rounded to fp16, by one for each warp that
-// follows the largest scale it has met: values below 2^-24 of that lose bits.
+// power of two for each query, and P scale, rounded to fp16, is taken relative to a reference
+// that follows its largest values, as the softmax's own reference follows the scores: what
+// loses bits, or is left out, is 2^-24 of the largest term or less.
 // Each warp has a ring of two stages of 32 keys, two bulk copies each.
 #include "fa_cache4.cuh"
 #include "fa_launch.h"
@@ -31,6 +32,9 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kRescale = 8.f;  // the reference maximum moves when passed by 2^8
+// P scale in units of its reference: the reference moves when passed by kMost, a number that
+// fp16 still has; it is at least kLeast.
+constexpr float kMost = 4096.f, kLeast = 0x1p-100f;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 32;              // keys of a warp's stage: two blocks of the cache
@@ -208,7 +212,7 @@ struct Tile {
   // reference, -c times it (0 if there is none yet), weight sum of this lane's keys, and the
   // score that moves the reference
   float m[NT][2], ref[NT][2], l[NT][2], top[NT][2];
-  float v_ref, v_inv, v_top;  // o is in units of v_ref; the scale that moves it
+  float v_ref[NT][2], v_inv[NT][2];  // o is in units of v_ref
 
   // The lane's part of the queries' rows.
   struct Raw {
@@ -276,10 +280,10 @@ struct Tile {
         c[n][e] = __shfl_sync(0xffffffffu, unit, 8 * t + 4 * e) * 0x1p24f * scale_log2;
         m[n][e] = top[n][e] = -INFINITY;
         ref[n][e] = l[n][e] = 0.f;
+        v_ref[n][e] = kLeast;
+        v_inv[n][e] = 1.f / kLeast;
       }
     }
-    v_ref = v_inv = 0.f;
-    v_top = -1.f;
   }
 
   // The first `keys` of a stage's two blocks, side by side: one block's chain of products,
@@ -339,12 +343,7 @@ struct Tile {
             for (int j = 0; j < G; ++j) sv[k][h][j] = mv[k][h][j] = 0.f;
           }
     }
-    float most = -1.f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int j = 0; j < G; ++j) most = max3f(most, sv[k][0][j], sv[k][1][j]);
-    bool over = most > v_top;
+    bool over = false;
     float high[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -354,16 +353,6 @@ struct Tile {
         over |= high[n][e] > top[n][e];
       }
     if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-      for (int x = 4; x < 32; x *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
-      float back = 1.f;
-      if (most > v_top) {
-        const float next = power_of_two(most);
-        back = v_ref / next;
-        v_ref = next;
-        v_inv = 1.f / next;
-        v_top = 16.f * next;  // with weights up to 2^8, P scale stays below 2^13
-      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -379,39 +368,86 @@ struct Tile {
           top[n][e] = x + kRescale / c[n][e];
           l[n][e] *= f;
 #pragma unroll
-          for (int j = 0; j < G; ++j) {
-            z[n][j][e] *= f;
+          for (int j = 0; j < G; ++j) z[n][j][e] *= f;
+          v_ref[n][e] = fmaxf(v_ref[n][e] * f, kLeast);  // for o
+          v_inv[n][e] = 1.f / v_ref[n][e];
+        }
+    }
+    // P, and P scale in units of v_ref
+    float p[2][NT][4], ps[2][NT][G][4], most = 0.f;
+    auto scaled = [&]() {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float f = p[k][n][i] * v_inv[n][i & 1];
+#pragma unroll
+            for (int j = 0; j < G; ++j) ps[k][n][j][i] = f * sv[k][i >> 1][j];
+          }
+    };
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          p[k][n][e] = ex2(fmaf(s[k][n][e], c[n][e], ref[n][e]));
+          p[k][n][2 + e] = ex2(fmaf(s[k][n][2 + e], c[n][e], ref[n][e]));
+          l[n][e] += p[k][n][e] + p[k][n][2 + e];
+#pragma unroll
+          for (int j = 0; j < G; ++j)
+            z[n][j][e] = fmaf(p[k][n][e], mv[k][0][j], fmaf(p[k][n][2 + e], mv[k][1][j], z[n][j][e]));
+        }
+    scaled();
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          most = max3f(most, ps[k][n][j][0], ps[k][n][j][1]);
+          most = max3f(most, ps[k][n][j][2], ps[k][n][j][3]);
+        }
+    if (__any_sync(0xffffffffu, most > kMost)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = kLeast;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < G; ++j)
+              x = max3f(x, p[k][n][e] * sv[k][0][j], p[k][n][2 + e] * sv[k][1][j]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          x = fmaxf(x, v_ref[n][e]);
+          const float f = v_ref[n][e] / x;
+          v_ref[n][e] = x;
+          v_inv[n][e] = 1.f / x;
+#pragma unroll
+          for (int j = 0; j < G; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              o[n][j][i][e] *= f * back;
-              o[n][j][i][2 + e] *= f * back;
+              o[n][j][i][e] *= f;
+              o[n][j][i][2 + e] *= f;
             }
-          }
         }
+      scaled();
     }
     uint32_t b[2][NT][G][2];
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float p[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          p[e] = ex2(fmaf(s[k][n][e], c[n][e], ref[n][e]));
-          p[2 + e] = ex2(fmaf(s[k][n][2 + e], c[n][e], ref[n][e]));
-          l[n][e] += p[e] + p[2 + e];
-#pragma unroll
-          for (int j = 0; j < G; ++j)
-            z[n][j][e] = fmaf(p[e], mv[k][0][j], fmaf(p[2 + e], mv[k][1][j], z[n][j][e]));
-        }
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < G; ++j)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float f = sv[k][h][j] * v_inv;
-            b[k][n][j][h] = transpose8(pack_f16(p[2 * h] * f, p[2 * h + 1] * f));
-          }
-      }
+          for (int h = 0; h < 2; ++h)
+            b[k][n][j][h] = transpose8(pack_f16(ps[k][n][j][2 * h], ps[k][n][j][2 * h + 1]));
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -448,8 +484,8 @@ struct Tile {
           const float add = all(z[n][j][e]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // even channels came times 2^-24, odd ones 2^-20
-            o[n][j][i][e] = fmaf(o[n][j][i][e] * 0x1p24f, v_ref, add);
-            o[n][j][i][2 + e] = fmaf(o[n][j][i][2 + e] * 0x1p20f, v_ref, add);
+            o[n][j][i][e] = fmaf(o[n][j][i][e] * 0x1p24f, v_ref[n][e], add);
+            o[n][j][i][2 + e] = fmaf(o[n][j][i][2 + e] * 0x1p20f, v_ref[n][e], add);
           }
         }
       }

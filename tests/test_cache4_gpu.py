@@ -238,6 +238,27 @@ def test_decode_growing_scores():
         _check_decode(q, c, table, lens, codes, p, place)
 
 
+@pytest.mark.parametrize("at", [0, 77, 199])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_a_large_value_of_small_weight(at, d):
+    """The other keys' values keep their bits beside a value 2^20 times as large whose weight is
+    e^-40, and so do values that grow, or shrink, by 2^40 along the keys."""
+    q, cache, table, lens, codes, pairs, place = _decode_inputs([200], 4, 1, d, 16, 84)
+    q.fill_(0.5)
+    pg, r = place[0]
+    p = pairs.clone()
+    p[0, pg[at], 0, r[at], :, 0] = 0.0
+    p[0, pg[at], 0, r[at], :, 1] = -10.0 * math.sqrt(64 / d)
+    p[1, pg[at], 0, r[at]] *= 2.0 ** 20
+    _check_decode(q, ref.pack(codes, p, d, cache).cuda(), table, lens, codes, p, place)
+    for sign in (1, -1):
+        p = pairs.clone()
+        p[1, pg, 0, r] *= (2.0 ** (sign * torch.linspace(-20, 20, 200, dtype=torch.float64)))[
+            :, None, None]
+        p = p.to(torch.bfloat16).double()
+        _check_decode(q, ref.pack(codes, p, d, cache).cuda(), table, lens, codes, p, place)
+
+
 def test_decode_a_key_that_is_not_a_number_reaches_its_head_only():
     q, cache, table, lens, codes, pairs, place = _decode_inputs([100, 100], 8, 2, 128, 16, 73)
     want = fa.fa_cache4_decode(q, cache, table, lens)

@@ -2,8 +2,9 @@
 // requests over its own keys.
 //
 //   split kernel  the keys of all (row tile, key/value head, request) units lie end to end in
-//                 chunks of 128, and every block takes an even piece of that axis (Split),
-//                 whatever the lengths, 32 keys of each chunk per warp. A unit that lies in
+//                 chunks of 128, each unit behind two steps for its start and end, and every
+//                 block takes an even piece of that axis (Split), whatever the lengths, 32
+//                 keys of each chunk per warp. A unit that lies in
 //                 one piece is finished there; else each piece gives a part (o, e) as in
 //                 fa_prefix.cu.
 //   join kernel   joins the parts, and fills the rows of requests without keys.
@@ -39,6 +40,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 32;              // keys of a warp's stage: two blocks of the cache
 constexpr int kChunk = kKeys * kWarps;  // keys per step of the split
+constexpr int kRunSteps = 2;            // steps that a unit's start and end count as, besides
 constexpr int kMaxSms = 160;         // slots are reserved for this many SMs
 
 // Blocks of the split kernel per SM at most, by the registers: 12 warps of 168, or 8 of more for
@@ -54,7 +56,7 @@ struct Sizes {
   int slot_rows;
   int blocks;      // launched
   float *o, *e;    // [slot][slot_rows][d], [slot][slot_rows]
-  int* first;      // [B + 1] chunks before each request
+  int* first;      // [B + 1] steps before each request
 };
 
 Sizes sizes_of(int B, int Hq, int Hkv, int d) {
@@ -77,7 +79,7 @@ size_t lay_out(Sizes* s, void* base, int capacity) {
     return q;
   };
   const size_t units = (size_t)s->Hkv * s->row_tiles * s->B;
-  const size_t steps = units * (((size_t)capacity + kChunk - 1) / kChunk);
+  const size_t steps = units * (capacity ? ((size_t)capacity + kChunk - 1) / kChunk + kRunSteps : 0);
   const size_t workers = (size_t)kMaxSms * per_sm(1);
   const size_t slots = 2 * (steps < workers ? steps : workers);
   s->o = reinterpret_cast<float*>(take(slots * s->slot_rows * s->d * 4));
@@ -99,6 +101,10 @@ struct DecodeParams {
 
 FA_DEV int keys_of(const DecodeParams& p, int b) {
   return max(0, min(p.lens[b], p.max_pages << p.page_shift));
+}
+// Steps of a unit of so many keys.
+FA_DEV int steps_of(int keys) {
+  return keys > 0 ? (keys + kChunk - 1) / kChunk + kRunSteps : 0;
 }
 
 template <int G, int NT>
@@ -544,118 +550,135 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   grid_launch_dependents();
 
   const int me = (int)blockIdx.x;
-  int chunks = 0;  // of one (head, row tile)
-  int mine = 0;    // up to 32 requests: chunks before request `lane`, in every warp by itself
+  int steps = 0;  // of one (head, row tile)
+  int before = 0;  // up to 32 requests: steps before request `lane`, in every warp by itself
   const bool few = s.B <= 32;
   unsigned x_begin = 0, x_end = 0;
   if constexpr (!WHOLE) {
-    int run = 0;
-    if (few) {
-      int n = 0;
-      if (lane < s.B) {
-        const int len = p.lens[lane];
-        if ((len < 0 || len > p.max_pages << p.page_shift) && blockIdx.x == 0 && warp == 0)
-          atomicOr(&g_decode4_status, kDeviceIndexBit);
-        n = (max(0, min(len, p.max_pages << p.page_shift)) + kChunk - 1) / kChunk;
-      }
-      int x = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      run = __shfl_sync(0xffffffffu, x, 31);
-      mine = x - n;
-    } else {
-      // Chunks before each request (exclusive scan of the lengths).
-      for (int b0 = 0; b0 < s.B; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        int n = 0;
-        if (b < s.B) {
-          const int len = p.lens[b];
-          if ((len < 0 || len > p.max_pages << p.page_shift) && blockIdx.x == 0)
-            atomicOr(&g_decode4_status, kDeviceIndexBit);
-          n = (max(0, min(len, p.max_pages << p.page_shift)) + kChunk - 1) / kChunk;
-        }
-        int x = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        if (lane == 31) warp_sums[warp] = x;
-        __syncthreads();
-        int before = run, sum = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          if (w < warp) before += warp_sums[w];
-          sum += warp_sums[w];
-        }
-        if (b < s.B) first[b] = before + x - n;
-        run += sum;
-        __syncthreads();
-      }
-      if (threadIdx.x == 0) first[s.B] = run;
-      __syncthreads();
-      if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b <= s.B; b += kThreads) s.first[b] = first[b];
+    // Steps before each request: an exclusive scan of the lengths, of neighbouring ones by a
+    // thread each.
+    const int per = few ? 1 : (s.B + kThreads - 1) / kThreads;
+    const int b0 = few ? lane : (int)threadIdx.x * per;
+    int n = 0;
+    bool bad = false;
+#pragma unroll 8
+    for (int i = 0; i < per; ++i) {
+      const int len = b0 + i < s.B ? p.lens[b0 + i] : 0;
+      bad |= len < 0 || len > p.max_pages << p.page_shift;
+      n += steps_of(max(0, min(len, p.max_pages << p.page_shift)));
     }
-    chunks = uniform(run);
-    const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)chunks, (unsigned)s.blocks);
+    if (bad && blockIdx.x == 0) atomicOr(&g_decode4_status, kDeviceIndexBit);
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    before = x - n;
+    steps = __shfl_sync(0xffffffffu, x, 31);
+    if (!few) {
+      if (lane == 31) warp_sums[warp] = x;
+      __syncthreads();
+      steps = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += warp_sums[w];
+        steps += warp_sums[w];
+      }
+      int at = before;
+#pragma unroll 8
+      for (int i = 0; i < per; ++i) {
+        if (b0 + i < s.B) {
+          first[b0 + i] = at;
+          if (blockIdx.x == 0) s.first[b0 + i] = at;
+          at += steps_of(keys_of(p, b0 + i));
+        }
+      }
+      if (threadIdx.x == 0) {
+        first[s.B] = steps;
+        if (blockIdx.x == 0) s.first[s.B] = steps;
+      }
+      __syncthreads();
+    }
+    steps = uniform(steps);
+    const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)steps, (unsigned)s.blocks);
     if (me >= sp.workers) return;
-    x_begin = sp.start(me);
-    x_end = sp.start(me + 1);
+    x_begin = (unsigned)uniform((int)sp.start(me));
+    x_end = (unsigned)uniform((int)sp.start(me + 1));
   }
-
-  // A run of chunks of one unit.
-  struct Run {
-    int b, ht, len;
-    unsigned x0, x1, u0, u1;  // this run's chunks, the unit's chunks
+  // Steps before request b, at most B.
+  auto first_of = [&](int b) {
+    int f = steps;
+    if (!few)
+      f = first[b];
+    else if (b < s.B)
+      f = __shfl_sync(0xffffffffu, before, b);
+    return uniform(f);
   };
-  auto run_at = [&](unsigned x) {
+
+  // A run of steps of one unit: chunks c0 .. c1 - 1 of its keys.
+  struct Run {
+    int b, ht, len, c0, c1;
+    unsigned x1;  // the end of its steps
+    int begins, ends;  // the unit
+  };
+  auto run_of = [&](int ht, int b, unsigned x) {  // from step x on
     Run r;
+    const unsigned u0 = (unsigned)(ht * steps + first_of(b));
+    const unsigned u1 = (unsigned)(ht * steps + first_of(b + 1));
+    r.b = uniform(b);
+    r.ht = uniform(ht);
+    r.x1 = (unsigned)uniform((int)min(u1, x_end));
+    r.c0 = uniform(max(0, (int)(x - u0) - kRunSteps));
+    r.c1 = uniform(max(0, (int)(r.x1 - u0) - kRunSteps));
+    r.begins = uniform(x == u0);
+    r.ends = uniform(r.x1 == u1);
+    r.len = uniform(keys_of(p, b));
+    return r;
+  };
+  auto first_run = [&]() {
     if constexpr (WHOLE) {
+      Run r;
       r.ht = me / s.B;
       r.b = me - r.ht * s.B;
       r.len = uniform(keys_of(p, r.b));
-      r.x0 = r.u0 = 0;
-      r.x1 = r.u1 = (unsigned)((r.len + kChunk - 1) / kChunk);
+      r.c0 = 0;
+      r.c1 = (r.len + kChunk - 1) / kChunk;
+      r.x1 = 0;
+      r.begins = r.ends = true;
       return r;
     }
-    r.ht = (int)(x / (unsigned)chunks);
-    const int in = (int)(x - (unsigned)(r.ht * chunks));
-    if (few) {  // the last request with chunks before it that are no more than `in`
-      const unsigned under = __ballot_sync(0xffffffffu, lane < s.B && mine <= in);
-      r.b = 31 - __clz(under);
-      r.u0 = (unsigned)(r.ht * chunks + __shfl_sync(0xffffffffu, mine, r.b));
-      r.u1 = (unsigned)(r.ht * chunks +
-                        (r.b + 1 < s.B ? __shfl_sync(0xffffffffu, mine, r.b + 1) : chunks));
-      r.x0 = x;
-      r.x1 = min(r.u1, x_end);
-      r.len = uniform(keys_of(p, r.b));
-      return r;
+    const int ht = (int)(x_begin / (unsigned)steps), in = (int)(x_begin - (unsigned)(ht * steps));
+    int lo = 0, hi = s.B;  // the last request with steps before it that are no more than `in`
+    if (few) {
+      lo = 31 - __clz(__ballot_sync(0xffffffffu, lane < s.B && before <= in));
+    } else {
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= in)
+          lo = mid;
+        else
+          hi = mid;
+      }
     }
-    int lo = 0, hi = s.B;  // first[lo] <= in < first[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first[mid] <= in)
-        lo = mid;
-      else
-        hi = mid;
+    return run_of(ht, uniform(lo), x_begin);
+  };
+  auto next_run = [&](const Run& r) {  // r.x1 < x_end
+    int ht = r.ht, b = r.b + 1;
+    for (;;) {  // requests without keys have no steps
+      if (b == s.B) {
+        b = 0;
+        ++ht;
+      }
+      if (first_of(b + 1) > first_of(b)) return run_of(ht, b, r.x1);
+      ++b;
     }
-    r.b = uniform(lo);
-    r.u0 = (unsigned)(r.ht * chunks + uniform(first[lo]));
-    r.u1 = (unsigned)(r.ht * chunks + uniform(first[lo + 1]));
-    r.x0 = x;
-    r.x1 = min(r.u1, x_end);
-    r.len = uniform(keys_of(p, lo));
-    return r;
   };
 
   // Stages of a run in which this warp has keys.
   auto stages_of = [&](const Run& r) {
-    const int key = (int)(r.x0 - r.u0) * kChunk + kKeys * warp;
-    return min((int)(r.x1 - r.x0), max(0, r.len - key + kChunk - 1) / kChunk);
+    const int key = r.c0 * kChunk + kKeys * warp;
+    return min(r.c1 - r.c0, max(0, r.len - key + kChunk - 1) / kChunk);
   };
 
   const uint32_t ring = smem_u32(smem4) + warp * C::STAGES * C::STAGE;
@@ -663,12 +686,12 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   const WaitCtx wait{&abort_flag, &g_decode4_status};
   // ---- the issuing side, up to STAGES stages ahead of the products: lanes 2 i and 2 i + 1 have
   // the addresses of the two blocks of stage i of the next 16, and issue their copies.
-  Run ir = run_at(x_begin);
+  Run ir = first_run();
+  const Run ir_first = ir;
   if constexpr (WHOLE) {
     const int len = p.lens[ir.b];
     if ((len < 0 || len > p.max_pages << p.page_shift) && threadIdx.x == 0)
       atomicOr(&g_decode4_status, kDeviceIndexBit);
-    x_end = ir.x1;
   }
   int ij = 0, i_stages = stages_of(ir);  // stages of the run that lanes have had, and all
   int i_at = 0, i_end = 0;               // of the 16
@@ -681,12 +704,11 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
         more = false;
         return;
       }
-      ir = run_at(ir.x1);
+      ir = next_run(ir);
       i_stages = stages_of(ir);
       ij = 0;
     }
-    const int key = ((int)(ir.x0 - ir.u0) + ij + (lane >> 1)) * kChunk + kKeys * warp +
-                    kRows4 * (lane & 1);
+    const int key = (ir.c0 + ij + (lane >> 1)) * kChunk + kKeys * warp + kRows4 * (lane & 1);
     src = nullptr;
     if (ij + (lane >> 1) < i_stages && key < ir.len) {
       int page = p.table[(size_t)ir.b * p.max_pages + (key >> p.page_shift)];
@@ -720,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   bool alive = true;
   Tile<G, NT> tile;
   typename Tile<G, NT>::Raw raw;
-  Run r = WHOLE ? ir : run_at(x_begin);
+  Run r = ir_first;
   int rows;
   size_t row0;
   auto load_queries = [&]() {  // of run r
@@ -740,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   }
   for (;;) {
     tile.start(raw, p.scale_log2, lane);
-    int keys = r.len - ((int)(r.x0 - r.u0) * kChunk + kKeys * warp);  // from the stage on
+    int keys = r.len - (r.c0 * kChunk + kKeys * warp);  // from the stage on
     for (int j = stages_of(r); j > 0; --j, keys -= kChunk) {
       if (alive) alive = warp_wait(&full[warp][stage], phase, wait);
       if (!alive) break;
@@ -767,12 +789,12 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
           stats[warp][8 * n + 2 * lane + e] =
               make_float2(tile.m[n][e] * tile.c[n][e], tile.l[n][e]);
     }
-    const bool whole = r.x0 == r.u0 && r.x1 == r.u1, last = r.x1 == x_end;
-    const unsigned slot = 2u * (unsigned)me + (r.x0 == r.u0 ? 1u : 0u);  // Split::slot
+    const bool whole = r.begins && r.ends, last = r.x1 == x_end;
+    const unsigned slot = 2u * (unsigned)me + (r.begins ? 1u : 0u);  // Split::slot
     const int done_rows = rows;
     const size_t done_row0 = row0;
     if (!last) {  // the next run's queries come while this one's parts are joined
-      r = run_at(r.x1);
+      r = next_run(r);
       load_queries();
     }
     __syncthreads();
@@ -841,21 +863,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   // The lengths are the call's inputs: they were written before the split kernel, which launched
   // this one, had started, so that the parts are found while that kernel runs. Many requests'
   // lengths take longer to sum up than to read from where the split kernel puts their sums.
-  int f0 = 0, f1 = 0, chunks = 0;
+  int f0 = 0, f1 = 0, steps = 0;
   if (s.B <= 256) {
     for (int i = lane; i < s.B; i += 32) {
-      const int n = (keys_of(p, i) + kChunk - 1) / kChunk;
-      chunks += n;
+      const int n = steps_of(keys_of(p, i));
+      steps += n;
       if (i < b) f0 += n;
       if (i == b) f1 = n;
     }
-    chunks = __reduce_add_sync(0xffffffffu, chunks);
+    steps = __reduce_add_sync(0xffffffffu, steps);
     f0 = __reduce_add_sync(0xffffffffu, f0);
     f1 = __reduce_add_sync(0xffffffffu, f1) + f0;
     grid_wait();
   } else {
     grid_wait();
-    chunks = s.first[s.B];
+    steps = s.first[s.B];
     f0 = s.first[b];
     f1 = s.first[b + 1];
   }
@@ -867,9 +889,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     if (mine == 0 && lane == 0) p.L[row] = -INFINITY;
     return;
   }
-  const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)chunks, (unsigned)s.blocks);
-  const int w0 = sp.owner((unsigned)(ht * chunks + f0));
-  const int parts = sp.owner((unsigned)(ht * chunks + f1) - 1u) - w0 + 1;
+  const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)steps, (unsigned)s.blocks);
+  const int w0 = sp.owner((unsigned)(ht * steps + f0));
+  const int parts = sp.owner((unsigned)(ht * steps + f1) - 1u) - w0 + 1;
   if (parts == 1) return;
 
   // Part i of the row in s.o and s.e.
@@ -961,8 +983,9 @@ cudaError_t launch(const Decode4Args& a, cudaStream_t stream) {
   // As many blocks as fit (an SM has 227 KB for them, and 1 KB of each is the system's), and no
   // more than the capacities can keep busy.
   const int fit = 227 * 1024 / (smem + 1024 + 1024), most = fit < per_sm(NT) ? fit : per_sm(NT);
+  const long long units = (long long)a.Hkv * p.s.row_tiles * a.B;
   const long long steps =
-      (long long)a.Hkv * p.s.row_tiles * a.B * ceil_div(a.max_pages * a.page, kChunk);
+      a.max_pages ? units * (ceil_div(a.max_pages * a.page, kChunk) + kRunSteps) : 0;
   const long long blocks = (long long)sms * most;
   p.s.blocks = (int)(blocks < steps ? blocks : steps > 0 ? steps : 1);
   p.Q = static_cast<const __nv_bfloat16*>(a.Q);
@@ -976,7 +999,6 @@ cudaError_t launch(const Decode4Args& a, cudaStream_t stream) {
   p.page_shift = 0;
   while ((1 << p.page_shift) < a.page) ++p.page_shift;
   p.scale_log2 = a.scale * kLog2e;
-  const long long units = (long long)a.Hkv * p.s.row_tiles * a.B;
   const bool whole =
       ceil_div(a.max_pages * a.page, kChunk) <= kWholeChunks && units <= (long long)sms * per_sm(NT);
   auto kernel = whole ? decode4_kernel<G, NT, true> : decode4_kernel<G, NT, false>;

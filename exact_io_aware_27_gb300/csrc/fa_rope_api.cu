@@ -328,7 +328,7 @@ int fa_cache4_decode(const void* Q, const void* cache, const int* block_table, i
   if ((rc = check_scale_value(scale)) != FA_OK) return rc;
   if (max_pages < 0 || (long long)max_pages * page > kMaxKeys) return FA_ERR_INVALID_ARG;
   // the kernels count chunks of keys in 32 bits
-  if ((long long)Hkv * ((Hq / Hkv + 15) / 16) * B * (((long long)max_pages * page + 63) / 64) >
+  if ((long long)Hkv * ((Hq / Hkv + 7) / 8) * B * (((long long)max_pages * page + 63) / 64) >
       0x7fffffffLL)
     return FA_ERR_INVALID_ARG;
   if (!Q || !cache || !lens || !O || !L || !workspace || (max_pages > 0 && !block_table))

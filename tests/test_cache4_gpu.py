@@ -203,7 +203,8 @@ def _check_decode(q, cache, table, lens, codes, pairs, place, scale=None, O=None
     ([15, 16, 17, 1, 31, 32, 33], 8, 2, 64, 16), ([63, 64, 65, 127, 128, 129], 4, 1, 128, 32),
     ([300, 5], 7, 1, 72, 64), ([200, 70, 0, 1000], 8, 1, 96, 128), ([500, 3], 18, 2, 64, 16),
     ([130, 64], 16, 1, 128, 16), ([77, 400], 20, 1, 128, 64), ([90], 128, 1, 64, 16),
-    ([257, 0, 31], 40, 2, 120, 16), ([5000], 32, 8, 128, 64), ([1, 9000], 3, 3, 40, 1024),
+    ([257, 0, 31], 40, 2, 120, 16), ([70, 33], 24, 1, 128, 16), ([200], 32, 1, 64, 16),
+    ([150, 20], 48, 1, 128, 16), ([5000], 32, 8, 128, 64), ([1, 9000], 3, 3, 40, 1024),
     ([i % 37 for i in range(300)], 4, 2, 64, 16), ([40000], 16, 2, 128, 32)])
 @pytest.mark.parametrize("capacity", ["as needed", "wide"])
 def test_decode(lens, hq, hkv, d, page, capacity):

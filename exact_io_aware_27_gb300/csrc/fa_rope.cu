@@ -7,7 +7,11 @@
 //             dx = r (g o w - n mean(g o w o n))
 //
 // Bound by memory: a row is read once and written once (forward), or dy and x read and dx
-// written (backward), and everything between stays in registers (fa_rope.cuh).
+// written (backward), and everything between stays in registers (fa_rope.cuh). 16384 rows of
+// 32/8 heads, d = 128, norm and rotation: forward 53 us (336 MB, 6.3 TB/s, 93 % of the measured
+// copy rate), backward 80 us (503 MB, 6.3 TB/s), with the sums of dw over the blocks 140 us
+// together. Both took 179 us with a block per eight rows and loads into registers: the registers
+// that hide the loads' way are then the limit.
 #include "fa_launch.h"
 #include "fa_rope.cuh"
 

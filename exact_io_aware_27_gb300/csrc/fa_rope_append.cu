@@ -5,7 +5,10 @@
 // (position mod page) of page table[i, position / page] and turns by that position's angles.
 // Bound by memory: every row is read once and written once. A warp takes a few heads of Q, K or
 // V of one token after another, all warps side by side, and looks a request up only where
-// another one begins. Indices are checked as in fa_cache.cu: a place out of range is not written and
+// another one begins. 32768 rows of 32/8 heads, d = 128, into the bf16 cache: 137 us (805 MB,
+// 5.9 TB/s, 87 % of the measured copy rate). Into the cache in 4 bits the codes cost about as many
+// instructions as norm and rotation together, and the kernel is bound by those: 8192 rows 49 us
+// (177 MB). Indices are checked as in fa_cache.cu: a place out of range is not written and
 // raises kDeviceIndexBit, and so do bounds that break the rule.
 #include "fa_cache4.cuh"
 #include "fa_launch.h"
@@ -362,7 +365,8 @@ FA_DEV uint4 values8(uint32_t code, uint32_t pair) {
 // A warp takes a head of 16 rows of `total`, and of those the runs that lie in one block of the
 // cache: it reads the block's words in their order and writes eight channels a lane, 128 bytes
 // of four rows at a time. Neighbouring warps take the heads of the same rows, so that whole
-// rows leave together.
+// rows leave together (70700 rows, 8 heads, d = 128: 64 us, 378 MB, 5.9 TB/s; with the heads of
+// a row one after another in a warp 74).
 template <int G>
 __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_constant__ ReadParams p) {
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;

@@ -2,11 +2,11 @@
 // requests over its own keys.
 //
 //   split kernel  the keys of all (row tile, key/value head, request) units lie end to end in
-//                 chunks of 128, each unit behind two steps for its start and end, and every
-//                 block takes an even piece of that axis (Split), whatever the lengths, 32
-//                 keys of each chunk per warp. A unit that lies in
-//                 one piece is finished there; else each piece gives a part (o, e) as in
-//                 fa_prefix.cu.
+//                 chunks, each unit behind two steps for its start and end, and every worker
+//                 takes an even piece of that axis (Split), whatever the lengths. A worker is a
+//                 block with chunks of 128 keys, 32 of them per warp, or, where there are many
+//                 units, a warp with chunks of 32. A unit that lies in one piece is finished
+//                 there; else each piece gives a part (o, e) as in fa_prefix.cu.
 //   join kernel   joins the parts, and fills the rows of requests without keys.
 //
 // Warp-level products (16 x 8 x 16) with the keys as the 16 rows and the queries of a
@@ -20,17 +20,18 @@
 // that follows its largest values, as the softmax's own reference follows the scores: what
 // loses bits, or is left out, is 2^-24 of the largest term or less.
 // Each warp has a ring of two stages of 32 keys, two bulk copies each; the values of a run (a
-// unit, or the part of it in a block's piece) that are the same in all lanes are told to be so
+// unit, or the part of it in a worker's piece) that are the same in all lanes are told to be so
 // (uniform()), which takes them out of the registers that the products need. That, and 32 keys
 // at a time instead of 16, is what 12 warps an SM with 168 registers each allow.
 //
 // Bound by instructions, just before memory: about 520 a warp for 32 keys (d = 128), 176 of them
-// to take codes apart. 256 requests of up to 8192 keys, 32/8 heads, d = 128 (1.2 GB): 206 us,
-// 5.8 TB/s, 86 % of the measured copy rate; with all keys in L2 it takes as long. The first
+// to take codes apart. 256 requests of up to 8192 keys, 32/8 heads, d = 128 (1.2 GB): 201 us,
+// 6.0 TB/s, 88 % of the measured copy rate; with all keys in L2 it takes as long. The first
 // form, 16 keys a step with the codes as bf16 values 128 + code, took 385 us. 32 requests of up
 // to 4096 keys (73 MB): 23 us, of which 3.5 until the first keys are there, 13 at that rate,
 // and the rest the ends of units and the join.
 #include "fa_cache4.cuh"
+#include "fa_decode.h"
 #include "fa_launch.h"
 #include "fa_rope.cuh"
 #include "fa_split.cuh"
@@ -49,10 +50,16 @@ constexpr float kMost = 4096.f, kLeast = 0x1p-100f;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 32;              // keys of a warp's stage: two blocks of the cache
-constexpr int kChunk = kKeys * kWarps;  // keys per step of the split
+constexpr int kChunk = kKeys * kWarps;  // keys of a block's step
 // Steps that a unit's start and end count as, besides (1000 requests of up to 1000 keys, 8/2
-// heads, d = 128: 50 us; with 1 step 53, with 3 51).
+// heads, d = 128, on whole blocks: 50 us; with 1 step 53, with 3 51; on single warps 3 are as
+// good as 2).
 constexpr int kRunSteps = 2;
+// From so many units on, each warp has its own: a unit's start and end cost a warp what they cost
+// a block, and there is nothing to join between warps. With fewer, pieces of a unit are so many
+// that joining them costs more (d = 128; 128 units of up to 4096 keys: 18 us with blocks, 20 with
+// warps; 256: 23 and 23; 2000 of up to 1000 keys: 50 and 43; 8000 of up to 500: 111 and 74).
+constexpr int kSoloUnits = 320;
 constexpr int kMaxSms = 160;         // slots are reserved for this many SMs
 
 // Blocks of the split kernel per SM at most, by the registers: 12 warps of 168, or 8 of more for
@@ -68,12 +75,15 @@ struct Sizes {
   int tile;        // queries of a tile, 8 or 16
   int row_tiles;   // tiles of a key/value head's queries
   int slot_rows;
-  int blocks;      // launched
+  bool solo;       // a worker of the split is a warp, not a block
+  int chunk;       // keys of a step
+  int workers;     // of the split
+  long long units, steps;  // steps of all units, at most
   float *o, *e;    // [slot][slot_rows][d], [slot][slot_rows]
   int* first;      // [B + 1] steps before each request
 };
 
-Sizes sizes_of(int B, int Hq, int Hkv, int d) {
+Sizes sizes_of(int B, int Hq, int Hkv, int d, int capacity) {
   Sizes s{};
   s.B = B;
   s.Hq = Hq;
@@ -86,9 +96,16 @@ Sizes sizes_of(int B, int Hq, int Hkv, int d) {
   s.tile = 7 * ceil_div(s.per_kv, 16) < 4 * ceil_div(s.per_kv, 8) ? 16 : 8;
   s.row_tiles = ceil_div(s.per_kv, s.tile);
   s.slot_rows = s.per_kv < s.tile ? s.per_kv : s.tile;
+  s.units = (long long)Hkv * s.row_tiles * B;
+  auto steps = [&](int chunk) {
+    return capacity ? s.units * (((long long)capacity + chunk - 1) / chunk + kRunSteps) : 0;
+  };
+  s.solo = s.units >= kSoloUnits && steps(kKeys) <= 0x7fffffff;  // counted in 32 bits
+  s.chunk = s.solo ? kKeys : kChunk;
+  s.steps = steps(s.chunk);
   return s;
 }
-size_t lay_out(Sizes* s, void* base, int capacity) {
+size_t lay_out(Sizes* s, void* base) {
   uint8_t* p = static_cast<uint8_t*>(base);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -96,10 +113,9 @@ size_t lay_out(Sizes* s, void* base, int capacity) {
     at += (bytes + 255) / 256 * 256;
     return q;
   };
-  const size_t units = (size_t)s->Hkv * s->row_tiles * s->B;
-  const size_t steps = units * (capacity ? ((size_t)capacity + kChunk - 1) / kChunk + kRunSteps : 0);
-  const size_t workers = (size_t)kMaxSms * per_sm(1);
-  const size_t slots = 2 * (steps < workers ? steps : workers);
+  // no fewer for more keys, with which warps may not be counted any longer
+  const size_t workers = (size_t)kMaxSms * per_sm(1) * (s->units >= kSoloUnits ? kWarps : 1);
+  const size_t slots = 2 * ((size_t)s->steps < workers ? (size_t)s->steps : workers);
   s->o = reinterpret_cast<float*>(take(slots * s->slot_rows * s->d * 4));
   s->e = reinterpret_cast<float*>(take(slots * s->slot_rows * 4));
   s->first = reinterpret_cast<int*>(take(((size_t)s->B + 1) * 4));
@@ -121,8 +137,8 @@ FA_DEV int keys_of(const DecodeParams& p, int b) {
   return max(0, min(p.lens[b], p.max_pages << p.page_shift));
 }
 // Steps of a unit of so many keys.
-FA_DEV int steps_of(int keys) {
-  return keys > 0 ? (keys + kChunk - 1) / kChunk + kRunSteps : 0;
+FA_DEV int steps_of(int keys, int chunk) {
+  return keys > 0 ? (keys + chunk - 1) / chunk + kRunSteps : 0;
 }
 
 template <int G, int NT>
@@ -515,6 +531,43 @@ struct Tile {
       }
   }
 
+  // The first `rows` rows as they are: O and L of a whole unit, or o and e of a part. A lane has
+  // eight neighbouring channels of each group.
+  FA_DEV void write(int rows, int d, int lane, bool whole, __nv_bfloat16* O, float* part,
+                    float* stat) const {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * n + 2 * t + e;
+        if (row >= rows) continue;
+        const float sum = l[n][e], top = m[n][e] * c[n][e] + lg2(sum);
+        const float inv = whole || sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          const int col = 64 * j + 8 * g;
+          if (col >= d) continue;
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[2 * i] = o[n][j][i][e] * inv;
+            v[2 * i + 1] = o[n][j][i][2 + e] * inv;
+          }
+          if (whole) {
+            *reinterpret_cast<uint4*>(O + row * d + col) =
+                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                           pack_bf16(v[6], v[7]));
+          } else {
+            float4* const to = reinterpret_cast<float4*>(part + row * d + col);
+            to[0] = make_float4(v[0], v[1], v[2], v[3]);
+            to[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
+        }
+        if (g == 0) stat[row] = whole ? top * kLn2 : top;
+      }
+  }
+
   // Rows [0, 8 NT) of o as floats [row][64 G]: two channels at a time, pair x of every four
   // at x ^ (row % 8 / 2), which puts a half warp's stores into different banks.
   FA_DEV void store(float* part, int lane) const {
@@ -543,11 +596,15 @@ struct Tile {
 
 FA_DEV float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }  // of a part
 
-// WHOLE: a block per unit.
-template <int G, int NT, bool WHOLE>
+// A block takes a piece of the split (kPieces) or a unit (kWhole), 32 keys of each chunk a warp,
+// or each warp takes a piece by itself (kSolo).
+enum Mode { kPieces, kWhole, kSolo };
+template <int G, int NT, Mode MODE>
 __global__ void __launch_bounds__(kThreads, per_sm(NT))
     decode4_kernel(const __grid_constant__ DecodeParams p) {
   using C = Cfg<G, NT>;
+  constexpr bool WHOLE = MODE == kWhole, SOLO = MODE == kSolo;
+  constexpr int CHUNK = SOLO ? kKeys : kChunk;
   extern __shared__ __align__(128) uint8_t smem4[];
   __shared__ uint64_t full[kWarps][C::STAGES];
   __shared__ float2 stats[kWarps][C::ROWS];  // a warp's reference and weight sum
@@ -556,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   const Sizes& s = p.s;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   float* const parts = reinterpret_cast<float*>(smem4 + C::RINGS);
-  int* const first = reinterpret_cast<int*>(smem4 + C::BYTES);
+  int* const first = reinterpret_cast<int*>(smem4 + (SOLO ? C::RINGS : C::BYTES));
 
   if (lane == 0) {
     for (int i = 0; i < C::STAGES; ++i) mbar_init(&full[warp][i], 2);
@@ -567,7 +624,9 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   grid_wait();
   grid_launch_dependents();
 
-  const int me = (int)blockIdx.x;
+  // neighbouring pieces on different SMs
+  const int me = SOLO ? warp * (int)gridDim.x + (int)blockIdx.x : (int)blockIdx.x;
+  const int shift = SOLO ? 0 : kKeys * warp;  // of the warp's keys in a chunk
   int steps = 0;  // of one (head, row tile)
   int before = 0;  // up to 32 requests: steps before request `lane`, in every warp by itself
   const bool few = s.B <= 32;
@@ -583,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
     for (int i = 0; i < per; ++i) {
       const int len = b0 + i < s.B ? p.lens[b0 + i] : 0;
       bad |= len < 0 || len > p.max_pages << p.page_shift;
-      n += steps_of(max(0, min(len, p.max_pages << p.page_shift)));
+      n += steps_of(max(0, min(len, p.max_pages << p.page_shift)), CHUNK);
     }
     if (bad && blockIdx.x == 0) atomicOr(&g_decode4_status, kDeviceIndexBit);
     int x = n;
@@ -609,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
         if (b0 + i < s.B) {
           first[b0 + i] = at;
           if (blockIdx.x == 0) s.first[b0 + i] = at;
-          at += steps_of(keys_of(p, b0 + i));
+          at += steps_of(keys_of(p, b0 + i), CHUNK);
         }
       }
       if (threadIdx.x == 0) {
@@ -619,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
       __syncthreads();
     }
     steps = uniform(steps);
-    const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)steps, (unsigned)s.blocks);
+    const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)steps, (unsigned)s.workers);
     if (me >= sp.workers) return;
     x_begin = (unsigned)uniform((int)sp.start(me));
     x_end = (unsigned)uniform((int)sp.start(me + 1));
@@ -661,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
       r.b = me - r.ht * s.B;
       r.len = uniform(keys_of(p, r.b));
       r.c0 = 0;
-      r.c1 = (r.len + kChunk - 1) / kChunk;
+      r.c1 = (r.len + CHUNK - 1) / CHUNK;
       r.x1 = 0;
       r.begins = r.ends = true;
       return r;
@@ -695,8 +754,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
 
   // Stages of a run in which this warp has keys.
   auto stages_of = [&](const Run& r) {
-    const int key = r.c0 * kChunk + kKeys * warp;
-    return min(r.c1 - r.c0, max(0, r.len - key + kChunk - 1) / kChunk);
+    const int key = r.c0 * CHUNK + shift;
+    return min(r.c1 - r.c0, max(0, r.len - key + CHUNK - 1) / CHUNK);
   };
 
   const uint32_t ring = smem_u32(smem4) + warp * C::STAGES * C::STAGE;
@@ -726,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
       i_stages = stages_of(ir);
       ij = 0;
     }
-    const int key = (ir.c0 + ij + (lane >> 1)) * kChunk + kKeys * warp + kRows4 * (lane & 1);
+    const int key = (ir.c0 + ij + (lane >> 1)) * CHUNK + shift + kRows4 * (lane & 1);
     src = nullptr;
     if (ij + (lane >> 1) < i_stages && key < ir.len) {
       int page = p.table[(size_t)ir.b * p.max_pages + (key >> p.page_shift)];
@@ -780,8 +839,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   }
   for (;;) {
     tile.start(raw, p.scale_log2, lane);
-    int keys = r.len - (r.c0 * kChunk + kKeys * warp);  // from the stage on
-    for (int j = stages_of(r); j > 0; --j, keys -= kChunk) {
+    int keys = r.len - (r.c0 * CHUNK + shift);  // from the stage on
+    for (int j = stages_of(r); j > 0; --j, keys -= CHUNK) {
       if (alive) alive = warp_wait(&full[warp][stage], phase, wait);
       if (!alive) break;
       const uint32_t at = ring + stage * C::STAGE;
@@ -798,6 +857,24 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
       tile.step(w, keys, lane);
     }
     tile.finish();
+    const bool whole = r.begins && r.ends, last = r.x1 == x_end;
+    const unsigned slot = 2u * (unsigned)me + (r.begins ? 1u : 0u);  // Split::slot
+    const int done_rows = rows;
+    const size_t done_row0 = row0;
+    if constexpr (SOLO) {
+      if (!last) {  // the next run's queries come while this one's results go
+        r = next_run(r);
+        load_queries();
+      }
+      if (whole)
+        tile.write(done_rows, s.d, lane, true, p.O + done_row0 * s.d, (float*)nullptr,
+                   p.L + done_row0);
+      else
+        tile.write(done_rows, s.d, lane, false, (__nv_bfloat16*)nullptr,
+                   s.o + (size_t)slot * s.slot_rows * s.d, s.e + (size_t)slot * s.slot_rows);
+      if (last) break;
+      continue;
+    }
     tile.store(parts + warp * C::ROWS * C::D, lane);
     if (lane < 4) {
 #pragma unroll
@@ -807,10 +884,6 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
           stats[warp][8 * n + 2 * lane + e] =
               make_float2(tile.m[n][e] * tile.c[n][e], tile.l[n][e]);
     }
-    const bool whole = r.begins && r.ends, last = r.x1 == x_end;
-    const unsigned slot = 2u * (unsigned)me + (r.begins ? 1u : 0u);  // Split::slot
-    const int done_rows = rows;
-    const size_t done_row0 = row0;
     if (!last) {  // the next run's queries come while this one's parts are joined
       r = next_run(r);
       load_queries();
@@ -863,20 +936,92 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
   }
 }
 
-// A row (request, query head) is joined by one warp, or by kJoinWarps where there are few rows:
-// lane i looks up part i's e, and the warp adds the parts up, four columns a lane, of which the
-// first 6 or 16 are on their way beside e: the kernel is a chain of waits for memory, about 3 us
-// behind the split kernel. Rows that the split kernel has finished are left alone.
-constexpr int kJoinWarps = 8;
+// A row (request, query head) is joined by one warp, or by kJoinWarps where there are few rows or
+// the row has more than kAlone parts (a request much longer than the others; one of 131072 keys
+// among 320, a key/value head of 8 queries: 47 us for the call, with a warp for each row 245).
+// Rows of a block are gridDim.x apart, so that such a request's are many blocks' work. Lane i
+// looks up part i's e, and the warp adds the parts up, four columns a lane, of which the first 6
+// or 16 are on their way beside e: the kernel is a chain of waits for memory, about 3 us behind
+// the split kernel. Rows that the split kernel has finished are left alone.
+constexpr int kJoinWarps = 8, kAlone = 32;
+
+// What a row's parts come to, for one warp of WARPS: sum_i w_i o_i and sum_i w_i (this lane's),
+// w_i = 2^(e_i - ref).
+struct Joined {
+  float ref, sum;
+  float4 acc;
+};
+template <int WARPS, int U>  // U parts on their way at a time
+FA_DEV Joined join_parts(const Sizes& s, int in, int w0, int parts, int mine, int lane) {
+  // Part i of the row in s.o and s.e.
+  auto place = [&](int i) {
+    return (size_t)Split::slot(0, 0, parts, w0, i) * s.slot_rows + in % s.tile;
+  };
+  const bool has = 4 * lane < s.d;
+  Joined r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int base = mine; base < parts; base += 32 * WARPS) {
+    const int i = base + lane * WARPS;
+    const float e = i < parts ? s.e[place(i)] : -INFINITY;
+    const int n = min(32, (parts - base + WARPS - 1) / WARPS);  // lanes with a part
+    float4 v[U];
+    auto load = [&](int j) {  // the first ones on their way beside e
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j + u < n && has)
+          v[u] = reinterpret_cast<const float4*>(s.o + place(base + (j + u) * WARPS) * s.d)[lane];
+      }
+    };
+    load(0);
+    float top = e;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float next = fmaxf(r.ref, top);
+    const float back = r.ref == next ? 1.f : ex2(r.ref - next);  // 0 on the first round
+    r.ref = next;
+    const float weight = i < parts ? ex2(e - (r.ref == -INFINITY ? 0.f : r.ref)) : 0.f;
+    r.sum = r.sum * back + weight;
+    r.acc.x *= back;
+    r.acc.y *= back;
+    r.acc.z *= back;
+    r.acc.w *= back;
+    for (int j = 0; j < n; j += U) {
+      if (j > 0) load(j);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float w = __shfl_sync(0xffffffffu, weight, (j + u) & 31);
+        if (j + u >= n) break;
+        r.acc.x += w * v[u].x;
+        r.acc.y += w * v[u].y;
+        r.acc.z += w * v[u].z;
+        r.acc.w += w * v[u].w;
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) r.sum += __shfl_xor_sync(0xffffffffu, r.sum, x);
+  return r;
+}
+
+FA_DEV void write_row(const DecodeParams& p, int row, int lane, const Joined& r) {
+  const float inv = 1.f / r.sum;
+  if (4 * lane < p.s.d)
+    reinterpret_cast<uint2*>(p.O + (size_t)row * p.s.d)[lane] =
+        make_uint2(pack_bf16(r.acc.x * inv, r.acc.y * inv),
+                   pack_bf16(r.acc.z * inv, r.acc.w * inv));
+  if (lane == 0) p.L[row] = (r.ref + lg2(r.sum)) * kLn2;
+}
+
 template <int WARPS>  // of a row
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(32 * kJoinWarps, WARPS == 1 ? 4 : 2)
     join4_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ float4 sums[kJoinWarps][32];
   __shared__ float2 stats[kJoinWarps];
+  __shared__ int4 many[kJoinWarps];  // row, head's query, first worker and parts of a warp's row
   const Sizes& s = p.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = WARPS == 1 ? blockIdx.x * kJoinWarps + warp : blockIdx.x;
-  const int mine = WARPS == 1 ? 0 : warp;
+  const int row = WARPS == 1 ? warp * gridDim.x + blockIdx.x : blockIdx.x;
+  const bool mine = (WARPS == 1 || warp == 0) && row < s.B * s.Hq;
   const int b = min(row / s.Hq, s.B - 1), hq = min(row - b * s.Hq, s.Hq - 1);
   const int hk = hq / s.per_kv, in = hq - hk * s.per_kv, ht = hk * s.row_tiles + in / s.tile;
   // The lengths are the call's inputs: they were written before the split kernel, which launched
@@ -885,7 +1030,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   int f0 = 0, f1 = 0, steps = 0;
   if (s.B <= 256) {
     for (int i = lane; i < s.B; i += 32) {
-      const int n = steps_of(keys_of(p, i));
+      const int n = steps_of(keys_of(p, i), s.chunk);
       steps += n;
       if (i < b) f0 += n;
       if (i == b) f1 = n;
@@ -901,112 +1046,72 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     f1 = s.first[b + 1];
   }
   grid_launch_dependents();
-  if (row >= s.B * s.Hq) return;  // WARPS == 1 only: no barrier follows
-  if (f0 == f1) {
-    if (mine == 0 && 4 * lane < s.d)
+  int w0 = 0, parts = 1;  // 1: nothing to join
+  if (f0 < f1) {
+    const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)steps, (unsigned)s.workers);
+    w0 = sp.owner((unsigned)(ht * steps + f0));
+    parts = sp.owner((unsigned)(ht * steps + f1) - 1u) - w0 + 1;
+  } else if (mine) {
+    if (4 * lane < s.d)
       reinterpret_cast<uint2*>(p.O + (size_t)row * s.d)[lane] = make_uint2(0, 0);
-    if (mine == 0 && lane == 0) p.L[row] = -INFINITY;
-    return;
+    if (lane == 0) p.L[row] = -INFINITY;
   }
-  const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)steps, (unsigned)s.blocks);
-  const int w0 = sp.owner((unsigned)(ht * steps + f0));
-  const int parts = sp.owner((unsigned)(ht * steps + f1) - 1u) - w0 + 1;
-  if (parts == 1) return;
 
-  // Part i of the row in s.o and s.e.
-  auto place = [&](int i) {
-    return (size_t)Split::slot(0, 0, parts, w0, i) * s.slot_rows + in % s.tile;
-  };
-  const bool has = 4 * lane < s.d;
-  float ref = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int base = mine; base < parts; base += 32 * WARPS) {
-    const int i = base + lane * WARPS;
-    const float e = i < parts ? s.e[place(i)] : -INFINITY;
-    const int n = min(32, (parts - base + WARPS - 1) / WARPS);  // lanes with a part
-    constexpr int U = WARPS == 1 ? 6 : 16;
-    float4 v[U];
-    auto load = [&](int j) {  // the first ones on their way beside e
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j + u < n && has)
-          v[u] = reinterpret_cast<const float4*>(s.o + place(base + (j + u) * WARPS) * s.d)[lane];
-      }
-    };
-    load(0);
-    float top = e;
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    const float next = fmaxf(ref, top);
-    const float back = ref == next ? 1.f : ex2(ref - next);  // 0 on the first round
-    ref = next;
-    const float weight = i < parts ? ex2(e - (ref == -INFINITY ? 0.f : ref)) : 0.f;
-    sum = sum * back + weight;  // this lane's parts
-    acc.x *= back;
-    acc.y *= back;
-    acc.z *= back;
-    acc.w *= back;
-    for (int j = 0; j < n; j += U) {
-      if (j > 0) load(j);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float w = __shfl_sync(0xffffffffu, weight, (j + u) & 31);
-        if (j + u >= n) break;
-        acc.x += w * v[u].x;
-        acc.y += w * v[u].y;
-        acc.z += w * v[u].z;
-        acc.w += w * v[u].w;
-      }
-    }
-  }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-  if (WARPS > 1) {
-    sums[warp][lane] = acc;
-    if (lane == 0) stats[warp] = make_float2(ref, sum);
+  // A row joined by the block; every thread calls.
+  auto join = [&](int row, int in, int w0, int parts) {
+    Joined r = join_parts<kJoinWarps, WARPS == 1 ? 6 : 16>(s, in, w0, parts, warp, lane);
+    sums[warp][lane] = r.acc;
+    if (lane == 0) stats[warp] = make_float2(r.ref, r.sum);
     __syncthreads();
     if (warp != 0) return;
     float top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, stats[w].x);
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    sum = 0.f;
+    r = {top, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
       // a warp without parts has reference -inf and adds nothing
       const float f = w < parts ? ex2(stats[w].x - (top == -INFINITY ? 0.f : top)) : 0.f;
       const float4 v = sums[w][lane];
-      acc.x += f * v.x;
-      acc.y += f * v.y;
-      acc.z += f * v.z;
-      acc.w += f * v.w;
-      sum += f * stats[w].y;
+      r.acc.x += f * v.x;
+      r.acc.y += f * v.y;
+      r.acc.z += f * v.z;
+      r.acc.w += f * v.w;
+      r.sum += f * stats[w].y;
     }
-    ref = top;
+    write_row(p, row, lane, r);
+  };
+  if (WARPS > 1) {
+    if (parts > 1) join(row, in, w0, parts);  // the block's row
+    return;
   }
-  const float inv = 1.f / sum;
-  if (4 * lane < s.d)
-    reinterpret_cast<uint2*>(p.O + (size_t)row * s.d)[lane] =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (lane == 0) p.L[row] = (ref + lg2(sum)) * kLn2;
+  const bool alone = parts <= kAlone;
+  if (lane == 0) many[warp] = make_int4(row, in, w0, mine && !alone ? parts : 0);
+  if (mine && alone && parts > 1)
+    write_row(p, row, lane, join_parts<1, 6>(s, in, w0, parts, 0, lane));
+  if (!__syncthreads_or(mine && !alone)) return;
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const int4 m = many[w];
+    if (m.w == 0) continue;
+    join(m.x, m.y, m.z, m.w);
+    __syncthreads();
+  }
 }
 
 template <int G, int NT>
 cudaError_t launch(const Decode4Args& a, cudaStream_t stream) {
   using C = Cfg<G, NT>;
   DecodeParams p;
-  p.s = sizes_of(a.B, a.Hq, a.Hkv, a.d);
-  lay_out(&p.s, a.workspace, a.max_pages * a.page);
-  const int count = sm_count(), sms = count < kMaxSms ? count : kMaxSms, smem = C::BYTES + (a.B + 1) * 4;
+  p.s = sizes_of(a.B, a.Hq, a.Hkv, a.d, a.max_pages * a.page);
+  lay_out(&p.s, a.workspace);
+  const int count = sm_count(), sms = count < kMaxSms ? count : kMaxSms;
+  const int fixed = p.s.solo ? C::RINGS : C::BYTES, smem = fixed + (a.B + 1) * 4;
   // As many blocks as fit (an SM has 227 KB for them, and 1 KB of each is the system's), and no
   // more than the capacities can keep busy.
   const int fit = 227 * 1024 / (smem + 1024 + 1024), most = fit < per_sm(NT) ? fit : per_sm(NT);
-  const long long units = (long long)a.Hkv * p.s.row_tiles * a.B;
-  const long long steps =
-      a.max_pages ? units * (ceil_div(a.max_pages * a.page, kChunk) + kRunSteps) : 0;
-  const long long blocks = (long long)sms * most;
-  p.s.blocks = (int)(blocks < steps ? blocks : steps > 0 ? steps : 1);
+  const long long need = p.s.solo ? (p.s.steps + kWarps - 1) / kWarps : p.s.steps;
+  const int blocks = need == 0 ? 1 : (int)(need < sms * most ? need : sms * most);
+  p.s.workers = p.s.solo ? blocks * kWarps : blocks;
   p.Q = static_cast<const __nv_bfloat16*>(a.Q);
   p.cache = static_cast<const uint8_t*>(a.cache);
   p.table = a.table;
@@ -1019,15 +1124,18 @@ cudaError_t launch(const Decode4Args& a, cudaStream_t stream) {
   while ((1 << p.page_shift) < a.page) ++p.page_shift;
   p.scale_log2 = a.scale * kLog2e;
   const bool whole =
-      ceil_div(a.max_pages * a.page, kChunk) <= kWholeChunks && units <= (long long)sms * per_sm(NT);
-  auto kernel = whole ? decode4_kernel<G, NT, true> : decode4_kernel<G, NT, false>;
+      ceil_div(a.max_pages * a.page, kChunk) <= kWholeChunks && p.s.units <= sms * per_sm(NT);
+  auto kernel = whole      ? decode4_kernel<G, NT, kWhole>
+                : p.s.solo ? decode4_kernel<G, NT, kSolo>
+                           : decode4_kernel<G, NT, kPieces>;
+  const int dynamic = whole ? C::BYTES : smem;
   cudaError_t e = cudaSuccess;
-  if (C::BYTES + (8192 + 1) * 4 > 48 * 1024 && !(whole && C::BYTES <= 48 * 1024))
+  if (dynamic > 48 * 1024)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::BYTES + (8192 + 1) * 4);
+                             C::BYTES + (kMaxBatch + 1) * 4);
   if (e != cudaSuccess) return e;
-  e = launch_early(kernel, dim3((unsigned)(whole ? units : p.s.blocks)), kThreads,
-                   whole ? C::BYTES : smem, stream, p);
+  const unsigned grid = (unsigned)(whole ? p.s.units : blocks);
+  e = launch_early(kernel, dim3(grid), kThreads, dynamic, stream, p);
   if (e != cudaSuccess || whole) return e;
   const int rows = a.B * a.Hq;
   // A warp per row once there is a row for every fourth warp slot of the GPU's SMs.
@@ -1041,12 +1149,12 @@ cudaError_t launch(const Decode4Args& a, cudaStream_t stream) {
 }  // namespace
 
 size_t decode4_workspace_bytes(int B, int Hq, int Hkv, int d, int capacity) {
-  Sizes s = sizes_of(B, Hq, Hkv, d);
-  return lay_out(&s, nullptr, capacity);
+  Sizes s = sizes_of(B, Hq, Hkv, d, capacity);
+  return lay_out(&s, nullptr);
 }
 
 cudaError_t launch_decode4(const Decode4Args& a, cudaStream_t s) {
-  const bool two = sizes_of(a.B, a.Hq, a.Hkv, a.d).tile == 16;
+  const bool two = sizes_of(a.B, a.Hq, a.Hkv, a.d, 0).tile == 16;
   if (a.d > 64) return two ? launch<2, 2>(a, s) : launch<2, 1>(a, s);
   return two ? launch<1, 2>(a, s) : launch<1, 1>(a, s);
 }

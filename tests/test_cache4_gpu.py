@@ -216,6 +216,17 @@ def test_decode(lens, hq, hkv, d, page, capacity):
     _check_decode(*args)
 
 
+@pytest.mark.parametrize("others,hq,hkv,d", [(330, 1, 1, 128), (330, 7, 1, 64), (45, 16, 8, 128),
+                                             (100, 64, 4, 72), (41, 32, 8, 64)])
+@pytest.mark.parametrize("long", [0, 20])
+def test_decode_one_long_request_among_many(others, hq, hkv, d, long):
+    """More than 320 units: single warps take even pieces of them, and the long request's rows are
+    joined from well over 32 pieces each."""
+    lens = [(11 * i) % 40 for i in range(others)]
+    lens.insert(long, 6000)
+    _check_decode(*_decode_inputs(lens, hq, hkv, d, 16, others + hq + d))
+
+
 @pytest.mark.parametrize("std,scale", [(4.0, None), (0.0, None), (1.0, 1e-6), (1.0, 3.0),
                                        (1e-20, None)])
 def test_decode_scores(std, scale):

@@ -140,6 +140,18 @@ def test_read(lib):
         assert f() in REACHED
 
 
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 8, 64), (32, 4, 128), (40, 2, 128), (7, 1, 40)])
+def test_decode_workspace_holds_for_fewer_requests_and_keys(lib, Hq, Hkv, d):
+    size = lib.fa_cache4_workspace_bytes
+    for B in (1, 39, 41, 330, 8192):
+        sizes = [size(B, Hq, Hkv, d, n) for n in (0, 1, 16, 100, 1000, 1 << 14, 1 << 19, 1 << 20,
+                                                  1 << 21, 1 << 24, 1 << 27)]
+        assert sizes == sorted(sizes)
+    for n in (0, 16, 1000, 1 << 21):
+        sizes = [size(B, Hq, Hkv, d, n) for B in (*range(1, 400), 4000, 8192)]
+        assert sizes == sorted(sizes)
+
+
 def test_decode(lib):
     size = lib.fa_cache4_workspace_bytes
     assert size(0, 8, 2, 64, 10) == 0 and size(2, 8, 3, 64, 10) == 0

@@ -141,6 +141,17 @@ FA_DEV int steps_of(int keys, int chunk) {
   return keys > 0 ? (keys + chunk - 1) / chunk + kRunSteps : 0;
 }
 
+// The workers' pieces of all units, of so many steps for each tile of queries. A warp's has
+// kLeastSteps, so that a long request among short ones is not in more parts than the keys are
+// worth (one of 131072 keys among 320: 40 us; without a least piece 47, and with 8 steps 32, but
+// 300 requests of up to 1000 keys, 8/2 heads, 21 instead of 20).
+constexpr unsigned kLeastSteps = 4;
+FA_DEV Split split_of(const Sizes& s, int steps) {
+  const unsigned all = (unsigned)(s.Hkv * s.row_tiles) * (unsigned)steps;
+  const unsigned most = (unsigned)s.workers;
+  return Split(all, s.solo ? min(most, (all + kLeastSteps - 1) / kLeastSteps) : most);
+}
+
 template <int G, int NT>
 struct Cfg {
   static constexpr int BLOCK = G * kBlock4;
@@ -678,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
       __syncthreads();
     }
     steps = uniform(steps);
-    const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)steps, (unsigned)s.workers);
+    const Split sp = split_of(s, steps);
     if (me >= sp.workers) return;
     x_begin = (unsigned)uniform((int)sp.start(me));
     x_end = (unsigned)uniform((int)sp.start(me + 1));
@@ -938,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NT))
 
 // A row (request, query head) is joined by one warp, or by kJoinWarps where there are few rows or
 // the row has more than kAlone parts (a request much longer than the others; one of 131072 keys
-// among 320, a key/value head of 8 queries: 47 us for the call, with a warp for each row 245).
+// among 320, a key/value head of 8 queries: 40 us for the call, with a warp for each row 245).
 // Rows of a block are gridDim.x apart, so that such a request's are many blocks' work. Lane i
 // looks up part i's e, and the warp adds the parts up, four columns a lane, of which the first 6
 // or 16 are on their way beside e: the kernel is a chain of waits for memory, about 3 us behind
@@ -1048,7 +1059,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, WARPS == 1 ? 4 : 2)
   grid_launch_dependents();
   int w0 = 0, parts = 1;  // 1: nothing to join
   if (f0 < f1) {
-    const Split sp((unsigned)(s.Hkv * s.row_tiles) * (unsigned)steps, (unsigned)s.workers);
+    const Split sp = split_of(s, steps);
     w0 = sp.owner((unsigned)(ht * steps + f0));
     parts = sp.owner((unsigned)(ht * steps + f1) - 1u) - w0 + 1;
   } else if (mine) {

@@ -39,8 +39,11 @@ def _inputs(total, hq, hkv, d, rot, seed, norm=True, std=1.0, positions=4000, sl
 
 
 def _near(name, got, want, bound):
-    bad = (got.double() - want).abs() > bound
-    assert not bool(bad.any()), (name, int(bad.sum()), float((got.double() - want).abs().max()))
+    """Within the bound, or the same infinity, or both NaN."""
+    got = got.double()
+    good = ((got - want).abs() <= bound) | (got == want) | (got.isnan() & want.isnan())
+    bad = ~good
+    assert not bool(bad.any()), (name, int(bad.sum()), float((got - want).abs().max()))
 
 
 def _check(q, k, pos, table, wq, wk, dq, dk, inter, eps=EPS):

@@ -328,7 +328,9 @@ struct Tile {
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        c[n][e] = __shfl_sync(0xffffffffu, unit, 8 * t + 4 * e) * 0x1p24f * scale_log2;
+        // never 0, which would make -infinity times it NaN
+        c[n][e] = fmaxf(__shfl_sync(0xffffffffu, unit, 8 * t + 4 * e) * 0x1p24f * scale_log2,
+                        0x1p-149f);
         m[n][e] = top[n][e] = -INFINITY;
         ref[n][e] = l[n][e] = 0.f;
         v_ref[n][e] = kLeast;

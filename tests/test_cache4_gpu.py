@@ -234,6 +234,17 @@ def test_decode_scores(std, scale):
     _check_decode(*_decode_inputs([333, 64, 2000], 8, 2, 128, 16, 71, std=std), scale=scale)
 
 
+@pytest.mark.parametrize("scale", [1e-18, 1e-25, 1e-38])
+@pytest.mark.parametrize("others", [0, 330])
+def test_decode_scales_that_leave_nothing_of_a_score(scale, others):
+    """All weights alike, also of queries that are zero, and pieces and warps without a key."""
+    q, cache, table, lens, codes, pairs, place = _decode_inputs(
+        [2000, 33, 130] + [7] * others, 4, 1, 64, 16, 85)
+    q[:, 1] = 0
+    q[:, 2] *= 1e-30
+    _check_decode(q, cache, table, lens, codes, pairs, place, scale=scale)
+
+
 def test_decode_growing_scores():
     """The reference maximum moves many times in both directions of the keys."""
     q, cache, table, lens, codes, pairs, place = _decode_inputs([1000], 4, 1, 64, 16, 72)

@@ -415,14 +415,14 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   bool made;
   const Tensor dQ = gradient("dQ", a[10], Q, &lddq, &made);
   const Tensor dK = gradient("dK", a[11], K, &lddk, &made);
-  Tensor dw, ws;  // both weights' gradients
+  Tensor dw[2], ws;
   float *dwq = nullptr, *dwk = nullptr;
   void* space = nullptr;
   size_t bytes = 0;
   if (how.q_weight || how.k_weight) {
-    dw = at::empty({2, d}, Q.options().dtype(at::kFloat));
-    dwq = static_cast<float*>(dw.data_ptr());
-    dwk = dwq + d;
+    for (Tensor& w : dw) w = at::empty({d}, Q.options().dtype(at::kFloat));
+    dwq = static_cast<float*>(dw[0].data_ptr());
+    dwk = static_cast<float*>(dw[1].data_ptr());
     if (a[12] == Py_None) {
       const size_t need = fa_qk_norm_rope_workspace_bytes(as_int(hq), as_int(hkv), as_int(d));
       if (need == 0) value_error("invalid sizes for the workspace");
@@ -441,7 +441,7 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   PyObject* w[2];
   for (int i = 0; i < 2; ++i) {
     if (i == 0 ? how.q_weight : how.k_weight) {
-      w[i] = THPVariable_Wrap(dw.select(0, i));
+      w[i] = THPVariable_Wrap(dw[i]);
     } else {
       Py_INCREF(Py_None);
       w[i] = Py_None;

@@ -45,8 +45,9 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kRescale = 8.f;  // the reference maximum moves when passed by 2^8
 // P scale in units of its reference: the reference moves when passed by kMost, a number that
-// fp16 still has; it is at least kLeast.
-constexpr float kMost = 4096.f, kLeast = 0x1p-100f;
+// fp16 still has; it is at least kLeast, whose inverse times a weight (2^8, or 2^16 where the
+// scores' own rounding is a step of that size) fp32 still has.
+constexpr float kMost = 4096.f, kLeast = 0x1p-110f;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 32;              // keys of a warp's stage: two blocks of the cache
@@ -406,6 +407,8 @@ struct Tile {
         over |= high[n][e] > top[n][e];
       }
     if (__any_sync(0xffffffffu, over)) {
+      float rest[NT][2];
+      bool shrinks = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -416,15 +419,34 @@ struct Tile {
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
           x = fmaxf(x, m[n][e]);
           const float f = x == -INFINITY ? 1.f : ex2((m[n][e] - x) * c[n][e]);
+          const bool met = m[n][e] > -INFINITY;
           m[n][e] = x;
           ref[n][e] = x == -INFINITY ? 0.f : -x * c[n][e];
           top[n][e] = x + kRescale / c[n][e];
           l[n][e] *= f;
 #pragma unroll
           for (int j = 0; j < G; ++j) z[n][j][e] *= f;
-          v_ref[n][e] = fmaxf(v_ref[n][e] * f, kLeast);  // for o
+          // o shrinks with its unit, and by itself where the unit may not
+          rest[n][e] = v_ref[n][e] * f;
+          shrinks |= met && rest[n][e] < kLeast;
+          v_ref[n][e] = fmaxf(rest[n][e], kLeast);
           v_inv[n][e] = 1.f / v_ref[n][e];
         }
+      if (__any_sync(0xffffffffu, shrinks)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float f = rest[n][e] / v_ref[n][e];
+#pragma unroll
+            for (int j = 0; j < G; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[n][j][i][e] *= f;
+                o[n][j][i][2 + e] *= f;
+              }
+          }
+      }
     }
     // P, and P scale in units of v_ref
     float p[2][NT][4], ps[2][NT][G][4], most = 0.f;

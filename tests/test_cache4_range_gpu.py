@@ -1,0 +1,73 @@
+"""Decode over the cache in 4 bits at the ends of its number ranges, against 64-bit values with
+the bounds of its arithmetic (tests/cache4_ref.py)."""
+import math
+
+import pytest
+import torch
+
+import exact_io_aware_27_gb300 as fa
+from tests import cache4_ref, rope_ref as ref
+from tests.test_cache4_gpu import _decode_inputs
+from tests.test_rope_gpu import _near
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _built():
+    fa.build()
+    yield
+    assert fa.fa_get_device_status() == 0
+
+
+def _check(q, cache, table, lens, codes, pairs, place, scale=None, **kw):
+    """Decodes with the cache's pairs replaced by `pairs`, and compares."""
+    d, hkv = q.shape[2], cache.shape[1]
+    g = q.shape[1] // hkv
+    q = q.cuda()
+    O, L = fa.fa_cache4_decode(q, ref.pack(codes, pairs, d, cache).cuda(), table, lens, scale, **kw)
+    s = 1 / math.sqrt(d) if scale is None else scale
+    for b, (pg, r) in enumerate(place):
+        for h in range(hkv if len(pg) else 0):
+            rows = slice(h * g, (h + 1) * g)
+            o, l = cache4_ref.decode_bounds(q[b, rows].double().cpu(), codes[:, pg, h, r],
+                                            pairs[:, pg, h, r], s)
+            _near("O", O[b, rows].cpu(), *o)
+            _near("L", L[b, rows].cpu(), *l)
+    return O, L
+
+
+def _scaled(pairs, which, by):
+    """Both numbers of the pairs of K (0) or V (1) times `by`, in bf16 again."""
+    p = pairs.clone()
+    p[which] *= by
+    return p.to(torch.bfloat16).double()
+
+
+def _growing(args, rises, reverse=False):
+    """Scores of each request that grow along its keys by `rises` in all."""
+    q, cache, table, lens, codes, pairs, place = args
+    q, p = torch.ones_like(q), pairs.clone()
+    for pg, r in place:
+        n = len(pg)
+        if n == 0:
+            continue
+        ramp = torch.linspace(0.0, rises, n, dtype=torch.float64)
+        if reverse:
+            ramp = ramp.flip(0)
+        p[0, pg, :, r, :, 0] = 2.0 ** -6
+        p[0, pg, :, r, :, 1] = (ramp / math.sqrt(q.shape[2]))[:, None, None]
+    return q, cache, table, lens, codes, p.to(torch.bfloat16).double(), place
+
+
+@pytest.mark.parametrize("exponent", [-60, -86, -90, -100, -110, -118])
+@pytest.mark.parametrize("lens,hq,hkv,d,reverse", [
+    ([1000], 4, 1, 64, False), ([1000], 4, 1, 64, True), ([300, 40], 8, 2, 128, False),
+    ([90], 16, 1, 72, False), ([70] * 330, 1, 1, 64, False),
+    ([70] * 500, 1, 1, 64, False)])
+def test_small_values_and_growing_scores(exponent, lens, hq, hkv, d, reverse):
+    """What earlier keys added shrinks with each reference that later scores set, whatever the
+    values' size."""
+    args = _growing(_decode_inputs(lens, hq, hkv, d, 16, 90 + d), 200.0, reverse)
+    q, cache, table, lens, codes, pairs, place = args
+    _check(q, cache, table, lens, codes, _scaled(pairs, 1, 2.0 ** exponent), place)

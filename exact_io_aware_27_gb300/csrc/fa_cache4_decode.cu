@@ -18,7 +18,9 @@
 // operands, exactly, without an addition. Q is brought to a largest value of 256 to 512 by a
 // power of two for each query, and P scale, rounded to fp16, is taken relative to a reference
 // that follows its largest values, as the softmax's own reference follows the scores: what
-// loses bits, or is left out, is 2^-24 of the largest term or less.
+// loses bits is below 2^-14 of the largest term, and off by 2^-25 of it at most. The two groups
+// have references of their own, since they are outputs of their own: with one for both, a group
+// whose values were 2^20 times smaller than the other's was off by percents.
 // Each warp has a ring of two stages of 32 keys, two bulk copies each; the values of a run (a
 // unit, or the part of it in a worker's piece) that are the same in all lanes are told to be so
 // (uniform()), which takes them out of the registers that the products need. That, and 32 keys
@@ -44,10 +46,11 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kRescale = 8.f;  // the reference maximum moves when passed by 2^8
-// P scale in units of its reference: the reference moves when passed by kMost, a number that
-// fp16 still has; it is at least kLeast, whose inverse times a weight (2^8, or 2^16 where the
-// scores' own rounding is a step of that size) fp32 still has.
-constexpr float kMost = 4096.f, kLeast = 0x1p-110f;
+// P scale in units of a reference, of each query and group: it moves when passed by kMost, a
+// number that fp16 still has. Its inverse is held: at most kMostInverse, which fp32 still has
+// times a weight (2^8, or 2^16 where the scores' own rounding is a step of that size), and no less
+// than the least normal number, with which P scale, 2^140 at most, is one that fp16 has.
+constexpr float kMost = 4096.f, kMostInverse = 0x1p110f, kLeastInverse = 0x1p-126f;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 32;              // keys of a warp's stage: two blocks of the cache
@@ -210,6 +213,14 @@ FA_DEV void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, ui
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
+// 1 / x, 2^-23 off at most. Exact quotients call a routine with registers of its own: with them
+// the two ends of a unit took 1.5 us longer (32 requests of up to 4096 keys, 32/8 heads, d = 128:
+// 25.5 us against 23.5), and d > 64 spilled.
+FA_DEV float about_inverse(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // The power of two at or below x, at least 2^-100.
 FA_DEV float power_of_two(float x) {
   return fmaxf(__uint_as_float(__float_as_uint(x) & 0x7f800000u), 0x1p-100f);
@@ -264,7 +275,7 @@ struct Tile {
   // reference, -c times it (0 if there is none yet), weight sum of this lane's keys, and the
   // score that moves the reference
   float m[NT][2], ref[NT][2], l[NT][2], top[NT][2];
-  float v_ref[NT][2], v_inv[NT][2];  // o is in units of v_ref
+  float v_inv[NT][G][2];  // o is in units of its inverse
 
   // The lane's part of the queries' rows.
   struct Raw {
@@ -298,7 +309,9 @@ struct Tile {
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
       // 2^-8 of the query's power of two; an infinite entry stays one
-      const float unit = most < INFINITY ? power_of_two(most) * 0x1p-8f : 1.f, inv = 1.f / unit;
+      const float unit = most < INFINITY ? power_of_two(most) * 0x1p-8f : 1.f;
+      // 2^-e from 2^e
+      const float inv = __uint_as_float(0x7f000000u - __float_as_uint(unit));
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         float sum = 0.f;
@@ -326,6 +339,7 @@ struct Tile {
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[n][j][i][e] = 0.f;
         z[n][j][0] = z[n][j][1] = 0.f;
+        v_inv[n][j][0] = v_inv[n][j][1] = kMostInverse;
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -334,8 +348,6 @@ struct Tile {
                         0x1p-149f);
         m[n][e] = top[n][e] = -INFINITY;
         ref[n][e] = l[n][e] = 0.f;
-        v_ref[n][e] = kLeast;
-        v_inv[n][e] = 1.f / kLeast;
       }
     }
   }
@@ -407,7 +419,7 @@ struct Tile {
         over |= high[n][e] > top[n][e];
       }
     if (__any_sync(0xffffffffu, over)) {
-      float rest[NT][2];
+      float f[NT][2], was[NT][G][2];
       bool shrinks = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -418,37 +430,39 @@ struct Tile {
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
           x = fmaxf(x, m[n][e]);
-          const float f = x == -INFINITY ? 1.f : ex2((m[n][e] - x) * c[n][e]);
+          f[n][e] = x == -INFINITY ? 1.f : ex2((m[n][e] - x) * c[n][e]);
           const bool met = m[n][e] > -INFINITY;
           m[n][e] = x;
           ref[n][e] = x == -INFINITY ? 0.f : -x * c[n][e];
-          top[n][e] = x + kRescale / c[n][e];
-          l[n][e] *= f;
+          top[n][e] = x + kRescale * about_inverse(c[n][e]);
+          l[n][e] *= f[n][e];
+          const float grow = about_inverse(f[n][e]);
 #pragma unroll
-          for (int j = 0; j < G; ++j) z[n][j][e] *= f;
-          // o shrinks with its unit, and by itself where the unit may not
-          rest[n][e] = v_ref[n][e] * f;
-          shrinks |= met && rest[n][e] < kLeast;
-          v_ref[n][e] = fmaxf(rest[n][e], kLeast);
-          v_inv[n][e] = 1.f / v_ref[n][e];
+          for (int j = 0; j < G; ++j) {
+            z[n][j][e] *= f[n][e];
+            // o shrinks with its unit, and by itself where the unit may not
+            was[n][j][e] = v_inv[n][j][e];
+            v_inv[n][j][e] = fminf(was[n][j][e] * grow, kMostInverse);
+            shrinks |= met && v_inv[n][j][e] == kMostInverse;
+          }
         }
       if (__any_sync(0xffffffffu, shrinks)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float f = rest[n][e] / v_ref[n][e];
+          for (int j = 0; j < G; ++j)
 #pragma unroll
-            for (int j = 0; j < G; ++j)
+            for (int e = 0; e < 2; ++e) {
+              const float g = f[n][e] * v_inv[n][j][e] * about_inverse(was[n][j][e]);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                o[n][j][i][e] *= f;
-                o[n][j][i][2 + e] *= f;
+                o[n][j][i][e] *= g;
+                o[n][j][i][2 + e] *= g;
               }
-          }
+            }
       }
     }
-    // P, and P scale in units of v_ref
+    // P, and P scale in o's units
     float p[2][NT][4], ps[2][NT][G][4], most = 0.f;
     auto scaled = [&]() {
 #pragma unroll
@@ -456,11 +470,13 @@ struct Tile {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float f = p[k][n][i] * v_inv[n][i & 1];
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < G; ++j) ps[k][n][j][i] = f * sv[k][i >> 1][j];
-          }
+            for (int j = 0; j < G; ++j)
+              f2unpack(fmul2(fmul2(f2pack(p[k][n][2 * h], p[k][n][2 * h + 1]),
+                                   f2pack(v_inv[n][j][0], v_inv[n][j][1])),
+                             f2pack(sv[k][h][j], sv[k][h][j])),
+                       ps[k][n][j][2 * h], ps[k][n][j][2 * h + 1]);
     };
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -489,28 +505,25 @@ struct Tile {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = kLeast;
+        for (int j = 0; j < G; ++j)
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int e = 0; e < 2; ++e) {
+            float x = 0.f;
 #pragma unroll
-            for (int j = 0; j < G; ++j)
+            for (int k = 0; k < 2; ++k)
               x = max3f(x, p[k][n][e] * sv[k][0][j], p[k][n][2 + e] * sv[k][1][j]);
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          x = fmaxf(x, v_ref[n][e]);
-          const float f = v_ref[n][e] / x;
-          v_ref[n][e] = x;
-          v_inv[n][e] = 1.f / x;
-#pragma unroll
-          for (int j = 0; j < G; ++j)
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            x = fminf(fmaxf(about_inverse(x), kLeastInverse), v_inv[n][j][e]);
+            const float f = x * about_inverse(v_inv[n][j][e]);
+            v_inv[n][j][e] = x;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               o[n][j][i][e] *= f;
               o[n][j][i][2 + e] *= f;
             }
-        }
+          }
       scaled();
     }
     uint32_t b[2][NT][G][2];
@@ -556,11 +569,11 @@ struct Tile {
         l[n][e] = all(l[n][e]);
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-          const float add = all(z[n][j][e]);
+          const float add = all(z[n][j][e]), unit = about_inverse(v_inv[n][j][e]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // even channels came times 2^-24, odd ones 2^-20
-            o[n][j][i][e] = fmaf(o[n][j][i][e] * 0x1p24f, v_ref[n][e], add);
-            o[n][j][i][2 + e] = fmaf(o[n][j][i][2 + e] * 0x1p20f, v_ref[n][e], add);
+            o[n][j][i][e] = fmaf(o[n][j][i][e] * 0x1p24f, unit, add);
+            o[n][j][i][2 + e] = fmaf(o[n][j][i][2 + e] * 0x1p20f, unit, add);
           }
         }
       }

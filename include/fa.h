@@ -420,7 +420,8 @@ FA_API int fa_rope_append(const void* Q, const void* K, const void* V, long long
  * keys. The products take the codes as they are; scores, softmax and sums are fp32. Q is held in
  * fp16 times a power of two for each row, whose largest magnitude becomes 256 to 512 (entries
  * 2^-18 of it and larger keep all their bits), and the weights times V's scales in fp16 times
- * one that follows the largest scale met (11 bits, and none below 2^-24 of that scale).
+ * one for each row and group of 64 channels, which follows the largest of these products (11
+ * bits down to 2^-14 of that, and 2^-25 of it off at most below; scales under 2^-124 keep fewer).
  * Hq a multiple of Hkv, Hq / Hkv <= 128, 1 <= B <= 8192, ceil(Hq / Hkv / 8) * Hkv * B *
  * max_pages * page < 2^37. `workspace`: caller-owned device memory of at least
  * fa_cache4_workspace_bytes() bytes for `capacity` = max_pages * page keys a request (more for

@@ -71,3 +71,17 @@ def test_small_values_and_growing_scores(exponent, lens, hq, hkv, d, reverse):
     args = _growing(_decode_inputs(lens, hq, hkv, d, 16, 90 + d), 200.0, reverse)
     q, cache, table, lens, codes, pairs, place = args
     _check(q, cache, table, lens, codes, _scaled(pairs, 1, 2.0 ** exponent), place)
+
+
+@pytest.mark.parametrize("apart", [12, 18, 24, 40, 100])
+@pytest.mark.parametrize("large", [0, 1])
+@pytest.mark.parametrize("lens,hq,hkv,d", [([200, 33], 4, 1, 128), ([500], 16, 1, 72),
+                                           ([40] * 330, 2, 1, 128), ([3000], 8, 2, 104)])
+def test_groups_of_values_far_apart(apart, large, lens, hq, hkv, d):
+    """Each group of 64 channels keeps its bits beside one whose values are 2^apart times as
+    large."""
+    q, cache, table, lens, codes, pairs, place = _decode_inputs(lens, hq, hkv, d, 16, 91 + d)
+    p = pairs.clone()
+    p[1, ..., large, :] *= 2.0 ** (apart - apart // 2)
+    p[1, ..., 1 - large, :] *= 2.0 ** -(apart // 2)
+    _check(q, cache, table, lens, codes, p.to(torch.bfloat16).double(), place)

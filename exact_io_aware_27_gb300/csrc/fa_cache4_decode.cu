@@ -264,12 +264,16 @@ struct Words {
 
 // The queries of a tile and their running softmax over the keys that a warp has seen. Lane
 // (g, t) has columns (queries) 2 t and 2 t + 1 of every 8 x 8 accumulator. Scores are in units
-// of a query's own: c is what makes them exponents of 2.
+// of a query's own: c is what makes them exponents of 2. Queries so large that c has no room in
+// fp32 (2^24 of it are the codes') are raised: their scores are kRaise times as large, c as
+// much smaller.
+constexpr float kRaise = 0x1p64f;
 template <int G, int NT>
 struct Tile {
   uint32_t q[NT][G][4][2];  // every second pair divided by 16
   float qs[NT][G][2];       // sums of a query over a group, times 2^-24
   float c[NT][2];
+  unsigned raised[NT];      // bit 4 r: query r is
   float o[NT][G][4][4];     // channels 64 j + 8 g + 2 i + (e / 2), query 2 t + e % 2
   float z[NT][G][2];        // sums of P min, of this lane's keys
   // reference, -c times it (0 if there is none yet), weight sum of this lane's keys, and the
@@ -312,6 +316,10 @@ struct Tile {
       const float unit = most < INFINITY ? power_of_two(most) * 0x1p-8f : 1.f;
       // 2^-e from 2^e
       const float inv = __uint_as_float(0x7f000000u - __float_as_uint(unit));
+      float to_log2 = unit * 0x1p24f * scale_log2;
+      const bool raise = !(to_log2 < 0x1p120f);
+      if (raise) to_log2 = unit * (0x1p24f / kRaise) * scale_log2;
+      raised[n] = __ballot_sync(0xffffffffu, raise);
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         float sum = 0.f;
@@ -331,7 +339,7 @@ struct Tile {
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum *= 0x1p-24f;
+        sum *= raise ? 0x1p-24f * kRaise : 0x1p-24f;
         qs[n][j][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
         qs[n][j][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
 #pragma unroll
@@ -344,8 +352,7 @@ struct Tile {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         // never 0, which would make -infinity times it NaN
-        c[n][e] = fmaxf(__shfl_sync(0xffffffffu, unit, 8 * t + 4 * e) * 0x1p24f * scale_log2,
-                        0x1p-149f);
+        c[n][e] = fmaxf(__shfl_sync(0xffffffffu, to_log2, 8 * t + 4 * e), 0x1p-149f);
         m[n][e] = top[n][e] = -INFINITY;
         ref[n][e] = l[n][e] = 0.f;
       }
@@ -375,6 +382,18 @@ struct Tile {
               mma_f16(acc[k][n][j], a, q[n][j][x][0], q[n][j][x][1]);
           }
         }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (raised[n] != 0) {  // warp-uniform
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float by = raised[n] >> (8 * (lane & 3) + 4 * (i & 1)) & 1 ? kRaise : 1.f;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < G; ++j) acc[k][n][j][i] *= by;
+        }
+      }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll

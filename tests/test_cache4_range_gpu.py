@@ -85,3 +85,17 @@ def test_groups_of_values_far_apart(apart, large, lens, hq, hkv, d):
     p[1, ..., large, :] *= 2.0 ** (apart - apart // 2)
     p[1, ..., 1 - large, :] *= 2.0 ** -(apart // 2)
     _check(q, cache, table, lens, codes, p.to(torch.bfloat16).double(), place)
+
+
+@pytest.mark.parametrize("size", [100, 112, 115, 124])
+@pytest.mark.parametrize("small", ["scale", "keys"])
+@pytest.mark.parametrize("hq,d", [(4, 64), (4, 128), (16, 128)])
+def test_large_queries_of_ordinary_scores(size, small, hq, d):
+    """Queries of 2^size whose scores are small by the scale or by the keys, beside ordinary
+    ones."""
+    q, cache, table, lens, codes, pairs, place = _decode_inputs([300, 17], hq, 1, d, 16, 92 + d)
+    q[:, 1::2] = q[:, 1::2].clamp(-4, 4).mul(2.0 ** min(size, 100)).mul(2.0 ** (size - min(size, 100)))
+    if small == "scale":
+        _check(q, cache, table, lens, codes, pairs, place, scale=2.0 ** -size / math.sqrt(d))
+    else:
+        _check(q, cache, table, lens, codes, _scaled(pairs, 0, 2.0 ** -size), place)

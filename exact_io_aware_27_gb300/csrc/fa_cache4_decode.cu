@@ -276,8 +276,8 @@ struct Tile {
   unsigned raised[NT];      // bit 4 r: query r is
   float o[NT][G][4][4];     // channels 64 j + 8 g + 2 i + (e / 2), query 2 t + e % 2
   float z[NT][G][2];        // sums of P min, of this lane's keys
-  // reference, -c times it (0 if there is none yet), weight sum of this lane's keys, and the
-  // score that moves the reference
+  // reference, what is added to scores (minus it, or 0 if there is none yet), weight sum of this
+  // lane's keys, and the score that moves the reference
   float m[NT][2], ref[NT][2], l[NT][2], top[NT][2];
   float v_inv[NT][G][2];  // o is in units of its inverse
 
@@ -452,7 +452,7 @@ struct Tile {
           f[n][e] = x == -INFINITY ? 1.f : ex2((m[n][e] - x) * c[n][e]);
           const bool met = m[n][e] > -INFINITY;
           m[n][e] = x;
-          ref[n][e] = x == -INFINITY ? 0.f : -x * c[n][e];
+          ref[n][e] = x == -INFINITY ? 0.f : -x;
           top[n][e] = x + kRescale * about_inverse(c[n][e]);
           l[n][e] *= f[n][e];
           const float grow = about_inverse(f[n][e]);
@@ -501,15 +501,27 @@ struct Tile {
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
+      {
+        // The difference first: beside a large reference times c, rounded, the product of the same
+        // score with c may be off by any power of two.
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x[2];
+          f2unpack(fmul2(fadd2(f2pack(s[k][n][2 * h], s[k][n][2 * h + 1]),
+                               f2pack(ref[n][0], ref[n][1])),
+                         f2pack(c[n][0], c[n][1])),
+                   x[0], x[1]);
+          p[k][n][2 * h] = ex2(x[0]);
+          p[k][n][2 * h + 1] = ex2(x[1]);
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          p[k][n][e] = ex2(fmaf(s[k][n][e], c[n][e], ref[n][e]));
-          p[k][n][2 + e] = ex2(fmaf(s[k][n][2 + e], c[n][e], ref[n][e]));
           l[n][e] += p[k][n][e] + p[k][n][2 + e];
 #pragma unroll
           for (int j = 0; j < G; ++j)
             z[n][j][e] = fmaf(p[k][n][e], mv[k][0][j], fmaf(p[k][n][2 + e], mv[k][1][j], z[n][j][e]));
         }
+      }
     scaled();
 #pragma unroll
     for (int k = 0; k < 2; ++k)

@@ -99,3 +99,55 @@ def test_large_queries_of_ordinary_scores(size, small, hq, d):
         _check(q, cache, table, lens, codes, pairs, place, scale=2.0 ** -size / math.sqrt(d))
     else:
         _check(q, cache, table, lens, codes, _scaled(pairs, 0, 2.0 ** -size), place)
+
+
+@pytest.mark.parametrize("size", [10, 20, 27, 31, 33, 40, 80, 100, 112])
+@pytest.mark.parametrize("lens", [[300], [2000, 5], [40] * 330, [40] * 500])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_large_scores(size, lens, sign):
+    """Scores of 2^size: all alike (O is the mean of V), then one key above the rest by a part
+    in 32 (O is its value)."""
+    d = 64
+    q, cache, table, n, codes, pairs, place = _decode_inputs(lens, 4, 1, d, 16, 93)
+    q = torch.full_like(q, sign * 2.0 ** (size // 2) * 1.375)
+    codes = codes.clone()
+    codes[0] = 0
+    p = pairs.clone()
+    p[0, ..., 0] = 1.0
+    p[0, ..., 1] = 2.0 ** (size - size // 2 - 3) * 1.2109375
+    score = sign * 2.0 ** size * 1.375 * 1.2109375  # 64 / sqrt(64) / 8 = 1
+    O, L = fa.fa_cache4_decode(q, ref.pack(codes, p, d, cache).cuda(), table, n)
+    for b, (pg, r) in enumerate(place):
+        one = ref.values(codes[1, pg, 0, r], p[1, pg, 0, r])
+        s, m = cache4_ref.wide(p[1, pg, 0, r], d)
+        # as in decode_bounds, with equal weights
+        e = (cache4_ref.H + 2.0 ** -16) * (s * codes[1, pg, 0, r]).mean(0)
+        e = e + (len(pg) / 16 + 64) * 2.0 ** -22 * (s * codes[1, pg, 0, r] + m.abs()).mean(0)
+        want = one.mean(0)
+        # Where a unit may be cut, parts are joined by the fp32 logarithms of their sums, m c and
+        # m c + lg2(sum) rounded to 2^-24 of themselves: weights are off by 2^-22 |L| relative to
+        # each other, and O by that part, twice, of what the values differ by.
+        if lens in ([2000, 5], [40] * 500):
+            off = min(1.0, 2 * math.expm1(min(1.0, 2.0 ** -22 * (abs(score) + 10))))
+            e = e + off * (one.amax(0) - one.amin(0))
+        _near("O", O[b].cpu(), want.expand(4, d), (ref.U * (want.abs() + e) + e).expand(4, d))
+        L64 = torch.full((4,), score + math.log(len(pg)), dtype=torch.float64)
+        _near("L", L[b].cpu(), L64, 2.0 ** -20 * (1 + L64.abs()))
+    if size < 20:
+        return  # a part in 32 would leave the others some weight
+    for at in (0, 0.4, 1.0):
+        p2 = p.clone()
+        for pg, r in place:
+            i = int(at * (len(pg) - 1))
+            p2[0, pg[i], 0, r[i], :, 1] *= 1 + sign / 32
+        p2 = p2.to(torch.bfloat16).double()
+        O, L = fa.fa_cache4_decode(q, ref.pack(codes, p2, d, cache).cuda(), table, n)
+        for b, (pg, r) in enumerate(place):
+            i = int(at * (len(pg) - 1))
+            want = ref.values(codes[1, pg[i], 0, r[i]], p2[1, pg[i], 0, r[i]])
+            s, m = cache4_ref.wide(p2[1, pg[i], 0, r[i]], d)
+            e = (cache4_ref.H + 2.0 ** -16) * (s * codes[1, pg[i], 0, r[i]] + m.abs())
+            _near("O", O[b].cpu(), want.expand(4, d), (ref.U * (want.abs() + e) + e).expand(4, d))
+            L64 = score * float(p2[0, pg[i], 0, r[i], 0, 1] / p[0, pg[i], 0, r[i], 0, 1])
+            _near("L", L[b].cpu(), torch.full((4,), L64, dtype=torch.float64),
+                  torch.full((4,), 2.0 ** -20 * (1 + abs(L64)), dtype=torch.float64))

@@ -500,8 +500,7 @@ struct Tile {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-      {
+      for (int n = 0; n < NT; ++n) {
         // The difference first: beside a large reference times c, rounded, the product of the same
         // score with c may be off by any power of two.
 #pragma unroll
@@ -1177,6 +1176,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps, WARPS == 1 ? 4 : 2)
   }
 }
 
+// Bytes of the kernel's shared memory that are not dynamic, at most.
+constexpr int kStatic = 1024;
+
 template <int G, int NT>
 cudaError_t launch(const Decode4Args& a, cudaStream_t stream) {
   using C = Cfg<G, NT>;
@@ -1187,7 +1189,7 @@ cudaError_t launch(const Decode4Args& a, cudaStream_t stream) {
   const int fixed = p.s.solo ? C::RINGS : C::BYTES, smem = fixed + (a.B + 1) * 4;
   // As many blocks as fit (an SM has 227 KB for them, and 1 KB of each is the system's), and no
   // more than the capacities can keep busy.
-  const int fit = 227 * 1024 / (smem + 1024 + 1024), most = fit < per_sm(NT) ? fit : per_sm(NT);
+  const int fit = 227 * 1024 / (smem + kStatic + 1024), most = fit < per_sm(NT) ? fit : per_sm(NT);
   const long long need = p.s.solo ? (p.s.steps + kWarps - 1) / kWarps : p.s.steps;
   const int blocks = need == 0 ? 1 : (int)(need < sms * most ? need : sms * most);
   p.s.workers = p.s.solo ? blocks * kWarps : blocks;
@@ -1209,7 +1211,7 @@ cudaError_t launch(const Decode4Args& a, cudaStream_t stream) {
                            : decode4_kernel<G, NT, kPieces>;
   const int dynamic = whole ? C::BYTES : smem;
   cudaError_t e = cudaSuccess;
-  if (dynamic > 48 * 1024)
+  if (dynamic + kStatic > 48 * 1024)  // what a block may have of both without asking
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::BYTES + (kMaxBatch + 1) * 4);
   if (e != cudaSuccess) return e;

@@ -1,6 +1,9 @@
 """Decode over the cache in 4 bits at the ends of its number ranges, against 64-bit values with
 the bounds of its arithmetic (tests/cache4_ref.py)."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -151,3 +154,30 @@ def test_large_scores(size, lens, sign):
             L64 = score * float(p2[0, pg[i], 0, r[i], 0, 1] / p[0, pg[i], 0, r[i], 0, 1])
             _near("L", L[b].cpu(), torch.full((4,), L64, dtype=torch.float64),
                   torch.full((4,), 2.0 ** -20 * (1 + abs(L64)), dtype=torch.float64))
+
+
+@pytest.mark.parametrize("d,B", [(128, 3039), (128, 3040), (128, 3071), (128, 3100), (64, 7647),
+                                 (64, 7648), (64, 7679), (64, 7700)])
+def test_batches_at_the_end_of_the_default_shared_memory(d, B):
+    """In a process of its own: a larger batch before it would raise the kernel's limit."""
+    code = f"""
+import torch
+import exact_io_aware_27_gb300 as fa
+cache = fa.alloc_cache4(2, 1, 16, {d}, "cuda")
+x = torch.randn(20, 1, {d}, device="cuda", dtype=torch.bfloat16)
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+fa.fa_cache4_append(None, x, x, i32([0, 20]), i32([0]), i32([[0, 1]]), cache)
+table = i32([[0, 1]]).repeat({B}, 1)
+q = torch.randn(1, 2, {d}, device="cuda", dtype=torch.bfloat16)
+lens = torch.arange({B}, device="cuda", dtype=torch.int32) % 21
+O, L = fa.fa_cache4_decode(q.repeat({B}, 1, 1), cache, table, lens)
+for n in range(21):
+    o, l = fa.fa_cache4_decode(q, cache, table[:1], i32([n]))
+    # two orders of the same sums
+    assert ((O[n::21].float() - o.float()).abs() <= 2.0 ** -6 * o.float().abs() + 2.0 ** -9).all()
+    assert ((L[n::21] - l).abs() <= 1e-4).all() or n == 0
+assert fa.fa_get_device_status() == 0
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]

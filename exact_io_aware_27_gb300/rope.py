@@ -71,7 +71,8 @@ def _dense_rows(t):
     rows, heads, d = t.shape
     ok = (t.stride(2) == 1 and t.stride(1) == d and t.stride(0) >= heads * d
           and t.stride(0) % 8 == 0 and t.data_ptr() % 16 == 0)
-    return t if ok else t.contiguous()
+    # a copy, also of one that is dense but starts between two 16-byte boundaries
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
 
 
 class QKNormRope(torch.autograd.Function):

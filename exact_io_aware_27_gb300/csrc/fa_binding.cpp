@@ -350,7 +350,8 @@ fa_rope how_of(PyObject* const* a, long long d, int dev) {
   const double eps = PyFloat_AsDouble(a[3]);
   if (eps == -1.0 && PyErr_Occurred()) throw python_error();
   h.eps = (float)eps;
-  h.interleaved = PyObject_IsTrue(a[4]) == 1;
+  h.interleaved = PyObject_IsTrue(a[4]);
+  if (h.interleaved < 0) throw python_error();
   return h;
 }
 

@@ -28,3 +28,9 @@ def test_a_gradient_off_its_alignment():
     got = torch.autograd.grad(out, (x, y), off)
     want = fa.fa_qk_norm_rope_backward(dq, dk, q, k, pos, table, wq, wk)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_an_argument_without_a_truth_value():
+    q, k, pos, table, wq, wk, dq, dk = _inputs(5, 4, 2, 64, 64, 97)
+    with pytest.raises(RuntimeError):
+        fa.fa_qk_norm_rope(q, k, pos, table, wq, wk, interleaved=torch.zeros(2))

@@ -422,6 +422,8 @@ FA_API int fa_rope_append(const void* Q, const void* K, const void* V, long long
  * 2^-18 of it and larger keep all their bits), and the weights times V's scales in fp16 times
  * one for each row and group of 64 channels, which follows the largest of these products (11
  * bits down to 2^-14 of that, and 2^-25 of it off at most below; scales under 2^-124 keep fewer).
+ * Scores have to be finite in fp32, and the sums over V are fp32 with weights of up to 2^8: a
+ * request's largest value times its keys has to stay below 2^119.
  * Hq a multiple of Hkv, Hq / Hkv <= 128, 1 <= B <= 8192, ceil(Hq / Hkv / 8) * Hkv * B *
  * max_pages * page < 2^37. `workspace`: caller-owned device memory of at least
  * fa_cache4_workspace_bytes() bytes for `capacity` = max_pages * page keys a request (more for

@@ -181,3 +181,24 @@ assert fa.fa_get_device_status() == 0
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("exponent", [60, 90, 100])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_large_values(exponent, reverse):
+    """The largest values that the sums have room for."""
+    args = _growing(_decode_inputs([300, 40], 8, 2, 128, 16, 94), 60.0, reverse)
+    q, cache, table, lens, codes, pairs, place = args
+    _check(q, cache, table, lens, codes, _scaled(pairs, 1, 2.0 ** exponent), place)
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d,page", [
+    ([1], 1, 1, 8, 16), ([2, 3, 0, 20], 4, 1, 64, 16), ([129], 7, 1, 72, 64), ([5000], 32, 8, 128, 64),
+    ([1, 9000], 3, 3, 40, 1024), ([40000], 16, 2, 128, 32), ([300, 5], 20, 1, 96, 16),
+    ([6000] + [(11 * i) % 40 for i in range(330)], 1, 1, 128, 16),
+    ([700] * 330, 2, 1, 64, 16), ([2000, 0, 900], 128, 1, 64, 16)])
+def test_every_key_counts(lens, hq, hkv, d, page):
+    """Values for which each part of the keys, and each weight, moves O by many bounds."""
+    q, cache, table, n, codes, pairs, place = _decode_inputs(lens, hq, hkv, d, page, sum(lens) + d)
+    q, pairs = cache4_ref.telling(q, codes, pairs, place, 95)
+    _check(q, cache, table, n, codes, pairs, place)

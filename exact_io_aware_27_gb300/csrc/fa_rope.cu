@@ -302,7 +302,7 @@ int deal_sides(RopeParams& p, int total, int d, int per_sm) {
   const int sms = sm_count(), per = kPasses * (32 / rope_lanes(d));
   const int cq = ceil_div(p.q.heads, per), ck = ceil_div(p.k.heads, per);
   int blocks[2];
-  share_blocks<2>(blocks, {(long long)total * cq, (long long)total * ck}, {1, 1},
+  share_blocks<2>(blocks, {(long long)total * cq, (long long)total * ck},
                   (sms < kMaxSms ? sms : kMaxSms) * per_sm, kWarps);
   p.q.deal = deal(total, cq, blocks[0], kWarps);
   p.k.deal = deal(total, ck, blocks[1], kWarps);

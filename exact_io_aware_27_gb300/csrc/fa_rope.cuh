@@ -334,16 +334,15 @@ FA_DEV Piece piece_of(const Deal& d, int me) {
   return p;
 }
 
-// Thread blocks of each of N kinds: `most` in all, shared out by items times cost, one at least
-// where there is an item, and no more than there are items for.
+// Thread blocks of each of N kinds: `most` in all, shared out by items, one at least where there
+// is an item, and no more than there are items for.
 template <int N>
-void share_blocks(int (&blocks)[N], const long long (&items)[N], const int (&cost)[N], int most,
-                  int warps) {
+void share_blocks(int (&blocks)[N], const long long (&items)[N], int most, int warps) {
   long long all = 0;
-  for (int i = 0; i < N; ++i) all += items[i] * cost[i];
+  for (int i = 0; i < N; ++i) all += items[i];
   for (int i = 0; i < N; ++i) {
     const long long need = (items[i] + warps - 1) / warps;
-    long long b = all > 0 ? (long long)((double)most * items[i] * cost[i] / all) : 0;
+    long long b = all > 0 ? (long long)((double)most * items[i] / all) : 0;
     if (b < 1) b = 1;
     blocks[i] = (int)(b < need ? b : need);
   }

@@ -9,8 +9,10 @@ The cache is one uint8 tensor [pages, Hkv, page / 16, bytes of 16 rows]: 72 byte
 and group of 64 channels for K and V together, against 256 in bf16. Every row has a scale and
 a minimum per group, and a code of 0 to 15 per channel. Position p of request i lies in row
 p % page of page block_table[i, p // page], as in the bf16 cache. fa_cache4_append norms and
-turns queries and keys like fa_rope_append; fa_cache4_read gives rows back in bf16, for the
-attention of prompts that come in chunks (fa_packed_forward on what the cache holds).
+turns queries and keys like fa_rope_append; fa_cache4_read gives rows back in bf16, for
+attention of several tokens to what the cache holds. fa_packed_forward has as many queries as
+keys in each sequence: a prompt's next chunk goes through it with rows of zeros for the queries
+before the chunk, whose products are computed too.
 """
 from __future__ import annotations
 

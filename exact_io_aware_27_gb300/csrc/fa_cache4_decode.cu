@@ -24,14 +24,19 @@
 // Each warp has a ring of two stages of 32 keys, two bulk copies each; the values of a run (a
 // unit, or the part of it in a worker's piece) that are the same in all lanes are told to be so
 // (uniform()), which takes them out of the registers that the products need. That, and 32 keys
-// at a time instead of 16, is what 12 warps an SM with 168 registers each allow.
+// at a time instead of 16, is what 12 warps an SM with 168 registers each allow (d > 64, up to 8
+// queries; pieces of blocks spill 32 bytes, single warps none). With 16 queries it is 8 warps
+// of 254 registers, and 32 to 64 bytes spilled.
 //
-// Bound by instructions, just before memory: about 520 a warp for 32 keys (d = 128), 176 of them
-// to take codes apart. 256 requests of up to 8192 keys, 32/8 heads, d = 128 (1.2 GB): 201 us,
-// 6.0 TB/s, 88 % of the measured copy rate; with all keys in L2 it takes as long. The first
-// form, 16 keys a step with the codes as bf16 values 128 + code, took 385 us. 32 requests of up
-// to 4096 keys (73 MB): 23 us, of which 3.5 until the first keys are there, 13 at that rate,
-// and the rest the ends of units and the join.
+// Bound by chains of dependent instructions with few warps to hide them, just before memory:
+// about 520 a warp for 32 keys (d = 128), 176 of them to take codes apart. No unit is at its
+// limit (55 % of the issue slots, 56 % of the ALU's, 27 % of the products'); of the 4.9 cycles
+// from one instruction of a warp to its next, 1.3 are latencies of a fixed length, 0.8 lost to
+// another warp, 0.7 a busy pipe, and 0.4 waits for memory. 256 requests of up to 8192 keys, 32/8
+// heads, d = 128 (1.2 GB): 203 us, 5.9 TB/s, 87 % of the measured copy rate; with all keys in L2
+// it takes as long. The first form, 16 keys a step with the codes as bf16 values 128 + code,
+// took 385 us. 32 requests of up to 4096 keys (73 MB): 23.7 us, of which 3.5 until the first keys
+// are there, 13 at that rate, and the rest the ends of units and the join.
 #include "fa_cache4.cuh"
 #include "fa_decode.h"
 #include "fa_launch.h"

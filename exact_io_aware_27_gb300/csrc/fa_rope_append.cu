@@ -7,8 +7,11 @@
 // V of one token after another, all warps side by side, and looks a request up only where
 // another one begins. 32768 rows of 32/8 heads, d = 128, into the bf16 cache: 137 us (805 MB,
 // 5.9 TB/s, 87 % of the measured copy rate). Into the cache in 4 bits the codes cost about as many
-// instructions as norm and rotation together, and the kernel is bound by those: 8192 rows 49 us
-// (177 MB). Indices are checked as in fa_cache.cu: a place out of range is not written and
+// instructions as norm and rotation together: 8192 rows 49 us (177 MB, 26 at the copy rate). No
+// unit is at its limit there (67 % of the issue slots, 47 % of the ALU's); a pass over two rows
+// is one chain of sums, exchanges, extremes and quotients, and 20 warps an SM do not hide it (of
+// 6.6 cycles from one instruction of a warp to its next, 1.7 are latencies of a fixed length,
+// 1.2 lost to another warp, 0.8 shuffles and shared memory, 0.7 a busy pipe, 0.6 memory). Indices are checked as in fa_cache.cu: a place out of range is not written and
 // raises kDeviceIndexBit, and so do bounds that break the rule.
 #include "fa_cache4.cuh"
 #include "fa_launch.h"

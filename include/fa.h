@@ -409,7 +409,8 @@ FA_API int fa_rope_append(const void* Q, const void* K, const void* V, long long
  * values in fp32. One kernel launch.
  *
  * fa_cache4_read: rows back in bf16, for attention of more than one token to what the cache
- * holds: rows [cu_seqlens[i], cu_seqlens[i + 1]) of K and V, bf16 [total, Hkv, d], dense, are
+ * holds (fa_packed_forward wants as many queries as keys: those before a chunk's may be zeros,
+ * and are computed): rows [cu_seqlens[i], cu_seqlens[i + 1]) of K and V, bf16 [total, Hkv, d], dense, are
  * positions starts[i], starts[i] + 1, ... of request i. Bounds as in fa_cache_append. Rows
  * behind the last request, and rows whose place is out of range (FA_ERR_BAD_INDEX in
  * fa_get_device_status()), are left as they were, or set to 0 where `fill` is 1. One launch.

@@ -202,3 +202,15 @@ def test_every_key_counts(lens, hq, hkv, d, page):
     q, cache, table, n, codes, pairs, place = _decode_inputs(lens, hq, hkv, d, page, sum(lens) + d)
     q, pairs = cache4_ref.telling(q, codes, pairs, place, 95)
     _check(q, cache, table, n, codes, pairs, place)
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d", [
+    ([300, 40], 8, 2, 128), ([5000, 1, 700], 16, 2, 128), ([700, 0, 33] * 170, 4, 1, 64),
+    ([6000] + [40] * 400, 3, 1, 128)])
+def test_the_same_bits_each_time(lens, hq, hkv, d):
+    """One launch, pieces by blocks and by warps, and rows joined by blocks."""
+    q, cache, table, n, *_ = _decode_inputs(lens, hq, hkv, d, 16, 97)
+    O, L = fa.fa_cache4_decode(q, cache, table, n)
+    for _ in range(5):
+        o, l = fa.fa_cache4_decode(q, cache, table, n)
+        assert torch.equal(o, O) and torch.equal(l, L)

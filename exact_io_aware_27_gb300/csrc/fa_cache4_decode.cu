@@ -226,9 +226,9 @@ FA_DEV float about_inverse(float x) {
   asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// The power of two at or below x, at least 2^-100.
+// The power of two at or below x, at least 2^-118.
 FA_DEV float power_of_two(float x) {
-  return fmaxf(__uint_as_float(__float_as_uint(x) & 0x7f800000u), 0x1p-100f);
+  return fmaxf(__uint_as_float(__float_as_uint(x) & 0x7f800000u), 0x1p-118f);
 }
 // An 8 x 8 matrix of 16-bit values, a row of it in four lanes, transposed.
 FA_DEV uint32_t transpose8(uint32_t v) {

@@ -104,6 +104,17 @@ def test_large_queries_of_ordinary_scores(size, small, hq, d):
         _check(q, cache, table, lens, codes, _scaled(pairs, 0, 2.0 ** -size), place)
 
 
+@pytest.mark.parametrize("size", [100, 116, 121, 125])
+@pytest.mark.parametrize("hq,d", [(4, 64), (16, 128)])
+def test_small_queries_of_ordinary_scores(size, hq, d):
+    """Queries of 2^-size whose scores are ordinary by the keys."""
+    q, cache, table, lens, codes, pairs, place = _decode_inputs([300, 17], hq, 1, d, 16, 98 + d)
+    by = min(size, 120)
+    q = (q.double() * 2.0 ** -size).to(torch.bfloat16)
+    _check(q, cache, table, lens, codes, _scaled(pairs, 0, 2.0 ** by), place,
+           scale=2.0 ** (size - by + 1) / math.sqrt(d))
+
+
 @pytest.mark.parametrize("size", [10, 20, 27, 31, 33, 40, 80, 100, 112])
 @pytest.mark.parametrize("lens", [[300], [2000, 5], [40] * 330, [40] * 500])
 @pytest.mark.parametrize("sign", [1, -1])
